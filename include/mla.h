@@ -350,6 +350,116 @@ int mla_prefill_attn(const void *q, const void *k, const void *v,
                      void *out, float *lse, mla_stream_t stream);
 
 /* ---------------------------------------------------------------------
+ * Block-scaled 8-bit cache
+ * An e4m3 cache [num_blocks,64,576] with one fp32 scale for each block of
+ * scale_block tokens (16, 32 or 64) of its one latent head: kv_scales
+ * [num_blocks, 64/scale_block], element (s, c) of the cache standing for
+ *   kv_scales[s/64, (s%64)/scale_block] * e4m3(kv_cache[s, c])
+ * (s = block*64 + offset).  No calibration is needed: mla_rope_cache_append
+ * finds the scales, mla_decode_paged_scaled and mla_gather_cache_scaled
+ * read them.  Scales are >= 0 and finite.
+ *
+ * Append: mla_rope_cache_write for this cache.  For each new token t < T
+ *   q_out[t,h,:] = R(positions[t]) q_pe[t,h,:]      (h < H)
+ *   k_out[t,:]   = R(positions[t]) k_pe[t,:]
+ * with the rotation R of mla_rope_cache_write, and row slot_mapping[t] of
+ * the cache receives kv_c[t] || k_out[t].  For every block that the call
+ * writes to, with A the largest finite |element| of its new rows and s the
+ * block's scale (0 if the call writes the block's first row: it begins
+ * afresh; likewise if s is not a positive finite number),
+ *   s' = max(s, 2^max(-100, ceil(log2(A / 448))))
+ * becomes its scale, the new rows are stored as e4m3(x / s'), and if
+ * 0 < s < s' the block's other rows are stored again as e4m3(code * (s/s'))
+ * (a power of two where the append found s: only values that fall below the
+ * e4m3 normal range are rounded).  Rounding is to nearest even, infinities
+ * saturate, NaN stays NaN.  Rows of blocks that the call does not write to
+ * keep their bits.  Tokens of a block may stand anywhere in the call; where
+ * a slot comes up twice the later token's row stays.  A negative slot is
+ * padding: its q and k are rotated and nothing is stored; a slot >=
+ * num_blocks*64 does the same and sets MLA_DEVERR_BLOCK_ID.
+ *
+ * q_pe [T,H,64] bf16 with strides q_stride_t, q_stride_h (elements), NULL:
+ * no query; k_pe [T,64] with row stride k_stride; kv_c [T,512] with row
+ * stride c_stride (all rows start on 16 bytes: the strides are multiples of
+ * 8, so slices of one projection's output are read in place).  q_out
+ * [T,H,64], k_out [T,64] contiguous, or NULL: rotated in place.  positions,
+ * slot_mapping [T] int32.  1 < rope_base < inf, 1 <= H <= 4096 with a
+ * query, num_blocks < 2^25.  T == 0 is a no-op. */
+int mla_rope_cache_append(void *q_pe, int64_t q_stride_t, int64_t q_stride_h,
+                          void *k_pe, int64_t k_stride, const void *kv_c,
+                          int64_t c_stride, const int32_t *positions,
+                          const int32_t *slot_mapping, int T, int H,
+                          float rope_base, int rope_layout, void *q_out,
+                          void *k_out, void *kv_cache, float *kv_scales,
+                          int scale_block, int num_blocks,
+                          mla_stream_t stream);
+
+/* Gather: mla_gather_cache out of a block-scaled cache,
+ *   out[cu_out[b] + j] = bf16(RNE)(scale * fp32(e4m3))
+ * rows, ranges and errors as there. */
+int mla_gather_cache_scaled(const void *kv_cache, const float *kv_scales,
+                            int scale_block, const int32_t *block_table,
+                            const int32_t *seq_lens,
+                            const int32_t *seq_starts, const int32_t *cu_out,
+                            int B, int max_blocks, int num_blocks,
+                            int total_rows, void *out, mla_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Decode with a sliding window and sinks, and over a block-scaled cache
+ * For request b, query token i < q_len at position p = seq_lens[b] - q_len
+ * + i (the new tokens are in the cache), head h:
+ *   visible: j <= p and (window == 0 or j > p - window or j < sinks)
+ *   s_j  = sm_scale * q_deq[b,i,h,:] . K_j
+ *   lse[b,i,h] = ln sum_j exp(s_j),  out[b,i,h,:] = sum_j exp(s_j - lse) V_j
+ * over the visible j; no visible key (p < 0): out = 0, lse = -inf.  K_j, V_j,
+ * q_deq, slots and layouts as in mla_decode_paged; in the scaled form kv_deq
+ * takes the block's scale in place of k_scale and q is e4m3.
+ * Cache rows that no query token of a request sees (past seq_lens, behind
+ * the window) are never used, whatever they hold, and block-table entries
+ * of pages without a visible key are not read.
+ * window >= 0 (0: every earlier token), sinks >= 0 (of no effect without a
+ * window).  workspace: mla_decode_window_workspace_size(B, q_len, H,
+ * max_blocks*64, window, sinks, split_tiles) bytes, 16-byte aligned, written before it
+ * is read (calls on different streams need workspaces of their own).
+ * split_tiles as in mla_decode_paged, in tiles of 128 tokens.  Limits as
+ * there. */
+int mla_decode_window_workspace_size(int B, int q_len, int H, int max_seq_len,
+                                     int window, int sinks, int split_tiles,
+                                     size_t *bytes);
+
+int mla_decode_paged_window(const void *q, int q_dtype, float q_scale,
+                            const void *kv_cache, int kv_dtype, float k_scale,
+                            const int32_t *block_table,
+                            const int32_t *seq_lens, int B, int q_len, int H,
+                            int max_blocks, int num_blocks, float sm_scale,
+                            int window, int sinks, int split_tiles, void *out,
+                            int out_dtype, float *lse, void *workspace,
+                            size_t ws_bytes, mla_stream_t stream);
+
+int mla_decode_paged_scaled(const void *q, float q_scale, const void *kv_cache,
+                            const float *kv_scales, int scale_block,
+                            const int32_t *block_table,
+                            const int32_t *seq_lens, int B, int q_len, int H,
+                            int max_blocks, int num_blocks, float sm_scale,
+                            int window, int sinks, int split_tiles, void *out,
+                            int out_dtype, float *lse, void *workspace,
+                            size_t ws_bytes, mla_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Prefill attention with a sliding window and sinks
+ * mla_prefill_attn, causal, where query i of a request with nq queries and
+ * nk keys stands at p = i + nk - nq and sees the keys
+ *   j <= p and (j > p - window or j < sinks),     window >= 1, sinks >= 0.
+ * The window is the same whether the keys before the queries are new tokens
+ * or gathered context, so one call attends to both.  What a query does not
+ * see does not reach its row, NaN and infinities included. */
+int mla_prefill_attn_window(const void *q, const void *k, const void *v,
+                            const int32_t *cu_q, const int32_t *cu_k, int B,
+                            int Tq, int Nk, int H, int max_q_len, int window,
+                            int sinks, float sm_scale, void *out, float *lse,
+                            mla_stream_t stream);
+
+/* ---------------------------------------------------------------------
  * Host staging of a step's inputs and results
  * [BLOG] §MLA Prefill vs Decode (each decode step takes the new tokens'
  * queries in and hands the attention output on).  No page defines the

@@ -23,7 +23,9 @@ __all__ = [
     "mla_absorb_q", "mla_decode_workspace_size", "mla_decode_paged",
     "mla_decode_plan", "mla_merge_states", "mla_v_up", "mla_gather_cache",
     "mla_gather_cache_reorg", "mla_expand_kv", "mla_prefill_attn", "mla_rope_cache_write",
-    "mla_stage_copy",
+    "mla_stage_copy", "mla_rope_cache_append", "mla_gather_cache_scaled",
+    "mla_decode_window_workspace_size", "mla_decode_paged_window", "mla_decode_paged_scaled",
+    "mla_prefill_attn_window",
 ]
 
 BF16, E4M3, F32 = 0, 1, 2
@@ -31,6 +33,7 @@ _DTYPE_CODE = {torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3, torch.float32: F
 _CODE_DTYPE = {v: k for k, v in _DTYPE_CODE.items()}
 
 _p, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 _SIGNATURES = {
     "mla_status_string": ([_i], ctypes.c_char_p),
@@ -53,6 +56,16 @@ _SIGNATURES = {
     "mla_prefill_attn": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p], _i),
     "mla_rope_cache_write": ([_p, _p, _p, _p, _p, _i, _i, _f, _i, _p, _i, _f, _i, _p], _i),
     "mla_stage_copy": ([_p, _p, _sz, _p], _i),
+    "mla_rope_cache_append": ([_p, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i, _i, _f, _i, _p, _p,
+                               _p, _p, _i, _i, _p], _i),
+    "mla_gather_cache_scaled": ([_p, _p, _i, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p], _i),
+    "mla_decode_window_workspace_size": ([_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)], _i),
+    "mla_decode_paged_window": ([_p, _i, _f, _p, _i, _f, _p, _p, _i, _i, _i, _i, _i, _f, _i, _i,
+                                 _i, _p, _i, _p, _p, _sz, _p], _i),
+    "mla_decode_paged_scaled": ([_p, _f, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _f, _i, _i, _i,
+                                 _p, _i, _p, _p, _sz, _p], _i),
+    "mla_prefill_attn_window": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p],
+                                _i),
 }
 
 
@@ -347,6 +360,215 @@ def mla_rope_cache_write(q_pe, k_pe, kv_c, positions, slot_mapping, kv_cache, *,
         _ptr(q_pe), _ptr(k_pe), _ptr(kv_c), _ptr(positions), _ptr(slot_mapping), T, H,
         float(rope_base), _ROPE_LAYOUT[layout], _ptr(kv_cache), _DTYPE_CODE[kv_cache.dtype],
         float(k_scale), kv_cache.shape[0], _stream()))
+
+
+def _scale_block(kv_scales, kv_cache):
+    """Tokens per scale of kv_scales [num_blocks, 64 / scale_block]."""
+    _req(kv_scales, "kv_scales", torch.float32, 2)
+    if kv_scales.shape[0] != kv_cache.shape[0] or kv_scales.shape[1] not in (1, 2, 4):
+        raise ValueError("kv_scales must be [num_blocks, 64 / scale_block], scale_block 16, 32 or 64")
+    return 64 // kv_scales.shape[1]
+
+
+def _same_device(first, **others):
+    """Every tensor on the device of the first, which is the current one."""
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device}, not on the current device")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+
+
+def _rows(t, name, dims):
+    """A bf16 CUDA tensor whose last dim is contiguous; the others may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype} is not torch.bfloat16")
+    if t.dim() != dims:
+        raise ValueError(f"{name}: expected {dims} dims, got {tuple(t.shape)}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dim must be contiguous")
+    return t
+
+
+def mla_rope_cache_append(q_pe, k_pe, kv_c, positions, slot_mapping, kv_cache, kv_scales, *,
+                          rope_base=10000.0, layout="interleaved", q_out=None, k_out=None):
+    """Rotates q_pe [T,H,64] (or None) and k_pe [T,64] (bf16) by positions [T]
+    into q_out / k_out (None: in place) and appends kv_c [T,512] ‖ k_pe rows at
+    slot_mapping [T] (int32) to the block-scaled cache kv_cache [num_blocks,64,576]
+    e4m3, kv_scales [num_blocks, 64/scale_block] fp32, both updated.  q_pe, k_pe
+    and kv_c may be strided (slices of one projection): strides and offsets of
+    8 elements.  Returns (q_out, k_out)."""
+    _rows(k_pe, "k_pe", 2)
+    _rows(kv_c, "kv_c", 2)
+    _req(positions, "positions", torch.int32, 1)
+    _req(slot_mapping, "slot_mapping", torch.int32, 1)
+    _req(kv_cache, "kv_cache", torch.float8_e4m3fn, 3)
+    T, H, qt, qh = k_pe.shape[0], 0, 0, 0
+    if q_pe is not None:
+        _rows(q_pe, "q_pe", 3)
+        if q_pe.shape[0] != T or q_pe.shape[2] != 64:
+            raise ValueError("q_pe must be [T, H, 64]")
+        H, qt, qh = q_pe.shape[1], q_pe.stride(0), q_pe.stride(1)
+    if (k_pe.shape[1] != 64 or tuple(kv_c.shape) != (T, 512) or positions.shape[0] != T
+            or slot_mapping.shape[0] != T or tuple(kv_cache.shape[1:]) != (64, 576)):
+        raise ValueError("rope / cache-append shapes")
+    sb = _scale_block(kv_scales, kv_cache)
+    if q_out is not None:
+        _req(q_out, "q_out", torch.bfloat16, 3)
+        if q_pe is None or q_out.shape != q_pe.shape:
+            raise ValueError("q_out must have q_pe's shape")
+    if k_out is not None:
+        _req(k_out, "k_out", torch.bfloat16, 2)
+        if k_out.shape != k_pe.shape:
+            raise ValueError("k_out must have k_pe's shape")
+    _same_device(kv_cache, q_pe=q_pe, k_pe=k_pe, kv_c=kv_c, positions=positions,
+                 slot_mapping=slot_mapping, kv_scales=kv_scales, q_out=q_out, k_out=k_out)
+    _check("mla_rope_cache_append", lib.mla_rope_cache_append(
+        _ptr(q_pe), qt, qh, _ptr(k_pe), k_pe.stride(0), _ptr(kv_c), kv_c.stride(0),
+        _ptr(positions), _ptr(slot_mapping), T, H, float(rope_base), _ROPE_LAYOUT[layout],
+        _ptr(q_out), _ptr(k_out), _ptr(kv_cache), _ptr(kv_scales), sb, kv_cache.shape[0],
+        _stream()))
+    return (q_pe if q_out is None else q_out), (k_pe if k_out is None else k_out)
+
+
+def mla_gather_cache_scaled(kv_cache, kv_scales, block_table, seq_lens, cu_out, total_rows, *,
+                            seq_starts=None, out=None):
+    """mla_gather_cache out of a block-scaled e4m3 cache, as bf16 rows [total_rows, 576]."""
+    _req(kv_cache, "kv_cache", torch.float8_e4m3fn, 3)
+    _req(block_table, "block_table", torch.int32, 2)
+    _req(seq_lens, "seq_lens", torch.int32, 1)
+    _req(cu_out, "cu_out", torch.int32, 1)
+    B = block_table.shape[0]
+    if (tuple(kv_cache.shape[1:]) != (64, 576) or seq_lens.shape[0] != B
+            or cu_out.shape[0] != B + 1):
+        raise ValueError("gather shapes")
+    if seq_starts is not None:
+        _req(seq_starts, "seq_starts", torch.int32, 1)
+        if seq_starts.shape[0] != B:
+            raise ValueError("seq_starts must be [B]")
+    sb = _scale_block(kv_scales, kv_cache)
+    if out is None:
+        out = torch.empty((total_rows, 576), dtype=torch.bfloat16, device=kv_cache.device)
+    _req(out, "out", torch.bfloat16, 2)
+    if tuple(out.shape) != (total_rows, 576):
+        raise ValueError("out must be [total_rows, 576]")
+    _same_device(kv_cache, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens,
+                 cu_out=cu_out, seq_starts=seq_starts, out=out)
+    _check("mla_gather_cache_scaled", lib.mla_gather_cache_scaled(
+        _ptr(kv_cache), _ptr(kv_scales), sb, _ptr(block_table), _ptr(seq_lens), _ptr(seq_starts),
+        _ptr(cu_out), B, block_table.shape[1], kv_cache.shape[0], int(total_rows), _ptr(out),
+        _stream()))
+    return out
+
+
+def mla_decode_window_workspace_size(B, q_len, H, max_seq_len, window=0, sinks=0,
+                                     split_tiles=0) -> int:
+    n = _sz(0)
+    _check("mla_decode_window_workspace_size", lib.mla_decode_window_workspace_size(
+        B, q_len, H, max_seq_len, int(window), int(sinks), int(split_tiles), ctypes.byref(n)))
+    return n.value
+
+
+def _decode_window_args(q, kv_cache, block_table, seq_lens, window, sinks, split_tiles, out_dtype,
+                        out, lse, workspace, **others):
+    """Checks and allocations that the two windowed decodes share."""
+    _req(q, "q", (torch.bfloat16, torch.float8_e4m3fn), 4)
+    B, q_len, H, D = q.shape
+    _req(kv_cache, "kv_cache", q.dtype, 3)
+    _req(block_table, "block_table", torch.int32, 2)
+    _req(seq_lens, "seq_lens", torch.int32, 1)
+    if D != 576 or tuple(kv_cache.shape[1:]) != (64, 576) or block_table.shape[0] != B \
+            or seq_lens.shape[0] != B:
+        raise ValueError("decode shapes")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype {out_dtype} is neither bf16 nor fp32")
+    if out is None:
+        out = torch.empty((B, q_len, H, 512), dtype=out_dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, q_len, H), dtype=torch.float32, device=q.device)
+    _req(out, "out", out_dtype, 4)
+    _req(lse, "lse", torch.float32, 3)
+    if tuple(out.shape) != (B, q_len, H, 512) or tuple(lse.shape) != (B, q_len, H):
+        raise ValueError("out must be [B, q_len, H, 512] and lse [B, q_len, H]")
+    if workspace is None:
+        n = mla_decode_window_workspace_size(B, q_len, H, block_table.shape[1] * 64, window,
+                                             sinks, split_tiles)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _req(workspace, "workspace", torch.uint8, 1)
+    _same_device(q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, out=out,
+                 lse=lse, workspace=workspace, **others)
+    return out, lse, workspace
+
+
+def mla_decode_paged_window(q, kv_cache, block_table, seq_lens, *, sm_scale, window, sinks=0,
+                            q_scale=1.0, k_scale=1.0, split_tiles=0, out_dtype=torch.bfloat16,
+                            out=None, lse=None, workspace=None):
+    """mla_decode_paged (causal) where a query at position p sees the keys
+    j > p - window and the first `sinks` (window 0: every earlier key)."""
+    out, lse, workspace = _decode_window_args(q, kv_cache, block_table, seq_lens, window, sinks,
+                                              split_tiles, out_dtype, out, lse, workspace)
+    B, q_len, H, _ = q.shape
+    _check("mla_decode_paged_window", lib.mla_decode_paged_window(
+        _ptr(q), _DTYPE_CODE[q.dtype], float(q_scale), _ptr(kv_cache),
+        _DTYPE_CODE[kv_cache.dtype], float(k_scale), _ptr(block_table), _ptr(seq_lens), B, q_len,
+        H, block_table.shape[1], kv_cache.shape[0], float(sm_scale), int(window), int(sinks),
+        int(split_tiles), _ptr(out), _DTYPE_CODE[out_dtype], _ptr(lse), _ptr(workspace),
+        workspace.numel(), _stream()))
+    return out, lse
+
+
+def mla_decode_paged_scaled(q, kv_cache, kv_scales, block_table, seq_lens, *, sm_scale,
+                            q_scale=1.0, window=0, sinks=0, split_tiles=0,
+                            out_dtype=torch.bfloat16, out=None, lse=None, workspace=None):
+    """mla_decode_paged_window over a block-scaled e4m3 cache (q e4m3,
+    kv_scales [num_blocks, 64/scale_block] fp32)."""
+    _req(q, "q", torch.float8_e4m3fn, 4)
+    _req(kv_cache, "kv_cache", torch.float8_e4m3fn, 3)
+    sb = _scale_block(kv_scales, kv_cache)
+    out, lse, workspace = _decode_window_args(q, kv_cache, block_table, seq_lens, window, sinks,
+                                              split_tiles, out_dtype, out, lse, workspace,
+                                              kv_scales=kv_scales)
+    B, q_len, H, _ = q.shape
+    _check("mla_decode_paged_scaled", lib.mla_decode_paged_scaled(
+        _ptr(q), float(q_scale), _ptr(kv_cache), _ptr(kv_scales), sb, _ptr(block_table),
+        _ptr(seq_lens), B, q_len, H, block_table.shape[1], kv_cache.shape[0], float(sm_scale),
+        int(window), int(sinks), int(split_tiles), _ptr(out), _DTYPE_CODE[out_dtype], _ptr(lse),
+        _ptr(workspace), workspace.numel(), _stream()))
+    return out, lse
+
+
+def mla_prefill_attn_window(q, k, v, cu_q, cu_k, max_q_len, *, window, sinks=0, sm_scale, out=None,
+                            lse=None):
+    """mla_prefill_attn (causal) where a query at position p of its request sees
+    the keys j > p - window and the first `sinks`."""
+    _req(q, "q", torch.bfloat16, 3)
+    _req(k, "k", torch.bfloat16, 3)
+    _req(v, "v", torch.bfloat16, 3)
+    _req(cu_q, "cu_q", torch.int32, 1)
+    _req(cu_k, "cu_k", torch.int32, 1)
+    Tq, H, _ = q.shape
+    Nk = k.shape[0]
+    B = cu_q.shape[0] - 1
+    if q.shape[2] != 192 or tuple(k.shape) != (Nk, H, 192) or tuple(v.shape) != (Nk, H, 128) \
+            or cu_k.shape[0] != B + 1:
+        raise ValueError("prefill shapes")
+    if out is None:
+        out = torch.empty((Tq, H, 128), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
+    _req(out, "out", torch.bfloat16, 3)
+    _req(lse, "lse", torch.float32, 2)
+    if tuple(out.shape) != (Tq, H, 128) or tuple(lse.shape) != (Tq, H):
+        raise ValueError("out must be [Tq, H, 128] and lse [Tq, H]")
+    _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
+    _check("mla_prefill_attn_window", lib.mla_prefill_attn_window(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), B, Tq, Nk, H, int(max_q_len),
+        int(window), int(sinks), float(sm_scale), _ptr(out), _ptr(lse), _stream()))
+    return out, lse
 
 
 def mla_stage_copy(dst, src):

@@ -24,7 +24,8 @@ namespace {
 constexpr int kWarpsPerBlock = 8;
 constexpr int kMaxShards = 16;
 
-enum CopyMode { kCopyBf16 = 0, kCopyE4m3 = 1, kDequant = 2 };
+// kDequantRows: each row has a scale of its own (block-scaled cache)
+enum CopyMode { kCopyBf16 = 0, kCopyE4m3 = 1, kDequant = 2, kDequantRows = 3 };
 
 // Largest b in [0, n) with cu[b] <= row (cu non-decreasing, cu[0] <= row).
 __device__ __forceinline__ int find_segment(const int32_t *cu, int n, int row) {
@@ -61,6 +62,7 @@ __device__ __forceinline__ uint4 dequant8(uint2 v, float k_scale) {
 // holds row i's source (nullptr: the row is zeroed) and destination
 // (nullptr: the row is not written).  Lanes take consecutive 16-byte output
 // chunks, so every load and store instruction covers whole rows' runs.
+// kDequantRows: lane i < 8 holds row i's scale in k_scale.
 template <int MODE>
 __device__ __forceinline__ void copy_rows(const uint8_t *src_lane, uint8_t *dst_lane,
                                           float k_scale, int lane) {
@@ -76,8 +78,10 @@ __device__ __forceinline__ void copy_rows(const uint8_t *src_lane, uint8_t *dst_
     const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, s64, row));
     if (!src) {
       v[i] = make_uint4(0, 0, 0, 0);
-    } else if (MODE == kDequant) {
-      v[i] = dequant8(__ldcs(reinterpret_cast<const uint2 *>(src) + c), k_scale);
+    } else if (MODE == kDequant || MODE == kDequantRows) {
+      const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(src) + c);
+      if (MODE == kDequant) v[i] = dequant8(w, k_scale);
+      else v[i] = make_uint4(w.x, w.y, 0, 0);   // all loads first, then the scales
     } else {
       v[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + c);
     }
@@ -86,6 +90,10 @@ __device__ __forceinline__ void copy_rows(const uint8_t *src_lane, uint8_t *dst_
   for (int i = 0; i < N; ++i) {
     const int idx = lane + 32 * i, row = idx / C, c = idx - row * C;
     uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, d64, row));
+    if (MODE == kDequantRows) {
+      const float scale = __shfl_sync(0xffffffffu, k_scale, row);
+      v[i] = dequant8(make_uint2(v[i].x, v[i].y), scale);
+    }
     if (dst) reinterpret_cast<uint4 *>(dst)[c] = v[i];
   }
 }
@@ -97,7 +105,8 @@ gather_kernel(const uint8_t *__restrict__ cache, int in_row_bytes,
               const int32_t *__restrict__ seq_lens,
               const int32_t *__restrict__ seq_starts,
               const int32_t *__restrict__ cu_out, int B, int max_blocks,
-              int num_blocks, int total_rows, float k_scale, uint8_t *out,
+              int num_blocks, int total_rows, float k_scale,
+              const float *__restrict__ scales, int sb_shift, uint8_t *out,
               int out_row_bytes, int *err) {
   const int lane = threadIdx.x & 31;
   const int row0 = (blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5)) * kRowsPerWarp;
@@ -118,6 +127,8 @@ gather_kernel(const uint8_t *__restrict__ cache, int in_row_bytes,
       const int blk = __ldg(block_table + static_cast<int64_t>(b) * max_blocks + pos / kPage);
       if (blk < 0 || blk >= num_blocks) raise_error(err, MLA_DEVERR_BLOCK_ID);
       else src = cache + (static_cast<int64_t>(blk) * kPage + pos % kPage) * in_row_bytes;
+      if (MODE == kDequantRows && src)
+        k_scale = __ldg(scales + ((static_cast<int64_t>(blk) * kPage + pos % kPage) >> sb_shift));
     }
   }
   copy_rows<MODE>(src, dst, k_scale, lane);
@@ -243,11 +254,35 @@ extern "C" int mla_gather_cache(const void *kv_cache, int kv_dtype,
 #define MLA_GATHER(M)                                                        \
   gather_kernel<M><<<grid, kWarpsPerBlock * 32, 0, stream>>>(                \
       src, in_bytes, block_table, seq_lens, seq_starts, cu_out, B,           \
-      max_blocks, num_blocks, total_rows, k_scale, dst, out_bytes, err)
+      max_blocks, num_blocks, total_rows, k_scale, nullptr, 0, dst, out_bytes, err)
   if (mode == kCopyBf16) MLA_GATHER(kCopyBf16);
   else if (mode == kCopyE4m3) MLA_GATHER(kCopyE4m3);
   else MLA_GATHER(kDequant);
 #undef MLA_GATHER
+  return launch_status();
+}
+
+extern "C" int mla_gather_cache_scaled(const void *kv_cache, const float *kv_scales,
+                                       int scale_block, const int32_t *block_table,
+                                       const int32_t *seq_lens, const int32_t *seq_starts,
+                                       const int32_t *cu_out, int B, int max_blocks,
+                                       int num_blocks, int total_rows, void *out,
+                                       mla_stream_t stream) {
+  if (B < 1 || max_blocks < 1 || num_blocks < 1 || num_blocks >= (1 << 25) || total_rows < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (scale_block != 16 && scale_block != 32 && scale_block != 64) return MLA_ERR_INVALID_ARG;
+  if (!kv_cache || !kv_scales || !block_table || !seq_lens || !cu_out || (total_rows && !out))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(kv_cache) || !aligned16(out)) return MLA_ERR_INVALID_ARG;
+  if (total_rows == 0) return MLA_OK;
+  int *err = device_error_word();
+  if (!err) return MLA_ERR_CUDA;
+  constexpr int kRowsPerBlock = kWarpsPerBlock * kRowsPerWarp;
+  const int grid = (total_rows - 1) / kRowsPerBlock + 1;
+  gather_kernel<kDequantRows><<<grid, kWarpsPerBlock * 32, 0, stream>>>(
+      static_cast<const uint8_t *>(kv_cache), kDqk, block_table, seq_lens, seq_starts, cu_out, B,
+      max_blocks, num_blocks, total_rows, 1.f, kv_scales,
+      scale_block == 64 ? 6 : scale_block == 32 ? 5 : 4, static_cast<uint8_t *>(out), kDqk * 2, err);
   return launch_status();
 }
 

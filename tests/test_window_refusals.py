@@ -1,0 +1,113 @@
+"""Arguments that the window and block-scaled-cache entry points refuse on
+the host, before any launch (no GPU needed)."""
+
+import ctypes
+
+import pytest
+
+P = ctypes.c_void_p
+OK, INVALID, WORKSPACE = 0, 1, 3
+A = P(1 << 20)                  # an aligned address that nothing reads
+ODD = P((1 << 20) + 8)
+
+
+@pytest.fixture(scope="module")
+def L():
+    import mla_latent_kv_uk_gb300 as m
+    return m.lib
+
+
+def _change(base, **kw):
+    a = dict(base)
+    a.update(kw)
+    return list(a.values())
+
+
+APPEND = dict(q=A, qt=64 * 4, qh=64, k=A, ks=64, c=A, cs=512, pos=A, slots=A, T=3, H=4, theta=1e4, layout=0,
+              q_out=A, k_out=A, cache=A, scales=A, sb=64, nb=5, s=P(0))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(T=-1), dict(H=0), dict(H=4097), dict(nb=0), dict(nb=1 << 25), dict(layout=2), dict(theta=1.0),
+    dict(theta=float("inf")), dict(theta=float("nan")), dict(sb=0), dict(sb=8), dict(sb=48), dict(sb=128),
+    dict(k=P(0)), dict(c=P(0)), dict(pos=P(0)), dict(slots=P(0)), dict(cache=P(0)), dict(scales=P(0)),
+    dict(q=P(0)),                                       # q_out without q_pe
+    dict(q=ODD), dict(k=ODD), dict(c=ODD), dict(cache=ODD), dict(q_out=ODD), dict(k_out=ODD),
+    dict(ks=60), dict(ks=56), dict(cs=516), dict(cs=504), dict(qt=260), dict(qh=68), dict(qh=56),
+    dict(qt=128), dict(qt=-256), dict(ks=-64)])
+def test_append(L, bad):
+    assert L.mla_rope_cache_append(*_change(APPEND, **bad)) == INVALID
+
+
+def test_append_no_tokens(L):
+    assert L.mla_rope_cache_append(*_change(APPEND, T=0, k=P(0), c=P(0), cache=P(0))) == OK
+
+
+GATHER = dict(cache=A, scales=A, sb=32, bt=A, lens=A, starts=P(0), cu=A, B=2, mb=3, nb=5, rows=7, out=A, s=P(0))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(cache=P(0)), dict(scales=P(0)), dict(bt=P(0)), dict(lens=P(0)), dict(cu=P(0)), dict(out=P(0)),
+    dict(sb=1), dict(sb=63), dict(B=0), dict(mb=0), dict(nb=0), dict(nb=1 << 25), dict(rows=-1),
+    dict(cache=ODD), dict(out=ODD)])
+def test_gather(L, bad):
+    assert L.mla_gather_cache_scaled(*_change(GATHER, **bad)) == INVALID
+
+
+def test_gather_no_rows(L):
+    assert L.mla_gather_cache_scaled(*_change(GATHER, rows=0, out=P(0))) == OK
+
+
+DECODE = dict(q=A, qd=0, qs=1.0, kv=A, kd=0, ks=1.0, bt=A, lens=A, B=2, q_len=1, H=16, mb=3, nb=5, sm=0.1,
+              window=64, sinks=4, split=0, out=A, od=0, lse=A, ws=A, n=1 << 40, s=P(0))
+BAD_DECODE = [
+    dict(B=0), dict(q_len=0), dict(q_len=65), dict(H=0), dict(H=4097), dict(mb=0), dict(mb=(1 << 24) + 1),
+    dict(nb=0), dict(nb=1 << 25), dict(sm=0.0), dict(sm=float("nan")), dict(sm=float("inf")),
+    dict(window=-1), dict(sinks=-1), dict(split=-1), dict(q=P(0)), dict(kv=P(0)), dict(bt=P(0)),
+    dict(lens=P(0)), dict(out=P(0)), dict(lse=P(0)), dict(od=1), dict(q=ODD), dict(kv=ODD), dict(out=ODD),
+    dict(ws=ODD), dict(B=1 << 16, q_len=64, H=4096)]
+
+
+@pytest.mark.parametrize("bad", BAD_DECODE + [
+    dict(qd=1), dict(kd=1), dict(qd=2, kd=2), dict(qd=1, kd=1, qs=0.0), dict(qd=1, kd=1, ks=-1.0),
+    dict(qd=1, kd=1, ks=float("nan"))])
+def test_decode_window(L, bad):
+    assert L.mla_decode_paged_window(*_change(DECODE, **bad)) == INVALID
+
+
+SCALED = dict(q=A, qs=1.0, kv=A, scales=A, sb=64, bt=A, lens=A, B=2, q_len=1, H=16, mb=3, nb=5, sm=0.1, window=0,
+              sinks=0, split=0, out=A, od=0, lse=A, ws=A, n=1 << 40, s=P(0))
+
+
+@pytest.mark.parametrize("bad", BAD_DECODE + [dict(scales=P(0)), dict(sb=0), dict(sb=24), dict(qs=0.0)])
+def test_decode_scaled(L, bad):
+    assert L.mla_decode_paged_scaled(*_change(SCALED, **bad)) == INVALID
+
+
+def test_decode_workspace(L):
+    assert L.mla_decode_paged_window(*_change(DECODE, ws=P(0))) == WORKSPACE
+    assert L.mla_decode_paged_window(*_change(DECODE, n=8)) == WORKSPACE
+    assert L.mla_decode_paged_scaled(*_change(SCALED, n=8)) == WORKSPACE
+    n = ctypes.c_size_t(0)
+    for bad in ((0, 1, 16, 64, 0, 0, 0), (1, 65, 16, 64, 0, 0, 0), (1, 1, 16, -1, 0, 0, 0),
+                (1, 1, 16, 64, -1, 0, 0), (1, 1, 16, 64, 0, -1, 0), (1, 1, 16, 64, 0, 0, -1)):
+        assert L.mla_decode_window_workspace_size(*bad, ctypes.byref(n)) == INVALID
+    assert L.mla_decode_window_workspace_size(1, 1, 16, 64, 0, 0, 0, None) == INVALID
+    assert L.mla_decode_window_workspace_size(1, 1, 16, 64, 8, 1, 0, ctypes.byref(n)) == OK and n.value > 0
+
+
+PREFILL = dict(q=A, k=A, v=A, cu_q=A, cu_k=A, B=1, Tq=4, Nk=8, H=2, mq=4, window=16, sinks=0, sm=0.1, out=A, lse=A,
+               s=P(0))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(window=0), dict(window=-3), dict(sinks=-1), dict(B=0), dict(B=65536), dict(Tq=-1), dict(Nk=-1), dict(H=0),
+    dict(H=65536), dict(mq=-1), dict(sm=0.0), dict(sm=float("nan")), dict(q=P(0)), dict(k=P(0)), dict(v=P(0)),
+    dict(cu_q=P(0)), dict(cu_k=P(0)), dict(out=P(0)), dict(lse=P(0)), dict(q=ODD), dict(k=ODD), dict(v=ODD),
+    dict(out=ODD)])
+def test_prefill_window(L, bad):
+    assert L.mla_prefill_attn_window(*_change(PREFILL, **bad)) == INVALID
+
+
+def test_prefill_window_no_queries(L):
+    assert L.mla_prefill_attn_window(*_change(PREFILL, Tq=0, q=P(0))) == OK
