@@ -1,113 +1,1004 @@
 // Paged latent decode with a sliding window and sinks, over a bf16, an e4m3
 // or a block-scaled e4m3 cache (mla_decode_paged_window, _scaled).
 //
-// One warp per (request, query token, head): 18 of the 576 dims per lane,
-// one visible key after the other with an online softmax.
+// Rows and keys.  The q_len * H query rows of a request (query token outer,
+// head inner) all attend to the same latent rows, so they are taken in groups
+// of 128: per tile of 128 keys S = Q K^T is a dense [128 x 128 x 576] product
+// and O += P V a [128 x 512 x 128] one.  A request's keys are a list of
+// 64-token pages, the sinks' pages and then those from the window's first key
+// to the last query; only the list's pages are loaded.  Each row masks the
+// keys that it does not see.
+//
+// CTA pairs.  The fp32 output of 128 rows x 512 columns would fill one SM's
+// tensor memory, so two CTAs of a cluster run each product as one
+// tcgen05 MMA of cta_group::2 with M = 128: CTA c holds rows [64c, 64c + 64)
+// of Q, S, P and O (S and O in the layout of that shape: lanes 0..63 the
+// first half of the columns, lanes 64..127 the second), for Q K^T the tile's
+// page c (64 of the 128 key columns), and for P V the value columns
+// [256c, 256c + 256) of all 128 keys.  Scores and probabilities never cross
+// the pair; each key row is fetched twice, once as a key by its page's CTA
+// and once, by then from L2, as a value by halves.  Measured on the GB300: a
+// 32-byte K step costs 44.5 cycles at N = 128 (Q K^T: 18 or 36 per tile) and
+// 64 cycles at N = 256 (P V: 8 steps for 128 e4m3 keys, 16 for bf16).
+//
+// e4m3 probabilities.  P as one e4m3 value would be off by up to 2^-4 and the
+// output with it; P is held as the sum of two e4m3 values, hi = e4m3(p) and
+// lo = e4m3(p - hi), at twice the P V steps: off by at most 2^-8 p, as bf16,
+// or by half a subnormal step (2^-10) where p < 2^-2 and the row's largest p
+// is at least 2^5.
+//
+// Block scales.  With sigma the scale of a key's block and c = sm_scale *
+// log2(e) * q_scale, the scores in the log2 domain are sigma * c * raw, and
+// P' = sigma * 2^(s - m) = 2^(raw * (sigma c) + log2 sigma - m) goes against
+// the raw codes of V: one FMA and one exponential per score whatever the
+// scales.  m follows the largest s + log2 sigma; the normaliser is
+// sum P' / sigma, summed per block before the division.
+//
+// Warps: 0 walks the split plan, publishes the segments and loads Q and K,
+// 1 issues the MMAs (leader CTA), 2 loads V, 4..7 turn scores into
+// probabilities (one row and half of the tile's keys per thread) and write
+// the results.  Lazy rescaling: O is rescaled when a row's reference would
+// be exceeded by more than 2^8.
+//
+// Split: every row group of a request is a job of ceil(pages / 2) tiles plus
+// kJobCost units for the switch; jobs lie end to end and pair p takes units
+// [pC, (p+1)C).  Each CTA works the plan out for itself from the lengths
+// (no plan kernel).  A job that is cut leaves partials in the workspace,
+// which a merge kernel combines: at most two per span, whatever the number
+// of jobs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <algorithm>
+#include <mutex>
+
 #include "common.cuh"
+#include "merge_row.cuh"
 #include "sm100.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kWarps = 8;
+using namespace sm100;
+
+constexpr int kTile = 128;                // keys per tile: two pages
+constexpr int kThreads = 256;
+constexpr int kMinUnits = 3;              // smallest automatic span
+constexpr int kJobCost = 2;               // units of switching to a job
+constexpr int kSegSlots = 4;
+constexpr uint32_t kColO = 0, kColS = 256;   // O [0,256), S [256,320) and [320,384)
+
+// What differs between the formats.  A chunk is 64 rows x 128 bytes of keys
+// or queries; K and V come through rings of slots.
+template <bool FP8>
+struct Fmt {
+  static constexpr int kEsz = FP8 ? 1 : 2;
+  static constexpr int kCols = 128 / kEsz;                 // columns of a 128-byte box row
+  static constexpr int kLatChunks = kLatent / kCols;       // 4 / 8
+  // the rope columns: 64 bytes (a chunk of its own kind) / 128 bytes
+  static constexpr int kRowsBytes = 64 * kDqk * kEsz;      // 64 rows: 36 / 72 KB
+  static constexpr int kGroups = FP8 ? 1 : 3;              // K slots that a tile takes
+  static constexpr int kGroupBytes = kRowsBytes / kGroups; // 36 / 24 KB
+  static constexpr int kKSlots = FP8 ? 2 : 3;
+  static constexpr int kVTok = FP8 ? 64 : 32;              // keys of a V slot
+  static constexpr int kVBoxes = 256 / kCols;              // 2 / 4
+  static constexpr int kVBox = kVTok * 128;                // 8 / 4 KB
+  static constexpr int kVSlotBytes = kVBoxes * kVBox;      // 16 KB
+  static constexpr int kVPer = kTile / kVTok;              // slots of a tile: 2 / 4
+  static constexpr int kVSlots = FP8 ? 5 : 4;
+  static constexpr int kPBytes = 64 * 128 * 2;             // hi and lo, or bf16: 16 KB
+  static constexpr int kPBufs = FP8 ? 2 : 1;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kRowsBytes;
+  static constexpr int kOffV = kOffK + kKSlots * kGroupBytes;
+  static constexpr int kOffP = kOffV + kVSlots * kVSlotBytes;
+  static constexpr int kOffX = kOffP + kPBufs * kPBytes;   // row exchange [3][128] floats
+  static constexpr int kOffSeg = kOffX + 3 * 128 * 4;
+  static constexpr int kOffBars = kOffSeg + kSegSlots * 64;
+  static constexpr int kBarBytes = 256;
+  static constexpr int kSmem = kOffBars + kBarBytes + 1024;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+  static_assert(kGroupBytes % 1024 == 0 && kRowsBytes % 1024 == 0, "swizzled tiles");
+  // p' of a row's largest key after the reference moved, as a power of two
+  static constexpr float kTop = FP8 ? 5.f : 0.f;
+};
+constexpr float kLazy = 8.f;              // p' is at most 2^kLazy
 
 struct WindowArgs {
-  const uint8_t *q, *kv;
   const float *scales;          // nullptr: k_scale
-  int sb_shift;
-  float k_scale, scale_log2;    // sm_scale * log2(e) * q_scale
+  int sb_shift;                 // log2(tokens per scale)
+  float k_scale;                // cache value of code 1 (bf16: 1)
+  float scale_log2;             // sm_scale * log2(e) * q_scale
   const int32_t *block_table, *seq_lens;
   int B, q_len, H, max_blocks, num_blocks, window, sinks;
+  int RG, forced, spans_at_once;
   void *out;
   int out_f32;
   float *lse;
+  int *ws_head;                 // [0] C; then per job {first unit, end unit}
+  void *ws_o;                   // [slots, 128, 512] of the output's type
+  float *ws_lse;                // [slots, 128]
   int *err;
 };
 
-template <bool FP8>
-__device__ __forceinline__ float load1(const uint8_t *p, int i) {
-  if constexpr (FP8) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3);
-    return __half2float(*reinterpret_cast<const __half *>(&h));
-  } else {
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
+// One job: 128 rows of a request over its list of pages.
+struct Job {
+  int p0, p1;                   // positions of its first and last query
+  int lo_page, sink_pages, pages;
+  __device__ __forceinline__ int tiles() const { return (pages + 1) >> 1; }
+  // page of the list's entry i
+  __device__ __forceinline__ int page(int i) const {
+    return i < sink_pages ? i : i - sink_pages + lo_page;
   }
+};
+
+__device__ __forceinline__ Job job_of(int rg, int len, const WindowArgs &a) {
+  Job j;
+  const int i0 = rg * 128 / a.H, i1 = min(a.q_len - 1, (rg * 128 + 127) / a.H);
+  j.p0 = len - a.q_len + i0;
+  j.p1 = len - a.q_len + i1;
+  const int lo = a.window ? max(0, j.p0 - a.window + 1) : 0;
+  j.lo_page = lo / kPage;
+  j.sink_pages = min((min(a.sinks, lo) + kPage - 1) / kPage, j.lo_page);
+  j.pages = j.p1 < 0 ? 0 : j.sink_pages + j.p1 / kPage + 1 - j.lo_page;
+  return j;
+}
+
+__device__ __forceinline__ int length_of(int b, const WindowArgs &a, bool tell) {
+  const int len = __ldg(a.seq_lens + b), most = a.max_blocks * kPage;
+  if (tell && (len < 0 || len > most)) raise_error(a.err, MLA_DEVERR_SEQ_LEN);
+  return min(max(len, 0), most);
+}
+
+__device__ __forceinline__ int units_of(int j, const WindowArgs &a, int &len) {
+  len = length_of(j % a.B, a, blockIdx.x == 0 && j < a.B);
+  const int t = job_of(j / a.B, len, a).tiles();
+  return t > 0 ? t + kJobCost : 0;
+}
+
+struct Seg {
+  int b, rg, len;
+  int tile0, ntiles;            // ntiles < 0: the end
+  int whole, slot;
+};
+
+__device__ __forceinline__ int warp_incl_scan(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// The segments of one CTA pair, found by a whole warp.  Lane k holds the
+// jobs [k*per, (k+1)*per) in sum for the search of a span's first job, and
+// job base + k of the 32 that are being walked.
+struct Walk {
+  int J, per, lane_excl, total, C, span, span_lo, span_hi;
+  int base, k, len, units, excl;
+  bool open;
+
+  __device__ void init(const WindowArgs &a, int lane) {
+    J = a.B * a.RG;
+    per = (J + 31) / 32;
+    int sum = 0, n;
+    for (int j = lane * per; j < min(J, (lane + 1) * per); ++j) sum += units_of(j, a, n);
+    const int incl = warp_incl_scan(sum, lane);
+    lane_excl = incl - sum;
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    C = a.forced > 0 ? a.forced : max(kMinUnits, (total - 1) / a.spans_at_once + 1);
+    span = blockIdx.x >> 1;
+    open = false;
+  }
+  __device__ void load(const WindowArgs &a, int at, int before, int lane) {
+    base = at;
+    k = 0;
+    units = 0;
+    len = 0;
+    if (base + lane < J) units = units_of(base + lane, a, len);
+    const int incl = warp_incl_scan(units, lane);
+    excl = before + incl - units;
+  }
+  __device__ bool next(const WindowArgs &a, Seg &s, int lane) {
+    while (true) {
+      if (!open) {
+        if (static_cast<int64_t>(span) * C >= total) return false;
+        span_lo = span * C;
+        span_hi = min(total, span_lo + C);
+        // the last lane whose jobs begin at or before the span
+        const uint32_t le = __ballot_sync(0xffffffffu, lane_excl <= span_lo);
+        const int own = 31 - __clz(le);
+        load(a, own * per, __shfl_sync(0xffffffffu, lane_excl, own), lane);
+        open = true;
+      }
+      if (k == 32) load(a, base + 32, __shfl_sync(0xffffffffu, excl + units, 31), lane);
+      const int j = base + k;
+      const int t0 = __shfl_sync(0xffffffffu, excl, k & 31);
+      const int n = __shfl_sync(0xffffffffu, units, k & 31);
+      const int l = __shfl_sync(0xffffffffu, len, k & 31);
+      if (j >= J || t0 >= span_hi) {
+        span += a.spans_at_once;
+        open = false;
+        continue;
+      }
+      ++k;
+      const int first = t0 + kJobCost, end = t0 + n;
+      const int u0 = max(span_lo, first), u1 = min(span_hi, end);
+      if (n == 0 || u1 <= u0) continue;
+      s.b = j % a.B;
+      s.rg = j / a.B;
+      s.len = l;
+      s.tile0 = u0 - first;
+      s.ntiles = u1 - u0;
+      s.whole = first >= span_lo && end <= span_hi;
+      // two partials a span at most: one of a job that began before it, one
+      // of a job that goes on behind it
+      s.slot = 2 * span + (first >= span_lo ? 1 : 0);
+      if (first >= span_lo && (blockIdx.x & 1) == 0 && lane == 0) {
+        a.ws_head[2 + 2 * j] = first;
+        a.ws_head[3 + 2 * j] = end;
+      }
+      return true;
+    }
+  }
+};
+
+// ------------------------------------------------- pair forms of the PTX
+__device__ __forceinline__ void pair_alloc(uint32_t *dst) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst)), "r"(512) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512)
+               : "memory");
+}
+template <bool FP8>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t acc) {
+  if constexpr (FP8)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// Arrives once on the barrier at this offset in both CTAs when every MMA so
+// far of this thread has completed.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+               ".multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "h"(static_cast<uint16_t>(3)) : "memory");
+}
+// A load into this CTA whose bytes count on a barrier of either CTA.
+__device__ __forceinline__ void pair_load(void *dst, const CUtensorMap *map, uint32_t bar_cluster,
+                                          int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+               ".cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
+}
+
+// Probabilities (a, b) as two pairs of e4m3 codes, hi and lo.
+__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint32_t &lo) {
+  const __half2 p = __floats2half2_rn(a, b);
+  const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
+  // exact: both are multiples of p's last place (or of 2^-24)
+  const __half2 rest = __hsub2(p, *reinterpret_cast<const __half2 *>(&back));
+  hi = h;
+  lo = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kWarps * 32) window_kernel(WindowArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
+              const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ WindowArgs args) {
+  using F = Fmt<FP8>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sm_q = smem + F::kOffQ, *sm_k = smem + F::kOffK, *sm_v = smem + F::kOffV;
+  uint8_t *sm_p = smem + F::kOffP;
+  float *xchg = reinterpret_cast<float *>(smem + F::kOffX);
+  Seg *segq = reinterpret_cast<Seg *>(smem + F::kOffSeg);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + F::kOffBars);
+  // leader: written by both CTAs' loads or warps; the others exist in both
+  uint64_t *k_full = bars;                    // [kKSlots] leader
+  uint64_t *k_empty = k_full + F::kKSlots;    // [kKSlots]
+  uint64_t *v_full = k_empty + F::kKSlots;    // [kVSlots]
+  uint64_t *v_empty = v_full + F::kVSlots;    // [kVSlots]
+  uint64_t *s_full = v_empty + F::kVSlots;    // [2]
+  uint64_t *p_full = s_full + 2;              // [2] leader
+  uint64_t *pv_done = p_full + 2;             // [2]
+  uint64_t *q_full = pv_done + 2;             // leader
+  uint64_t *q_empty = q_full + 1;
+  uint64_t *seg_full = q_empty + 1;           // [kSegSlots]
+  uint64_t *seg_empty = seg_full + kSegSlots; // [kSegSlots]
+  uint64_t *drain = seg_empty + kSegSlots;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  static_assert((2 * (F::kKSlots + F::kVSlots) + 6 + 2 + 2 * kSegSlots + 1) * 8 + 8 <= F::kBarBytes,
+                "barriers");
+  static_assert(sizeof(Seg) <= 64, "segment slot");
+
+  const int warp = warp_id(), lane = lane_id();
+  const int rank = static_cast<int>(cluster_rank());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < F::kKSlots; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < F::kVSlots; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 8);               // the softmax warps of both CTAs
+      mbar_init(&pv_done[s], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < kSegSlots; ++s) {
+      mbar_init(&seg_full[s], 1);
+      mbar_init(&seg_empty[s], rank == 0 ? 6 : 5);   // V, softmax, and the leader's MMA warp
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) pair_alloc(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  cluster_sync();                             // both CTAs' barriers and memory are there
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // Every consumer of segments takes them in order: a warp, or (mask 1) the
+  // MMA thread.
+  auto take_seg = [&](int ns, Seg &s, uint32_t mask) -> bool {
+    const int slot = ns % kSegSlots;
+    if (!__all_sync(mask, mbar_wait(&seg_full[slot], (ns / kSegSlots) & 1, abort_flag)))
+      return false;
+    s = segq[slot];
+    __syncwarp(mask);
+    if (lane == 0) mbar_arrive(&seg_empty[slot]);
+    return s.ntiles > 0;
+  };
+  // Block ids of a segment's pages: lane k holds those of list entry
+  // base + k; entries behind the list and bad ids give -1.
+  struct Pages {
+    int base, blk;
+  };
+  auto block_at = [&](Pages &pg, const Job &job, int b, int entry) -> int {   // whole warp
+    if (entry < pg.base || entry >= pg.base + 32) {
+      pg.base = entry;
+      const int e = entry + lane;
+      pg.blk = -1;
+      if (e < job.pages) {
+        const int v = __ldg(args.block_table + static_cast<int64_t>(b) * args.max_blocks + job.page(e));
+        if (v < 0 || v >= args.num_blocks) raise_error(args.err, MLA_DEVERR_BLOCK_ID);
+        else pg.blk = v;
+      }
+    }
+    return __shfl_sync(0xffffffffu, pg.blk, entry - pg.base);
+  };
+  // rows out of the cache: TMA fills in zeros
+  const int no_row = args.num_blocks * kPage;
+
+  if (warp == 0) {
+    // ------------------------------------------------- plan, Q and K
+    if (lane == 0) {
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_q);
+      if (FP8) {
+        prefetch_tmap(&tm_kr);
+        prefetch_tmap(&tm_qr);
+      }
+    }
+    Walk walk;
+    walk.init(args, lane);
+    if (blockIdx.x == 0 && lane == 0) args.ws_head[0] = walk.C;
+    Seg sg;
+    int ns = 0, kc = 0;
+    bool ok = true;
+    auto publish = [&](const Seg &s) -> bool {
+      const int slot = ns % kSegSlots;
+      if (ns >= kSegSlots && !mbar_wait(&seg_empty[slot], ((ns / kSegSlots) - 1) & 1, abort_flag))
+        return false;
+      if (lane == 0) {
+        segq[slot] = s;
+        mbar_arrive(&seg_full[slot]);
+      }
+      __syncwarp();
+      return true;
+    };
+    const uint32_t q_bar = peer_smem(q_full, 0);
+    while (ok && walk.next(args, sg, lane)) {
+      if (!(ok = publish(sg))) break;
+      const Job job = job_of(sg.rg, sg.len, args);
+      // Q, once the last segment's last Q K^T has read it
+      if (ns > 0 && !(ok = mbar_wait_cluster(q_empty, (ns - 1) & 1, abort_flag))) break;
+      ++ns;
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kRowsBytes);
+        const int row = sg.b * args.q_len * args.H + sg.rg * 128 + 64 * rank;
+        for (int c = 0; c < F::kLatChunks; ++c)
+          pair_load(sm_q + c * 8192, &tm_q, q_bar, c * F::kCols, row);
+        pair_load(sm_q + F::kLatChunks * 8192, FP8 ? &tm_qr : &tm_q, q_bar, kLatent, row);
+      }
+      Pages pg{-64, -1};
+      for (int t = 0; ok && t < sg.ntiles; ++t) {
+        const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + rank);
+        const int row = blk < 0 ? no_row : blk * kPage;
+        for (int g = 0; g < F::kGroups; ++g, ++kc) {
+          const int s = kc % F::kKSlots;
+          if (kc >= F::kKSlots &&
+              !(ok = mbar_wait_cluster(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
+            break;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kGroupBytes);
+            const uint32_t bar = peer_smem(&k_full[s], 0);
+            uint8_t *dst = sm_k + s * F::kGroupBytes;
+            if constexpr (FP8) {
+              for (int c = 0; c < 4; ++c) pair_load(dst + c * 8192, &tm_k, bar, c * 128, row);
+              pair_load(dst + 4 * 8192, &tm_kr, bar, kLatent, row);
+            } else {
+              for (int c = 0; c < 3; ++c) pair_load(dst + c * 8192, &tm_k, bar, (3 * g + c) * 64, row);
+            }
+          }
+        }
+      }
+    }
+    if (ok) {
+      sg.ntiles = -1;
+      publish(sg);
+    }
+    if (*abort_flag && rank == 0 && lane == 0) {   // what is on its way lands first
+      volatile int no_abort = 0;
+      for (int u = max(0, kc - F::kKSlots); u < kc; ++u)
+        mbar_wait_cluster(&k_full[u % F::kKSlots], (u / F::kKSlots) & 1, &no_abort);
+      if (ns > 0) mbar_wait_cluster(q_full, (ns - 1) & 1, &no_abort);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------- V
+    if (lane == 0) prefetch_tmap(&tm_v);
+    const uint64_t policy = l2_evict_first_policy();   // the rows' second and last read
+    Seg sg;
+    int vc = 0;
+    bool ok = true;
+    for (int ns = 0; ok && take_seg(ns, sg, 0xffffffffu); ++ns) {
+      const Job job = job_of(sg.rg, sg.len, args);
+      Pages pg{-64, -1};
+      for (int t = 0; ok && t < sg.ntiles; ++t) {
+        for (int v = 0; v < F::kVPer; ++v, ++vc) {
+          const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + v * 2 / F::kVPer);
+          const int s = vc % F::kVSlots;
+          if (vc >= F::kVSlots &&
+              !(ok = mbar_wait_cluster(&v_empty[s], ((vc / F::kVSlots) - 1) & 1, abort_flag)))
+            break;
+          if (lane == 0) {
+            const int row = blk < 0 ? no_row : blk * kPage + (v * F::kVTok) % kPage;
+            mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
+            for (int j = 0; j < F::kVBoxes; ++j)
+              tma_load_2d_hint(sm_v + s * F::kVSlotBytes + j * F::kVBox, &tm_v, &v_full[s],
+                               256 * rank + j * F::kCols, row, policy);
+          }
+        }
+      }
+    }
+    if (*abort_flag && lane == 0) {
+      volatile int no_abort = 0;
+      for (int u = max(0, vc - F::kVSlots); u < vc; ++u)
+        mbar_wait(&v_full[u % F::kVSlots], (u / F::kVSlots) & 1, &no_abort);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      // ---------------------------------------------------------- MMAs
+      const uint32_t idesc_qk = FP8 ? idesc_e4m3(128, kTile, false, false)
+                                    : idesc_bf16(128, kTile, false, false);
+      const uint32_t idesc_pv = FP8 ? idesc_e4m3(128, 256, false, true)
+                                    : idesc_bf16(128, 256, false, true);
+      const uint64_t qd = sdesc(smem_u32(sm_q), 16, 1024, kSwizzle128B);
+      const uint64_t qr = sdesc(smem_u32(sm_q) + 4 * 8192, 16, 512, kSwizzle64B);   // e4m3 rope columns
+      Seg sg;
+      int kc = 0, vc = 0, uc = 0;             // K slots, V slots, tiles so far
+      bool ok = true;
+      auto issue_qk = [&](int u) -> bool {
+        const uint32_t d = tmem + kColS + 64 * (u & 1);
+#pragma unroll
+        for (int g = 0; g < F::kGroups; ++g, ++kc) {
+          const int s = kc % F::kKSlots;
+          if (!mbar_wait_cluster(&k_full[s], (kc / F::kKSlots) & 1, abort_flag)) return false;
+          tc_fence_after();
+          const uint32_t kb = smem_u32(sm_k + s * F::kGroupBytes);
+          // one descriptor a slot; steps add to its address field (16-byte units)
+          const uint64_t kd = sdesc(kb, 16, 1024, kSwizzle128B);
+          if constexpr (FP8) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              pair_mma<FP8>(d, qd + ((k >> 2) * 512 + (k & 3) * 2), kd + ((k >> 2) * 512 + (k & 3) * 2),
+                            idesc_qk, k > 0);
+            const uint64_t kr = sdesc(kb + 4 * 8192, 16, 512, kSwizzle64B);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) pair_mma<FP8>(d, qr + 2 * k, kr + 2 * k, idesc_qk, 1);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 12; ++k)
+              pair_mma<FP8>(d, qd + ((3 * g + (k >> 2)) * 512 + (k & 3) * 2),
+                            kd + ((k >> 2) * 512 + (k & 3) * 2), idesc_qk, g + k > 0);
+          }
+          pair_commit(&k_empty[s]);
+        }
+        pair_commit(&s_full[u & 1]);
+        return true;
+      };
+      auto issue_pv = [&](int u, bool first) {
+        const uint64_t pd =
+            sdesc(smem_u32(sm_p) + (u % F::kPBufs) * F::kPBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int v = 0; v < F::kVPer; ++v, ++vc) {
+          const int s = vc % F::kVSlots;
+          const uint64_t vd = sdesc(smem_u32(sm_v + s * F::kVSlotBytes), F::kVBox, 1024, kSwizzle128B);
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {    // 32 bytes of P: 32 e4m3 or 16 bf16 keys
+            const int step = 2 * v + kk;
+            const uint64_t pa = pd + (FP8 ? step * 2 : (step >> 2) * 512 + (step & 3) * 2);
+            const uint32_t acc = first && step == 0 ? 0u : 1u;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {     // value columns 128j .. 128j + 127 of either CTA
+              const uint64_t bd = vd + (FP8 ? (j * F::kVBox + kk * 4096) / 16
+                                            : (2 * j * F::kVBox + kk * 2048) / 16);
+              pair_mma<FP8>(tmem + kColO + 128 * j, pa, bd, idesc_pv, acc);
+              if constexpr (FP8) pair_mma<FP8>(tmem + kColO + 128 * j, pa + 512, bd, idesc_pv, 1);
+            }
+          }
+          pair_commit(&v_empty[s]);
+        }
+        pair_commit(&pv_done[u & 1]);
+      };
+      int ns = 0;
+      for (; ok && take_seg(ns, sg, 1u); ++ns) {
+        if (!(ok = mbar_wait_cluster(q_full, ns & 1, abort_flag))) break;
+        if (!(ok = issue_qk(uc))) break;
+        if (sg.ntiles == 1) pair_commit(q_empty);
+        for (int t = 0; t < sg.ntiles; ++t, ++uc) {
+          // the scores of tile t + 1 go where tile t - 1's were: read before
+          // its probabilities were handed over
+          if (t + 1 < sg.ntiles) {
+            if (!(ok = issue_qk(uc + 1))) break;
+            if (t + 2 == sg.ntiles) pair_commit(q_empty);
+          }
+          if (!(ok = mbar_wait_cluster(&p_full[uc & 1], (uc >> 1) & 1, abort_flag))) break;
+          tc_fence_after();
+          issue_pv(uc, t == 0);
+        }
+      }
+      if (*abort_flag) {
+        pair_commit(drain);
+        volatile int no_abort = 0;
+        mbar_wait_cluster(drain, 0, &no_abort);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------ softmax and results
+    const int quarter = warp & 3, half = quarter >> 1;
+    const int r = (quarter & 1) * 32 + lane;            // row of this CTA
+    const int tid = threadIdx.x - 128;
+    const uint32_t lane_base = tmem + ((quarter * 32u) << 16);
+    const uint32_t bar_id = 1 + (quarter & 1);          // the two warps of the same rows
+    const uint32_t p_bar[2] = {peer_smem(&p_full[0], 0), peer_smem(&p_full[1], 0)};
+    float *my_x = xchg + (half * 64 + r), *its_x = xchg + ((half ^ 1) * 64 + r);
+    auto all_ok = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+    Seg sg;
+    int uc = 0, vc = 0;
+    bool ok = true;
+    for (int ns = 0; ok && take_seg(ns, sg, 0xffffffffu); ++ns) {
+      const Job job = job_of(sg.rg, sg.len, args);
+      const int R = args.q_len * args.H;
+      const int grow = sg.rg * 128 + 64 * rank + r;     // row of the request
+      // (rows behind the request's last are computed and dropped)
+      const int p = grow < R ? sg.len - args.q_len + grow / args.H : job.p1;
+      const int wlo = args.window ? p - args.window + 1 : 0;
+      // scale of this thread's keys (a page of the tile), a tile ahead
+      const int32_t *bt = args.block_table + static_cast<int64_t>(sg.b) * args.max_blocks;
+      auto load_blk = [&](int t) -> int {
+        const int e = 2 * (sg.tile0 + t) + half;
+        if (!FP8 || !args.scales || t >= sg.ntiles || e >= job.pages) return -1;
+        const int v = __ldg(bt + job.page(e));
+        return v >= 0 && v < args.num_blocks ? v : -1;
+      };
+      auto load_scales = [&](int blk, float *sc) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          sc[g] = blk < 0 ? args.k_scale
+                          : __ldg(args.scales + ((static_cast<int64_t>(blk) * kPage + 16 * g) >> args.sb_shift));
+      };
+      float sc[4], sc_next[4];
+      int blk_next = load_blk(1);
+      load_scales(load_blk(0), sc);
+      float ref = -INFINITY, l = 0.f;
+      for (int t = 0; t < sg.ntiles; ++t, ++uc) {
+        const int sb = uc & 1;
+        load_scales(blk_next, sc_next);
+        blk_next = load_blk(t + 2);
+        const int entry = 2 * (sg.tile0 + t) + half;
+        const int key0 = entry < job.pages ? job.page(entry) * kPage : 1 << 30;
+        float c[4], lg[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          // (a scale of 0 stands for zeros: so does the smallest one)
+          const float sigma = fminf(fmaxf(sc[g], 0x1p-100f), 0x1p120f);
+          c[g] = sigma * args.scale_log2;
+          lg[g] = FP8 ? log2f(sigma) : 0.f;
+          sc[g] = sigma;
+        }
+        if (!(ok = all_ok(mbar_wait_cluster(&s_full[sb], (uc >> 1) & 1, abort_flag)))) break;
+        tc_fence_after();
+        float x[64];
+        tmem_ld_x64(lane_base + kColS + 64 * sb, reinterpret_cast<uint32_t *>(x));
+        if (key0 + 63 > p || (key0 < wlo && key0 + 64 > args.sinks)) {
+          const int e = p - key0, a = wlo - key0, z = args.sinks - key0;
+#pragma unroll
+          for (int k = 0; k < 64; ++k) x[k] = k <= e && (k >= a || k < z) ? x[k] : -INFINITY;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            m0 = fmax3(m0, x[16 * g + k], x[16 * g + k + 1]);
+            m1 = fmax3(m1, x[16 * g + k + 2], x[16 * g + k + 3]);
+          }
+          top = fmaxf(top, fmaf(fmaxf(m0, m1), c[g], lg[g]));
+        }
+        // the row's other half of the keys
+        my_x[128 * sb] = top;
+        named_sync(bar_id, 64);
+        top = fmaxf(top, its_x[128 * sb]);
+        const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
+        if (t == 0) {
+          if (move) ref = top - F::kTop;
+        } else if (__any_sync(0xffffffffu, move)) {
+          const int up = uc - 1;
+          if (!(ok = all_ok(mbar_wait_cluster(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
+          tc_fence_after();
+          const float f = move ? (ref == -INFINITY ? 0.f : ex2(ref - (top - F::kTop))) : 1.f;
+#pragma unroll 1
+          for (int q = 0; q < 256; q += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(lane_base + kColO + q, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st_x32(lane_base + kColO + q, o);
+          }
+          l *= f;
+          if (move) ref = top - F::kTop;
+        }
+        const float base = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float d = lg[g] - base;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+            fma_f32x2(x[k], x[k + 1], x[k], x[k + 1], c[g], c[g], d, d);
+            x[k] = ex2(x[k]);
+            x[k + 1] = ex2(x[k + 1]);
+            add_f32x2(s0, s1, s0, s1, x[k], x[k + 1]);
+          }
+          l += FP8 ? (s0 + s1) / sc[g] : s0 + s1;
+        }
+        // P goes where the P V of kPBufs tiles ago read
+        if (uc >= F::kPBufs) {
+          const int up = uc - F::kPBufs;
+          if (!(ok = all_ok(mbar_wait_cluster(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
+        }
+        uint8_t *pbuf = sm_p + (uc % F::kPBufs) * F::kPBytes;
+        if constexpr (FP8) {
+          uint4 *hi = reinterpret_cast<uint4 *>(pbuf + r * 128);
+          uint4 *lo = reinterpret_cast<uint4 *>(pbuf + 8192 + r * 128);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t h[4], w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h0, h1, l0, l1;
+              split_e4m3(x[16 * q + 4 * k], x[16 * q + 4 * k + 1], h0, l0);
+              split_e4m3(x[16 * q + 4 * k + 2], x[16 * q + 4 * k + 3], h1, l1);
+              h[k] = h0 | (h1 << 16);
+              w[k] = l0 | (l1 << 16);
+            }
+            const int ch = (4 * half + q) ^ (r & 7);
+            hi[ch] = make_uint4(h[0], h[1], h[2], h[3]);
+            lo[ch] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          uint4 *row = reinterpret_cast<uint4 *>(pbuf + half * 8192 + r * 128);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            row[q ^ (r & 7)] = make_uint4(bf16x2_rn(x[8 * q], x[8 * q + 1]),
+                                          bf16x2_rn(x[8 * q + 2], x[8 * q + 3]),
+                                          bf16x2_rn(x[8 * q + 4], x[8 * q + 5]),
+                                          bf16x2_rn(x[8 * q + 6], x[8 * q + 7]));
+        }
+        // the values are here; rows that not every query row sees are cleaned
+        for (int v = 0; ok && v < F::kVPer; ++v) {
+          const int u = vc + v, s = u % F::kVSlots;
+          ok = mbar_wait(&v_full[s], (u / F::kVSlots) & 1, abort_flag);
+          const int e = 2 * (sg.tile0 + t) + v * 2 / F::kVPer;
+          const int k0 = e < job.pages ? job.page(e) * kPage + (v * F::kVTok) % kPage : 1 << 30;
+          // every row sees all of them?
+          if (!ok || e >= job.pages ||
+              (k0 + F::kVTok - 1 <= job.p0 &&
+               (!args.window || k0 > job.p1 - args.window || k0 + F::kVTok <= args.sinks)))
+            continue;
+          for (int idx = tid; idx < F::kVSlotBytes / 16; idx += 128) {
+            const int tok = (idx >> 3) % F::kVTok, key = k0 + tok;
+            const bool sink = key < args.sinks;
+            const bool some = key <= job.p1 && (!args.window || sink || key > job.p0 - args.window);
+            const bool all = key <= job.p0 && (!args.window || sink || key > job.p1 - args.window);
+            if (all) continue;
+            uint4 *w = reinterpret_cast<uint4 *>(sm_v + s * F::kVSlotBytes) + idx;
+            uint4 val = make_uint4(0, 0, 0, 0);
+            if (some) {   // seen by some rows: only what is not finite goes (0 * NaN in the others)
+              val = *w;
+              uint32_t *e4 = reinterpret_cast<uint32_t *>(&val);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (FP8) {
+                  const uint32_t nan = (((e4[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+                  e4[i] &= ~(nan * 0xFFu);
+                } else {
+                  if ((e4[i] & 0x7F80u) == 0x7F80u) e4[i] &= 0xFFFF0000u;
+                  if ((e4[i] & 0x7F800000u) == 0x7F800000u) e4[i] &= 0xFFFFu;
+                }
+              }
+            }
+            *w = val;
+          }
+        }
+        vc += F::kVPer;
+        if (!(ok = all_ok(ok))) break;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(p_bar[sb]);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) sc[g] = sc_next[g];
+      }
+      if (!ok) break;
+      // ---- results: O / l of this row, value columns [256 * half, +256)
+      {
+        const int up = uc - 1;
+        if (!(ok = all_ok(mbar_wait_cluster(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
+      }
+      tc_fence_after();
+      my_x[256] = l;
+      named_sync(bar_id, 64);
+      l += its_x[256];
+      const bool empty = l == 0.f;
+      const float inv = empty ? 0.f : 1.f / l;
+      const int64_t row0 = static_cast<int64_t>(sg.b) * R + sg.rg * 128 + 64 * rank;
+      const int64_t at = sg.whole ? row0 : static_cast<int64_t>(sg.slot) * 128 + 64 * rank;
+      const int nrows = min(64, R - sg.rg * 128 - 64 * rank);
+      const int esz = args.out_f32 ? 4 : 2;
+      uint8_t *dst0 = static_cast<uint8_t *>(sg.whole ? args.out : args.ws_o) +
+                      (at * kLatent + 256 * half) * esz;
+      const int64_t rstride = static_cast<int64_t>(kLatent) * esz;
+      if (half == 0 && r < nrows) {
+        const float v = empty ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
+        (sg.whole ? args.lse : args.ws_lse)[at + r] = v;
+      }
+      // staged through 4 KB of this warp's own in the P tiles (e4m3: of the
+      // buffer that the next tile does not use)
+      uint4 *buf = reinterpret_cast<uint4 *>(
+          FP8 ? sm_p + ((uc + 1) % F::kPBufs) * F::kPBytes + half * 8192 + (quarter & 1) * 4096
+              : sm_p + half * 8192 + (quarter & 1) * 4096);
+#pragma unroll 1
+      for (int q = 0; q < 256; q += 64) {
+        uint32_t o[64];
+        tmem_ld_x64(lane_base + kColO + q, o);
+        auto f = [&](int k) { return __uint_as_float(o[k]) * inv; };
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc) {     // one (bf16) or two (fp32) 128-byte pieces of the row
+          if (!args.out_f32 && pc == 1) break;
+          __syncwarp();
+          if (!args.out_f32) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              buf[lane * 8 + (k ^ (lane & 7))] = make_uint4(
+                  bf16x2_rn(f(8 * k), f(8 * k + 1)), bf16x2_rn(f(8 * k + 2), f(8 * k + 3)),
+                  bf16x2_rn(f(8 * k + 4), f(8 * k + 5)), bf16x2_rn(f(8 * k + 6), f(8 * k + 7)));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int e = 32 * pc + 4 * k;
+              buf[lane * 8 + (k ^ (lane & 7))] =
+                  make_uint4(__float_as_uint(f(e)), __float_as_uint(f(e + 1)),
+                             __float_as_uint(f(e + 2)), __float_as_uint(f(e + 3)));
+            }
+          }
+          __syncwarp();
+          uint8_t *dst = dst0 + static_cast<int64_t>(q + 32 * pc) * esz;
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int row = it * 4 + (lane >> 3), ch = lane & 7;
+            const int rr = (quarter & 1) * 32 + row;
+            if (rr < nrows)
+              reinterpret_cast<uint4 *>(dst + rr * rstride)[ch] = buf[row * 8 + (ch ^ (row & 7))];
+          }
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (threadIdx.x == 0 && *abort_flag) raise_error(args.err, MLA_DEVERR_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    pair_dealloc(tmem);
+  }
+}
+
+// Combines the partials of the jobs that were cut, and writes the rows of
+// jobs without a key: one warp per row.  Part k of a job whose first span is
+// s0 lies in slot 2 s0 + 1 (k = 0) or 2 (s0 + k).
+constexpr int kMergeWarps = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+window_merge_kernel(const __grid_constant__ WindowArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
   const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  if (h >= a.H) return;
-  const int b = blockIdx.x / a.q_len, i = blockIdx.x % a.q_len;
-  int len = a.seq_lens[b];
-  if (len < 0 || len > a.max_blocks * kPage) {
-    raise_error(a.err, MLA_DEVERR_SEQ_LEN);
-    len = min(max(len, 0), a.max_blocks * kPage);
+  const int j = blockIdx.x, b = j % a.B, rg = j / a.B;
+  const int rr = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int R = a.q_len * a.H;
+  if (rg * 128 + rr >= R) return;
+  const int64_t row = static_cast<int64_t>(b) * R + rg * 128 + rr;
+  T *out = static_cast<T *>(a.out) + row * kLatent;
+  const int C = a.ws_head[0], first = a.ws_head[2 + 2 * j], end = a.ws_head[3 + 2 * j];
+  const Job job = job_of(rg, length_of(b, a, false), a);
+  if (job.tiles() == 0) {
+    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int k = 0; k < 2; ++k) store8(out + 8 * (lane + 32 * k), zero);
+    if (lane == 0) a.lse[row] = -INFINITY;
+    return;
   }
-  constexpr int kRow = kDqk * (FP8 ? 1 : 2);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.H + h;
-  float q[18], o[16];
+  const int s0 = first / C, n = (end - 1) / C - s0 + 1;
+  if (n == 1) return;
+  auto slot_row = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * s0 + 1 : 2 * (s0 + k)) * 128 + rr; };
+  float m = -INFINITY;
+  for (int k = lane; k < n; k += 32) m = fmaxf(m, a.ws_lse[slot_row(k)]);
 #pragma unroll
-  for (int k = 0; k < 18; ++k) q[k] = load1<FP8>(a.q + row * kRow, lane + 32 * k);
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float safe = m == -INFINITY ? 0.f : m;
+  float acc[16], z = 0.f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = 0.f;
-  const int p = len - a.q_len + i;
-  const int lo = a.window ? max(0, p - a.window + 1) : 0;
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j <= p; ++j) {
-    if (j >= a.sinks && j < lo) {
-      j = lo - 1;
-      continue;
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float w = k0 + lane < n ? expf(a.ws_lse[slot_row(k0 + lane)] - safe) : 0.f;
+    float zw = w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) zw += __shfl_xor_sync(0xffffffffu, zw, o);
+    z += zw;
+    const int here = min(32, n - k0);
+    for (int k = 0; k < here; k += 4) {
+      float v[4][16];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k + u < here) {
+          const T *src = static_cast<const T *>(a.ws_o) + slot_row(k0 + k + u) * kLatent;
+          load8(src + 8 * lane, v[u]);
+          load8(src + 8 * (lane + 32), v[u] + 8);
+        }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k + u < here) {
+          const float wu = __shfl_sync(0xffffffffu, w, k + u);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[e] = fmaf(wu, v[u][e], acc[e]);
+        }
     }
-    const int blk = a.block_table[static_cast<int64_t>(b) * a.max_blocks + j / kPage];
-    float kv[18], sc = a.k_scale;
-    if (blk < 0 || blk >= a.num_blocks) {
-      raise_error(a.err, MLA_DEVERR_BLOCK_ID);
-#pragma unroll
-      for (int k = 0; k < 18; ++k) kv[k] = 0.f;
-    } else {
-      const int64_t slot = static_cast<int64_t>(blk) * kPage + j % kPage;
-      if (a.scales) sc = a.scales[slot >> a.sb_shift];
-#pragma unroll
-      for (int k = 0; k < 18; ++k) kv[k] = load1<FP8>(a.kv + slot * kRow, lane + 32 * k) * sc;
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 18; ++k) s = fmaf(q[k], kv[k], s);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale_log2;
-    if (s > m) {
-      const float f = exp2f(m - s);
-      l *= f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] *= f;
-      m = s;
-    }
-    const float w = exp2f(s - m);
-    l += w;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = fmaf(w, kv[k], o[k]);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int64_t at = row * kLatent + lane + 32 * k;
-    if (a.out_f32) static_cast<float *>(a.out)[at] = o[k] * inv;
-    else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(o[k] * inv);
+  for (int e = 0; e < 16; ++e) acc[e] *= inv;
+  store8(out + 8 * lane, acc);
+  store8(out + 8 * (lane + 32), acc + 8);
+  if (lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(z);
+}
+
+// ------------------------------------------------------------------- host
+template <bool FP8>
+struct PairLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  PairLaunch(int pairs, cudaStream_t stream) {
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Fmt<FP8>::kSmem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
   }
-  if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+};
+
+// CTA pairs that are resident at once (a pair needs both SMs in one GPC), at
+// most one per two SMs; cached per device.
+int pairs_for_device() {
+  constexpr int kMaxDevices = 64;
+  static int cache[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  const int sms = device_sm_count();
+  int g = sms >= 2 ? sms / 2 : 1;
+  if (dev < 0 || dev >= kMaxDevices) return g;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev] > 0) return cache[dev];
+  int n = 0;
+  // (the larger of the two formats' shared memory)
+  if (cudaFuncSetAttribute(window_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Fmt<false>::kSmem) == cudaSuccess) {
+    PairLaunch<false> pl(g, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&n, window_kernel<false>, &pl.cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  if (n > 0) g = std::min(g, n);
+  cache[dev] = g;
+  return g;
 }
 
 bool shape_ok(int B, int q_len, int H) {
   if (B < 1 || q_len < 1 || q_len > 64 || H < 1 || H > 4096) return false;
   return static_cast<int64_t>(B) * q_len * ((H + 127) / 128) <= (1 << 22);
+}
+
+struct WsLayout {
+  size_t o_off, lse_off, total;
+};
+
+WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sinks,
+                   int split_tiles) {
+  const int64_t RG = (static_cast<int64_t>(q_len) * H + 127) / 128, J = B * RG;
+  int64_t spans = pairs_for_device();
+  if (split_tiles > 0) {
+    int64_t pages = (static_cast<int64_t>(max_seq_len) + kPage - 1) / kPage;
+    if (window > 0)   // the sinks' pages and the window's, either of which may begin inside a page
+      pages = std::min(pages, (static_cast<int64_t>(window) + q_len) / kPage + 2 +
+                                  (static_cast<int64_t>(sinks) + kPage - 1) / kPage);
+    spans = (J * ((pages + 1) / 2 + kJobCost) + split_tiles - 1) / split_tiles;
+  }
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  WsLayout w;
+  w.o_off = up((2 + 2 * static_cast<size_t>(J)) * sizeof(int));
+  w.lse_off = w.o_off + static_cast<size_t>(2 * spans) * 128 * kLatent * sizeof(float);
+  w.total = w.lse_off + static_cast<size_t>(2 * spans) * 128 * sizeof(float);
+  return w;
 }
 
 int check_window(const void *q, int q_dtype, float q_scale, const void *kv_cache, int kv_dtype,
@@ -130,7 +1021,33 @@ int check_window(const void *q, int q_dtype, float q_scale, const void *kv_cache
   return MLA_OK;
 }
 
-size_t ws_bytes_for(int, int, int, int, int) { return 256; }
+template <bool FP8>
+int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArgs &a,
+                 mla_stream_t stream) {
+  using F = Fmt<FP8>;
+  const CUtensorMapDataType dt =
+      FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t strides[1] = {static_cast<uint64_t>(kDqk) * F::kEsz};
+  const uint64_t kv_dims[2] = {kDqk, static_cast<uint64_t>(a.num_blocks) * kPage};
+  const uint64_t q_dims[2] = {kDqk, static_cast<uint64_t>(a.B) * a.q_len * a.H};
+  const uint32_t box[2] = {F::kCols, 64}, box_r[2] = {64, 64}, box_v[2] = {F::kCols, F::kVTok};
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapSwizzle sw_r = FP8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  CUtensorMap tk, tkr, tv, tq, tqr;
+  if (!make_tmap(&tk, dt, 2, kv_cache, kv_dims, strides, box, sw) ||
+      !make_tmap(&tkr, dt, 2, kv_cache, kv_dims, strides, box_r, sw_r) ||
+      !make_tmap(&tv, dt, 2, kv_cache, kv_dims, strides, box_v, sw) ||
+      !make_tmap(&tq, dt, 2, q, q_dims, strides, box, sw) ||
+      !make_tmap(&tqr, dt, 2, q, q_dims, strides, box_r, sw_r))
+    return MLA_ERR_CUDA;
+  if (cudaFuncSetAttribute(window_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           F::kSmem) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  PairLaunch<FP8> pl(pairs, stream);
+  return cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8>, tk, tkr, tv, tq, tqr, a) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
 
 int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, float k_scale,
                   const float *scales, int sb_shift, const int32_t *block_table,
@@ -138,13 +1055,11 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
                   float sm_scale, int window, int sinks, int split_tiles, void *out, int out_dtype,
                   float *lse, void *workspace, size_t ws_bytes, mla_stream_t stream) {
   if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < ws_bytes_for(B, q_len, H, max_blocks * kPage, split_tiles))
-    return MLA_ERR_WORKSPACE;
+  const WsLayout w = ws_layout(B, q_len, H, max_blocks * kPage, window, sinks, split_tiles);
+  if (!workspace || ws_bytes < w.total) return MLA_ERR_WORKSPACE;
   WindowArgs a{};
   a.err = device_error_word();
   if (!a.err) return MLA_ERR_CUDA;
-  a.q = static_cast<const uint8_t *>(q);
-  a.kv = static_cast<const uint8_t *>(kv_cache);
   a.scales = scales;
   a.sb_shift = sb_shift;
   a.k_scale = fp8 ? k_scale : 1.f;
@@ -156,15 +1071,28 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.H = H;
   a.max_blocks = max_blocks;
   a.num_blocks = num_blocks;
-  a.window = window < (1 << 30) ? window : 1 << 30;
-  a.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+  // (a table holds at most 2^30 tokens: sums with these stay within 32 bits)
+  a.window = std::min(window, 1 << 30);
+  a.sinks = std::min(sinks, 1 << 30);
+  a.RG = static_cast<int>((static_cast<int64_t>(q_len) * H + 127) / 128);
+  a.forced = split_tiles;
+  a.spans_at_once = pairs_for_device();
   a.out = out;
   a.out_f32 = out_dtype == MLA_F32;
   a.lse = lse;
-  const dim3 grid(B * q_len, (H + kWarps - 1) / kWarps);
-  if (fp8) window_kernel<true><<<grid, kWarps * 32, 0, stream>>>(a);
-  else window_kernel<false><<<grid, kWarps * 32, 0, stream>>>(a);
-  return launch_status();
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.ws_head = reinterpret_cast<int *>(ws);
+  a.ws_o = ws + w.o_off;
+  a.ws_lse = reinterpret_cast<float *>(ws + w.lse_off);
+  const int st = fp8 ? launch_pairs<true>(q, kv_cache, a.spans_at_once, a, stream)
+                     : launch_pairs<false>(q, kv_cache, a.spans_at_once, a, stream);
+  if (st != MLA_OK) return st;
+  const int rows = std::min(128, q_len * H);
+  const dim3 grid(B * a.RG, (rows + kMergeWarps - 1) / kMergeWarps), block(kMergeWarps * 32);
+  const cudaError_t e = a.out_f32
+                            ? launch_pdl(window_merge_kernel<float>, grid, block, 0, stream, a)
+                            : launch_pdl(window_merge_kernel<__nv_bfloat16>, grid, block, 0, stream, a);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace
@@ -178,7 +1106,7 @@ extern "C" int mla_decode_window_workspace_size(int B, int q_len, int H, int max
   if (!bytes || !shape_ok(B, q_len, H) || max_seq_len < 0 || window < 0 || sinks < 0 ||
       split_tiles < 0)
     return MLA_ERR_INVALID_ARG;
-  *bytes = ws_bytes_for(B, q_len, H, max_seq_len, split_tiles);
+  *bytes = ws_layout(B, q_len, H, max_seq_len, window, sinks, split_tiles).total;
   return MLA_OK;
 }
 
