@@ -283,9 +283,26 @@ __device__ __forceinline__ void pair_load(void *dst, const CUtensorMap *map, uin
                "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
                : "memory");
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-               : "memory");
+// Bounded wait that first tests the phase: most waits here find it complete,
+// and a test costs about 70 cycles where try_wait costs about 190.  What the
+// barriers order across the pair is read by the tensor cores and the TMA
+// only, so no wait needs cluster-scope acquire (one took about 200 cycles
+// more, and a cluster-scope release of the probabilities 1600 a tile).
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+  return mbar_test(bar, parity) || mbar_wait(bar, parity, abort_flag);
+}
+
+// Shared-memory descriptors as a constant high word and an address word, to
+// which a step adds its offset in 16-byte units.
+template <uint32_t SBO, uint32_t SWIZZLE>
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo) {
+  constexpr uint32_t hi = (SBO >> 4) | (1u << 14) | (SWIZZLE << 29);
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ uint32_t desc_lo(const void *p, uint32_t lbo) {
+  return ((smem_u32(p) & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
 // Probabilities (a, b) as two pairs of e4m3 codes, hi and lo.
@@ -371,7 +388,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   // MMA thread.
   auto take_seg = [&](int ns, Seg &s, uint32_t mask) -> bool {
     const int slot = ns % kSegSlots;
-    if (!__all_sync(mask, mbar_wait(&seg_full[slot], (ns / kSegSlots) & 1, abort_flag)))
+    if (!__all_sync(mask, wait_for(&seg_full[slot], (ns / kSegSlots) & 1, abort_flag)))
       return false;
     s = segq[slot];
     __syncwarp(mask);
@@ -417,7 +434,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     bool ok = true;
     auto publish = [&](const Seg &s) -> bool {
       const int slot = ns % kSegSlots;
-      if (ns >= kSegSlots && !mbar_wait(&seg_empty[slot], ((ns / kSegSlots) - 1) & 1, abort_flag))
+      if (ns >= kSegSlots && !wait_for(&seg_empty[slot], ((ns / kSegSlots) - 1) & 1, abort_flag))
         return false;
       if (lane == 0) {
         segq[slot] = s;
@@ -431,7 +448,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       if (!(ok = publish(sg))) break;
       const Job job = job_of(sg.rg, sg.len, args);
       // Q, once the last segment's last Q K^T has read it
-      if (ns > 0 && !(ok = mbar_wait_cluster(q_empty, (ns - 1) & 1, abort_flag))) break;
+      if (ns > 0 && !(ok = wait_for(q_empty, (ns - 1) & 1, abort_flag))) break;
       ++ns;
       if (lane == 0) {
         if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kRowsBytes);
@@ -447,7 +464,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         for (int g = 0; g < F::kGroups; ++g, ++kc) {
           const int s = kc % F::kKSlots;
           if (kc >= F::kKSlots &&
-              !(ok = mbar_wait_cluster(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
+              !(ok = wait_for(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
             break;
           if (lane == 0) {
             if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kGroupBytes);
@@ -470,8 +487,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (*abort_flag && rank == 0 && lane == 0) {   // what is on its way lands first
       volatile int no_abort = 0;
       for (int u = max(0, kc - F::kKSlots); u < kc; ++u)
-        mbar_wait_cluster(&k_full[u % F::kKSlots], (u / F::kKSlots) & 1, &no_abort);
-      if (ns > 0) mbar_wait_cluster(q_full, (ns - 1) & 1, &no_abort);
+        wait_for(&k_full[u % F::kKSlots], (u / F::kKSlots) & 1, &no_abort);
+      if (ns > 0) wait_for(q_full, (ns - 1) & 1, &no_abort);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------- V
@@ -488,7 +505,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + v * 2 / F::kVPer);
           const int s = vc % F::kVSlots;
           if (vc >= F::kVSlots &&
-              !(ok = mbar_wait_cluster(&v_empty[s], ((vc / F::kVSlots) - 1) & 1, abort_flag)))
+              !(ok = wait_for(&v_empty[s], ((vc / F::kVSlots) - 1) & 1, abort_flag)))
             break;
           if (lane == 0) {
             const int row = blk < 0 ? no_row : blk * kPage + (v * F::kVTok) % kPage;
@@ -503,7 +520,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (*abort_flag && lane == 0) {
       volatile int no_abort = 0;
       for (int u = max(0, vc - F::kVSlots); u < vc; ++u)
-        mbar_wait(&v_full[u % F::kVSlots], (u / F::kVSlots) & 1, &no_abort);
+        wait_for(&v_full[u % F::kVSlots], (u / F::kVSlots) & 1, &no_abort);
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
@@ -512,8 +529,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                     : idesc_bf16(128, kTile, false, false);
       const uint32_t idesc_pv = FP8 ? idesc_e4m3(128, 256, false, true)
                                     : idesc_bf16(128, 256, false, true);
-      const uint64_t qd = sdesc(smem_u32(sm_q), 16, 1024, kSwizzle128B);
-      const uint64_t qr = sdesc(smem_u32(sm_q) + 4 * 8192, 16, 512, kSwizzle64B);   // e4m3 rope columns
+      const uint32_t qd = desc_lo(sm_q, 16);
       Seg sg;
       int kc = 0, vc = 0, uc = 0;             // K slots, V slots, tiles so far
       bool ok = true;
@@ -522,24 +538,26 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
         for (int g = 0; g < F::kGroups; ++g, ++kc) {
           const int s = kc % F::kKSlots;
-          if (!mbar_wait_cluster(&k_full[s], (kc / F::kKSlots) & 1, abort_flag)) return false;
+          if (!wait_for(&k_full[s], (kc / F::kKSlots) & 1, abort_flag)) return false;
           tc_fence_after();
-          const uint32_t kb = smem_u32(sm_k + s * F::kGroupBytes);
           // one descriptor a slot; steps add to its address field (16-byte units)
-          const uint64_t kd = sdesc(kb, 16, 1024, kSwizzle128B);
+          const uint32_t kd = desc_lo(sm_k + s * F::kGroupBytes, 16);
           if constexpr (FP8) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              pair_mma<FP8>(d, qd + ((k >> 2) * 512 + (k & 3) * 2), kd + ((k >> 2) * 512 + (k & 3) * 2),
-                            idesc_qk, k > 0);
-            const uint64_t kr = sdesc(kb + 4 * 8192, 16, 512, kSwizzle64B);
+              pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (k >> 2) * 512 + (k & 3) * 2),
+                            desc_at<1024, kSwizzle128B>(kd + (k >> 2) * 512 + (k & 3) * 2), idesc_qk,
+                            k > 0);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) pair_mma<FP8>(d, qr + 2 * k, kr + 2 * k, idesc_qk, 1);
+            for (int k = 0; k < 2; ++k)       // the rope columns: rows of 64 bytes
+              pair_mma<FP8>(d, desc_at<512, kSwizzle64B>(qd + 4 * 512 + 2 * k),
+                            desc_at<512, kSwizzle64B>(kd + 4 * 512 + 2 * k), idesc_qk, 1);
           } else {
 #pragma unroll
             for (int k = 0; k < 12; ++k)
-              pair_mma<FP8>(d, qd + ((3 * g + (k >> 2)) * 512 + (k & 3) * 2),
-                            kd + ((k >> 2) * 512 + (k & 3) * 2), idesc_qk, g + k > 0);
+              pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (3 * g + (k >> 2)) * 512 + (k & 3) * 2),
+                            desc_at<1024, kSwizzle128B>(kd + (k >> 2) * 512 + (k & 3) * 2), idesc_qk,
+                            g + k > 0);
           }
           pair_commit(&k_empty[s]);
         }
@@ -547,23 +565,24 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         return true;
       };
       auto issue_pv = [&](int u, bool first) {
-        const uint64_t pd =
-            sdesc(smem_u32(sm_p) + (u % F::kPBufs) * F::kPBytes, 16, 1024, kSwizzle128B);
+        const uint32_t pd = desc_lo(sm_p + (u % F::kPBufs) * F::kPBytes, 16);
 #pragma unroll
         for (int v = 0; v < F::kVPer; ++v, ++vc) {
           const int s = vc % F::kVSlots;
-          const uint64_t vd = sdesc(smem_u32(sm_v + s * F::kVSlotBytes), F::kVBox, 1024, kSwizzle128B);
+          const uint32_t vd = desc_lo(sm_v + s * F::kVSlotBytes, F::kVBox);
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk) {    // 32 bytes of P: 32 e4m3 or 16 bf16 keys
             const int step = 2 * v + kk;
-            const uint64_t pa = pd + (FP8 ? step * 2 : (step >> 2) * 512 + (step & 3) * 2);
+            const uint32_t pa = pd + (FP8 ? step * 2 : (step >> 2) * 512 + (step & 3) * 2);
             const uint32_t acc = first && step == 0 ? 0u : 1u;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {     // value columns 128j .. 128j + 127 of either CTA
-              const uint64_t bd = vd + (FP8 ? (j * F::kVBox + kk * 4096) / 16
-                                            : (2 * j * F::kVBox + kk * 2048) / 16);
-              pair_mma<FP8>(tmem + kColO + 128 * j, pa, bd, idesc_pv, acc);
-              if constexpr (FP8) pair_mma<FP8>(tmem + kColO + 128 * j, pa + 512, bd, idesc_pv, 1);
+              const uint64_t bd = desc_at<1024, kSwizzle128B>(
+                  vd + (FP8 ? j * F::kVBox + kk * 4096 : 2 * j * F::kVBox + kk * 2048) / 16);
+              pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa), bd, idesc_pv, acc);
+              if constexpr (FP8)
+                pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa + 512), bd,
+                              idesc_pv, 1);
             }
           }
           pair_commit(&v_empty[s]);
@@ -572,7 +591,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       };
       int ns = 0;
       for (; ok && take_seg(ns, sg, 1u); ++ns) {
-        if (!(ok = mbar_wait_cluster(q_full, ns & 1, abort_flag))) break;
+        if (!(ok = wait_for(q_full, ns & 1, abort_flag))) break;
         if (!(ok = issue_qk(uc))) break;
         if (sg.ntiles == 1) pair_commit(q_empty);
         for (int t = 0; t < sg.ntiles; ++t, ++uc) {
@@ -582,7 +601,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if (!(ok = issue_qk(uc + 1))) break;
             if (t + 2 == sg.ntiles) pair_commit(q_empty);
           }
-          if (!(ok = mbar_wait_cluster(&p_full[uc & 1], (uc >> 1) & 1, abort_flag))) break;
+          if (!(ok = wait_for(&p_full[uc & 1], (uc >> 1) & 1, abort_flag))) break;
           tc_fence_after();
           issue_pv(uc, t == 0);
         }
@@ -590,7 +609,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       if (*abort_flag) {
         pair_commit(drain);
         volatile int no_abort = 0;
-        mbar_wait_cluster(drain, 0, &no_abort);
+        wait_for(drain, 0, &no_abort);
       }
     }
   } else if (warp >= 4) {
@@ -646,7 +665,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           lg[g] = FP8 ? log2f(sigma) : 0.f;
           sc[g] = sigma;
         }
-        if (!(ok = all_ok(mbar_wait_cluster(&s_full[sb], (uc >> 1) & 1, abort_flag)))) break;
+        if (!(ok = all_ok(wait_for(&s_full[sb], (uc >> 1) & 1, abort_flag)))) break;
         tc_fence_after();
         float x[64];
         tmem_ld_x64(lane_base + kColS + 64 * sb, reinterpret_cast<uint32_t *>(x));
@@ -675,7 +694,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           if (move) ref = top - F::kTop;
         } else if (__any_sync(0xffffffffu, move)) {
           const int up = uc - 1;
-          if (!(ok = all_ok(mbar_wait_cluster(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
+          if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
           tc_fence_after();
           const float f = move ? (ref == -INFINITY ? 0.f : ex2(ref - (top - F::kTop))) : 1.f;
 #pragma unroll 1
@@ -706,7 +725,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         // P goes where the P V of kPBufs tiles ago read
         if (uc >= F::kPBufs) {
           const int up = uc - F::kPBufs;
-          if (!(ok = all_ok(mbar_wait_cluster(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
+          if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
         }
         uint8_t *pbuf = sm_p + (uc % F::kPBufs) * F::kPBytes;
         if constexpr (FP8) {
@@ -739,7 +758,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         // the values are here; rows that not every query row sees are cleaned
         for (int v = 0; ok && v < F::kVPer; ++v) {
           const int u = vc + v, s = u % F::kVSlots;
-          ok = mbar_wait(&v_full[s], (u / F::kVSlots) & 1, abort_flag);
+          ok = wait_for(&v_full[s], (u / F::kVSlots) & 1, abort_flag);
           const int e = 2 * (sg.tile0 + t) + v * 2 / F::kVPer;
           const int k0 = e < job.pages ? job.page(e) * kPage + (v * F::kVTok) % kPage : 1 << 30;
           // every row sees all of them?
@@ -777,7 +796,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(p_bar[sb]);
+        if (lane == 0) mbar_arrive_remote(p_bar[sb]);
 #pragma unroll
         for (int g = 0; g < 4; ++g) sc[g] = sc_next[g];
       }
@@ -785,7 +804,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       // ---- results: O / l of this row, value columns [256 * half, +256)
       {
         const int up = uc - 1;
-        if (!(ok = all_ok(mbar_wait_cluster(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
+        if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
       }
       tc_fence_after();
       my_x[256] = l;
