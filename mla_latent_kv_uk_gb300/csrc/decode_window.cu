@@ -35,9 +35,9 @@
 // sum P' / sigma, summed per block before the division.
 //
 // Warps: 0 walks the split plan, publishes the segments and loads Q and K,
-// 1 issues the MMAs (leader CTA), 2 loads V, 4..7 turn scores into
-// probabilities (one row and half of the tile's keys per thread) and write
-// the results.  Lazy rescaling: O is rescaled when a row's reference would
+// 1 issues the MMAs (leader CTA), 2 loads V, 4..11 turn scores into
+// probabilities (one row and a quarter of the tile's keys per thread) and
+// write the results.  Lazy rescaling: O is rescaled when a row's reference would
 // be exceeded by more than 2^8.
 //
 // Split: every row group of a request is a job of ceil(pages / 2) tiles plus
@@ -64,7 +64,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kTile = 128;                // keys per tile: two pages
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kSoftWarps = 8;              // warps 4..11
 constexpr int kMinUnits = 3;              // smallest automatic span
 constexpr int kJobCost = 2;               // units of switching to a job
 constexpr int kSegSlots = 4;
@@ -94,11 +95,11 @@ struct Fmt {
   static constexpr int kOffK = kOffQ + kRowsBytes;
   static constexpr int kOffV = kOffK + kKSlots * kGroupBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVSlotBytes;
-  static constexpr int kOffX = kOffP + kPBufs * kPBytes;   // row exchange [3][128] floats
-  static constexpr int kOffSeg = kOffX + 3 * 128 * 4;
+  static constexpr int kOffX = kOffP + kPBufs * kPBytes;   // row exchange [2][4][64] floats
+  static constexpr int kOffSeg = kOffX + 2 * 256 * 4;
   static constexpr int kOffBars = kOffSeg + kSegSlots * 64;
   static constexpr int kBarBytes = 256;
-  static constexpr int kSmem = kOffBars + kBarBytes + 1024;
+  static constexpr int kSmem = kOffBars + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
   static_assert(kGroupBytes % 1024 == 0 && kRowsBytes % 1024 == 0, "swizzled tiles");
   // p' of a row's largest key after the reference moved, as a power of two
@@ -305,6 +306,15 @@ __device__ __forceinline__ uint32_t desc_lo(const void *p, uint32_t lbo) {
   return ((smem_u32(p) & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
+// Named barrier of `count` threads that tells each whether `v` held for all.
+__device__ __forceinline__ bool named_and(uint32_t id, uint32_t count, bool v) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %3, 0;\n\t"
+               "barrier.cta.red.and.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r) : "r"(id), "r"(count), "r"(static_cast<uint32_t>(v)) : "memory");
+  return r != 0;
+}
+
 // Probabilities (a, b) as two pairs of e4m3 codes, hi and lo.
 __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint32_t &lo) {
   const __half2 p = __floats2half2_rn(a, b);
@@ -323,8 +333,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ WindowArgs args) {
   using F = Fmt<FP8>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *smem = smem_raw;   // (no static shared memory: starts on 1024 bytes)
   uint8_t *sm_q = smem + F::kOffQ, *sm_k = smem + F::kOffK, *sm_v = smem + F::kOffV;
   uint8_t *sm_p = smem + F::kOffP;
   float *xchg = reinterpret_cast<float *>(smem + F::kOffX);
@@ -349,6 +358,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 "barriers");
   static_assert(sizeof(Seg) <= 64, "segment slot");
 
+  if (smem_u32(smem) & 1023u) {   // (never seen: the swizzled tiles need it)
+    if (threadIdx.x == 0) raise_error(args.err, MLA_DEVERR_TIMEOUT);
+    return;
+  }
   const int warp = warp_id(), lane = lane_id();
   const int rank = static_cast<int>(cluster_rank());
   if (threadIdx.x == 0) {
@@ -362,14 +375,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 8);               // the softmax warps of both CTAs
+      mbar_init(&p_full[s], 2 * kSoftWarps);  // the softmax warps of both CTAs
       mbar_init(&pv_done[s], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(&seg_full[s], 1);
-      mbar_init(&seg_empty[s], rank == 0 ? 6 : 5);   // V, softmax, and the leader's MMA warp
+      mbar_init(&seg_empty[s], kSoftWarps + (rank == 0 ? 2 : 1));   // V, softmax, the leader's MMAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -614,13 +627,29 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ softmax and results
-    const int quarter = warp & 3, half = quarter >> 1;
+    // Four threads share a row, each with 32 of the tile's keys: `half` (the
+    // TMEM lanes: which page), `sub` (which half of the page).
+    const int quarter = warp & 3, half = quarter >> 1, sub = (warp - 4) >> 2;
     const int r = (quarter & 1) * 32 + lane;            // row of this CTA
     const int tid = threadIdx.x - 128;
     const uint32_t lane_base = tmem + ((quarter * 32u) << 16);
-    const uint32_t bar_id = 1 + (quarter & 1);          // the two warps of the same rows
+    const uint32_t bar_id = 1 + (quarter & 1);          // the four warps of the same rows
     const uint32_t p_bar[2] = {peer_smem(&p_full[0], 0), peer_smem(&p_full[1], 0)};
-    float *my_x = xchg + (half * 64 + r), *its_x = xchg + ((half ^ 1) * 64 + r);
+    const int mine = (2 * half + sub) * 64 + r;
+    // largest / sum over the row's four threads; the two tables alternate, so
+    // that a thread may still read one while the next is written
+    int turn = 0;
+    // The hardware barrier has no limit, so no warp may leave the others in
+    // it: it takes along whether all is well, a warp whose wait ran out goes
+    // through it once more before it leaves, and the others leave behind it.
+    bool told = false;
+    auto exchange = [&](float &v, auto op) -> bool {
+      float *x = xchg + 256 * (turn ^= 1);
+      x[mine] = v;
+      told = !named_and(bar_id, 128, true);
+      v = op(op(x[r], x[64 + r]), op(x[128 + r], x[192 + r]));
+      return !told;
+    };
     auto all_ok = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
     Seg sg;
     int uc = 0, vc = 0;
@@ -632,7 +661,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       // (rows behind the request's last are computed and dropped)
       const int p = grow < R ? sg.len - args.q_len + grow / args.H : job.p1;
       const int wlo = args.window ? p - args.window + 1 : 0;
-      // scale of this thread's keys (a page of the tile), a tile ahead
+      // every query row of the job sees keys [clean_lo, job.p0] and the sinks
+      const int clean_lo = args.window ? job.p1 - args.window + 1 : 0;
+      // scales of this thread's keys, a tile ahead
       const int32_t *bt = args.block_table + static_cast<int64_t>(sg.b) * args.max_blocks;
       auto load_blk = [&](int t) -> int {
         const int e = 2 * (sg.tile0 + t) + half;
@@ -642,11 +673,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       };
       auto load_scales = [&](int blk, float *sc) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 2; ++g)
           sc[g] = blk < 0 ? args.k_scale
-                          : __ldg(args.scales + ((static_cast<int64_t>(blk) * kPage + 16 * g) >> args.sb_shift));
+                          : __ldg(args.scales + ((static_cast<int64_t>(blk) * kPage + 32 * sub + 16 * g) >>
+                                                 args.sb_shift));
       };
-      float sc[4], sc_next[4];
+      float sc[2], sc_next[2];
       int blk_next = load_blk(1);
       load_scales(load_blk(0), sc);
       float ref = -INFINITY, l = 0.f;
@@ -654,29 +686,37 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const int sb = uc & 1;
         load_scales(blk_next, sc_next);
         blk_next = load_blk(t + 2);
-        const int entry = 2 * (sg.tile0 + t) + half;
-        const int key0 = entry < job.pages ? job.page(entry) * kPage : 1 << 30;
-        float c[4], lg[4];
+        const int e0 = 2 * (sg.tile0 + t);
+        const int page0 = job.page(e0) * kPage;
+        const int page1 = e0 + 1 < job.pages ? job.page(e0 + 1) * kPage : 1 << 30;
+        const int key0 = (half ? page1 : page0) + 32 * sub;
+        const bool masked = key0 + 31 > p || (key0 < wlo && key0 + 32 > args.sinks);
+        auto clean = [&](int k0) {
+          return k0 == 1 << 30 ||
+                 (k0 + kPage - 1 <= job.p0 && (k0 >= clean_lo || k0 + kPage <= args.sinks));
+        };
+        const bool all_clean = clean(page0) && clean(page1);
+        float c[2], lg[2];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           // (a scale of 0 stands for zeros: so does the smallest one)
           const float sigma = fminf(fmaxf(sc[g], 0x1p-100f), 0x1p120f);
           c[g] = sigma * args.scale_log2;
           lg[g] = FP8 ? log2f(sigma) : 0.f;
-          sc[g] = sigma;
+          sc[g] = FP8 ? 1.f / sigma : 1.f;
         }
         if (!(ok = all_ok(wait_for(&s_full[sb], (uc >> 1) & 1, abort_flag)))) break;
         tc_fence_after();
-        float x[64];
-        tmem_ld_x64(lane_base + kColS + 64 * sb, reinterpret_cast<uint32_t *>(x));
-        if (key0 + 63 > p || (key0 < wlo && key0 + 64 > args.sinks)) {
+        float x[32];
+        tmem_ld_x32(lane_base + kColS + 64 * sb + 32 * sub, reinterpret_cast<uint32_t *>(x));
+        if (masked) {
           const int e = p - key0, a = wlo - key0, z = args.sinks - key0;
 #pragma unroll
-          for (int k = 0; k < 64; ++k) x[k] = k <= e && (k >= a || k < z) ? x[k] : -INFINITY;
+          for (int k = 0; k < 32; ++k) x[k] = k <= e && (k >= a || k < z) ? x[k] : -INFINITY;
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 16; k += 4) {
@@ -685,10 +725,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           }
           top = fmaxf(top, fmaf(fmaxf(m0, m1), c[g], lg[g]));
         }
-        // the row's other half of the keys
-        my_x[128 * sb] = top;
-        named_sync(bar_id, 64);
-        top = fmaxf(top, its_x[128 * sb]);
+        if (!(ok = exchange(top, [](float a, float b) { return fmaxf(a, b); }))) break;
         const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
         if (t == 0) {
           if (move) ref = top - F::kTop;
@@ -697,8 +734,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
           tc_fence_after();
           const float f = move ? (ref == -INFINITY ? 0.f : ex2(ref - (top - F::kTop))) : 1.f;
+          // (the two warps of a quadrant take 128 columns each)
 #pragma unroll 1
-          for (int q = 0; q < 256; q += 32) {
+          for (int q = 128 * sub; q < 128 * sub + 128; q += 32) {
             uint32_t o[32];
             tmem_ld_x32(lane_base + kColO + q, o);
 #pragma unroll
@@ -710,7 +748,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         const float base = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           const float d = lg[g] - base;
           float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -720,7 +758,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             x[k + 1] = ex2(x[k + 1]);
             add_f32x2(s0, s1, s0, s1, x[k], x[k + 1]);
           }
-          l += FP8 ? (s0 + s1) / sc[g] : s0 + s1;
+          l = fmaf(s0 + s1, sc[g], l);
         }
         // P goes where the P V of kPBufs tiles ago read
         if (uc >= F::kPBufs) {
@@ -732,7 +770,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           uint4 *hi = reinterpret_cast<uint4 *>(pbuf + r * 128);
           uint4 *lo = reinterpret_cast<uint4 *>(pbuf + 8192 + r * 128);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t h[4], w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -742,53 +780,54 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
               h[k] = h0 | (h1 << 16);
               w[k] = l0 | (l1 << 16);
             }
-            const int ch = (4 * half + q) ^ (r & 7);
+            const int ch = (4 * half + 2 * sub + q) ^ (r & 7);
             hi[ch] = make_uint4(h[0], h[1], h[2], h[3]);
             lo[ch] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
           uint4 *row = reinterpret_cast<uint4 *>(pbuf + half * 8192 + r * 128);
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            row[q ^ (r & 7)] = make_uint4(bf16x2_rn(x[8 * q], x[8 * q + 1]),
-                                          bf16x2_rn(x[8 * q + 2], x[8 * q + 3]),
-                                          bf16x2_rn(x[8 * q + 4], x[8 * q + 5]),
-                                          bf16x2_rn(x[8 * q + 6], x[8 * q + 7]));
+          for (int q = 0; q < 4; ++q)
+            row[(4 * sub + q) ^ (r & 7)] =
+                make_uint4(bf16x2_rn(x[8 * q], x[8 * q + 1]), bf16x2_rn(x[8 * q + 2], x[8 * q + 3]),
+                           bf16x2_rn(x[8 * q + 4], x[8 * q + 5]), bf16x2_rn(x[8 * q + 6], x[8 * q + 7]));
         }
-        // the values are here; rows that not every query row sees are cleaned
-        for (int v = 0; ok && v < F::kVPer; ++v) {
-          const int u = vc + v, s = u % F::kVSlots;
-          ok = wait_for(&v_full[s], (u / F::kVSlots) & 1, abort_flag);
-          const int e = 2 * (sg.tile0 + t) + v * 2 / F::kVPer;
-          const int k0 = e < job.pages ? job.page(e) * kPage + (v * F::kVTok) % kPage : 1 << 30;
-          // every row sees all of them?
-          if (!ok || e >= job.pages ||
-              (k0 + F::kVTok - 1 <= job.p0 &&
-               (!args.window || k0 > job.p1 - args.window || k0 + F::kVTok <= args.sinks)))
-            continue;
-          for (int idx = tid; idx < F::kVSlotBytes / 16; idx += 128) {
-            const int tok = (idx >> 3) % F::kVTok, key = k0 + tok;
-            const bool sink = key < args.sinks;
-            const bool some = key <= job.p1 && (!args.window || sink || key > job.p0 - args.window);
-            const bool all = key <= job.p0 && (!args.window || sink || key > job.p1 - args.window);
-            if (all) continue;
-            uint4 *w = reinterpret_cast<uint4 *>(sm_v + s * F::kVSlotBytes) + idx;
-            uint4 val = make_uint4(0, 0, 0, 0);
-            if (some) {   // seen by some rows: only what is not finite goes (0 * NaN in the others)
-              val = *w;
-              uint32_t *e4 = reinterpret_cast<uint32_t *>(&val);
+        // the values are here (the MMA thread goes by this CTA's word)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (FP8) {
-                  const uint32_t nan = (((e4[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
-                  e4[i] &= ~(nan * 0xFFu);
-                } else {
-                  if ((e4[i] & 0x7F80u) == 0x7F80u) e4[i] &= 0xFFFF0000u;
-                  if ((e4[i] & 0x7F800000u) == 0x7F800000u) e4[i] &= 0xFFFFu;
+        for (int v = 0; v < F::kVPer; ++v) {
+          const int u = vc + v;
+          ok = ok && wait_for(&v_full[u % F::kVSlots], (u / F::kVSlots) & 1, abort_flag);
+        }
+        if (ok && !all_clean) {
+          // rows that not every query row sees: 0 where none does, and where
+          // some do, 0 in place of what is not finite (0 times it in the others)
+#pragma unroll 1
+          for (int v = 0; v < F::kVPer; ++v) {
+            const int page = v * 2 < F::kVPer ? page0 : page1;
+            if (clean(page)) continue;
+            const int k0 = page + (v * F::kVTok) % kPage;
+            uint4 *slot = reinterpret_cast<uint4 *>(sm_v + ((vc + v) % F::kVSlots) * F::kVSlotBytes);
+            for (int idx = tid; idx < F::kVSlotBytes / 16; idx += 32 * kSoftWarps) {
+              const int key = k0 + (idx >> 3) % F::kVTok;
+              const bool sink = key < args.sinks;
+              if (key <= job.p0 && (sink || key >= clean_lo)) continue;
+              uint4 val = make_uint4(0, 0, 0, 0);
+              if (key <= job.p1 && (!args.window || sink || key > job.p0 - args.window)) {
+                val = slot[idx];
+                uint32_t *e4 = reinterpret_cast<uint32_t *>(&val);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if constexpr (FP8) {
+                    const uint32_t nan = (((e4[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+                    e4[i] &= ~(nan * 0xFFu);
+                  } else {
+                    if ((e4[i] & 0x7F80u) == 0x7F80u) e4[i] &= 0xFFFF0000u;
+                    if ((e4[i] & 0x7F800000u) == 0x7F800000u) e4[i] &= 0xFFFFu;
+                  }
                 }
               }
+              slot[idx] = val;
             }
-            *w = val;
           }
         }
         vc += F::kVPer;
@@ -798,18 +837,16 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(p_bar[sb]);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) sc[g] = sc_next[g];
+        for (int g = 0; g < 2; ++g) sc[g] = sc_next[g];
       }
       if (!ok) break;
-      // ---- results: O / l of this row, value columns [256 * half, +256)
+      // ---- results: O / l of this row, value columns [256 half + 128 sub, +128)
       {
         const int up = uc - 1;
         if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
       }
       tc_fence_after();
-      my_x[256] = l;
-      named_sync(bar_id, 64);
-      l += its_x[256];
+      if (!(ok = exchange(l, [](float a, float b) { return a + b; }))) break;
       const bool empty = l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
       const int64_t row0 = static_cast<int64_t>(sg.b) * R + sg.rg * 128 + 64 * rank;
@@ -817,55 +854,51 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const int nrows = min(64, R - sg.rg * 128 - 64 * rank);
       const int esz = args.out_f32 ? 4 : 2;
       uint8_t *dst0 = static_cast<uint8_t *>(sg.whole ? args.out : args.ws_o) +
-                      (at * kLatent + 256 * half) * esz;
+                      (at * kLatent + 256 * half + 128 * sub) * esz;
       const int64_t rstride = static_cast<int64_t>(kLatent) * esz;
-      if (half == 0 && r < nrows) {
+      if (half + sub == 0 && r < nrows) {
         const float v = empty ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
         (sg.whole ? args.lse : args.ws_lse)[at + r] = v;
       }
-      // staged through 4 KB of this warp's own in the P tiles (e4m3: of the
-      // buffer that the next tile does not use)
-      uint4 *buf = reinterpret_cast<uint4 *>(
-          FP8 ? sm_p + ((uc + 1) % F::kPBufs) * F::kPBytes + half * 8192 + (quarter & 1) * 4096
-              : sm_p + half * 8192 + (quarter & 1) * 4096);
+      // pieces of 64 bytes a row, staged through 2 KB of this warp's own in
+      // the P tile (its rows are written again behind the next exchange of
+      // the four warps that share them) so that stores cover whole sectors
+      uint4 *buf = reinterpret_cast<uint4 *>(sm_p + half * 8192 + (quarter & 1) * 4096 + sub * 2048);
 #pragma unroll 1
-      for (int q = 0; q < 256; q += 64) {
-        uint32_t o[64];
-        tmem_ld_x64(lane_base + kColO + q, o);
+      for (int q = 0; q < 128; q += 32) {
+        uint32_t o[32];
+        tmem_ld_x32(lane_base + kColO + 128 * sub + q, o);
         auto f = [&](int k) { return __uint_as_float(o[k]) * inv; };
 #pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {     // one (bf16) or two (fp32) 128-byte pieces of the row
+        for (int pc = 0; pc < 2; ++pc) {     // one (bf16) or two (fp32) pieces
           if (!args.out_f32 && pc == 1) break;
           __syncwarp();
-          if (!args.out_f32) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              buf[lane * 8 + (k ^ (lane & 7))] = make_uint4(
-                  bf16x2_rn(f(8 * k), f(8 * k + 1)), bf16x2_rn(f(8 * k + 2), f(8 * k + 3)),
-                  bf16x2_rn(f(8 * k + 4), f(8 * k + 5)), bf16x2_rn(f(8 * k + 6), f(8 * k + 7)));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int e = 32 * pc + 4 * k;
-              buf[lane * 8 + (k ^ (lane & 7))] =
-                  make_uint4(__float_as_uint(f(e)), __float_as_uint(f(e + 1)),
-                             __float_as_uint(f(e + 2)), __float_as_uint(f(e + 3)));
-            }
+          for (int k = 0; k < 4; ++k) {
+            const int e = 16 * pc + 4 * k;
+            buf[lane * 4 + (k ^ ((lane >> 1) & 3))] =
+                args.out_f32 ? make_uint4(__float_as_uint(f(e)), __float_as_uint(f(e + 1)),
+                                          __float_as_uint(f(e + 2)), __float_as_uint(f(e + 3)))
+                             : make_uint4(bf16x2_rn(f(8 * k), f(8 * k + 1)),
+                                          bf16x2_rn(f(8 * k + 2), f(8 * k + 3)),
+                                          bf16x2_rn(f(8 * k + 4), f(8 * k + 5)),
+                                          bf16x2_rn(f(8 * k + 6), f(8 * k + 7)));
           }
           __syncwarp();
-          uint8_t *dst = dst0 + static_cast<int64_t>(q + 32 * pc) * esz;
+          uint8_t *dst = dst0 + static_cast<int64_t>(q + 16 * pc) * esz;
 #pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int row = it * 4 + (lane >> 3), ch = lane & 7;
+          for (int it = 0; it < 4; ++it) {
+            const int row = it * 8 + (lane >> 2), ch = lane & 3;
             const int rr = (quarter & 1) * 32 + row;
             if (rr < nrows)
-              reinterpret_cast<uint4 *>(dst + rr * rstride)[ch] = buf[row * 8 + (ch ^ (row & 7))];
+              reinterpret_cast<uint4 *>(dst + rr * rstride)[ch] = buf[row * 4 + (ch ^ ((row >> 1) & 3))];
           }
         }
       }
       __syncwarp();
       tc_fence_before();
     }
+    if (!told) named_and(bar_id, 128, ok && !*abort_flag);
   }
   __syncthreads();
   cluster_sync();
