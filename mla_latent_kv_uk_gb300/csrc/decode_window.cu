@@ -18,8 +18,8 @@
 // [256c, 256c + 256) of all 128 keys.  Scores and probabilities never cross
 // the pair; each key row is fetched twice, once as a key by its page's CTA
 // and once, by then from L2, as a value by halves.  Measured on the GB300: a
-// 32-byte K step costs 44.5 cycles at N = 128 (Q K^T: 18 or 36 per tile) and
-// 64 cycles at N = 256 (P V: 8 steps for 128 e4m3 keys, 16 for bf16).
+// 32-byte K step costs 32 cycles at N = 128 (Q K^T: 18 or 36 per tile) and 66
+// at N = 256 (P V: 16 per tile in either format).
 //
 // e4m3 probabilities.  P as one e4m3 value would be off by up to 2^-4 and the
 // output with it; P is held as the sum of two e4m3 values, hi = e4m3(p) and
@@ -257,24 +257,36 @@ __device__ __forceinline__ void pair_dealloc(uint32_t taddr) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512)
                : "memory");
 }
+// One lane of a converged warp, chosen the same way every time.  The MMA
+// warp runs its loops as a whole with this lane's instructions predicated on:
+// addresses and descriptors then stay in uniform registers, and the 18 MMAs
+// of a tile's Q K^T issue in 574 cycles (32 each, their full rate), against
+// 1070 when one lane runs a branch of its own.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(e));
+  return e;
+}
 template <bool FP8>
 __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t acc) {
+                                         uint32_t acc, uint32_t me) {
   if constexpr (FP8)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(me) : "memory");
   else
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(me) : "memory");
 }
 // Arrives once on the barrier at this offset in both CTAs when every MMA so
 // far of this thread has completed.
-__device__ __forceinline__ void pair_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
-               ".multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-               "h"(static_cast<uint16_t>(3)) : "memory");
+__device__ __forceinline__ void pair_commit(uint64_t *bar, uint32_t me) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+               "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+               ".multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+               "h"(static_cast<uint16_t>(3)), "r"(me) : "memory");
 }
 // A load into this CTA whose bytes count on a barrier of either CTA.
 __device__ __forceinline__ void pair_load(void *dst, const CUtensorMap *map, uint32_t bar_cluster,
@@ -362,7 +374,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (threadIdx.x == 0) raise_error(args.err, MLA_DEVERR_TIMEOUT);
     return;
   }
-  const int warp = warp_id(), lane = lane_id();
+  // (a shuffle: the same for the warp, as far as the compiler can tell)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0), lane = lane_id();
   const int rank = static_cast<int>(cluster_rank());
   if (threadIdx.x == 0) {
     for (int s = 0; s < F::kKSlots; ++s) {
@@ -397,14 +410,13 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   grid_dep_wait();
   grid_dep_launch();
 
-  // Every consumer of segments takes them in order: a warp, or (mask 1) the
-  // MMA thread.
-  auto take_seg = [&](int ns, Seg &s, uint32_t mask) -> bool {
+  // Every consuming warp takes the segments in order.
+  auto take_seg = [&](int ns, Seg &s) -> bool {
     const int slot = ns % kSegSlots;
-    if (!__all_sync(mask, wait_for(&seg_full[slot], (ns / kSegSlots) & 1, abort_flag)))
+    if (!__all_sync(0xffffffffu, wait_for(&seg_full[slot], (ns / kSegSlots) & 1, abort_flag)))
       return false;
     s = segq[slot];
-    __syncwarp(mask);
+    __syncwarp();
     if (lane == 0) mbar_arrive(&seg_empty[slot]);
     return s.ntiles > 0;
   };
@@ -510,7 +522,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     Seg sg;
     int vc = 0;
     bool ok = true;
-    for (int ns = 0; ok && take_seg(ns, sg, 0xffffffffu); ++ns) {
+    for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
       const Job job = job_of(sg.rg, sg.len, args);
       Pages pg{-64, -1};
       for (int t = 0; ok && t < sg.ntiles; ++t) {
@@ -536,14 +548,17 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         wait_for(&v_full[u % F::kVSlots], (u / F::kVSlots) & 1, &no_abort);
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       // ---------------------------------------------------------- MMAs
       const uint32_t idesc_qk = FP8 ? idesc_e4m3(128, kTile, false, false)
                                     : idesc_bf16(128, kTile, false, false);
       const uint32_t idesc_pv = FP8 ? idesc_e4m3(128, 256, false, true)
                                     : idesc_bf16(128, 256, false, true);
+      const uint32_t me = elect_one();
       const uint32_t qd = desc_lo(sm_q, 16);
-      Seg sg;
+      auto wait = [&](uint64_t *bar, int phase) -> bool {
+        return __all_sync(0xffffffffu, wait_for(bar, phase & 1, abort_flag));
+      };
       int kc = 0, vc = 0, uc = 0;             // K slots, V slots, tiles so far
       bool ok = true;
       auto issue_qk = [&](int u) -> bool {
@@ -551,7 +566,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
         for (int g = 0; g < F::kGroups; ++g, ++kc) {
           const int s = kc % F::kKSlots;
-          if (!wait_for(&k_full[s], (kc / F::kKSlots) & 1, abort_flag)) return false;
+          if (!wait(&k_full[s], kc / F::kKSlots)) return false;
           tc_fence_after();
           // one descriptor a slot; steps add to its address field (16-byte units)
           const uint32_t kd = desc_lo(sm_k + s * F::kGroupBytes, 16);
@@ -560,67 +575,71 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             for (int k = 0; k < 16; ++k)
               pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (k >> 2) * 512 + (k & 3) * 2),
                             desc_at<1024, kSwizzle128B>(kd + (k >> 2) * 512 + (k & 3) * 2), idesc_qk,
-                            k > 0);
+                            k > 0, me);
 #pragma unroll
             for (int k = 0; k < 2; ++k)       // the rope columns: rows of 64 bytes
               pair_mma<FP8>(d, desc_at<512, kSwizzle64B>(qd + 4 * 512 + 2 * k),
-                            desc_at<512, kSwizzle64B>(kd + 4 * 512 + 2 * k), idesc_qk, 1);
+                            desc_at<512, kSwizzle64B>(kd + 4 * 512 + 2 * k), idesc_qk, 1, me);
           } else {
 #pragma unroll
             for (int k = 0; k < 12; ++k)
               pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (3 * g + (k >> 2)) * 512 + (k & 3) * 2),
                             desc_at<1024, kSwizzle128B>(kd + (k >> 2) * 512 + (k & 3) * 2), idesc_qk,
-                            g + k > 0);
+                            g + k > 0, me);
           }
-          pair_commit(&k_empty[s]);
+          pair_commit(&k_empty[s], me);
         }
-        pair_commit(&s_full[u & 1]);
+        pair_commit(&s_full[u & 1], me);
         return true;
       };
+      // All steps of one accumulator, then of the other: an MMA that adds to
+      // what the last but one wrote waits for it (232 cycles a change).
       auto issue_pv = [&](int u, bool first) {
         const uint32_t pd = desc_lo(sm_p + (u % F::kPBufs) * F::kPBytes, 16);
 #pragma unroll
-        for (int v = 0; v < F::kVPer; ++v, ++vc) {
-          const int s = vc % F::kVSlots;
-          const uint32_t vd = desc_lo(sm_v + s * F::kVSlotBytes, F::kVBox);
+        for (int j = 0; j < 2; ++j) {         // value columns 128j .. 128j + 127 of either CTA
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {    // 32 bytes of P: 32 e4m3 or 16 bf16 keys
-            const int step = 2 * v + kk;
-            const uint32_t pa = pd + (FP8 ? step * 2 : (step >> 2) * 512 + (step & 3) * 2);
-            const uint32_t acc = first && step == 0 ? 0u : 1u;
+          for (int v = 0; v < F::kVPer; ++v) {
+            const int s = (vc + v) % F::kVSlots;
+            const uint32_t vd = desc_lo(sm_v + s * F::kVSlotBytes, F::kVBox);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {     // value columns 128j .. 128j + 127 of either CTA
+            for (int kk = 0; kk < 2; ++kk) {  // 32 bytes of P: 32 e4m3 or 16 bf16 keys
+              const int step = 2 * v + kk;
+              const uint32_t pa = pd + (FP8 ? step * 2 : (step >> 2) * 512 + (step & 3) * 2);
               const uint64_t bd = desc_at<1024, kSwizzle128B>(
                   vd + (FP8 ? j * F::kVBox + kk * 4096 : 2 * j * F::kVBox + kk * 2048) / 16);
-              pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa), bd, idesc_pv, acc);
+              pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa), bd, idesc_pv,
+                            first && step == 0 ? 0u : 1u, me);
               if constexpr (FP8)
                 pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa + 512), bd,
-                              idesc_pv, 1);
+                              idesc_pv, 1, me);
             }
+            if (j == 1) pair_commit(&v_empty[s], me);
           }
-          pair_commit(&v_empty[s]);
         }
-        pair_commit(&pv_done[u & 1]);
+        vc += F::kVPer;
+        pair_commit(&pv_done[u & 1], me);
       };
-      int ns = 0;
-      for (; ok && take_seg(ns, sg, 1u); ++ns) {
-        if (!(ok = wait_for(q_full, ns & 1, abort_flag))) break;
+      Seg sg;
+      for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
+        const int n = __shfl_sync(0xffffffffu, sg.ntiles, 0);
+        if (!(ok = wait(q_full, ns))) break;
         if (!(ok = issue_qk(uc))) break;
-        if (sg.ntiles == 1) pair_commit(q_empty);
-        for (int t = 0; t < sg.ntiles; ++t, ++uc) {
+        if (n == 1) pair_commit(q_empty, me);
+        for (int t = 0; t < n; ++t, ++uc) {
           // the scores of tile t + 1 go where tile t - 1's were: read before
           // its probabilities were handed over
-          if (t + 1 < sg.ntiles) {
+          if (t + 1 < n) {
             if (!(ok = issue_qk(uc + 1))) break;
-            if (t + 2 == sg.ntiles) pair_commit(q_empty);
+            if (t + 2 == n) pair_commit(q_empty, me);
           }
-          if (!(ok = wait_for(&p_full[uc & 1], (uc >> 1) & 1, abort_flag))) break;
+          if (!(ok = wait(&p_full[uc & 1], uc >> 1))) break;
           tc_fence_after();
           issue_pv(uc, t == 0);
         }
       }
       if (*abort_flag) {
-        pair_commit(drain);
+        pair_commit(drain, me);
         volatile int no_abort = 0;
         wait_for(drain, 0, &no_abort);
       }
@@ -654,7 +673,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     Seg sg;
     int uc = 0, vc = 0;
     bool ok = true;
-    for (int ns = 0; ok && take_seg(ns, sg, 0xffffffffu); ++ns) {
+    for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
       const Job job = job_of(sg.rg, sg.len, args);
       const int R = args.q_len * args.H;
       const int grow = sg.rg * 128 + 64 * rank + r;     // row of the request
