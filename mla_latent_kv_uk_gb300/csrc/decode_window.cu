@@ -687,13 +687,13 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       auto load_blk = [&](int t) -> int {
         const int e = 2 * (sg.tile0 + t) + half;
         if (!FP8 || !args.scales || t >= sg.ntiles || e >= job.pages) return -1;
-        const int v = __ldg(bt + job.page(e));
-        return v >= 0 && v < args.num_blocks ? v : -1;
+        return __ldg(bt + job.page(e));   // (looked at a tile later: nothing waits for it here)
       };
       auto load_scales = [&](int blk, float *sc) {
 #pragma unroll
         for (int g = 0; g < 2; ++g)
-          sc[g] = blk < 0 ? args.k_scale
+          sc[g] = blk < 0 || blk >= args.num_blocks
+                          ? args.k_scale
                           : __ldg(args.scales + ((static_cast<int64_t>(blk) * kPage + 32 * sub + 16 * g) >>
                                                  args.sb_shift));
       };
@@ -746,24 +746,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         if (!(ok = exchange(top, [](float a, float b) { return fmaxf(a, b); }))) break;
         const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
-        if (t == 0) {
-          if (move) ref = top - F::kTop;
-        } else if (__any_sync(0xffffffffu, move)) {
-          const int up = uc - 1;
-          if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
-          tc_fence_after();
-          const float f = move ? (ref == -INFINITY ? 0.f : ex2(ref - (top - F::kTop))) : 1.f;
-          // (the two warps of a quadrant take 128 columns each)
-#pragma unroll 1
-          for (int q = 128 * sub; q < 128 * sub + 128; q += 32) {
-            uint32_t o[32];
-            tmem_ld_x32(lane_base + kColO + q, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st_x32(lane_base + kColO + q, o);
-          }
+        const bool rescale = t > 0 && __any_sync(0xffffffffu, move);
+        float f = 1.f;
+        if (move) {
+          f = ref == -INFINITY ? 0.f : ex2(ref - (top - F::kTop));
+          ref = top - F::kTop;
           l *= f;
-          if (move) ref = top - F::kTop;
         }
         const float base = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
@@ -810,6 +798,21 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             row[(4 * sub + q) ^ (r & 7)] =
                 make_uint4(bf16x2_rn(x[8 * q], x[8 * q + 1]), bf16x2_rn(x[8 * q + 2], x[8 * q + 3]),
                            bf16x2_rn(x[8 * q + 4], x[8 * q + 5]), bf16x2_rn(x[8 * q + 6], x[8 * q + 7]));
+        }
+        if (rescale) {
+          // O follows the reference, now that the last P V (long done, mostly)
+          // is; the two warps of a quadrant take 128 columns each
+          const int up = uc - 1;
+          if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 128 * sub; q < 128 * sub + 128; q += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(lane_base + kColO + q, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st_x32(lane_base + kColO + q, o);
+          }
         }
         // the values are here (the MMA thread goes by this CTA's word)
 #pragma unroll
