@@ -419,10 +419,11 @@ int mla_gather_cache_scaled(const void *kv_cache, const float *kv_scales,
  * of pages without a visible key are not read.
  * window >= 0 (0: every earlier token), sinks >= 0 (of no effect without a
  * window).  workspace: mla_decode_window_workspace_size(B, q_len, H,
- * max_blocks*64, window, sinks, split_tiles) bytes, 16-byte aligned, written before it
- * is read (calls on different streams need workspaces of their own).
- * split_tiles as in mla_decode_paged, in tiles of 128 tokens.  Limits as
- * there. */
+ * max_blocks*64, window, sinks, split_tiles) bytes, 16-byte aligned, written
+ * before it is read (calls on different streams need workspaces of their
+ * own); 0 bytes, and workspace may be NULL, where no request can have more
+ * than a few tiles.  split_tiles as in mla_decode_paged, in tiles of 128
+ * tokens.  Limits as there. */
 int mla_decode_window_workspace_size(int B, int q_len, int H, int max_seq_len,
                                      int window, int sinks, int split_tiles,
                                      size_t *bytes);

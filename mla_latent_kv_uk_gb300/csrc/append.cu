@@ -5,7 +5,7 @@
 // depends on the angle's fraction of a turn only, so the host hands over
 // turns-per-position theta_i / 2pi as a 64-bit binary fraction, and the
 // position times it, modulo 2^64, is the exact fraction of a turn (off by at
-// most position * 2^-53 turns, the host's rounding of theta_i / 2pi).  Its
+// most position * 2^-53 turns, the host's roundings of theta_i / 2pi).  Its
 // upper 32 bits go through sincospi in fp32.  (The fp64 sine and cosine that
 // mla_rope_cache_write takes cost more than the call's memory traffic once
 // there are thousands of tokens: this GPU runs two fp64 FMAs a clock and SM.)
@@ -347,11 +347,16 @@ extern "C" int mla_rope_cache_append(void *q_pe, int64_t q_stride_t, int64_t q_s
   p.num_slots = static_cast<int64_t>(num_blocks) * kPage;
   p.err = device_error_word();
   if (!p.err) return MLA_ERR_CUDA;
+  // base^(-i/32) as products of base^(-1/2), base^(-1/4), ... by i's bits: at
+  // most five roundings, where 32 calls of exp2 cost a microsecond
   Turns turns;
-  const double log2_base = std::log2(static_cast<double>(rope_base));
-  for (int i = 0; i < kPairs; ++i)
-    turns.per_pos[i] = static_cast<unsigned long long>(
-        std::ldexp(std::exp2(-(2.0 * i / kRope) * log2_base) * 0.15915494309189533577, 64));
+  double f[kPairs];
+  f[0] = 0.15915494309189533577 * 0x1p64;   // 2^64 / 2 pi
+  for (int bit = 1; bit < kPairs; bit <<= 1) {
+    const double step = std::pow(static_cast<double>(rope_base), -static_cast<double>(bit) / kPairs);
+    for (int i = 0; i < bit; ++i) f[bit + i] = f[i] * step;
+  }
+  for (int i = 0; i < kPairs; ++i) turns.per_pos[i] = static_cast<unsigned long long>(f[i]);
   const dim3 grid(T, 1 + (q_pe ? (H + kHeadsPerCta - 1) / kHeadsPerCta : 0));
   append_kernel<<<grid, kThreads, 0, stream>>>(p, turns);
   return launch_status();

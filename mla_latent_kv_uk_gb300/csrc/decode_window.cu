@@ -68,6 +68,9 @@ constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;              // warps 4..11
 constexpr int kMinUnits = 3;              // smallest automatic span
 constexpr int kJobCost = 2;               // units of switching to a job
+// Jobs that cannot have more tiles than this are not cut: each is one pair's
+// from end to end, written directly, and no merge kernel follows.
+constexpr int kSoloTiles = 3;
 constexpr int kSegSlots = 4;
 constexpr uint32_t kColO = 0, kColS = 256;   // O [0,256), S [256,320) and [320,384)
 
@@ -114,7 +117,7 @@ struct WindowArgs {
   float scale_log2;             // sm_scale * log2(e) * q_scale
   const int32_t *block_table, *seq_lens;
   int B, q_len, H, max_blocks, num_blocks, window, sinks;
-  int RG, forced, spans_at_once;
+  int RG, forced, spans_at_once, solo;
   void *out;
   int out_f32;
   float *lse;
@@ -161,7 +164,7 @@ __device__ __forceinline__ int units_of(int j, const WindowArgs &a, int &len) {
 
 struct Seg {
   int b, rg, len;
-  int tile0, ntiles;            // ntiles < 0: the end
+  int tile0, ntiles;            // ntiles 0: a job without a key (uncut jobs only); < 0: the end
   int whole, slot;
 };
 
@@ -193,6 +196,23 @@ struct Walk {
     C = a.forced > 0 ? a.forced : max(kMinUnits, (total - 1) / a.spans_at_once + 1);
     span = blockIdx.x >> 1;
     open = false;
+  }
+  __device__ void init_solo(const WindowArgs &a) {
+    J = a.B * a.RG;
+    span = blockIdx.x >> 1;
+  }
+  // Uncut: jobs span, span + pairs, ...
+  __device__ bool next_solo(const WindowArgs &a, Seg &s) {
+    if (span >= J) return false;
+    s.b = span % a.B;
+    s.rg = span / a.B;
+    s.len = length_of(s.b, a, s.rg == 0);
+    s.tile0 = 0;
+    s.ntiles = job_of(s.rg, s.len, a).tiles();
+    s.whole = 1;
+    s.slot = 0;
+    span += a.spans_at_once;
+    return true;
   }
   __device__ void load(const WindowArgs &a, int at, int before, int lane) {
     base = at;
@@ -418,7 +438,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     s = segq[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&seg_empty[slot]);
-    return s.ntiles > 0;
+    return s.ntiles >= 0;
   };
   // Block ids of a segment's pages: lane k holds those of list entry
   // base + k; entries behind the list and bad ids give -1.
@@ -452,10 +472,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       }
     }
     Walk walk;
-    walk.init(args, lane);
-    if (blockIdx.x == 0 && lane == 0) args.ws_head[0] = walk.C;
+    if (args.solo) {
+      walk.init_solo(args);
+    } else {
+      walk.init(args, lane);
+      if (blockIdx.x == 0 && lane == 0) args.ws_head[0] = walk.C;
+    }
     Seg sg;
-    int ns = 0, kc = 0;
+    int ns = 0, nq = 0, kc = 0;             // segments, queries, K slots so far
     bool ok = true;
     auto publish = [&](const Seg &s) -> bool {
       const int slot = ns % kSegSlots;
@@ -469,12 +493,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       return true;
     };
     const uint32_t q_bar = peer_smem(q_full, 0);
-    while (ok && walk.next(args, sg, lane)) {
+    while (ok && (args.solo ? walk.next_solo(args, sg) : walk.next(args, sg, lane))) {
       if (!(ok = publish(sg))) break;
+      ++ns;
+      if (sg.ntiles == 0) continue;
       const Job job = job_of(sg.rg, sg.len, args);
       // Q, once the last segment's last Q K^T has read it
-      if (ns > 0 && !(ok = wait_for(q_empty, (ns - 1) & 1, abort_flag))) break;
-      ++ns;
+      if (nq > 0 && !(ok = wait_for(q_empty, (nq - 1) & 1, abort_flag))) break;
+      ++nq;
       if (lane == 0) {
         if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kRowsBytes);
         const int row = sg.b * args.q_len * args.H + sg.rg * 128 + 64 * rank;
@@ -513,7 +539,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       volatile int no_abort = 0;
       for (int u = max(0, kc - F::kKSlots); u < kc; ++u)
         wait_for(&k_full[u % F::kKSlots], (u / F::kKSlots) & 1, &no_abort);
-      if (ns > 0) wait_for(q_full, (ns - 1) & 1, &no_abort);
+      if (nq > 0) wait_for(q_full, (nq - 1) & 1, &no_abort);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------- V
@@ -621,9 +647,11 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         pair_commit(&pv_done[u & 1], me);
       };
       Seg sg;
+      int nq = 0;
       for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
         const int n = __shfl_sync(0xffffffffu, sg.ntiles, 0);
-        if (!(ok = wait(q_full, ns))) break;
+        if (n == 0) continue;
+        if (!(ok = wait(q_full, nq++))) break;
         if (!(ok = issue_qk(uc))) break;
         if (n == 1) pair_commit(q_empty, me);
         for (int t = 0; t < n; ++t, ++uc) {
@@ -674,8 +702,17 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     int uc = 0, vc = 0;
     bool ok = true;
     for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
-      const Job job = job_of(sg.rg, sg.len, args);
       const int R = args.q_len * args.H;
+      if (sg.ntiles == 0) {
+        const int row0 = sg.rg * 128 + 64 * rank, n = min(64, R - row0);
+        const int64_t at = static_cast<int64_t>(sg.b) * R + row0;
+        const int chunks = kLatent * (args.out_f32 ? 4 : 2) / 16;
+        uint4 *o = static_cast<uint4 *>(args.out) + at * chunks;
+        for (int k = tid; k < n * chunks; k += 32 * kSoftWarps) o[k] = make_uint4(0, 0, 0, 0);
+        if (tid < n) args.lse[at + tid] = -INFINITY;
+        continue;
+      }
+      const Job job = job_of(sg.rg, sg.len, args);
       const int grow = sg.rg * 128 + 64 * rank + r;     // row of the request
       // (rows behind the request's last are computed and dropped)
       const int p = grow < R ? sg.len - args.q_len + grow / args.H : job.p1;
@@ -1022,26 +1059,27 @@ struct PairLaunch {
 };
 
 // CTA pairs that are resident at once (a pair needs both SMs in one GPC), at
-// most one per two SMs; cached per device.
+// most one per two SMs; cached per device, with the kernels' shared memory
+// allowance, which is set on the way.
 int pairs_for_device() {
   constexpr int kMaxDevices = 64;
   static int cache[kMaxDevices] = {};
   static std::mutex mu;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  const int sms = device_sm_count();
-  int g = sms >= 2 ? sms / 2 : 1;
-  if (dev < 0 || dev >= kMaxDevices) return g;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (cache[dev] > 0) return cache[dev];
-  int n = 0;
-  // (the larger of the two formats' shared memory)
+  const int sms = device_sm_count();
+  int g = sms >= 2 ? sms / 2 : 1, n = 0;
+  PairLaunch<false> pl(g, nullptr);   // (the larger of the two formats' shared memory)
   if (cudaFuncSetAttribute(window_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Fmt<false>::kSmem) == cudaSuccess) {
-    PairLaunch<false> pl(g, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&n, window_kernel<false>, &pl.cfg) != cudaSuccess) n = 0;
+                           Fmt<false>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(window_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Fmt<true>::kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, window_kernel<false>, &pl.cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
   }
-  cudaGetLastError();
   if (n > 0) g = std::min(g, n);
   cache[dev] = g;
   return g;
@@ -1054,21 +1092,25 @@ bool shape_ok(int B, int q_len, int H) {
 
 struct WsLayout {
   size_t o_off, lse_off, total;
+  bool solo;
 };
 
 WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sinks,
-                   int split_tiles) {
+                   int split_tiles, int pairs) {
   const int64_t RG = (static_cast<int64_t>(q_len) * H + 127) / 128, J = B * RG;
-  int64_t spans = pairs_for_device();
-  if (split_tiles > 0) {
-    int64_t pages = (static_cast<int64_t>(max_seq_len) + kPage - 1) / kPage;
-    if (window > 0)   // the sinks' pages and the window's, either of which may begin inside a page
-      pages = std::min(pages, (static_cast<int64_t>(window) + q_len) / kPage + 2 +
-                                  (static_cast<int64_t>(sinks) + kPage - 1) / kPage);
-    spans = (J * ((pages + 1) / 2 + kJobCost) + split_tiles - 1) / split_tiles;
-  }
+  // most pages of a job: the sinks' and the window's, which may begin inside
+  // a page and is q_len - 1 tokens longer for the job's queries together
+  int64_t pages = (static_cast<int64_t>(max_seq_len) + kPage - 1) / kPage;
+  if (window > 0)
+    pages = std::min(pages, (static_cast<int64_t>(window) + q_len) / kPage + 2 +
+                                (static_cast<int64_t>(sinks) + kPage - 1) / kPage);
+  const int64_t tiles = (pages + 1) / 2;
+  WsLayout w{};
+  w.solo = split_tiles == 0 && tiles <= kSoloTiles;
+  if (w.solo) return w;   // nothing to keep
+  const int64_t spans =
+      split_tiles > 0 ? (J * (tiles + kJobCost) + split_tiles - 1) / split_tiles : pairs;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  WsLayout w;
   w.o_off = up((2 + 2 * static_cast<size_t>(J)) * sizeof(int));
   w.lse_off = w.o_off + static_cast<size_t>(2 * spans) * 128 * kLatent * sizeof(float);
   w.total = w.lse_off + static_cast<size_t>(2 * spans) * 128 * sizeof(float);
@@ -1107,16 +1149,20 @@ int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArg
   const uint32_t box[2] = {F::kCols, 64}, box_r[2] = {64, 64}, box_v[2] = {F::kCols, F::kVTok};
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const CUtensorMapSwizzle sw_r = FP8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  // (each format encodes the maps that it uses)
   CUtensorMap tk, tkr, tv, tq, tqr;
-  if (!make_tmap(&tk, dt, 2, kv_cache, kv_dims, strides, box, sw) ||
-      !make_tmap(&tkr, dt, 2, kv_cache, kv_dims, strides, box_r, sw_r) ||
-      !make_tmap(&tv, dt, 2, kv_cache, kv_dims, strides, box_v, sw) ||
-      !make_tmap(&tq, dt, 2, q, q_dims, strides, box, sw) ||
-      !make_tmap(&tqr, dt, 2, q, q_dims, strides, box_r, sw_r))
-    return MLA_ERR_CUDA;
-  if (cudaFuncSetAttribute(window_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           F::kSmem) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  bool ok = make_tmap(&tk, dt, 2, kv_cache, kv_dims, strides, box, sw) &&
+            make_tmap(&tq, dt, 2, q, q_dims, strides, box, sw);
+  if constexpr (FP8) {
+    ok = ok && make_tmap(&tkr, dt, 2, kv_cache, kv_dims, strides, box_r, sw_r) &&
+         make_tmap(&tqr, dt, 2, q, q_dims, strides, box_r, sw_r);
+    tv = tk;
+  } else {
+    ok = ok && make_tmap(&tv, dt, 2, kv_cache, kv_dims, strides, box_v, sw);
+    tkr = tk;
+    tqr = tq;
+  }
+  if (!ok) return MLA_ERR_CUDA;
   PairLaunch<FP8> pl(pairs, stream);
   return cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8>, tk, tkr, tv, tq, tqr, a) == cudaSuccess
              ? MLA_OK
@@ -1129,8 +1175,10 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
                   float sm_scale, int window, int sinks, int split_tiles, void *out, int out_dtype,
                   float *lse, void *workspace, size_t ws_bytes, mla_stream_t stream) {
   if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
-  const WsLayout w = ws_layout(B, q_len, H, max_blocks * kPage, window, sinks, split_tiles);
-  if (!workspace || ws_bytes < w.total) return MLA_ERR_WORKSPACE;
+  const int pairs = pairs_for_device();
+  if (pairs == 0) return MLA_ERR_CUDA;
+  const WsLayout w = ws_layout(B, q_len, H, max_blocks * kPage, window, sinks, split_tiles, pairs);
+  if (!w.solo && (!workspace || ws_bytes < w.total)) return MLA_ERR_WORKSPACE;
   WindowArgs a{};
   a.err = device_error_word();
   if (!a.err) return MLA_ERR_CUDA;
@@ -1150,7 +1198,9 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.sinks = std::min(sinks, 1 << 30);
   a.RG = static_cast<int>((static_cast<int64_t>(q_len) * H + 127) / 128);
   a.forced = split_tiles;
-  a.spans_at_once = pairs_for_device();
+  a.solo = w.solo;
+  const int64_t jobs = static_cast<int64_t>(B) * a.RG;
+  a.spans_at_once = w.solo ? static_cast<int>(std::min<int64_t>(pairs, jobs)) : pairs;
   a.out = out;
   a.out_f32 = out_dtype == MLA_F32;
   a.lse = lse;
@@ -1160,7 +1210,7 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.ws_lse = reinterpret_cast<float *>(ws + w.lse_off);
   const int st = fp8 ? launch_pairs<true>(q, kv_cache, a.spans_at_once, a, stream)
                      : launch_pairs<false>(q, kv_cache, a.spans_at_once, a, stream);
-  if (st != MLA_OK) return st;
+  if (st != MLA_OK || w.solo) return st;
   const int rows = std::min(128, q_len * H);
   const dim3 grid(B * a.RG, (rows + kMergeWarps - 1) / kMergeWarps), block(kMergeWarps * 32);
   const cudaError_t e = a.out_f32
@@ -1180,7 +1230,9 @@ extern "C" int mla_decode_window_workspace_size(int B, int q_len, int H, int max
   if (!bytes || !shape_ok(B, q_len, H) || max_seq_len < 0 || window < 0 || sinks < 0 ||
       split_tiles < 0)
     return MLA_ERR_INVALID_ARG;
-  *bytes = ws_layout(B, q_len, H, max_seq_len, window, sinks, split_tiles).total;
+  // (without a device: what an upper bound of pairs needs)
+  const int pairs = pairs_for_device();
+  *bytes = ws_layout(B, q_len, H, max_seq_len, window, sinks, split_tiles, pairs ? pairs : 128).total;
   return MLA_OK;
 }
 

@@ -4,6 +4,7 @@ the host, before any launch (no GPU needed)."""
 import ctypes
 
 import pytest
+import torch
 
 P = ctypes.c_void_p
 OK, INVALID, WORKSPACE = 0, 1, 3
@@ -84,16 +85,24 @@ def test_decode_scaled(L, bad):
     assert L.mla_decode_paged_scaled(*_change(SCALED, **bad)) == INVALID
 
 
+@pytest.mark.gpu
+def test_decode_workspace_missing(L):
+    """(The size depends on the device.)  Refused before any launch."""
+    assert L.mla_decode_paged_window(*_change(DECODE, mb=99, window=0, ws=P(0))) == WORKSPACE
+    assert L.mla_decode_paged_window(*_change(DECODE, mb=99, window=0, n=8)) == WORKSPACE
+    assert L.mla_decode_paged_scaled(*_change(SCALED, mb=99, n=8)) == WORKSPACE
+    assert torch.cuda.current_device() == 0
+
+
 def test_decode_workspace(L):
-    assert L.mla_decode_paged_window(*_change(DECODE, ws=P(0))) == WORKSPACE
-    assert L.mla_decode_paged_window(*_change(DECODE, n=8)) == WORKSPACE
-    assert L.mla_decode_paged_scaled(*_change(SCALED, n=8)) == WORKSPACE
     n = ctypes.c_size_t(0)
+    assert L.mla_decode_window_workspace_size(2, 1, 16, 64 * 99, 0, 0, 0, ctypes.byref(n)) == OK and n.value > 8
+    assert L.mla_decode_window_workspace_size(2, 1, 16, 64 * 99, 64, 4, 0, ctypes.byref(n)) == OK and n.value == 0
     for bad in ((0, 1, 16, 64, 0, 0, 0), (1, 65, 16, 64, 0, 0, 0), (1, 1, 16, -1, 0, 0, 0),
                 (1, 1, 16, 64, -1, 0, 0), (1, 1, 16, 64, 0, -1, 0), (1, 1, 16, 64, 0, 0, -1)):
         assert L.mla_decode_window_workspace_size(*bad, ctypes.byref(n)) == INVALID
     assert L.mla_decode_window_workspace_size(1, 1, 16, 64, 0, 0, 0, None) == INVALID
-    assert L.mla_decode_window_workspace_size(1, 1, 16, 64, 8, 1, 0, ctypes.byref(n)) == OK and n.value > 0
+    assert L.mla_decode_window_workspace_size(1, 1, 16, 64, 8, 1, 2, ctypes.byref(n)) == OK and n.value > 0
 
 
 PREFILL = dict(q=A, k=A, v=A, cu_q=A, cu_k=A, B=1, Tq=4, Nk=8, H=2, mq=4, window=16, sinks=0, sm=0.1, out=A, lse=A,
