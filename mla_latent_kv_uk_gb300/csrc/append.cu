@@ -29,7 +29,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kHeadsPerCta = 64;
+constexpr int kHeadsPerCta = 128;   // query heads that a CTA rotates: four 16-byte chunks a thread
 constexpr int kPairs = kRope / 2;
 constexpr int kMinExp = -100;
 
@@ -244,7 +244,7 @@ __device__ void append_block(const AppendArgs &p, const Turns &turns, int t) {
 }
 
 // Grid (T, 1 + head groups): the first CTA of a token takes its cache row,
-// the others rotate 64 heads each.
+// the others rotate 128 heads each.
 __global__ void __launch_bounds__(kThreads)
 append_kernel(const __grid_constant__ AppendArgs p, const __grid_constant__ Turns turns) {
   const int t = blockIdx.x;
@@ -254,28 +254,54 @@ append_kernel(const __grid_constant__ AppendArgs p, const __grid_constant__ Turn
     else append_block<2>(p, turns, t);
     return;
   }
-  __shared__ float cs[kPairs], sn[kPairs];
+  // every load of the thread goes out before the angles are there
+  __shared__ __align__(16) float cs[kPairs], sn[kPairs];
   const int tid = threadIdx.x;
-  if (tid < kPairs) turn(p.positions[t], turns.per_pos[tid], sn[tid], cs[tid]);
-  __syncthreads();
   const int h0 = (blockIdx.y - 1) * kHeadsPerCta, nh = min(kHeadsPerCta, p.H - h0);
-  const uint8_t *q = p.q_pe + t * p.q_st;
-  uint8_t *o = p.q_out + t * p.qo_st;
-  if (!p.half_layout) {
-    for (int i = tid; i < nh * 8; i += kThreads) {   // 8 dims: pairs 4ch .. 4ch + 3
-      const int h = h0 + (i >> 3), ch = i & 7;
-      uint4 v = reinterpret_cast<const uint4 *>(q + h * p.q_sh)[ch];
-      uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+  const uint8_t *q = p.q_pe + t * p.q_st + h0 * p.q_sh;
+  uint8_t *o = p.q_out + t * p.qo_st + h0 * p.qo_sh;
+  if (!p.half_layout) {                // 8 dims: pairs 4ch .. 4ch + 3
+    constexpr int kPer = kHeadsPerCta * 8 / kThreads;
+    uint4 v[kPer];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = rot_pair(bf_lo(w[k]), bf_hi(w[k]), cs[4 * ch + k], sn[4 * ch + k]);
-      reinterpret_cast<uint4 *>(o + h * p.qo_sh)[ch] = v;
+    for (int i = 0; i < kPer; ++i) {
+      const int h = (tid + i * kThreads) >> 3;
+      if (h < nh) v[i] = reinterpret_cast<const uint4 *>(q + h * p.q_sh)[tid & 7];
     }
-  } else {
-    for (int i = tid; i < nh * 4; i += kThreads) {   // dims 8ch .. and 32 + 8ch ..
-      const int h = h0 + (i >> 2), ch = i & 3;
-      const uint4 *row = reinterpret_cast<const uint4 *>(q + h * p.q_sh);
-      uint4 va = row[ch], vb = row[ch + 4];
-      uint32_t *a = reinterpret_cast<uint32_t *>(&va), *b = reinterpret_cast<uint32_t *>(&vb);
+    if (tid < kPairs) turn(p.positions[t], turns.per_pos[tid], sn[tid], cs[tid]);
+    __syncthreads();
+    const int ch = tid & 7;
+    const float4 c = reinterpret_cast<const float4 *>(cs)[ch], sv = reinterpret_cast<const float4 *>(sn)[ch];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int h = (tid + i * kThreads) >> 3;
+      if (h < nh)
+        reinterpret_cast<uint4 *>(o + h * p.qo_sh)[ch] =
+            make_uint4(rot_pair(bf_lo(v[i].x), bf_hi(v[i].x), c.x, sv.x),
+                       rot_pair(bf_lo(v[i].y), bf_hi(v[i].y), c.y, sv.y),
+                       rot_pair(bf_lo(v[i].z), bf_hi(v[i].z), c.z, sv.z),
+                       rot_pair(bf_lo(v[i].w), bf_hi(v[i].w), c.w, sv.w));
+    }
+  } else {                             // dims 8ch .. and 32 + 8ch ..
+    constexpr int kPer = kHeadsPerCta * 4 / kThreads;
+    uint4 va[kPer], vb[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int h = (tid + i * kThreads) >> 2;
+      if (h < nh) {
+        const uint4 *row = reinterpret_cast<const uint4 *>(q + h * p.q_sh);
+        va[i] = row[tid & 3];
+        vb[i] = row[(tid & 3) + 4];
+      }
+    }
+    if (tid < kPairs) turn(p.positions[t], turns.per_pos[tid], sn[tid], cs[tid]);
+    __syncthreads();
+    const int ch = tid & 3;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int h = (tid + i * kThreads) >> 2;
+      if (h >= nh) continue;
+      uint32_t *a = reinterpret_cast<uint32_t *>(&va[i]), *b = reinterpret_cast<uint32_t *>(&vb[i]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int j = 8 * ch + 2 * k;
@@ -285,8 +311,8 @@ append_kernel(const __grid_constant__ AppendArgs p, const __grid_constant__ Turn
         b[k] = __byte_perm(r0, r1, 0x7632);
       }
       uint4 *dst = reinterpret_cast<uint4 *>(o + h * p.qo_sh);
-      dst[ch] = va;
-      dst[ch + 4] = vb;
+      dst[ch] = va[i];
+      dst[ch + 4] = vb[i];
     }
   }
 }

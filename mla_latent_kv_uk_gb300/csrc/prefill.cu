@@ -33,6 +33,31 @@ namespace {
 
 using namespace sm100;
 
+// One lane of a converged warp, and MMAs that only this lane issues.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_f16_ss_if(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t acc, uint32_t me) {
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
+               "l"(b), "r"(idesc), "r"(acc), "r"(me) : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts_if(uint32_t d, uint32_t a_tmem, uint64_t b,
+                                              uint32_t idesc, uint32_t acc, uint32_t me) {
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+               "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(me) : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(uint64_t *bar, uint32_t me) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+               ::"r"(smem_u32(bar)), "r"(me) : "memory");
+}
+
 // L2 prefetch of one tensor-map box (no shared memory, no completion).
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
@@ -158,7 +183,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
   uint64_t *q_full = pv_done + kQT, *drain = q_full + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0), lane = lane_id();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kKStages; ++s) {
@@ -244,55 +269,62 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (vt > 0) mbar_wait(v_full, (vt - 1) & 1, &no_abort);
       if (ntiles > 0) mbar_wait(q_full, 0, &no_abort);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ----------------------------------------------------------- MMA
+    // The whole warp runs this converged, with one lane's MMAs predicated on:
+    // descriptors then stay in uniform registers.
+    const uint32_t me = elect_one();
     const uint32_t idesc_qk = idesc_bf16(128, kBN, false, false);
     const uint32_t idesc_pv = idesc_bf16(128, kDv, false, true);
-    bool ok = ntiles == 0 || mbar_wait(q_full, 0, abort_flag);
+    auto wait = [&](uint64_t *bar, int phase) -> bool {
+      return __all_sync(0xffffffffu, mbar_test(bar, phase & 1) || mbar_wait(bar, phase & 1, abort_flag));
+    };
+    bool ok = ntiles == 0 || wait(q_full, 0);
     auto issue_qk = [&](int g, int t) {
       const uint32_t qa = smem_u32(sm_q + g * kQBytes);
       const uint32_t kb = smem_u32(sm_k + (t % kKStages) * kKBytes);
       const uint32_t d = tmem + 256 * g;
 #pragma unroll
       for (int k = 0; k < kDq / 16; ++k)
-        mma_f16_ss(d, sdesc(qa + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSwizzle128B),
-                   sdesc(kb + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSwizzle128B),
-                   idesc_qk, k > 0);
-      mma_commit(&s_full[g]);
+        mma_f16_ss_if(d, sdesc(qa + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSwizzle128B),
+                      sdesc(kb + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSwizzle128B),
+                      idesc_qk, k > 0, me);
+      mma_commit_if(&s_full[g], me);
     };
     auto issue_pv = [&](int g, int t) {
       const uint32_t vb = smem_u32(sm_v);
 #pragma unroll
       for (int kk = 0; kk < kBN / 16; ++kk)
-        mma_f16_ts(tmem + 256 * g + 128, tmem + 256 * g + 8 * kk,
-                   sdesc(vb + kk * 2048, kBox, 1024, kSwizzle128B), idesc_pv,
-                   (t > 0 || kk > 0) ? 1u : 0u);
-      mma_commit(&pv_done[g]);
+        mma_f16_ts_if(tmem + 256 * g + 128, tmem + 256 * g + 8 * kk,
+                      sdesc(vb + kk * 2048, kBox, 1024, kSwizzle128B), idesc_pv,
+                      (t > 0 || kk > 0) ? 1u : 0u, me);
+      mma_commit_if(&pv_done[g], me);
     };
     // Tile 0's QKs; then per tile t: P.V_A(t), QK_A(t+1), P.V_B(t),
     // QK_B(t+1).  QK_g(t+1) overwrites S_g after P.V_g(t) has read P_g from
     // the same columns (the tensor core runs one thread's MMAs in order).
-    if (ok && ntiles > 0 && (ok = mbar_wait(&k_full[0], 0, abort_flag))) {
+    if (ok && ntiles > 0 && (ok = wait(&k_full[0], 0))) {
       tc_fence_after();
+#pragma unroll
       for (int g = 0; g < kQT; ++g)
         if (nt_g[g] > 0) issue_qk(g, 0);
-      mma_commit(&k_empty[0]);
+      mma_commit_if(&k_empty[0], me);
     }
     for (int t = 0; ok && t < ntiles; ++t) {
-      if (!(ok = mbar_wait(v_full, t & 1, abort_flag))) break;
+      if (!(ok = wait(v_full, t))) break;
       bool k_next = false;   // K(t+1) has landed
+#pragma unroll
       for (int g = 0; g < kQT; ++g) {
+        if (!ok) break;
         if (t < nt_g[g]) {
-          if (!(ok = mbar_wait(&p_full[g], t & 1, abort_flag))) break;
+          if (!(ok = wait(&p_full[g], t))) break;
           tc_fence_after();
           issue_pv(g, t);
         }
-        if (g == kQT - 1) mma_commit(v_empty);   // both P.Vs of tile t issued
+        if (g == kQT - 1) mma_commit_if(v_empty, me);   // both P.Vs of tile t issued
         if (t + 1 < nt_g[g]) {
           if (!k_next) {
-            if (!(ok = mbar_wait(&k_full[(t + 1) % kKStages], ((t + 1) / kKStages) & 1,
-                                 abort_flag)))
-              break;
+            if (!(ok = wait(&k_full[(t + 1) % kKStages], (t + 1) / kKStages))) break;
             tc_fence_after();
             k_next = true;
           }
@@ -300,10 +332,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
       }
       if (!ok) break;
-      if (k_next) mma_commit(&k_empty[(t + 1) % kKStages]);   // both QKs of tile t+1 issued
+      if (k_next) mma_commit_if(&k_empty[(t + 1) % kKStages], me);   // both QKs of tile t+1 issued
     }
     if (!ok) {
-      mma_commit(drain);
+      mma_commit_if(drain, me);
       volatile int no_abort = 0;
       mbar_wait(drain, 0, &no_abort);
     }
