@@ -85,6 +85,7 @@ struct Fmt {
   static constexpr int kRowsBytes = 64 * kDqk * kEsz;      // 64 rows: 36 / 72 KB
   static constexpr int kGroups = FP8 ? 1 : 3;              // K slots that a tile takes
   static constexpr int kGroupBytes = kRowsBytes / kGroups; // 36 / 24 KB
+  static constexpr int kGroupChunks = (kLatChunks + 1) / kGroups;   // loads: 5 / 3
   static constexpr int kKSlots = FP8 ? 2 : 3;
   static constexpr int kVTok = FP8 ? 64 : 32;              // keys of a V slot
   static constexpr int kVBoxes = 256 / kCols;              // 2 / 4
@@ -140,7 +141,11 @@ struct Job {
 
 __device__ __forceinline__ Job job_of(int rg, int len, const WindowArgs &a) {
   Job j;
-  const int i0 = rg * 128 / a.H, i1 = min(a.q_len - 1, (rg * 128 + 127) / a.H);
+  int i0 = 0, i1 = a.q_len - 1;               // (one group: no divisions)
+  if (a.RG > 1) {
+    i0 = rg * 128 / a.H;
+    i1 = min(i1, (rg * 128 + 127) / a.H);
+  }
   j.p0 = len - a.q_len + i0;
   j.p1 = len - a.q_len + i1;
   const int lo = a.window ? max(0, j.p0 - a.window + 1) : 0;
@@ -157,8 +162,9 @@ __device__ __forceinline__ int length_of(int b, const WindowArgs &a, bool tell) 
 }
 
 __device__ __forceinline__ int units_of(int j, const WindowArgs &a, int &len) {
-  len = length_of(j % a.B, a, blockIdx.x == 0 && j < a.B);
-  const int t = job_of(j / a.B, len, a).tiles();
+  const int rg = a.RG > 1 ? j / a.B : 0;
+  len = length_of(j - rg * a.B, a, blockIdx.x == 0 && rg == 0);
+  const int t = job_of(rg, len, a).tiles();
   return t > 0 ? t + kJobCost : 0;
 }
 
@@ -188,10 +194,14 @@ struct Walk {
   __device__ void init(const WindowArgs &a, int lane) {
     J = a.B * a.RG;
     per = (J + 31) / 32;
-    int sum = 0, n;
-    for (int j = lane * per; j < min(J, (lane + 1) * per); ++j) sum += units_of(j, a, n);
+    int sum = 0;
+    len = 0;
+    for (int j = lane * per; j < min(J, (lane + 1) * per); ++j) sum += units_of(j, a, len);
     const int incl = warp_incl_scan(sum, lane);
     lane_excl = incl - sum;
+    units = sum;                // (one job a lane: the walk's window is there already)
+    excl = lane_excl;
+    base = 0;
     total = __shfl_sync(0xffffffffu, incl, 31);
     C = a.forced > 0 ? a.forced : max(kMinUnits, (total - 1) / a.spans_at_once + 1);
     span = blockIdx.x >> 1;
@@ -204,8 +214,8 @@ struct Walk {
   // Uncut: jobs span, span + pairs, ...
   __device__ bool next_solo(const WindowArgs &a, Seg &s) {
     if (span >= J) return false;
-    s.b = span % a.B;
-    s.rg = span / a.B;
+    s.rg = a.RG > 1 ? span / a.B : 0;
+    s.b = span - s.rg * a.B;
     s.len = length_of(s.b, a, s.rg == 0);
     s.tile0 = 0;
     s.ntiles = job_of(s.rg, s.len, a).tiles();
@@ -232,7 +242,8 @@ struct Walk {
         // the last lane whose jobs begin at or before the span
         const uint32_t le = __ballot_sync(0xffffffffu, lane_excl <= span_lo);
         const int own = 31 - __clz(le);
-        load(a, own * per, __shfl_sync(0xffffffffu, lane_excl, own), lane);
+        if (per == 1) k = own;
+        else load(a, own * per, __shfl_sync(0xffffffffu, lane_excl, own), lane);
         open = true;
       }
       if (k == 32) load(a, base + 32, __shfl_sync(0xffffffffu, excl + units, 31), lane);
@@ -249,8 +260,8 @@ struct Walk {
       const int first = t0 + kJobCost, end = t0 + n;
       const int u0 = max(span_lo, first), u1 = min(span_hi, end);
       if (n == 0 || u1 <= u0) continue;
-      s.b = j % a.B;
-      s.rg = j / a.B;
+      s.rg = a.RG > 1 ? j / a.B : 0;
+      s.b = j - s.rg * a.B;
       s.len = l;
       s.tile0 = u0 - first;
       s.ntiles = u1 - u0;
@@ -276,6 +287,12 @@ __device__ __forceinline__ void pair_alloc(uint32_t *dst) {
 __device__ __forceinline__ void pair_dealloc(uint32_t taddr) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512)
                : "memory");
+}
+// Cluster barrier without release: nothing that one CTA wrote is read by the
+// other's threads, and the barriers' initialisation has a fence of its own.
+// (With release the last one waits for the results' stores to arrive.)
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // One lane of a converged warp, chosen the same way every time.  The MMA
 // warp runs its loops as a whole with this lane's instructions predicated on:
@@ -426,7 +443,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  cluster_sync();                             // both CTAs' barriers and memory are there
+  pair_sync();                                // both CTAs' barriers and memory are there
   grid_dep_wait();
   grid_dep_launch();
 
@@ -498,42 +515,42 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       ++ns;
       if (sg.ntiles == 0) continue;
       const Job job = job_of(sg.rg, sg.len, args);
-      // Q, once the last segment's last Q K^T has read it
+      Pages pg{-64, -1};
+      int blk = block_at(pg, job, sg.b, 2 * sg.tile0 + rank);
+      // Q, once the last segment's last Q K^T has read it.  (Each lane issues
+      // one chunk: one after the other they took longer than the copies.)
       if (nq > 0 && !(ok = wait_for(q_empty, (nq - 1) & 1, abort_flag))) break;
       ++nq;
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kRowsBytes);
-        const int row = sg.b * args.q_len * args.H + sg.rg * 128 + 64 * rank;
-        for (int c = 0; c < F::kLatChunks; ++c)
-          pair_load(sm_q + c * 8192, &tm_q, q_bar, c * F::kCols, row);
-        pair_load(sm_q + F::kLatChunks * 8192, FP8 ? &tm_qr : &tm_q, q_bar, kLatent, row);
-      }
-      Pages pg{-64, -1};
+      if (lane == 0 && rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kRowsBytes);
+      __syncwarp();
+      if (lane <= F::kLatChunks)
+        pair_load(sm_q + lane * 8192, FP8 && lane == F::kLatChunks ? &tm_qr : &tm_q, q_bar,
+                  lane * F::kCols, sg.b * args.q_len * args.H + sg.rg * 128 + 64 * rank);
       for (int t = 0; ok && t < sg.ntiles; ++t) {
-        const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + rank);
+        if (t > 0) blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + rank);
         const int row = blk < 0 ? no_row : blk * kPage;
         for (int g = 0; g < F::kGroups; ++g, ++kc) {
           const int s = kc % F::kKSlots;
           if (kc >= F::kKSlots &&
               !(ok = wait_for(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
             break;
-          if (lane == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kGroupBytes);
-            const uint32_t bar = peer_smem(&k_full[s], 0);
-            uint8_t *dst = sm_k + s * F::kGroupBytes;
-            if constexpr (FP8) {
-              for (int c = 0; c < 4; ++c) pair_load(dst + c * 8192, &tm_k, bar, c * 128, row);
-              pair_load(dst + 4 * 8192, &tm_kr, bar, kLatent, row);
-            } else {
-              for (int c = 0; c < 3; ++c) pair_load(dst + c * 8192, &tm_k, bar, (3 * g + c) * 64, row);
-            }
-          }
+          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kGroupBytes);
+          __syncwarp();
+          if (lane < F::kGroupChunks)
+            pair_load(sm_k + s * F::kGroupBytes + lane * 8192, FP8 && lane == 4 ? &tm_kr : &tm_k,
+                      peer_smem(&k_full[s], 0), (F::kGroupChunks * g + lane) * F::kCols, row);
         }
       }
     }
     if (ok) {
       sg.ntiles = -1;
       publish(sg);
+    }
+    // neither CTA leaves before the last signals to it have arrived
+    if (ok) {
+      for (int u = max(0, kc - F::kKSlots); ok && u < kc; ++u)
+        ok = wait_for(&k_empty[u % F::kKSlots], (u / F::kKSlots) & 1, abort_flag);
+      if (ok && nq > 0) wait_for(q_empty, (nq - 1) & 1, abort_flag);
     }
     if (*abort_flag && rank == 0 && lane == 0) {   // what is on its way lands first
       volatile int no_abort = 0;
@@ -558,16 +575,17 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           if (vc >= F::kVSlots &&
               !(ok = wait_for(&v_empty[s], ((vc / F::kVSlots) - 1) & 1, abort_flag)))
             break;
-          if (lane == 0) {
-            const int row = blk < 0 ? no_row : blk * kPage + (v * F::kVTok) % kPage;
-            mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
-            for (int j = 0; j < F::kVBoxes; ++j)
-              tma_load_2d_hint(sm_v + s * F::kVSlotBytes + j * F::kVBox, &tm_v, &v_full[s],
-                               256 * rank + j * F::kCols, row, policy);
-          }
+          const int row = blk < 0 ? no_row : blk * kPage + (v * F::kVTok) % kPage;
+          if (lane == 0) mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
+          __syncwarp();
+          if (lane < F::kVBoxes)
+            tma_load_2d_hint(sm_v + s * F::kVSlotBytes + lane * F::kVBox, &tm_v, &v_full[s],
+                             256 * rank + lane * F::kCols, row, policy);
         }
       }
     }
+    for (int u = max(0, vc - F::kVSlots); ok && u < vc; ++u)
+      ok = wait_for(&v_empty[u % F::kVSlots], (u / F::kVSlots) & 1, abort_flag);
     if (*abort_flag && lane == 0) {
       volatile int no_abort = 0;
       for (int u = max(0, vc - F::kVSlots); u < vc; ++u)
@@ -859,20 +877,26 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         if (ok && !all_clean) {
           // rows that not every query row sees: 0 where none does, and where
-          // some do, 0 in place of what is not finite (0 times it in the others)
-#pragma unroll 1
-          for (int v = 0; v < F::kVPer; ++v) {
-            const int page = v * 2 < F::kVPer ? page0 : page1;
+          // some do, 0 in place of what is not finite (0 times it in the
+          // others).  A row of this CTA's columns is one (bf16) or half a
+          // (e4m3) warp's 16-byte chunks.
+          constexpr int kChunks = F::kVBoxes * 8, kRowsAtOnce = 32 / kChunks;
+          const int lr = lane / kChunks, box = (lane % kChunks) >> 3, chunk = lane & 7;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int page = h ? page1 : page0;
             if (clean(page)) continue;
-            const int k0 = page + (v * F::kVTok) % kPage;
-            uint4 *slot = reinterpret_cast<uint4 *>(sm_v + ((vc + v) % F::kVSlots) * F::kVSlotBytes);
-            for (int idx = tid; idx < F::kVSlotBytes / 16; idx += 32 * kSoftWarps) {
-              const int key = k0 + (idx >> 3) % F::kVTok;
+#pragma unroll 1
+            for (int t0 = (warp - 4) * kRowsAtOnce; t0 < kPage; t0 += kSoftWarps * kRowsAtOnce) {
+              const int tok = t0 + lr, key = page + tok;
               const bool sink = key < args.sinks;
               if (key <= job.p0 && (sink || key >= clean_lo)) continue;
+              const int slot = (vc + (h * kPage + tok) / F::kVTok) % F::kVSlots;
+              uint4 *at = reinterpret_cast<uint4 *>(sm_v + slot * F::kVSlotBytes + box * F::kVBox +
+                                                    (tok % F::kVTok) * 128) + chunk;
               uint4 val = make_uint4(0, 0, 0, 0);
               if (key <= job.p1 && (!args.window || sink || key > job.p0 - args.window)) {
-                val = slot[idx];
+                val = *at;
                 uint32_t *e4 = reinterpret_cast<uint32_t *>(&val);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -885,7 +909,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                   }
                 }
               }
-              slot[idx] = val;
+              *at = val;
             }
           }
         }
@@ -960,7 +984,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (!told) named_and(bar_id, 128, ok && !*abort_flag);
   }
   __syncthreads();
-  cluster_sync();
+  pair_sync();                                // neither CTA's MMAs or signals need the other any more
   if (threadIdx.x == 0 && *abort_flag) raise_error(args.err, MLA_DEVERR_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
@@ -969,32 +993,40 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 }
 
 // Combines the partials of the jobs that were cut, and writes the rows of
-// jobs without a key: one warp per row.  Part k of a job whose first span is
-// s0 lies in slot 2 s0 + 1 (k = 0) or 2 (s0 + k).
+// jobs without a key.  Part k of a job whose first span is s0 lies in slot
+// 2 s0 + 1 (k = 0) or 2 (s0 + k).  SPLIT warps share a row and take every
+// SPLIT-th part, joined through shared memory: one request over all pairs
+// has 76 parts a row, which a single warp would read four at a time (the
+// 131072-token request's merge: 28 us with one warp a row).
 constexpr int kMergeWarps = 8;
 
-template <typename T>
+template <typename T, int SPLIT>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 window_merge_kernel(const __grid_constant__ WindowArgs a) {
+  constexpr int kRows = kMergeWarps / SPLIT;    // rows of this CTA
+  __shared__ float part_o[SPLIT > 1 ? kMergeWarps : 1][kLatent];
+  __shared__ float part_z[kMergeWarps];
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const int j = blockIdx.x, b = j % a.B, rg = j / a.B;
-  const int rr = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % SPLIT;
+  const int j = blockIdx.x, rg = a.RG > 1 ? j / a.B : 0, b = j - rg * a.B;
+  const int rr = blockIdx.y * kRows + warp / SPLIT;
   const int R = a.q_len * a.H;
-  if (rg * 128 + rr >= R) return;
+  const bool row_ok = rg * 128 + rr < R;
+  if (SPLIT == 1 && !row_ok) return;
   const int64_t row = static_cast<int64_t>(b) * R + rg * 128 + rr;
   T *out = static_cast<T *>(a.out) + row * kLatent;
   const int C = a.ws_head[0], first = a.ws_head[2 + 2 * j], end = a.ws_head[3 + 2 * j];
-  const Job job = job_of(rg, length_of(b, a, false), a);
-  if (job.tiles() == 0) {
-    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int k = 0; k < 2; ++k) store8(out + 8 * (lane + 32 * k), zero);
-    if (lane == 0) a.lse[row] = -INFINITY;
+  if (job_of(rg, length_of(b, a, false), a).tiles() == 0) {   // (the words above hold nothing)
+    if (mine == 0 && row_ok) {
+      const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int k = 0; k < 2; ++k) store8(out + 8 * (lane + 32 * k), zero);
+      if (lane == 0) a.lse[row] = -INFINITY;
+    }
     return;
   }
   const int s0 = first / C, n = (end - 1) / C - s0 + 1;
-  if (n == 1) return;
+  if (n == 1) return;   // written by its pair
   auto slot_row = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * s0 + 1 : 2 * (s0 + k)) * 128 + rr; };
   float m = -INFINITY;
   for (int k = lane; k < n; k += 32) m = fmaxf(m, a.ws_lse[slot_row(k)]);
@@ -1004,37 +1036,69 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   float acc[16], z = 0.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    float w = k0 + lane < n ? expf(a.ws_lse[slot_row(k0 + lane)] - safe) : 0.f;
-    float zw = w;
+  for (int k0 = mine; k0 < n; k0 += 4 * SPLIT) {
+    float v[4][16], w[4];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) zw += __shfl_xor_sync(0xffffffffu, zw, o);
-    z += zw;
-    const int here = min(32, n - k0);
-    for (int k = 0; k < here; k += 4) {
-      float v[4][16];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (k + u < here) {
-          const T *src = static_cast<const T *>(a.ws_o) + slot_row(k0 + k + u) * kLatent;
-          load8(src + 8 * lane, v[u]);
-          load8(src + 8 * (lane + 32), v[u] + 8);
-        }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (k + u < here) {
-          const float wu = __shfl_sync(0xffffffffu, w, k + u);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[e] = fmaf(wu, v[u][e], acc[e]);
-        }
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * SPLIT;
+      w[u] = -INFINITY;
+      if (k < n) {
+        const int64_t at = slot_row(k);
+        const T *src = static_cast<const T *>(a.ws_o) + at * kLatent;
+        w[u] = __ldg(a.ws_lse + at);
+        load8(src + 8 * lane, v[u]);
+        load8(src + 8 * (lane + 32), v[u] + 8);
+      }
     }
-  }
-  const float inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] *= inv;
-  store8(out + 8 * lane, acc);
-  store8(out + 8 * (lane + 32), acc + 8);
-  if (lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(z);
+    for (int u = 0; u < 4; ++u)
+      if (k0 + u * SPLIT < n) {
+        const float wu = expf(w[u] - safe);
+        z += wu;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] = fmaf(wu, v[u][e], acc[e]);
+      }
+  }
+  if constexpr (SPLIT > 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      part_o[warp][8 * lane + e] = acc[e];
+      part_o[warp][8 * (lane + 32) + e] = acc[8 + e];
+    }
+    if (lane == 0) part_z[warp] = z;
+    __syncthreads();
+    // 512 / SPLIT columns a warp, in the warps' order
+    constexpr int kCols = kLatent / SPLIT;
+    z = 0.f;
+#pragma unroll
+    for (int w = 0; w < SPLIT; ++w) z += part_z[warp - mine + w];
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    if (!row_ok) return;
+#pragma unroll
+    for (int c = lane; c < kCols; c += 32) {
+      float x = 0.f;
+#pragma unroll
+      for (int w = 0; w < SPLIT; ++w) x += part_o[warp - mine + w][mine * kCols + c];
+      if constexpr (sizeof(T) == 4) out[mine * kCols + c] = x * inv;
+      else out[mine * kCols + c] = __float2bfloat16_rn(x * inv);
+    }
+    if (mine == 0 && lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(z);
+  } else {
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] *= inv;
+    store8(out + 8 * lane, acc);
+    store8(out + 8 * (lane + 32), acc + 8);
+    if (lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(z);
+  }
+}
+
+template <typename T, int SPLIT>
+cudaError_t launch_merge(const WindowArgs &a, mla_stream_t stream) {
+  constexpr int kRows = kMergeWarps / SPLIT;
+  const int rows = std::min(128, a.q_len * a.H);
+  return launch_pdl(window_merge_kernel<T, SPLIT>, dim3(a.B * a.RG, (rows + kRows - 1) / kRows),
+                    dim3(kMergeWarps * 32), 0, stream, a);
 }
 
 // ------------------------------------------------------------------- host
@@ -1211,11 +1275,11 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   const int st = fp8 ? launch_pairs<true>(q, kv_cache, a.spans_at_once, a, stream)
                      : launch_pairs<false>(q, kv_cache, a.spans_at_once, a, stream);
   if (st != MLA_OK || w.solo) return st;
-  const int rows = std::min(128, q_len * H);
-  const dim3 grid(B * a.RG, (rows + kMergeWarps - 1) / kMergeWarps), block(kMergeWarps * 32);
-  const cudaError_t e = a.out_f32
-                            ? launch_pdl(window_merge_kernel<float>, grid, block, 0, stream, a)
-                            : launch_pdl(window_merge_kernel<__nv_bfloat16>, grid, block, 0, stream, a);
+  // a job has about pairs / jobs parts: above eight, a CTA's warps share a row
+  const bool many = jobs * 8 < pairs;
+  const cudaError_t e = a.out_f32 ? (many ? launch_merge<float, 8>(a, stream) : launch_merge<float, 1>(a, stream))
+                                  : (many ? launch_merge<__nv_bfloat16, 8>(a, stream)
+                                          : launch_merge<__nv_bfloat16, 1>(a, stream));
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
