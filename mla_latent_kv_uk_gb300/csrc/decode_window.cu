@@ -85,7 +85,7 @@ struct Fmt {
   static constexpr int kRowsBytes = 64 * kDqk * kEsz;      // 64 rows: 36 / 72 KB
   static constexpr int kGroups = FP8 ? 1 : 3;              // K slots that a tile takes
   static constexpr int kGroupBytes = kRowsBytes / kGroups; // 36 / 24 KB
-  static constexpr int kGroupChunks = (kLatChunks + 1) / kGroups;   // loads: 5 / 3
+  static constexpr int kGroupChunks = FP8 ? kLatChunks : 3;   // 128-byte columns of a slot (e4m3: and the rope's)
   static constexpr int kKSlots = FP8 ? 2 : 3;
   static constexpr int kVTok = FP8 ? 64 : 32;              // keys of a V slot
   static constexpr int kVBoxes = 256 / kCols;              // 2 / 4
@@ -326,12 +326,21 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar, uint32_t me) {
                "h"(static_cast<uint16_t>(3)), "r"(me) : "memory");
 }
 // A load into this CTA whose bytes count on a barrier of either CTA.
+// (Maps: columns of a 128-byte box row, rows, box columns of the cache row; a
+// slot of several boxes is one load.)
 __device__ __forceinline__ void pair_load(void *dst, const CUtensorMap *map, uint32_t bar_cluster,
-                                          int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-               ".cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
+                                          int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+               ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
                : "memory");
+}
+__device__ __forceinline__ void load_3d_hint(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                             int y, int z, uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+               ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z),
+               "l"(policy) : "memory");
 }
 // Bounded wait that first tests the phase: most waits here find it complete,
 // and a test costs about 70 cycles where try_wait costs about 190.  What the
@@ -439,6 +448,15 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     fence_barrier_init();
   }
   if (warp == 1) pair_alloc(tmem_slot);
+  if (warp == 2 && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    if (FP8) {
+      prefetch_tmap(&tm_qr);
+      prefetch_tmap(&tm_kr);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -458,36 +476,29 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     return s.ntiles >= 0;
   };
   // Block ids of a segment's pages: lane k holds those of list entry
-  // base + k; entries behind the list and bad ids give -1.
+  // base + k, as loaded; entries behind the list and bad ids give -1.
   struct Pages {
     int base, blk;
   };
+  auto fetch_blocks = [&](Pages &pg, const Job &job, int b, int entry) {
+    pg.base = entry;
+    const int e = entry + lane;
+    pg.blk = e < job.pages
+                 ? __ldg(args.block_table + static_cast<int64_t>(b) * args.max_blocks + job.page(e))
+                 : -1;
+  };
   auto block_at = [&](Pages &pg, const Job &job, int b, int entry) -> int {   // whole warp
-    if (entry < pg.base || entry >= pg.base + 32) {
-      pg.base = entry;
-      const int e = entry + lane;
-      pg.blk = -1;
-      if (e < job.pages) {
-        const int v = __ldg(args.block_table + static_cast<int64_t>(b) * args.max_blocks + job.page(e));
-        if (v < 0 || v >= args.num_blocks) raise_error(args.err, MLA_DEVERR_BLOCK_ID);
-        else pg.blk = v;
-      }
-    }
-    return __shfl_sync(0xffffffffu, pg.blk, entry - pg.base);
+    if (entry >= pg.base + 32) fetch_blocks(pg, job, b, entry);
+    const int v = __shfl_sync(0xffffffffu, pg.blk, entry - pg.base);
+    if (v >= 0 && v < args.num_blocks) return v;
+    if (entry < job.pages && lane == 0) raise_error(args.err, MLA_DEVERR_BLOCK_ID);
+    return -1;
   };
   // rows out of the cache: TMA fills in zeros
   const int no_row = args.num_blocks * kPage;
 
   if (warp == 0) {
     // ------------------------------------------------- plan, Q and K
-    if (lane == 0) {
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_q);
-      if (FP8) {
-        prefetch_tmap(&tm_kr);
-        prefetch_tmap(&tm_qr);
-      }
-    }
     Walk walk;
     if (args.solo) {
       walk.init_solo(args);
@@ -515,30 +526,31 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       ++ns;
       if (sg.ntiles == 0) continue;
       const Job job = job_of(sg.rg, sg.len, args);
-      Pages pg{-64, -1};
-      int blk = block_at(pg, job, sg.b, 2 * sg.tile0 + rank);
-      // Q, once the last segment's last Q K^T has read it.  (Each lane issues
-      // one chunk: one after the other they took longer than the copies.)
+      Pages pg;
+      fetch_blocks(pg, job, sg.b, 2 * sg.tile0);
+      // Q, once the last segment's last Q K^T has read it
       if (nq > 0 && !(ok = wait_for(q_empty, (nq - 1) & 1, abort_flag))) break;
       ++nq;
-      if (lane == 0 && rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kRowsBytes);
-      __syncwarp();
-      if (lane <= F::kLatChunks)
-        pair_load(sm_q + lane * 8192, FP8 && lane == F::kLatChunks ? &tm_qr : &tm_q, q_bar,
-                  lane * F::kCols, sg.b * args.q_len * args.H + sg.rg * 128 + 64 * rank);
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kRowsBytes);
+        const int row = sg.b * args.q_len * args.H + sg.rg * 128 + 64 * rank;
+        pair_load(sm_q, &tm_q, q_bar, 0, row, 0);
+        if (FP8) pair_load(sm_q + 4 * 8192, &tm_qr, q_bar, kLatent, row, 0);
+      }
       for (int t = 0; ok && t < sg.ntiles; ++t) {
-        if (t > 0) blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + rank);
+        const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + rank);
         const int row = blk < 0 ? no_row : blk * kPage;
         for (int g = 0; g < F::kGroups; ++g, ++kc) {
           const int s = kc % F::kKSlots;
           if (kc >= F::kKSlots &&
               !(ok = wait_for(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
             break;
-          if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kGroupBytes);
-          __syncwarp();
-          if (lane < F::kGroupChunks)
-            pair_load(sm_k + s * F::kGroupBytes + lane * 8192, FP8 && lane == 4 ? &tm_kr : &tm_k,
-                      peer_smem(&k_full[s], 0), (F::kGroupChunks * g + lane) * F::kCols, row);
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kGroupBytes);
+            const uint32_t bar = peer_smem(&k_full[s], 0);
+            pair_load(sm_k + s * F::kGroupBytes, &tm_k, bar, 0, row, F::kGroupChunks * g);
+            if (FP8) pair_load(sm_k + s * F::kGroupBytes + 4 * 8192, &tm_kr, bar, kLatent, row, 0);
+          }
         }
       }
     }
@@ -560,14 +572,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------- V
-    if (lane == 0) prefetch_tmap(&tm_v);
     const uint64_t policy = l2_evict_first_policy();   // the rows' second and last read
     Seg sg;
     int vc = 0;
     bool ok = true;
     for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
       const Job job = job_of(sg.rg, sg.len, args);
-      Pages pg{-64, -1};
+      Pages pg;
+      fetch_blocks(pg, job, sg.b, 2 * sg.tile0);
       for (int t = 0; ok && t < sg.ntiles; ++t) {
         for (int v = 0; v < F::kVPer; ++v, ++vc) {
           const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + v * 2 / F::kVPer);
@@ -576,11 +588,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
               !(ok = wait_for(&v_empty[s], ((vc / F::kVSlots) - 1) & 1, abort_flag)))
             break;
           const int row = blk < 0 ? no_row : blk * kPage + (v * F::kVTok) % kPage;
-          if (lane == 0) mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
-          __syncwarp();
-          if (lane < F::kVBoxes)
-            tma_load_2d_hint(sm_v + s * F::kVSlotBytes + lane * F::kVBox, &tm_v, &v_full[s],
-                             256 * rank + lane * F::kCols, row, policy);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
+            load_3d_hint(sm_v + s * F::kVSlotBytes, &tm_v, &v_full[s], 0, row, F::kVBoxes * rank, policy);
+          }
         }
       }
     }
@@ -881,35 +892,39 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           // others).  A row of this CTA's columns is one (bf16) or half a
           // (e4m3) warp's 16-byte chunks.
           constexpr int kChunks = F::kVBoxes * 8, kRowsAtOnce = 32 / kChunks;
-          const int lr = lane / kChunks, box = (lane % kChunks) >> 3, chunk = lane & 7;
-#pragma unroll
+          const int lr = lane / kChunks, at = ((lane % kChunks) >> 3) * F::kVBox + (lane & 7) * 16;
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int page = h ? page1 : page0;
             if (clean(page)) continue;
+            // all rows see [0, a) (sinks) and [b, c) of the page's 64
+            const int c = min(max(job.p0 + 1 - page, 0), kPage);
+            const int b = min(max(clean_lo - page, 0), c), a = min(max(args.sinks - page, 0), b);
+            const int n = b - a + kPage - c;
 #pragma unroll 1
-            for (int t0 = (warp - 4) * kRowsAtOnce; t0 < kPage; t0 += kSoftWarps * kRowsAtOnce) {
-              const int tok = t0 + lr, key = page + tok;
-              const bool sink = key < args.sinks;
-              if (key <= job.p0 && (sink || key >= clean_lo)) continue;
+            for (int i = (warp - 4) * kRowsAtOnce + lr; i < n; i += kSoftWarps * kRowsAtOnce) {
+              const int tok = i < b - a ? a + i : c + i - (b - a);
               const int slot = (vc + (h * kPage + tok) / F::kVTok) % F::kVSlots;
-              uint4 *at = reinterpret_cast<uint4 *>(sm_v + slot * F::kVSlotBytes + box * F::kVBox +
-                                                    (tok % F::kVTok) * 128) + chunk;
+              uint4 *w = reinterpret_cast<uint4 *>(sm_v + slot * F::kVSlotBytes + at +
+                                                   (tok % F::kVTok) * 128);
               uint4 val = make_uint4(0, 0, 0, 0);
-              if (key <= job.p1 && (!args.window || sink || key > job.p0 - args.window)) {
-                val = *at;
+              const int key = page + tok;
+              if (job.p0 != job.p1 && key <= job.p1 &&
+                  (!args.window || key < args.sinks || key > job.p0 - args.window)) {
+                val = *w;
                 uint32_t *e4 = reinterpret_cast<uint32_t *>(&val);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int k = 0; k < 4; ++k) {
                   if constexpr (FP8) {
-                    const uint32_t nan = (((e4[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
-                    e4[i] &= ~(nan * 0xFFu);
+                    const uint32_t nan = (((e4[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+                    e4[k] &= ~(nan * 0xFFu);
                   } else {
-                    if ((e4[i] & 0x7F80u) == 0x7F80u) e4[i] &= 0xFFFF0000u;
-                    if ((e4[i] & 0x7F800000u) == 0x7F800000u) e4[i] &= 0xFFFFu;
+                    if ((e4[k] & 0x7F80u) == 0x7F80u) e4[k] &= 0xFFFF0000u;
+                    if ((e4[k] & 0x7F800000u) == 0x7F800000u) e4[k] &= 0xFFFFu;
                   }
                 }
               }
-              *at = val;
+              *w = val;
             }
           }
         }
@@ -947,11 +962,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       // the P tile (its rows are written again behind the next exchange of
       // the four warps that share them) so that stores cover whole sectors
       uint4 *buf = reinterpret_cast<uint4 *>(sm_p + half * 8192 + (quarter & 1) * 4096 + sub * 2048);
-#pragma unroll 1
+      uint32_t all[128];
+      tmem_ld_x64(lane_base + kColO + 128 * sub, all);
+      tmem_ld_x64(lane_base + kColO + 128 * sub + 64, all + 64);
+#pragma unroll
       for (int q = 0; q < 128; q += 32) {
-        uint32_t o[32];
-        tmem_ld_x32(lane_base + kColO + 128 * sub + q, o);
-        auto f = [&](int k) { return __uint_as_float(o[k]) * inv; };
+        auto f = [&](int k) { return __uint_as_float(all[q + k]) * inv; };
 #pragma unroll
         for (int pc = 0; pc < 2; ++pc) {     // one (bf16) or two (fp32) pieces
           if (!args.out_f32 && pc == 1) break;
@@ -1207,23 +1223,28 @@ int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArg
   using F = Fmt<FP8>;
   const CUtensorMapDataType dt =
       FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const uint64_t strides[1] = {static_cast<uint64_t>(kDqk) * F::kEsz};
-  const uint64_t kv_dims[2] = {kDqk, static_cast<uint64_t>(a.num_blocks) * kPage};
-  const uint64_t q_dims[2] = {kDqk, static_cast<uint64_t>(a.B) * a.q_len * a.H};
-  const uint32_t box[2] = {F::kCols, 64}, box_r[2] = {64, 64}, box_v[2] = {F::kCols, F::kVTok};
-  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  const CUtensorMapSwizzle sw_r = FP8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  // (each format encodes the maps that it uses)
+  // {columns of a 128-byte box row, rows, box columns}; the e4m3 rope columns
+  // are half a box row and have maps of their own
+  const uint64_t row_bytes = static_cast<uint64_t>(kDqk) * F::kEsz;
+  const uint64_t boxes = FP8 ? 4 : 9;
+  const uint64_t strides[2] = {row_bytes, 128};
+  const uint64_t kv_rows = static_cast<uint64_t>(a.num_blocks) * kPage;
+  const uint64_t q_rows = static_cast<uint64_t>(a.B) * a.q_len * a.H;
+  const uint64_t kv_dims[3] = {F::kCols, kv_rows, boxes}, q_dims[3] = {F::kCols, q_rows, boxes};
+  const uint64_t kvr_dims[3] = {kDqk, kv_rows, 1}, qr_dims[3] = {kDqk, q_rows, 1};
+  const uint32_t box_k[3] = {F::kCols, 64, F::kGroupChunks};
+  const uint32_t box_q[3] = {F::kCols, 64, static_cast<uint32_t>(boxes)};
+  const uint32_t box_v[3] = {F::kCols, F::kVTok, F::kVBoxes}, box_r[3] = {64, 64, 1};
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, sw_r = CU_TENSOR_MAP_SWIZZLE_64B;
   CUtensorMap tk, tkr, tv, tq, tqr;
-  bool ok = make_tmap(&tk, dt, 2, kv_cache, kv_dims, strides, box, sw) &&
-            make_tmap(&tq, dt, 2, q, q_dims, strides, box, sw);
+  bool ok = make_tmap(&tk, dt, 3, kv_cache, kv_dims, strides, box_k, sw) &&
+            make_tmap(&tv, dt, 3, kv_cache, kv_dims, strides, box_v, sw) &&
+            make_tmap(&tq, dt, 3, q, q_dims, strides, box_q, sw);
   if constexpr (FP8) {
-    ok = ok && make_tmap(&tkr, dt, 2, kv_cache, kv_dims, strides, box_r, sw_r) &&
-         make_tmap(&tqr, dt, 2, q, q_dims, strides, box_r, sw_r);
-    tv = tk;
+    ok = ok && make_tmap(&tkr, dt, 3, kv_cache, kvr_dims, strides, box_r, sw_r) &&
+         make_tmap(&tqr, dt, 3, q, qr_dims, strides, box_r, sw_r);
   } else {
-    ok = ok && make_tmap(&tv, dt, 2, kv_cache, kv_dims, strides, box_v, sw);
-    tkr = tk;
+    tkr = tk;   // (not used)
     tqr = tq;
   }
   if (!ok) return MLA_ERR_CUDA;
