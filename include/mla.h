@@ -423,7 +423,7 @@ int mla_gather_cache_scaled(const void *kv_cache, const float *kv_scales,
  * before it is read (calls on different streams need workspaces of their
  * own); 0 bytes, and workspace may be NULL, where no request can have more
  * than a few tiles.  split_tiles as in mla_decode_paged, in tiles of 128
- * tokens.  Limits as there. */
+ * (e4m3) or 64 (bf16) tokens.  Limits as there. */
 int mla_decode_window_workspace_size(int B, int q_len, int H, int max_seq_len,
                                      int window, int sinks, int split_tiles,
                                      size_t *bytes);

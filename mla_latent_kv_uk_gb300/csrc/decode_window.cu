@@ -3,8 +3,8 @@
 //
 // Rows and keys.  The q_len * H query rows of a request (query token outer,
 // head inner) all attend to the same latent rows, so they are taken in groups
-// of 128: per tile of 128 keys S = Q K^T is a dense [128 x 128 x 576] product
-// and O += P V a [128 x 512 x 128] one.  A request's keys are a list of
+// of 128: per tile of T keys (e4m3: 128, bf16: 64) S = Q K^T is a dense
+// [128 x T x 576] product and O += P V a [128 x 512 x T] one.  A request's keys are a list of
 // 64-token pages, the sinks' pages and then those from the window's first key
 // to the last query; only the list's pages are loaded.  Each row masks the
 // keys that it does not see.
@@ -13,9 +13,9 @@
 // tensor memory, so two CTAs of a cluster run each product as one
 // tcgen05 MMA of cta_group::2 with M = 128: CTA c holds rows [64c, 64c + 64)
 // of Q, S, P and O (S and O in the layout of that shape: lanes 0..63 the
-// first half of the columns, lanes 64..127 the second), for Q K^T the tile's
-// page c (64 of the 128 key columns), and for P V the value columns
-// [256c, 256c + 256) of all 128 keys.  Scores and probabilities never cross
+// first half of the columns, lanes 64..127 the second), for Q K^T half c of
+// the tile's keys, and for P V the value columns [256c, 256c + 256) of all
+// of them.  Scores and probabilities never cross
 // the pair; each key row is fetched twice, once as a key by its page's CTA
 // and once, by then from L2, as a value by halves.  Measured on the GB300: a
 // 32-byte K step costs 32 cycles at N = 128 (Q K^T: 18 or 36 per tile) and 66
@@ -40,7 +40,7 @@
 // write the results.  Lazy rescaling: O is rescaled when a row's reference would
 // be exceeded by more than 2^8.
 //
-// Split: every row group of a request is a job of ceil(pages / 2) tiles plus
+// Split: every row group of a request is a job of its list's tiles plus
 // kJobCost units for the switch; jobs lie end to end and pair p takes units
 // [pC, (p+1)C).  Each CTA works the plan out for itself from the lengths
 // (no plan kernel).  A job that is cut leaves partials in the workspace,
@@ -63,49 +63,57 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = 128;                // keys per tile: two pages
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;              // warps 4..11
-constexpr int kMinUnits = 3;              // smallest automatic span
-constexpr int kJobCost = 2;               // units of switching to a job
-// Jobs that cannot have more tiles than this are not cut: each is one pair's
+constexpr int kMinPages = 6;               // smallest automatic span, in pages
+constexpr int kJobPages = 4;               // what switching to a job costs, in pages
+// Jobs that cannot have more pages than this are not cut: each is one pair's
 // from end to end, written directly, and no merge kernel follows.
-constexpr int kSoloTiles = 3;
+constexpr int kSoloPages = 6;
 constexpr int kSegSlots = 4;
-constexpr uint32_t kColO = 0, kColS = 256;   // O [0,256), S [256,320) and [320,384)
+constexpr uint32_t kColO = 0, kColS = 256;   // O [0,256), then two S tiles
 
-// What differs between the formats.  A chunk is 64 rows x 128 bytes of keys
-// or queries; K and V come through rings of slots.
+// What differs between the formats.  K and V come through rings of slots.
+// The bf16 tile is one page: its query takes 72 KB, and the other 152 KB then
+// hold two tiles of keys and values, so that a tile's values are on their way
+// while the last one's are read (with two-page tiles, one of each, the
+// speculative batch took 162 us).
 template <bool FP8>
 struct Fmt {
   static constexpr int kEsz = FP8 ? 1 : 2;
+  static constexpr int kPages = FP8 ? 2 : 1;               // pages of a tile
+  static constexpr int kTile = kPages * kPage;             // its keys: 128 / 64
+  static constexpr int kMine = kTile / 4;                  // keys of one softmax thread
+  static constexpr int kMinUnits = (kMinPages + kPages - 1) / kPages;
+  static constexpr int kJobCost = kJobPages / kPages;      // in tiles, as all units
   static constexpr int kCols = 128 / kEsz;                 // columns of a 128-byte box row
-  static constexpr int kLatChunks = kLatent / kCols;       // 4 / 8
-  // the rope columns: 64 bytes (a chunk of its own kind) / 128 bytes
-  static constexpr int kRowsBytes = 64 * kDqk * kEsz;      // 64 rows: 36 / 72 KB
+  static constexpr int kLatChunks = kLatent / kCols;       // 4 / 8 boxes (the rope: half a one / one)
+  static constexpr int kQBytes = 64 * kDqk * kEsz;         // 64 query rows: 36 / 72 KB
+  static constexpr int kKRows = kTile / 2;                 // key rows of one CTA
+  static constexpr int kKBox = kKRows * 128;
   static constexpr int kGroups = FP8 ? 1 : 3;              // K slots that a tile takes
-  static constexpr int kGroupBytes = kRowsBytes / kGroups; // 36 / 24 KB
-  static constexpr int kGroupChunks = FP8 ? kLatChunks : 3;   // 128-byte columns of a slot (e4m3: and the rope's)
-  static constexpr int kKSlots = FP8 ? 2 : 3;
-  static constexpr int kVTok = FP8 ? 64 : 32;              // keys of a V slot
+  static constexpr int kGroupBytes = kKRows * kDqk * kEsz / kGroups;   // 36 / 12 KB
+  static constexpr int kGroupChunks = FP8 ? kLatChunks : 3;   // boxes of a slot (e4m3: and the rope's)
+  static constexpr int kKSlots = 2 * kGroups;              // two tiles
+  static constexpr int kVTok = kTile / 2;                  // keys of a V slot
   static constexpr int kVBoxes = 256 / kCols;              // 2 / 4
   static constexpr int kVBox = kVTok * 128;                // 8 / 4 KB
   static constexpr int kVSlotBytes = kVBoxes * kVBox;      // 16 KB
-  static constexpr int kVPer = kTile / kVTok;              // slots of a tile: 2 / 4
+  static constexpr int kVPer = 2;                          // slots of a tile
   static constexpr int kVSlots = FP8 ? 5 : 4;
-  static constexpr int kPBytes = 64 * 128 * 2;             // hi and lo, or bf16: 16 KB
-  static constexpr int kPBufs = FP8 ? 2 : 1;
+  static constexpr int kPBytes = 64 * 128 * (FP8 ? 2 : 1); // hi and lo, or bf16: 128 bytes a row
+  static constexpr int kPBufs = 2;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kRowsBytes;
+  static constexpr int kOffK = kOffQ + kQBytes;
   static constexpr int kOffV = kOffK + kKSlots * kGroupBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVSlotBytes;
   static constexpr int kOffX = kOffP + kPBufs * kPBytes;   // row exchange [2][4][64] floats
   static constexpr int kOffSeg = kOffX + 2 * 256 * 4;
   static constexpr int kOffBars = kOffSeg + kSegSlots * 64;
-  static constexpr int kBarBytes = 256;
+  static constexpr int kBarBytes = 384;
   static constexpr int kSmem = kOffBars + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
-  static_assert(kGroupBytes % 1024 == 0 && kRowsBytes % 1024 == 0, "swizzled tiles");
+  static_assert(kGroupBytes % 1024 == 0 && kQBytes % 1024 == 0 && kKBox % 1024 == 0, "swizzled tiles");
   // p' of a row's largest key after the reference moved, as a power of two
   static constexpr float kTop = FP8 ? 5.f : 0.f;
 };
@@ -132,7 +140,7 @@ struct WindowArgs {
 struct Job {
   int p0, p1;                   // positions of its first and last query
   int lo_page, sink_pages, pages;
-  __device__ __forceinline__ int tiles() const { return (pages + 1) >> 1; }
+  __device__ __forceinline__ int tiles(int per) const { return (pages + per - 1) / per; }
   // page of the list's entry i
   __device__ __forceinline__ int page(int i) const {
     return i < sink_pages ? i : i - sink_pages + lo_page;
@@ -161,11 +169,12 @@ __device__ __forceinline__ int length_of(int b, const WindowArgs &a, bool tell) 
   return min(max(len, 0), most);
 }
 
+template <bool FP8>
 __device__ __forceinline__ int units_of(int j, const WindowArgs &a, int &len) {
   const int rg = a.RG > 1 ? j / a.B : 0;
   len = length_of(j - rg * a.B, a, blockIdx.x == 0 && rg == 0);
-  const int t = job_of(rg, len, a).tiles();
-  return t > 0 ? t + kJobCost : 0;
+  const int t = job_of(rg, len, a).tiles(Fmt<FP8>::kPages);
+  return t > 0 ? t + Fmt<FP8>::kJobCost : 0;
 }
 
 struct Seg {
@@ -186,6 +195,7 @@ __device__ __forceinline__ int warp_incl_scan(int x, int lane) {
 // The segments of one CTA pair, found by a whole warp.  Lane k holds the
 // jobs [k*per, (k+1)*per) in sum for the search of a span's first job, and
 // job base + k of the 32 that are being walked.
+template <bool FP8>
 struct Walk {
   int J, per, lane_excl, total, C, span, span_lo, span_hi;
   int base, k, len, units, excl;
@@ -196,14 +206,14 @@ struct Walk {
     per = (J + 31) / 32;
     int sum = 0;
     len = 0;
-    for (int j = lane * per; j < min(J, (lane + 1) * per); ++j) sum += units_of(j, a, len);
+    for (int j = lane * per; j < min(J, (lane + 1) * per); ++j) sum += units_of<FP8>(j, a, len);
     const int incl = warp_incl_scan(sum, lane);
     lane_excl = incl - sum;
     units = sum;                // (one job a lane: the walk's window is there already)
     excl = lane_excl;
     base = 0;
     total = __shfl_sync(0xffffffffu, incl, 31);
-    C = a.forced > 0 ? a.forced : max(kMinUnits, (total - 1) / a.spans_at_once + 1);
+    C = a.forced > 0 ? a.forced : max(Fmt<FP8>::kMinUnits, (total - 1) / a.spans_at_once + 1);
     span = blockIdx.x >> 1;
     open = false;
   }
@@ -218,7 +228,7 @@ struct Walk {
     s.b = span - s.rg * a.B;
     s.len = length_of(s.b, a, s.rg == 0);
     s.tile0 = 0;
-    s.ntiles = job_of(s.rg, s.len, a).tiles();
+    s.ntiles = job_of(s.rg, s.len, a).tiles(Fmt<FP8>::kPages);
     s.whole = 1;
     s.slot = 0;
     span += a.spans_at_once;
@@ -229,7 +239,7 @@ struct Walk {
     k = 0;
     units = 0;
     len = 0;
-    if (base + lane < J) units = units_of(base + lane, a, len);
+    if (base + lane < J) units = units_of<FP8>(base + lane, a, len);
     const int incl = warp_incl_scan(units, lane);
     excl = before + incl - units;
   }
@@ -257,7 +267,7 @@ struct Walk {
         continue;
       }
       ++k;
-      const int first = t0 + kJobCost, end = t0 + n;
+      const int first = t0 + Fmt<FP8>::kJobCost, end = t0 + n;
       const int u0 = max(span_lo, first), u1 = min(span_hi, end);
       if (n == 0 || u1 <= u0) continue;
       s.rg = a.RG > 1 ? j / a.B : 0;
@@ -499,7 +509,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 
   if (warp == 0) {
     // ------------------------------------------------- plan, Q and K
-    Walk walk;
+    Walk<FP8> walk;
     if (args.solo) {
       walk.init_solo(args);
     } else {
@@ -527,19 +537,20 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       if (sg.ntiles == 0) continue;
       const Job job = job_of(sg.rg, sg.len, args);
       Pages pg;
-      fetch_blocks(pg, job, sg.b, 2 * sg.tile0);
+      fetch_blocks(pg, job, sg.b, F::kPages * sg.tile0);
       // Q, once the last segment's last Q K^T has read it
       if (nq > 0 && !(ok = wait_for(q_empty, (nq - 1) & 1, abort_flag))) break;
       ++nq;
       if (lane == 0) {
-        if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kRowsBytes);
+        if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * F::kQBytes);
         const int row = sg.b * args.q_len * args.H + sg.rg * 128 + 64 * rank;
         pair_load(sm_q, &tm_q, q_bar, 0, row, 0);
         if (FP8) pair_load(sm_q + 4 * 8192, &tm_qr, q_bar, kLatent, row, 0);
       }
       for (int t = 0; ok && t < sg.ntiles; ++t) {
-        const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + rank);
-        const int row = blk < 0 ? no_row : blk * kPage;
+        // this CTA's key rows: a page of the two, or half of the one
+        const int blk = block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + (F::kPages - 1) * rank);
+        const int row = blk < 0 ? no_row : blk * kPage + (2 - F::kPages) * F::kKRows * rank;
         for (int g = 0; g < F::kGroups; ++g, ++kc) {
           const int s = kc % F::kKSlots;
           if (kc >= F::kKSlots &&
@@ -549,7 +560,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kGroupBytes);
             const uint32_t bar = peer_smem(&k_full[s], 0);
             pair_load(sm_k + s * F::kGroupBytes, &tm_k, bar, 0, row, F::kGroupChunks * g);
-            if (FP8) pair_load(sm_k + s * F::kGroupBytes + 4 * 8192, &tm_kr, bar, kLatent, row, 0);
+            if (FP8) pair_load(sm_k + s * F::kGroupBytes + 4 * F::kKBox, &tm_kr, bar, kLatent, row, 0);
           }
         }
       }
@@ -579,15 +590,15 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
       const Job job = job_of(sg.rg, sg.len, args);
       Pages pg;
-      fetch_blocks(pg, job, sg.b, 2 * sg.tile0);
+      fetch_blocks(pg, job, sg.b, F::kPages * sg.tile0);
       for (int t = 0; ok && t < sg.ntiles; ++t) {
         for (int v = 0; v < F::kVPer; ++v, ++vc) {
-          const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + v * 2 / F::kVPer);
+          const int blk = block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + (F::kPages - 1) * v);
           const int s = vc % F::kVSlots;
           if (vc >= F::kVSlots &&
               !(ok = wait_for(&v_empty[s], ((vc / F::kVSlots) - 1) & 1, abort_flag)))
             break;
-          const int row = blk < 0 ? no_row : blk * kPage + (v * F::kVTok) % kPage;
+          const int row = blk < 0 ? no_row : blk * kPage + (2 - F::kPages) * F::kVTok * v;
           if (lane == 0) {
             mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
             load_3d_hint(sm_v + s * F::kVSlotBytes, &tm_v, &v_full[s], 0, row, F::kVBoxes * rank, policy);
@@ -605,8 +616,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   } else if (warp == 1) {
     if (rank == 0) {
       // ---------------------------------------------------------- MMAs
-      const uint32_t idesc_qk = FP8 ? idesc_e4m3(128, kTile, false, false)
-                                    : idesc_bf16(128, kTile, false, false);
+      const uint32_t idesc_qk = FP8 ? idesc_e4m3(128, F::kTile, false, false)
+                                    : idesc_bf16(128, F::kTile, false, false);
       const uint32_t idesc_pv = FP8 ? idesc_e4m3(128, 256, false, true)
                                     : idesc_bf16(128, 256, false, true);
       const uint32_t me = elect_one();
@@ -617,7 +628,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       int kc = 0, vc = 0, uc = 0;             // K slots, V slots, tiles so far
       bool ok = true;
       auto issue_qk = [&](int u) -> bool {
-        const uint32_t d = tmem + kColS + 64 * (u & 1);
+        const uint32_t d = tmem + kColS + F::kTile / 2 * (u & 1);
 #pragma unroll
         for (int g = 0; g < F::kGroups; ++g, ++kc) {
           const int s = kc % F::kKSlots;
@@ -629,18 +640,18 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < 16; ++k)
               pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (k >> 2) * 512 + (k & 3) * 2),
-                            desc_at<1024, kSwizzle128B>(kd + (k >> 2) * 512 + (k & 3) * 2), idesc_qk,
-                            k > 0, me);
+                            desc_at<1024, kSwizzle128B>(kd + (k >> 2) * (F::kKBox / 16) + (k & 3) * 2),
+                            idesc_qk, k > 0, me);
 #pragma unroll
             for (int k = 0; k < 2; ++k)       // the rope columns: rows of 64 bytes
               pair_mma<FP8>(d, desc_at<512, kSwizzle64B>(qd + 4 * 512 + 2 * k),
-                            desc_at<512, kSwizzle64B>(kd + 4 * 512 + 2 * k), idesc_qk, 1, me);
+                            desc_at<512, kSwizzle64B>(kd + 4 * (F::kKBox / 16) + 2 * k), idesc_qk, 1, me);
           } else {
 #pragma unroll
             for (int k = 0; k < 12; ++k)
               pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (3 * g + (k >> 2)) * 512 + (k & 3) * 2),
-                            desc_at<1024, kSwizzle128B>(kd + (k >> 2) * 512 + (k & 3) * 2), idesc_qk,
-                            g + k > 0, me);
+                            desc_at<1024, kSwizzle128B>(kd + (k >> 2) * (F::kKBox / 16) + (k & 3) * 2),
+                            idesc_qk, g + k > 0, me);
           }
           pair_commit(&k_empty[s], me);
         }
@@ -660,7 +671,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {  // 32 bytes of P: 32 e4m3 or 16 bf16 keys
               const int step = 2 * v + kk;
-              const uint32_t pa = pd + (FP8 ? step * 2 : (step >> 2) * 512 + (step & 3) * 2);
+              const uint32_t pa = pd + step * 2;
               const uint64_t bd = desc_at<1024, kSwizzle128B>(
                   vd + (FP8 ? j * F::kVBox + kk * 4096 : 2 * j * F::kVBox + kk * 2048) / 16);
               pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa), bd, idesc_pv,
@@ -703,8 +714,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ softmax and results
-    // Four threads share a row, each with 32 of the tile's keys: `half` (the
-    // TMEM lanes: which page), `sub` (which half of the page).
+    // Four threads share a row, each with kMine of the tile's keys: `half`
+    // (the TMEM lanes: which CTA's key rows), `sub` (which half of those).
     const int quarter = warp & 3, half = quarter >> 1, sub = (warp - 4) >> 2;
     const int r = (quarter & 1) * 32 + lane;            // row of this CTA
     const int tid = threadIdx.x - 128;
@@ -751,7 +762,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       // scales of this thread's keys, a tile ahead
       const int32_t *bt = args.block_table + static_cast<int64_t>(sg.b) * args.max_blocks;
       auto load_blk = [&](int t) -> int {
-        const int e = 2 * (sg.tile0 + t) + half;
+        const int e = F::kPages * (sg.tile0 + t) + half;
         if (!FP8 || !args.scales || t >= sg.ntiles || e >= job.pages) return -1;
         return __ldg(bt + job.page(e));   // (looked at a tile later: nothing waits for it here)
       };
@@ -771,11 +782,11 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const int sb = uc & 1;
         load_scales(blk_next, sc_next);
         blk_next = load_blk(t + 2);
-        const int e0 = 2 * (sg.tile0 + t);
+        const int e0 = F::kPages * (sg.tile0 + t);
         const int page0 = job.page(e0) * kPage;
-        const int page1 = e0 + 1 < job.pages ? job.page(e0 + 1) * kPage : 1 << 30;
-        const int key0 = (half ? page1 : page0) + 32 * sub;
-        const bool masked = key0 + 31 > p || (key0 < wlo && key0 + 32 > args.sinks);
+        const int page1 = F::kPages == 2 && e0 + 1 < job.pages ? job.page(e0 + 1) * kPage : 1 << 30;
+        const int key0 = (F::kPages == 2 ? (half ? page1 : page0) : page0 + F::kKRows * half) + F::kMine * sub;
+        const bool masked = key0 + F::kMine - 1 > p || (key0 < wlo && key0 + F::kMine > args.sinks);
         auto clean = [&](int k0) {
           return k0 == 1 << 30 ||
                  (k0 + kPage - 1 <= job.p0 && (k0 >= clean_lo || k0 + kPage <= args.sinks));
@@ -792,16 +803,18 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         if (!(ok = all_ok(wait_for(&s_full[sb], (uc >> 1) & 1, abort_flag)))) break;
         tc_fence_after();
-        float x[32];
-        tmem_ld_x32(lane_base + kColS + 64 * sb + 32 * sub, reinterpret_cast<uint32_t *>(x));
+        float x[F::kMine];
+        const uint32_t s_at = lane_base + kColS + F::kTile / 2 * sb + F::kMine * sub;
+        if constexpr (FP8) tmem_ld_x32(s_at, reinterpret_cast<uint32_t *>(x));
+        else tmem_ld_x16(s_at, reinterpret_cast<uint32_t *>(x));
         if (masked) {
           const int e = p - key0, a = wlo - key0, z = args.sinks - key0;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = k <= e && (k >= a || k < z) ? x[k] : -INFINITY;
+          for (int k = 0; k < F::kMine; ++k) x[k] = k <= e && (k >= a || k < z) ? x[k] : -INFINITY;
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < F::kMine / 16; ++g) {
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 16; k += 4) {
@@ -821,7 +834,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         const float base = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < F::kMine / 16; ++g) {
           const float d = lg[g] - base;
           float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -858,10 +871,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             lo[ch] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          uint4 *row = reinterpret_cast<uint4 *>(pbuf + half * 8192 + r * 128);
+          uint4 *row = reinterpret_cast<uint4 *>(pbuf + r * 128);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            row[(4 * sub + q) ^ (r & 7)] =
+          for (int q = 0; q < 2; ++q)
+            row[(4 * half + 2 * sub + q) ^ (r & 7)] =
                 make_uint4(bf16x2_rn(x[8 * q], x[8 * q + 1]), bf16x2_rn(x[8 * q + 2], x[8 * q + 3]),
                            bf16x2_rn(x[8 * q + 4], x[8 * q + 5]), bf16x2_rn(x[8 * q + 6], x[8 * q + 7]));
         }
@@ -894,7 +907,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           constexpr int kChunks = F::kVBoxes * 8, kRowsAtOnce = 32 / kChunks;
           const int lr = lane / kChunks, at = ((lane % kChunks) >> 3) * F::kVBox + (lane & 7) * 16;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < F::kPages; ++h) {
             const int page = h ? page1 : page0;
             if (clean(page)) continue;
             // all rows see [0, a) (sinks) and [b, c) of the page's 64
@@ -962,6 +975,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       // the P tile (its rows are written again behind the next exchange of
       // the four warps that share them) so that stores cover whole sectors
       uint4 *buf = reinterpret_cast<uint4 *>(sm_p + half * 8192 + (quarter & 1) * 4096 + sub * 2048);
+      static_assert(F::kPBufs * F::kPBytes >= 16384, "staging");
       uint32_t all[128];
       tmem_ld_x64(lane_base + kColO + 128 * sub, all);
       tmem_ld_x64(lane_base + kColO + 128 * sub + 64, all + 64);
@@ -1033,7 +1047,7 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   const int64_t row = static_cast<int64_t>(b) * R + rg * 128 + rr;
   T *out = static_cast<T *>(a.out) + row * kLatent;
   const int C = a.ws_head[0], first = a.ws_head[2 + 2 * j], end = a.ws_head[3 + 2 * j];
-  if (job_of(rg, length_of(b, a, false), a).tiles() == 0) {   // (the words above hold nothing)
+  if (job_of(rg, length_of(b, a, false), a).pages == 0) {   // (the words above hold nothing)
     if (mine == 0 && row_ok) {
       const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       for (int k = 0; k < 2; ++k) store8(out + 8 * (lane + 32 * k), zero);
@@ -1184,12 +1198,12 @@ WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sin
   if (window > 0)
     pages = std::min(pages, (static_cast<int64_t>(window) + q_len) / kPage + 2 +
                                 (static_cast<int64_t>(sinks) + kPage - 1) / kPage);
-  const int64_t tiles = (pages + 1) / 2;
   WsLayout w{};
-  w.solo = split_tiles == 0 && tiles <= kSoloTiles;
+  w.solo = split_tiles == 0 && pages <= kSoloPages;
   if (w.solo) return w;   // nothing to keep
+  // (a forced split counts tiles: the smaller ones, of one page, make more)
   const int64_t spans =
-      split_tiles > 0 ? (J * (tiles + kJobCost) + split_tiles - 1) / split_tiles : pairs;
+      split_tiles > 0 ? (J * (pages + kJobPages) + split_tiles - 1) / split_tiles : pairs;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   w.o_off = up((2 + 2 * static_cast<size_t>(J)) * sizeof(int));
   w.lse_off = w.o_off + static_cast<size_t>(2 * spans) * 128 * kLatent * sizeof(float);
@@ -1232,7 +1246,7 @@ int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArg
   const uint64_t q_rows = static_cast<uint64_t>(a.B) * a.q_len * a.H;
   const uint64_t kv_dims[3] = {F::kCols, kv_rows, boxes}, q_dims[3] = {F::kCols, q_rows, boxes};
   const uint64_t kvr_dims[3] = {kDqk, kv_rows, 1}, qr_dims[3] = {kDqk, q_rows, 1};
-  const uint32_t box_k[3] = {F::kCols, 64, F::kGroupChunks};
+  const uint32_t box_k[3] = {F::kCols, F::kKRows, F::kGroupChunks};
   const uint32_t box_q[3] = {F::kCols, 64, static_cast<uint32_t>(boxes)};
   const uint32_t box_v[3] = {F::kCols, F::kVTok, F::kVBoxes}, box_r[3] = {64, 64, 1};
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, sw_r = CU_TENSOR_MAP_SWIZZLE_64B;
