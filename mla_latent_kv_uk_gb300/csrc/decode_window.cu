@@ -36,8 +36,8 @@
 //
 // Warps: 0 walks the split plan, publishes the segments and loads Q and K,
 // 1 issues the MMAs (leader CTA), 2 loads V, 4..11 turn scores into
-// probabilities (one row and a quarter of the tile's keys per thread) and
-// write the results.  Lazy rescaling: O is rescaled when a row's reference would
+// probabilities (two groups taking the tiles in turn, one row and half of the
+// tile's keys per thread) and write the results.  Lazy rescaling: O is rescaled when a row's reference would
 // be exceeded by more than 2^8.
 //
 // Split: every row group of a request is a job of its list's tiles plus
@@ -83,7 +83,7 @@ struct Fmt {
   static constexpr int kEsz = FP8 ? 1 : 2;
   static constexpr int kPages = FP8 ? 2 : 1;               // pages of a tile
   static constexpr int kTile = kPages * kPage;             // its keys: 128 / 64
-  static constexpr int kMine = kTile / 4;                  // keys of one softmax thread
+  static constexpr int kMine = kTile / 2;                  // keys of one softmax thread
   static constexpr int kMinUnits = (kMinPages + kPages - 1) / kPages;
   static constexpr int kJobCost = kJobPages / kPages;      // in tiles, as all units
   static constexpr int kCols = 128 / kEsz;                 // columns of a 128-byte box row
@@ -107,9 +107,9 @@ struct Fmt {
   static constexpr int kOffK = kOffQ + kQBytes;
   static constexpr int kOffV = kOffK + kKSlots * kGroupBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVSlotBytes;
-  static constexpr int kOffX = kOffP + kPBufs * kPBytes;   // row exchange [2][4][64] floats
-  static constexpr int kOffSeg = kOffX + 2 * 256 * 4;
-  static constexpr int kOffBars = kOffSeg + kSegSlots * 64;
+  static constexpr int kOffX = kOffP + kPBufs * kPBytes;   // [2][128] maxima, [2][64] references, [256] sums
+  static constexpr int kOffSeg = kOffX + (256 + 128 + 256) * 4;
+  static constexpr int kOffBars = kOffSeg + kSegSlots * 32;
   static constexpr int kBarBytes = 384;
   static constexpr int kSmem = kOffBars + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -419,12 +419,15 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   uint64_t *q_empty = q_full + 1;
   uint64_t *seg_full = q_empty + 1;           // [kSegSlots]
   uint64_t *seg_empty = seg_full + kSegSlots; // [kSegSlots]
-  uint64_t *drain = seg_empty + kSegSlots;
+  uint64_t *ref_there = seg_empty + kSegSlots;   // [2 groups][2 row blocks]
+  uint64_t *sum_there = ref_there + 4;        // [2 row blocks]
+  uint64_t *o_free = sum_there + 2;           // leader: the last segment's O has been read
+  uint64_t *drain = o_free + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((2 * (F::kKSlots + F::kVSlots) + 6 + 2 + 2 * kSegSlots + 1) * 8 + 8 <= F::kBarBytes,
+  static_assert((2 * (F::kKSlots + F::kVSlots) + 6 + 2 + 2 * kSegSlots + 8) * 8 + 8 <= F::kBarBytes,
                 "barriers");
-  static_assert(sizeof(Seg) <= 64, "segment slot");
+  static_assert(sizeof(Seg) <= 32, "segment slot");
 
   if (smem_u32(smem) & 1023u) {   // (never seen: the swizzled tiles need it)
     if (threadIdx.x == 0) raise_error(args.err, MLA_DEVERR_TIMEOUT);
@@ -444,7 +447,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 2 * kSoftWarps);  // the softmax warps of both CTAs
+      mbar_init(&p_full[s], kSoftWarps);      // a softmax group of either CTA
       mbar_init(&pv_done[s], 1);
     }
     mbar_init(q_full, 1);
@@ -453,6 +456,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       mbar_init(&seg_full[s], 1);
       mbar_init(&seg_empty[s], kSoftWarps + (rank == 0 ? 2 : 1));   // V, softmax, the leader's MMAs
     }
+    for (int s = 0; s < 4; ++s) mbar_init(&ref_there[s], 2);   // the two warps of a row block
+    for (int s = 0; s < 2; ++s) mbar_init(&sum_there[s], 4);   // its four, of both groups
+    mbar_init(o_free, 2 * kSoftWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -701,11 +707,13 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if (!(ok = issue_qk(uc + 1))) break;
             if (t + 2 == n) pair_commit(q_empty, me);
           }
+          if (t == 0 && nq > 1 && !(ok = wait(o_free, nq - 2))) break;
           if (!(ok = wait(&p_full[uc & 1], uc >> 1))) break;
           tc_fence_after();
           issue_pv(uc, t == 0);
         }
       }
+      if (ok && nq > 0) wait(o_free, nq - 1);   // (the other CTA's last signals are in)
       if (*abort_flag) {
         pair_commit(drain, me);
         volatile int no_abort = 0;
@@ -714,32 +722,33 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ softmax and results
-    // Four threads share a row, each with kMine of the tile's keys: `half`
-    // (the TMEM lanes: which CTA's key rows), `sub` (which half of those).
-    const int quarter = warp & 3, half = quarter >> 1, sub = (warp - 4) >> 2;
-    const int r = (quarter & 1) * 32 + lane;            // row of this CTA
-    const int tid = threadIdx.x - 128;
+    // Two groups of four warps take the tiles in turn (group 0 the even ones,
+    // over all segments), so that one tile's exponentials overlap the next
+    // one's scores.  In a group two threads share a row, each with kMine of
+    // the tile's keys (`half`: the TMEM lanes, which CTA's key rows).  What
+    // tile t + 1 needs of tile t is the row's reference; it is handed on
+    // through shared memory as soon as the row's maximum is known.
+    const int quarter = warp & 3, half = quarter >> 1, group = (warp - 4) >> 2;
+    const int block = quarter & 1;                      // row block: rows 32 block ..
+    const int r = block * 32 + lane;                    // row of this CTA
     const uint32_t lane_base = tmem + ((quarter * 32u) << 16);
-    const uint32_t bar_id = 1 + (quarter & 1);          // the four warps of the same rows
     const uint32_t p_bar[2] = {peer_smem(&p_full[0], 0), peer_smem(&p_full[1], 0)};
-    const int mine = (2 * half + sub) * 64 + r;
-    // largest / sum over the row's four threads; the two tables alternate, so
-    // that a thread may still read one while the next is written
-    int turn = 0;
-    // The hardware barrier has no limit, so no warp may leave the others in
-    // it: it takes along whether all is well, a warp whose wait ran out goes
-    // through it once more before it leaves, and the others leave behind it.
+    const uint32_t o_bar = peer_smem(o_free, 0);
+    float *x_max = xchg + 128 * group, *x_ref = xchg + 256, *x_sum = xchg + 384;
+    // The hardware barrier of the two warps has no limit, so neither may leave
+    // the other in it: it takes along whether all is well, a warp whose wait
+    // ran out goes through it once more before it leaves, and the other leaves
+    // behind it.
     bool told = false;
-    auto exchange = [&](float &v, auto op) -> bool {
-      float *x = xchg + 256 * (turn ^= 1);
-      x[mine] = v;
-      told = !named_and(bar_id, 128, true);
-      v = op(op(x[r], x[64 + r]), op(x[128 + r], x[192 + r]));
+    auto pair_max = [&](float &v) -> bool {             // over the row's two threads
+      x_max[64 * half + r] = v;
+      told = !named_and(1 + 2 * group + block, 64, true);
+      v = fmaxf(v, x_max[64 * (half ^ 1) + r]);
       return !told;
     };
     auto all_ok = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
     Seg sg;
-    int uc = 0, vc = 0;
+    int uc = 0, segs = 0;                               // tiles and segments (with tiles) so far
     bool ok = true;
     for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
       const int R = args.q_len * args.H;
@@ -748,6 +757,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const int64_t at = static_cast<int64_t>(sg.b) * R + row0;
         const int chunks = kLatent * (args.out_f32 ? 4 : 2) / 16;
         uint4 *o = static_cast<uint4 *>(args.out) + at * chunks;
+        const int tid = threadIdx.x - 128;
         for (int k = tid; k < n * chunks; k += 32 * kSoftWarps) o[k] = make_uint4(0, 0, 0, 0);
         if (tid < n) args.lse[at + tid] = -INFINITY;
         continue;
@@ -759,54 +769,58 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const int wlo = args.window ? p - args.window + 1 : 0;
       // every query row of the job sees keys [clean_lo, job.p0] and the sinks
       const int clean_lo = args.window ? job.p1 - args.window + 1 : 0;
-      // scales of this thread's keys, a tile ahead
+      // scales of this thread's keys, a tile of its group ahead
       const int32_t *bt = args.block_table + static_cast<int64_t>(sg.b) * args.max_blocks;
       auto load_blk = [&](int t) -> int {
         const int e = F::kPages * (sg.tile0 + t) + half;
         if (!FP8 || !args.scales || t >= sg.ntiles || e >= job.pages) return -1;
         return __ldg(bt + job.page(e));   // (looked at a tile later: nothing waits for it here)
       };
+      constexpr int kBlocks = FP8 ? 4 : 1;   // scales of 64 keys
       auto load_scales = [&](int blk, float *sc) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < kBlocks; ++g)
           sc[g] = blk < 0 || blk >= args.num_blocks
-                          ? args.k_scale
-                          : __ldg(args.scales + ((static_cast<int64_t>(blk) * kPage + 32 * sub + 16 * g) >>
-                                                 args.sb_shift));
+                      ? args.k_scale
+                      : __ldg(args.scales + ((static_cast<int64_t>(blk) * kPage + 16 * g) >> args.sb_shift));
       };
-      float sc[2], sc_next[2];
-      int blk_next = load_blk(1);
-      load_scales(load_blk(0), sc);
-      float ref = -INFINITY, l = 0.f;
-      for (int t = 0; t < sg.ntiles; ++t, ++uc) {
-        const int sb = uc & 1;
+      const int t_first = (uc ^ group) & 1;             // this group's first tile
+      float sc[kBlocks], sc_next[kBlocks];
+      int blk_next = load_blk(t_first + 2);
+      load_scales(load_blk(t_first), sc);
+      const int uc0 = uc;
+      uc += sg.ntiles;
+      float ref = -INFINITY, l = 0.f;                   // l in units of 2^ref
+      for (int t = t_first; t < sg.ntiles; t += 2) {
+        const int u = uc0 + t, half_u = u >> 1;         // (group u & 1)
         load_scales(blk_next, sc_next);
-        blk_next = load_blk(t + 2);
+        blk_next = load_blk(t + 4);
         const int e0 = F::kPages * (sg.tile0 + t);
         const int page0 = job.page(e0) * kPage;
         const int page1 = F::kPages == 2 && e0 + 1 < job.pages ? job.page(e0 + 1) * kPage : 1 << 30;
-        const int key0 = (F::kPages == 2 ? (half ? page1 : page0) : page0 + F::kKRows * half) + F::kMine * sub;
+        const int key0 = (F::kPages == 2 ? (half ? page1 : page0) : page0 + F::kKRows * half);
         const bool masked = key0 + F::kMine - 1 > p || (key0 < wlo && key0 + F::kMine > args.sinks);
         auto clean = [&](int k0) {
           return k0 == 1 << 30 ||
                  (k0 + kPage - 1 <= job.p0 && (k0 >= clean_lo || k0 + kPage <= args.sinks));
         };
         const bool all_clean = clean(page0) && clean(page1);
-        float c[2], lg[2];
+        float c[kBlocks], lg[kBlocks];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < kBlocks; ++g) {
           // (a scale of 0 stands for zeros: so does the smallest one)
           const float sigma = fminf(fmaxf(sc[g], 0x1p-100f), 0x1p120f);
           c[g] = sigma * args.scale_log2;
           lg[g] = FP8 ? log2f(sigma) : 0.f;
           sc[g] = FP8 ? 1.f / sigma : 1.f;
         }
-        if (!(ok = all_ok(wait_for(&s_full[sb], (uc >> 1) & 1, abort_flag)))) break;
+        constexpr int kRun = F::kMine / kBlocks;        // keys of one scale: 16 / 32
+        if (!(ok = all_ok(wait_for(&s_full[group], half_u & 1, abort_flag)))) break;
         tc_fence_after();
         float x[F::kMine];
-        const uint32_t s_at = lane_base + kColS + F::kTile / 2 * sb + F::kMine * sub;
-        if constexpr (FP8) tmem_ld_x32(s_at, reinterpret_cast<uint32_t *>(x));
-        else tmem_ld_x16(s_at, reinterpret_cast<uint32_t *>(x));
+        const uint32_t s_at = lane_base + kColS + F::kTile / 2 * group;
+        if constexpr (FP8) tmem_ld_x64(s_at, reinterpret_cast<uint32_t *>(x));
+        else tmem_ld_x32(s_at, reinterpret_cast<uint32_t *>(x));
         if (masked) {
           const int e = p - key0, a = wlo - key0, z = args.sinks - key0;
 #pragma unroll
@@ -814,31 +828,39 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < F::kMine / 16; ++g) {
+        for (int g = 0; g < kBlocks; ++g) {
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            m0 = fmax3(m0, x[16 * g + k], x[16 * g + k + 1]);
-            m1 = fmax3(m1, x[16 * g + k + 2], x[16 * g + k + 3]);
+          for (int k = 0; k < kRun; k += 4) {
+            m0 = fmax3(m0, x[kRun * g + k], x[kRun * g + k + 1]);
+            m1 = fmax3(m1, x[kRun * g + k + 2], x[kRun * g + k + 3]);
           }
           top = fmaxf(top, fmaf(fmaxf(m0, m1), c[g], lg[g]));
         }
-        if (!(ok = exchange(top, [](float a, float b) { return fmaxf(a, b); }))) break;
-        const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
-        const bool rescale = t > 0 && __any_sync(0xffffffffu, move);
-        float f = 1.f;
-        if (move) {
-          f = ref == -INFINITY ? 0.f : ex2(ref - (top - F::kTop));
-          ref = top - F::kTop;
-          l *= f;
+        if (!(ok = pair_max(top))) break;
+        // the reference that the tile before left, and what this one makes of it
+        float old = -INFINITY;
+        if (t > 0) {
+          if (!(ok = all_ok(wait_for(&ref_there[2 * (group ^ 1) + block], ((u - 1) >> 1) & 1, abort_flag))))
+            break;
+          old = x_ref[64 * (group ^ 1) + r];
         }
+        const bool move = top > old + kLazy || (old == -INFINITY && top > -INFINITY);
+        const float now = move ? top - F::kTop : old;
+        if (half == 0) x_ref[64 * group + r] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ref_there[2 * group + block]);
+        const bool rescale = t > 0 && __any_sync(0xffffffffu, move);
+        const float f = move ? (old == -INFINITY ? 0.f : ex2(old - now)) : 1.f;
+        if (ref != now && l != 0.f) l *= ex2(ref - now);
+        ref = now;
         const float base = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
-        for (int g = 0; g < F::kMine / 16; ++g) {
+        for (int g = 0; g < kBlocks; ++g) {
           const float d = lg[g] - base;
           float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-          for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+          for (int k = kRun * g; k < kRun * g + kRun; k += 2) {
             fma_f32x2(x[k], x[k + 1], x[k], x[k + 1], c[g], c[g], d, d);
             x[k] = ex2(x[k]);
             x[k + 1] = ex2(x[k + 1]);
@@ -846,17 +868,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           }
           l = fmaf(s0 + s1, sc[g], l);
         }
-        // P goes where the P V of kPBufs tiles ago read
-        if (uc >= F::kPBufs) {
-          const int up = uc - F::kPBufs;
-          if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
-        }
-        uint8_t *pbuf = sm_p + (uc % F::kPBufs) * F::kPBytes;
+        // P goes where the P V of this group's last tile read
+        if (u >= 2 && !(ok = all_ok(wait_for(&pv_done[group], (half_u - 1) & 1, abort_flag)))) break;
+        uint8_t *pbuf = sm_p + group * F::kPBytes;
         if constexpr (FP8) {
           uint4 *hi = reinterpret_cast<uint4 *>(pbuf + r * 128);
           uint4 *lo = reinterpret_cast<uint4 *>(pbuf + 8192 + r * 128);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             uint32_t h[4], w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -866,38 +885,37 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
               h[k] = h0 | (h1 << 16);
               w[k] = l0 | (l1 << 16);
             }
-            const int ch = (4 * half + 2 * sub + q) ^ (r & 7);
+            const int ch = (4 * half + q) ^ (r & 7);
             hi[ch] = make_uint4(h[0], h[1], h[2], h[3]);
             lo[ch] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
           uint4 *row = reinterpret_cast<uint4 *>(pbuf + r * 128);
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            row[(4 * half + 2 * sub + q) ^ (r & 7)] =
+          for (int q = 0; q < 4; ++q)
+            row[(4 * half + q) ^ (r & 7)] =
                 make_uint4(bf16x2_rn(x[8 * q], x[8 * q + 1]), bf16x2_rn(x[8 * q + 2], x[8 * q + 3]),
                            bf16x2_rn(x[8 * q + 4], x[8 * q + 5]), bf16x2_rn(x[8 * q + 6], x[8 * q + 7]));
         }
         if (rescale) {
-          // O follows the reference, now that the last P V (long done, mostly)
-          // is; the two warps of a quadrant take 128 columns each
-          const int up = uc - 1;
-          if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
+          // O follows the reference, now that the last P V is done
+          if (!(ok = all_ok(wait_for(&pv_done[group ^ 1], ((u - 1) >> 1) & 1, abort_flag)))) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int q = 128 * sub; q < 128 * sub + 128; q += 32) {
-            uint32_t o[32];
-            tmem_ld_x32(lane_base + kColO + q, o);
+          for (int q = 0; q < 256; q += 64) {
+            uint32_t o[64];
+            tmem_ld_x64(lane_base + kColO + q, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
             tmem_st_x32(lane_base + kColO + q, o);
+            tmem_st_x32(lane_base + kColO + q + 32, o + 32);
           }
         }
         // the values are here (the MMA thread goes by this CTA's word)
 #pragma unroll
         for (int v = 0; v < F::kVPer; ++v) {
-          const int u = vc + v;
-          ok = ok && wait_for(&v_full[u % F::kVSlots], (u / F::kVSlots) & 1, abort_flag);
+          const int w = F::kVPer * u + v;
+          ok = ok && wait_for(&v_full[w % F::kVSlots], (w / F::kVSlots) & 1, abort_flag);
         }
         if (ok && !all_clean) {
           // rows that not every query row sees: 0 where none does, and where
@@ -915,9 +933,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             const int b = min(max(clean_lo - page, 0), c), a = min(max(args.sinks - page, 0), b);
             const int n = b - a + kPage - c;
 #pragma unroll 1
-            for (int i = (warp - 4) * kRowsAtOnce + lr; i < n; i += kSoftWarps * kRowsAtOnce) {
+            for (int i = quarter * kRowsAtOnce + lr; i < n; i += 4 * kRowsAtOnce) {
               const int tok = i < b - a ? a + i : c + i - (b - a);
-              const int slot = (vc + (h * kPage + tok) / F::kVTok) % F::kVSlots;
+              const int slot = (F::kVPer * u + (h * kPage + tok) / F::kVTok) % F::kVSlots;
               uint4 *w = reinterpret_cast<uint4 *>(sm_v + slot * F::kVSlotBytes + at +
                                                    (tok % F::kVTok) * 128);
               uint4 val = make_uint4(0, 0, 0, 0);
@@ -941,23 +959,30 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             }
           }
         }
-        vc += F::kVPer;
         if (!(ok = all_ok(ok))) break;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(p_bar[sb]);
+        if (lane == 0) mbar_arrive_remote(p_bar[group]);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) sc[g] = sc_next[g];
+        for (int g = 0; g < kBlocks; ++g) sc[g] = sc_next[g];
       }
       if (!ok) break;
-      // ---- results: O / l of this row, value columns [256 half + 128 sub, +128)
-      {
-        const int up = uc - 1;
-        if (!(ok = all_ok(wait_for(&pv_done[up & 1], (up >> 1) & 1, abort_flag)))) break;
-      }
+      // ---- results: O / l of this row, value columns [256 half + 128 group, +128)
+      const int last = uc - 1, lg_last = last & 1;
+      if (!(ok = all_ok(wait_for(&ref_there[2 * lg_last + block], (last >> 1) & 1, abort_flag) &&
+                        wait_for(&pv_done[lg_last], (last >> 1) & 1, abort_flag))))
+        break;
       tc_fence_after();
-      if (!(ok = exchange(l, [](float a, float b) { return a + b; }))) break;
+      const float end_ref = x_ref[64 * lg_last + r];
+      if (l != 0.f) l *= ex2(ref - end_ref);
+      ref = end_ref;
+      x_sum[128 * group + 64 * half + r] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sum_there[block]);
+      if (!(ok = all_ok(wait_for(&sum_there[block], segs & 1, abort_flag)))) break;
+      ++segs;
+      l = (x_sum[r] + x_sum[64 + r]) + (x_sum[128 + r] + x_sum[192 + r]);
       const bool empty = l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
       const int64_t row0 = static_cast<int64_t>(sg.b) * R + sg.rg * 128 + 64 * rank;
@@ -965,20 +990,20 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const int nrows = min(64, R - sg.rg * 128 - 64 * rank);
       const int esz = args.out_f32 ? 4 : 2;
       uint8_t *dst0 = static_cast<uint8_t *>(sg.whole ? args.out : args.ws_o) +
-                      (at * kLatent + 256 * half + 128 * sub) * esz;
+                      (at * kLatent + 256 * half + 128 * group) * esz;
       const int64_t rstride = static_cast<int64_t>(kLatent) * esz;
-      if (half + sub == 0 && r < nrows) {
+      if (half + group == 0 && r < nrows) {
         const float v = empty ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
         (sg.whole ? args.lse : args.ws_lse)[at + r] = v;
       }
-      // pieces of 64 bytes a row, staged through 2 KB of this warp's own in
-      // the P tile (its rows are written again behind the next exchange of
-      // the four warps that share them) so that stores cover whole sectors
-      uint4 *buf = reinterpret_cast<uint4 *>(sm_p + half * 8192 + (quarter & 1) * 4096 + sub * 2048);
-      static_assert(F::kPBufs * F::kPBytes >= 16384, "staging");
+      // pieces of 64 bytes a row, staged through 2 KB of this warp's own in its
+      // group's P tile (in its row block, which the pair writes again behind
+      // its next barrier), so that stores cover whole sectors
+      uint4 *buf = reinterpret_cast<uint4 *>(sm_p + group * F::kPBytes + block * 4096 + half * 2048);
+      static_assert(F::kPBytes >= 4 * 2048, "staging");
       uint32_t all[128];
-      tmem_ld_x64(lane_base + kColO + 128 * sub, all);
-      tmem_ld_x64(lane_base + kColO + 128 * sub + 64, all + 64);
+      tmem_ld_x64(lane_base + kColO + 128 * group, all);
+      tmem_ld_x64(lane_base + kColO + 128 * group + 64, all + 64);
 #pragma unroll
       for (int q = 0; q < 128; q += 32) {
         auto f = [&](int k) { return __uint_as_float(all[q + k]) * inv; };
@@ -1002,16 +1027,17 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
             const int row = it * 8 + (lane >> 2), ch = lane & 3;
-            const int rr = (quarter & 1) * 32 + row;
+            const int rr = block * 32 + row;
             if (rr < nrows)
               reinterpret_cast<uint4 *>(dst + rr * rstride)[ch] = buf[row * 4 + (ch ^ ((row >> 1) & 3))];
           }
         }
       }
+      tc_fence_before();   // (O has been read: the next segment's P V may begin)
       __syncwarp();
-      tc_fence_before();
+      if (lane == 0) mbar_arrive_remote(o_bar);
     }
-    if (!told) named_and(bar_id, 128, ok && !*abort_flag);
+    if (!told) named_and(1 + 2 * group + block, 64, ok && !*abort_flag);
   }
   __syncthreads();
   pair_sync();                                // neither CTA's MMAs or signals need the other any more
