@@ -71,7 +71,8 @@ constexpr int kJobPages = 4;               // what switching to a job costs, in 
 // from end to end, written directly, and no merge kernel follows.
 constexpr int kSoloPages = 6;
 constexpr int kSegSlots = 4;
-constexpr uint32_t kColO = 0, kColS = 256;   // O [0,256), then two S tiles
+constexpr uint32_t kColO = 0, kColS = 256;   // O [0,256), then the S tiles
+constexpr int kSBufs = 4;                    // Q K^T runs two tiles ahead of P V
 
 // What differs between the formats.  K and V come through rings of slots.
 // The bf16 tile is one page: its query takes 72 KB, and the other 152 KB then
@@ -412,8 +413,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   uint64_t *k_empty = k_full + F::kKSlots;    // [kKSlots]
   uint64_t *v_full = k_empty + F::kKSlots;    // [kVSlots]
   uint64_t *v_empty = v_full + F::kVSlots;    // [kVSlots]
-  uint64_t *s_full = v_empty + F::kVSlots;    // [2]
-  uint64_t *p_full = s_full + 2;              // [2] leader
+  uint64_t *s_full = v_empty + F::kVSlots;    // [kSBufs]
+  uint64_t *p_full = s_full + kSBufs;         // [2] leader
   uint64_t *pv_done = p_full + 2;             // [2]
   uint64_t *q_full = pv_done + 2;             // leader
   uint64_t *q_empty = q_full + 1;
@@ -425,7 +426,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   uint64_t *drain = o_free + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((2 * (F::kKSlots + F::kVSlots) + 6 + 2 + 2 * kSegSlots + 8) * 8 + 8 <= F::kBarBytes,
+  static_assert((2 * (F::kKSlots + F::kVSlots) + kSBufs + 4 + 2 + 2 * kSegSlots + 8) * 8 + 8 <= F::kBarBytes,
                 "barriers");
   static_assert(sizeof(Seg) <= 32, "segment slot");
 
@@ -445,8 +446,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
+    for (int s = 0; s < kSBufs; ++s) mbar_init(&s_full[s], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], kSoftWarps);      // a softmax group of either CTA
       mbar_init(&pv_done[s], 1);
     }
@@ -634,7 +635,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       int kc = 0, vc = 0, uc = 0;             // K slots, V slots, tiles so far
       bool ok = true;
       auto issue_qk = [&](int u) -> bool {
-        const uint32_t d = tmem + kColS + F::kTile / 2 * (u & 1);
+        const uint32_t d = tmem + kColS + F::kTile / 2 * (u % kSBufs);
 #pragma unroll
         for (int g = 0; g < F::kGroups; ++g, ++kc) {
           const int s = kc % F::kKSlots;
@@ -661,7 +662,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           }
           pair_commit(&k_empty[s], me);
         }
-        pair_commit(&s_full[u & 1], me);
+        pair_commit(&s_full[u % kSBufs], me);
         return true;
       };
       // All steps of one accumulator, then of the other: an MMA that adds to
@@ -699,13 +700,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (n == 0) continue;
         if (!(ok = wait(q_full, nq++))) break;
         if (!(ok = issue_qk(uc))) break;
-        if (n == 1) pair_commit(q_empty, me);
+        if (n > 1 && !(ok = issue_qk(uc + 1))) break;
+        if (n <= 2) pair_commit(q_empty, me);
         for (int t = 0; t < n; ++t, ++uc) {
-          // the scores of tile t + 1 go where tile t - 1's were: read before
+          // the scores of tile t + 2 go where tile t - 2's were: read before
           // its probabilities were handed over
-          if (t + 1 < n) {
-            if (!(ok = issue_qk(uc + 1))) break;
-            if (t + 2 == n) pair_commit(q_empty, me);
+          if (t + 2 < n) {
+            if (!(ok = issue_qk(uc + 2))) break;
+            if (t + 3 == n) pair_commit(q_empty, me);
           }
           if (t == 0 && nq > 1 && !(ok = wait(o_free, nq - 2))) break;
           if (!(ok = wait(&p_full[uc & 1], uc >> 1))) break;
@@ -815,10 +817,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           sc[g] = FP8 ? 1.f / sigma : 1.f;
         }
         constexpr int kRun = F::kMine / kBlocks;        // keys of one scale: 16 / 32
-        if (!(ok = all_ok(wait_for(&s_full[group], half_u & 1, abort_flag)))) break;
+        if (!(ok = all_ok(wait_for(&s_full[u % kSBufs], (u / kSBufs) & 1, abort_flag)))) break;
         tc_fence_after();
         float x[F::kMine];
-        const uint32_t s_at = lane_base + kColS + F::kTile / 2 * group;
+        const uint32_t s_at = lane_base + kColS + F::kTile / 2 * (u % kSBufs);
         if constexpr (FP8) tmem_ld_x64(s_at, reinterpret_cast<uint32_t *>(x));
         else tmem_ld_x32(s_at, reinterpret_cast<uint32_t *>(x));
         if (masked) {
