@@ -92,21 +92,23 @@ struct Fmt {
   static constexpr int kQBytes = 64 * kDqk * kEsz;         // 64 query rows: 36 / 72 KB
   static constexpr int kKRows = kTile / 2;                 // key rows of one CTA
   static constexpr int kKBox = kKRows * 128;
-  static constexpr int kGroups = FP8 ? 1 : 3;              // K slots that a tile takes
-  static constexpr int kGroupBytes = kKRows * kDqk * kEsz / kGroups;   // 36 / 12 KB
-  static constexpr int kGroupChunks = FP8 ? kLatChunks : 3;   // boxes of a slot (e4m3: and the rope's)
-  static constexpr int kKSlots = 2 * kGroups;              // two tiles
-  static constexpr int kVTok = kTile / 2;                  // keys of a V slot
+  static constexpr int kBoxes = FP8 ? 4 : 9;               // whole box columns of a cache row
+  // A slot is one load: what a loading warp does for one (wait, expect, issue)
+  // takes about 500 cycles, so three loads a tile set the pace themselves.
+  static constexpr int kKSlotBytes = kKRows * kDqk * kEsz; // 36 KB
+  static constexpr int kKSlots = 2;
+  static constexpr int kVTok = kPage;                      // keys of a V slot
   static constexpr int kVBoxes = 256 / kCols;              // 2 / 4
-  static constexpr int kVBox = kVTok * 128;                // 8 / 4 KB
-  static constexpr int kVSlotBytes = kVBoxes * kVBox;      // 16 KB
-  static constexpr int kVPer = 2;                          // slots of a tile
-  static constexpr int kVSlots = FP8 ? 5 : 4;
+  static constexpr int kVBox = kVTok * 128;                // 8 KB
+  static constexpr int kVSlotBytes = kVBoxes * kVBox;      // 16 / 32 KB
+  static constexpr int kVPer = kPages;                     // slots of a tile
+  static constexpr int kVSteps = kVTok * kEsz / 32;        // K steps of a slot: 2 / 4
+  static constexpr int kVSlots = FP8 ? 5 : 2;
   static constexpr int kPBytes = 64 * 128 * (FP8 ? 2 : 1); // hi and lo, or bf16: 128 bytes a row
   static constexpr int kPBufs = 2;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kQBytes;
-  static constexpr int kOffV = kOffK + kKSlots * kGroupBytes;
+  static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVSlotBytes;
   static constexpr int kOffX = kOffP + kPBufs * kPBytes;   // [2][128] maxima, [2][64] references, [256] sums
   static constexpr int kOffSeg = kOffX + (256 + 128 + 256) * 4;
@@ -114,7 +116,7 @@ struct Fmt {
   static constexpr int kBarBytes = 384;
   static constexpr int kSmem = kOffBars + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
-  static_assert(kGroupBytes % 1024 == 0 && kQBytes % 1024 == 0 && kKBox % 1024 == 0, "swizzled tiles");
+  static_assert(kKSlotBytes % 1024 == 0 && kQBytes % 1024 == 0 && kKBox % 1024 == 0, "swizzled tiles");
   // p' of a row's largest key after the reference moved, as a power of two
   static constexpr float kTop = FP8 ? 5.f : 0.f;
 };
@@ -558,17 +560,16 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         // this CTA's key rows: a page of the two, or half of the one
         const int blk = block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + (F::kPages - 1) * rank);
         const int row = blk < 0 ? no_row : blk * kPage + (2 - F::kPages) * F::kKRows * rank;
-        for (int g = 0; g < F::kGroups; ++g, ++kc) {
-          const int s = kc % F::kKSlots;
-          if (kc >= F::kKSlots &&
-              !(ok = wait_for(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
-            break;
-          if (lane == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kGroupBytes);
-            const uint32_t bar = peer_smem(&k_full[s], 0);
-            pair_load(sm_k + s * F::kGroupBytes, &tm_k, bar, 0, row, F::kGroupChunks * g);
-            if (FP8) pair_load(sm_k + s * F::kGroupBytes + 4 * F::kKBox, &tm_kr, bar, kLatent, row, 0);
-          }
+        const int s = kc % F::kKSlots;
+        if (kc >= F::kKSlots &&
+            !(ok = wait_for(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
+          break;
+        ++kc;
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kKSlotBytes);
+          const uint32_t bar = peer_smem(&k_full[s], 0);
+          pair_load(sm_k + s * F::kKSlotBytes, &tm_k, bar, 0, row, 0);
+          if (FP8) pair_load(sm_k + s * F::kKSlotBytes + 4 * F::kKBox, &tm_kr, bar, kLatent, row, 0);
         }
       }
     }
@@ -600,12 +601,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       fetch_blocks(pg, job, sg.b, F::kPages * sg.tile0);
       for (int t = 0; ok && t < sg.ntiles; ++t) {
         for (int v = 0; v < F::kVPer; ++v, ++vc) {
-          const int blk = block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + (F::kPages - 1) * v);
+          const int blk = block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + v);
           const int s = vc % F::kVSlots;
           if (vc >= F::kVSlots &&
               !(ok = wait_for(&v_empty[s], ((vc / F::kVSlots) - 1) & 1, abort_flag)))
             break;
-          const int row = blk < 0 ? no_row : blk * kPage + (2 - F::kPages) * F::kVTok * v;
+          const int row = blk < 0 ? no_row : blk * kPage;
           if (lane == 0) {
             mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
             load_3d_hint(sm_v + s * F::kVSlotBytes, &tm_v, &v_full[s], 0, row, F::kVBoxes * rank, policy);
@@ -636,32 +637,24 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       bool ok = true;
       auto issue_qk = [&](int u) -> bool {
         const uint32_t d = tmem + kColS + F::kTile / 2 * (u % kSBufs);
+        const int s = kc % F::kKSlots;
+        if (!wait(&k_full[s], kc / F::kKSlots)) return false;
+        ++kc;
+        tc_fence_after();
+        // one descriptor a slot; steps add to its address field (16-byte units)
+        const uint32_t kd = desc_lo(sm_k + s * F::kKSlotBytes, 16);
 #pragma unroll
-        for (int g = 0; g < F::kGroups; ++g, ++kc) {
-          const int s = kc % F::kKSlots;
-          if (!wait(&k_full[s], kc / F::kKSlots)) return false;
-          tc_fence_after();
-          // one descriptor a slot; steps add to its address field (16-byte units)
-          const uint32_t kd = desc_lo(sm_k + s * F::kGroupBytes, 16);
-          if constexpr (FP8) {
+        for (int k = 0; k < 4 * F::kBoxes; ++k)
+          pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (k >> 2) * 512 + (k & 3) * 2),
+                        desc_at<1024, kSwizzle128B>(kd + (k >> 2) * (F::kKBox / 16) + (k & 3) * 2),
+                        idesc_qk, k > 0, me);
+        if constexpr (FP8) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (k >> 2) * 512 + (k & 3) * 2),
-                            desc_at<1024, kSwizzle128B>(kd + (k >> 2) * (F::kKBox / 16) + (k & 3) * 2),
-                            idesc_qk, k > 0, me);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)       // the rope columns: rows of 64 bytes
-              pair_mma<FP8>(d, desc_at<512, kSwizzle64B>(qd + 4 * 512 + 2 * k),
-                            desc_at<512, kSwizzle64B>(kd + 4 * (F::kKBox / 16) + 2 * k), idesc_qk, 1, me);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 12; ++k)
-              pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (3 * g + (k >> 2)) * 512 + (k & 3) * 2),
-                            desc_at<1024, kSwizzle128B>(kd + (k >> 2) * (F::kKBox / 16) + (k & 3) * 2),
-                            idesc_qk, g + k > 0, me);
-          }
-          pair_commit(&k_empty[s], me);
+          for (int k = 0; k < 2; ++k)         // the rope columns: rows of 64 bytes
+            pair_mma<FP8>(d, desc_at<512, kSwizzle64B>(qd + 4 * 512 + 2 * k),
+                          desc_at<512, kSwizzle64B>(kd + 4 * (F::kKBox / 16) + 2 * k), idesc_qk, 1, me);
         }
+        pair_commit(&k_empty[s], me);
         pair_commit(&s_full[u % kSBufs], me);
         return true;
       };
@@ -676,8 +669,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             const int s = (vc + v) % F::kVSlots;
             const uint32_t vd = desc_lo(sm_v + s * F::kVSlotBytes, F::kVBox);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {  // 32 bytes of P: 32 e4m3 or 16 bf16 keys
-              const int step = 2 * v + kk;
+            for (int kk = 0; kk < F::kVSteps; ++kk) {   // 32 bytes of P: 32 e4m3 or 16 bf16 keys
+              const int step = F::kVSteps * v + kk;
               const uint32_t pa = pd + step * 2;
               const uint64_t bd = desc_at<1024, kSwizzle128B>(
                   vd + (FP8 ? j * F::kVBox + kk * 4096 : 2 * j * F::kVBox + kk * 2048) / 16);
@@ -1268,14 +1261,12 @@ int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArg
   // {columns of a 128-byte box row, rows, box columns}; the e4m3 rope columns
   // are half a box row and have maps of their own
   const uint64_t row_bytes = static_cast<uint64_t>(kDqk) * F::kEsz;
-  const uint64_t boxes = FP8 ? 4 : 9;
   const uint64_t strides[2] = {row_bytes, 128};
   const uint64_t kv_rows = static_cast<uint64_t>(a.num_blocks) * kPage;
   const uint64_t q_rows = static_cast<uint64_t>(a.B) * a.q_len * a.H;
-  const uint64_t kv_dims[3] = {F::kCols, kv_rows, boxes}, q_dims[3] = {F::kCols, q_rows, boxes};
+  const uint64_t kv_dims[3] = {F::kCols, kv_rows, F::kBoxes}, q_dims[3] = {F::kCols, q_rows, F::kBoxes};
   const uint64_t kvr_dims[3] = {kDqk, kv_rows, 1}, qr_dims[3] = {kDqk, q_rows, 1};
-  const uint32_t box_k[3] = {F::kCols, F::kKRows, F::kGroupChunks};
-  const uint32_t box_q[3] = {F::kCols, 64, static_cast<uint32_t>(boxes)};
+  const uint32_t box_k[3] = {F::kCols, F::kKRows, F::kBoxes}, box_q[3] = {F::kCols, 64, F::kBoxes};
   const uint32_t box_v[3] = {F::kCols, F::kVTok, F::kVBoxes}, box_r[3] = {64, 64, 1};
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, sw_r = CU_TENSOR_MAP_SWIZZLE_64B;
   CUtensorMap tk, tkr, tv, tq, tqr;
