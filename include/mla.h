@@ -453,7 +453,8 @@ int mla_decode_paged_scaled(const void *q, float q_scale, const void *kv_cache,
  *   j <= p and (j > p - window or j < sinks),     window >= 1, sinks >= 0.
  * The window is the same whether the keys before the queries are new tokens
  * or gathered context, so one call attends to both.  What a query does not
- * see does not reach its row, NaN and infinities included. */
+ * see does not reach its row, NaN and infinities included.
+ * B * H * ceil(max_q_len / 256) < 2^31 - 1024. */
 int mla_prefill_attn_window(const void *q, const void *k, const void *v,
                             const int32_t *cu_q, const int32_t *cu_k, int B,
                             int Tq, int Nk, int H, int max_q_len, int window,

@@ -33,31 +33,6 @@ namespace {
 
 using namespace sm100;
 
-// One lane of a converged warp, and MMAs that only this lane issues.
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(e));
-  return e;
-}
-__device__ __forceinline__ void mma_f16_ss_if(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                              uint32_t acc, uint32_t me) {
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
-               "l"(b), "r"(idesc), "r"(acc), "r"(me) : "memory");
-}
-__device__ __forceinline__ void mma_f16_ts_if(uint32_t d, uint32_t a_tmem, uint64_t b,
-                                              uint32_t idesc, uint32_t acc, uint32_t me) {
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-               "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(me) : "memory");
-}
-__device__ __forceinline__ void mma_commit_if(uint64_t *bar, uint32_t me) {
-  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-               ::"r"(smem_u32(bar)), "r"(me) : "memory");
-}
-
 // L2 prefetch of one tensor-map box (no shared memory, no completion).
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
@@ -88,8 +63,6 @@ struct PrefillArgs {
   float scale_log2;
   __nv_bfloat16 *out;
   float *lse;
-  int window, sinks;             // WIN only
-  const __nv_bfloat16 *q, *k, *v;   // WIN only: the rows as plain pointers
 };
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -106,39 +79,8 @@ __device__ __forceinline__ int tiles_for(int row0, int rows, int nq, int nk, int
   return (key_end + kBN - 1) / kBN;
 }
 
-// The key tiles of a query tile pair under a sliding window with sinks: the
-// sinks' tiles, then those of the window; only the list's tiles are loaded.
-struct TileList {
-  int sink_tiles, lo_tile;
-  __device__ __forceinline__ int at(int u) const { return u < sink_tiles ? u : u - sink_tiles + lo_tile; }
-};
-
-// One row's 32 output columns from `c`, from the definition: taken when the
-// products over whole tiles gave NaN or infinity, which a value row that
-// this query does not see brings about too (0 times it).  p = 2^(s - m) over
-// the keys that the query sees, [0, sinks) and [lo, lim).
-__device__ __noinline__ void window_row(const __nv_bfloat16 *q, const __nv_bfloat16 *k,
-                                        const __nv_bfloat16 *v, int64_t k_stride, int64_t v_stride,
-                                        int sinks, int lo, int lim, float scale_log2, float m,
-                                        float *o) {
-  for (int e = 0; e < 32; ++e) o[e] = 0.f;
-  for (int j = 0; j < lim; ++j) {
-    if (j >= sinks && j < lo) {
-      j = lo - 1;
-      continue;
-    }
-    float s = 0.f;
-    for (int d = 0; d < kDq; ++d)
-      s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[j * k_stride + d]), s);
-    const float p = ex2(fmaf(s, scale_log2, -m));
-    for (int e = 0; e < 32; ++e) o[e] = fmaf(p, __bfloat162float(v[j * v_stride + e]), o[e]);
-  }
-}
-
-// WIN: causal with a sliding window and sinks (mla_prefill_attn_window).
 // 10 warps: blocks are given registers in units of four warps, so 12 warps'
 // worth (at most 168 registers a thread)
-template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                const __grid_constant__ CUtensorMap tm_k,
@@ -154,17 +96,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
     const int row0 = (qp * kQT + g) * kBM;
     rows_g[g] = max(0, min(kBM, nq - row0));
     nt_g[g] = tiles_for(row0, rows_g[g], nq, nk, args.causal);
-  }
-  TileList list{0, 0};
-  if constexpr (WIN) {
-    const int first = qp * kQT * kBM + nk - nq;            // the first query's position
-    const int lo = max(0, first - args.window + 1);
-    list.lo_tile = lo / kBN;
-    list.sink_tiles = min((min(args.sinks, lo) + kBN - 1) / kBN, list.lo_tile);
-    // tiles between the sinks' and the window's are left out
-#pragma unroll
-    for (int g = 0; g < kQT; ++g)
-      if (nt_g[g] > 0) nt_g[g] -= list.lo_tile - list.sink_tiles;
   }
   const int ntiles = max(nt_g[0], nt_g[1]);
 
@@ -183,7 +114,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
   uint64_t *q_full = pv_done + kQT, *drain = q_full + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0), lane = lane_id();
+  const int warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kKStages; ++s) {
@@ -232,13 +163,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (u >= kKStages && !mbar_wait(&k_empty[s], ((u / kKStages) - 1) & 1, abort_flag))
         return false;
       mbar_arrive_expect_tx(&k_full[s], kKBytes);
-      const int row = k0 + list.at(u) * kBN;
+      const int row = k0 + u * kBN;
       for (int d = 0; d < 3; ++d)
         tma_load_3d(sm_k + s * kKBytes + d * kBox, &tm_k, &k_full[s], 64 * d, h, row);
       // the tiles further ahead go to L2 now (the rings hold one or two)
       for (int a = (u == 0 ? 1 : kPrefetchAhead); a <= kPrefetchAhead; ++a) {
         if (u + a < ntiles) {
-          const int prow = k0 + list.at(u + a) * kBN;
+          const int prow = k0 + (u + a) * kBN;
           for (int d = 0; d < 3; ++d) tma_prefetch_3d(&tm_k, 64 * d, h, prow);
           for (int d = 0; d < 2; ++d) tma_prefetch_3d(&tm_v, 64 * d, h, prow);
         }
@@ -248,7 +179,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
     auto load_v = [&](int u) -> bool {
       if (u >= 1 && !mbar_wait(v_empty, (u - 1) & 1, abort_flag)) return false;
       mbar_arrive_expect_tx(v_full, kVBytes);
-      const int row = k0 + list.at(u) * kBN;
+      const int row = k0 + u * kBN;
       for (int d = 0; d < 2; ++d) tma_load_3d(sm_v + d * kBox, &tm_v, v_full, 64 * d, h, row);
       return true;
     };
@@ -269,62 +200,55 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (vt > 0) mbar_wait(v_full, (vt - 1) & 1, &no_abort);
       if (ntiles > 0) mbar_wait(q_full, 0, &no_abort);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && lane == 0) {
     // ----------------------------------------------------------- MMA
-    // The whole warp runs this converged, with one lane's MMAs predicated on:
-    // descriptors then stay in uniform registers.
-    const uint32_t me = elect_one();
     const uint32_t idesc_qk = idesc_bf16(128, kBN, false, false);
     const uint32_t idesc_pv = idesc_bf16(128, kDv, false, true);
-    auto wait = [&](uint64_t *bar, int phase) -> bool {
-      return __all_sync(0xffffffffu, mbar_test(bar, phase & 1) || mbar_wait(bar, phase & 1, abort_flag));
-    };
-    bool ok = ntiles == 0 || wait(q_full, 0);
+    bool ok = ntiles == 0 || mbar_wait(q_full, 0, abort_flag);
     auto issue_qk = [&](int g, int t) {
       const uint32_t qa = smem_u32(sm_q + g * kQBytes);
       const uint32_t kb = smem_u32(sm_k + (t % kKStages) * kKBytes);
       const uint32_t d = tmem + 256 * g;
 #pragma unroll
       for (int k = 0; k < kDq / 16; ++k)
-        mma_f16_ss_if(d, sdesc(qa + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSwizzle128B),
-                      sdesc(kb + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSwizzle128B),
-                      idesc_qk, k > 0, me);
-      mma_commit_if(&s_full[g], me);
+        mma_f16_ss(d, sdesc(qa + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSwizzle128B),
+                   sdesc(kb + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSwizzle128B),
+                   idesc_qk, k > 0);
+      mma_commit(&s_full[g]);
     };
     auto issue_pv = [&](int g, int t) {
       const uint32_t vb = smem_u32(sm_v);
 #pragma unroll
       for (int kk = 0; kk < kBN / 16; ++kk)
-        mma_f16_ts_if(tmem + 256 * g + 128, tmem + 256 * g + 8 * kk,
-                      sdesc(vb + kk * 2048, kBox, 1024, kSwizzle128B), idesc_pv,
-                      (t > 0 || kk > 0) ? 1u : 0u, me);
-      mma_commit_if(&pv_done[g], me);
+        mma_f16_ts(tmem + 256 * g + 128, tmem + 256 * g + 8 * kk,
+                   sdesc(vb + kk * 2048, kBox, 1024, kSwizzle128B), idesc_pv,
+                   (t > 0 || kk > 0) ? 1u : 0u);
+      mma_commit(&pv_done[g]);
     };
     // Tile 0's QKs; then per tile t: P.V_A(t), QK_A(t+1), P.V_B(t),
     // QK_B(t+1).  QK_g(t+1) overwrites S_g after P.V_g(t) has read P_g from
     // the same columns (the tensor core runs one thread's MMAs in order).
-    if (ok && ntiles > 0 && (ok = wait(&k_full[0], 0))) {
+    if (ok && ntiles > 0 && (ok = mbar_wait(&k_full[0], 0, abort_flag))) {
       tc_fence_after();
-#pragma unroll
       for (int g = 0; g < kQT; ++g)
         if (nt_g[g] > 0) issue_qk(g, 0);
-      mma_commit_if(&k_empty[0], me);
+      mma_commit(&k_empty[0]);
     }
     for (int t = 0; ok && t < ntiles; ++t) {
-      if (!(ok = wait(v_full, t))) break;
+      if (!(ok = mbar_wait(v_full, t & 1, abort_flag))) break;
       bool k_next = false;   // K(t+1) has landed
-#pragma unroll
       for (int g = 0; g < kQT; ++g) {
-        if (!ok) break;
         if (t < nt_g[g]) {
-          if (!(ok = wait(&p_full[g], t))) break;
+          if (!(ok = mbar_wait(&p_full[g], t & 1, abort_flag))) break;
           tc_fence_after();
           issue_pv(g, t);
         }
-        if (g == kQT - 1) mma_commit_if(v_empty, me);   // both P.Vs of tile t issued
+        if (g == kQT - 1) mma_commit(v_empty);   // both P.Vs of tile t issued
         if (t + 1 < nt_g[g]) {
           if (!k_next) {
-            if (!(ok = wait(&k_full[(t + 1) % kKStages], (t + 1) / kKStages))) break;
+            if (!(ok = mbar_wait(&k_full[(t + 1) % kKStages], ((t + 1) / kKStages) & 1,
+                                 abort_flag)))
+              break;
             tc_fence_after();
             k_next = true;
           }
@@ -332,10 +256,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
       }
       if (!ok) break;
-      if (k_next) mma_commit_if(&k_empty[(t + 1) % kKStages], me);   // both QKs of tile t+1 issued
+      if (k_next) mma_commit(&k_empty[(t + 1) % kKStages]);   // both QKs of tile t+1 issued
     }
     if (!ok) {
-      mma_commit_if(drain, me);
+      mma_commit(drain);
       volatile int no_abort = 0;
       mbar_wait(drain, 0, &no_abort);
     }
@@ -348,7 +272,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
     const uint32_t col_s = 256 * g, col_o = 256 * g + 128;
     const int i = (qp * kQT + g) * kBM + r;         // query index in request
     const int lim = args.causal ? min(nk, i + nk - nq + 1) : nk;
-    const int wlo = WIN ? lim - args.window : 0;    // the window's first key
     const int n = nt_g[g];
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -364,14 +287,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[c + k] = __uint_as_float(v[k]);
       }
-      if constexpr (WIN) {
-        const int key0 = list.at(t) * kBN;
-        if (key0 + kBN > lim || (key0 < wlo && key0 + kBN > args.sinks)) {
-          const int e = lim - key0, a = wlo - key0, z = args.sinks - key0;
-#pragma unroll
-          for (int k = 0; k < kBN; ++k) x[k] = k < e && (k >= a || k < z) ? x[k] : -INFINITY;
-        }
-      } else if ((t + 1) * kBN > lim) {
+      if ((t + 1) * kBN > lim) {
 #pragma unroll
         for (int k = 0; k < kBN; ++k) x[k] = t * kBN + k < lim ? x[k] : -INFINITY;
       }
@@ -437,26 +353,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
     if (ok && rows_g[g] > 0) {
       const bool row_ok = r < rows_g[g];
       const int64_t orow = static_cast<int64_t>(q0 + i) * args.H + h;
-      const bool empty = WIN ? l == 0.f : !(l > 0.f);
+      const bool empty = !(l > 0.f);
       const float inv = empty ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int c = 0; c < kDv; c += 32) {
         uint32_t o[32];
         if (n > 0) tmem_ld_x32(lane_base + col_o + c, o);
-        if constexpr (WIN) {
-          float nan = 0.f;   // NaN if a column is not finite
-#pragma unroll
-          for (int k = 0; k < 32; ++k) nan = fmaf(__uint_as_float(o[k]), 0.f, nan);
-          // (a row whose own scores are not finite, l NaN, stays NaN)
-          if (n > 0 && row_ok && l > 0.f && nan != 0.f) {
-            float row[32];
-            const int64_t ks = static_cast<int64_t>(args.H) * kDq, vs = static_cast<int64_t>(args.H) * kDv;
-            window_row(args.q + orow * kDq, args.k + k0 * ks + h * kDq, args.v + k0 * vs + h * kDv + c,
-                       ks, vs, args.sinks, wlo, lim, args.scale_log2, m, row);
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(row[k]);
-          }
-          __syncwarp();
-        }
         if (!row_ok) continue;
         uint4 *dst = reinterpret_cast<uint4 *>(args.out + orow * kDv + c);
 #pragma unroll
@@ -487,11 +389,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 using namespace mla;
 
-namespace {
-
-int check_prefill(const void *q, const void *k, const void *v, const int32_t *cu_q,
-                  const int32_t *cu_k, int B, int Tq, int Nk, int H, int max_q_len,
-                  float sm_scale, const void *out, const float *lse) {
+extern "C" int mla_prefill_attn(const void *q, const void *k, const void *v,
+                                const int32_t *cu_q, const int32_t *cu_k,
+                                int B, int Tq, int Nk, int H, int max_q_len,
+                                int causal, float sm_scale, void *out,
+                                float *lse, mla_stream_t stream) {
   if (B < 1 || Tq < 0 || Nk < 0 || H < 1 || H > 65535 || max_q_len < 0 || B > 65535)
     return MLA_ERR_INVALID_ARG;
   if (!(sm_scale > 0.f) || !(sm_scale < INFINITY)) return MLA_ERR_INVALID_ARG;
@@ -499,77 +401,38 @@ int check_prefill(const void *q, const void *k, const void *v, const int32_t *cu
   if (!q || !k || !v || !cu_q || !cu_k || !out || !lse) return MLA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
     return MLA_ERR_INVALID_ARG;
-  return MLA_OK;
-}
-
-template <bool WIN>
-int launch_prefill(const void *q, const void *k, const void *v, int B, int Tq, int Nk,
-                   int max_q_len, const PrefillArgs &a, mla_stream_t stream) {
-  const int H = a.H;
   int *err = device_error_word();
   if (!err) return MLA_ERR_CUDA;
   CUtensorMap tq, tk, tv;
   const uint32_t box[3] = {64, 1, 128};
+  {
+    const uint64_t dims[3] = {kDq, static_cast<uint64_t>(H), static_cast<uint64_t>(Tq)};
+    const uint64_t strides[2] = {kDq * 2, static_cast<uint64_t>(H) * kDq * 2};
+    if (!make_tmap(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return MLA_ERR_CUDA;
+  }
   const uint64_t nk_rows = Nk > 0 ? static_cast<uint64_t>(Nk) : 1;
-  auto encode = [&](CUtensorMap *map, const void *base, int width, uint64_t rows) {
-    const uint64_t dims[3] = {static_cast<uint64_t>(width), static_cast<uint64_t>(H), rows};
-    const uint64_t strides[2] = {static_cast<uint64_t>(width) * 2,
-                                 static_cast<uint64_t>(H) * width * 2};
-    return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
-                     CU_TENSOR_MAP_SWIZZLE_128B);
-  };
-  if (!encode(&tq, q, kDq, static_cast<uint64_t>(Tq)) || !encode(&tk, k, kDq, nk_rows) ||
-      !encode(&tv, v, kDv, nk_rows))
-    return MLA_ERR_CUDA;
-  if (cudaFuncSetAttribute(prefill_kernel<WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  {
+    const uint64_t dims[3] = {kDq, static_cast<uint64_t>(H), nk_rows};
+    const uint64_t strides[2] = {kDq * 2, static_cast<uint64_t>(H) * kDq * 2};
+    if (!make_tmap(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k, dims, strides, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return MLA_ERR_CUDA;
+  }
+  {
+    const uint64_t dims[3] = {kDv, static_cast<uint64_t>(H), nk_rows};
+    const uint64_t strides[2] = {kDv * 2, static_cast<uint64_t>(H) * kDv * 2};
+    if (!make_tmap(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v, dims, strides, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return MLA_ERR_CUDA;
+  }
+  PrefillArgs a{cu_q, cu_k, H, causal ? 1 : 0, sm_scale * 1.4426950408889634f,
+                static_cast<__nv_bfloat16 *>(out), lse};
+  if (cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
   dim3 grid((max_q_len + kQT * kBM - 1) / (kQT * kBM), H, B);
-  prefill_kernel<WIN><<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, a, err);
+  prefill_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, a, err);
   return launch_status();
-}
-
-}  // namespace
-
-extern "C" int mla_prefill_attn(const void *q, const void *k, const void *v,
-                                const int32_t *cu_q, const int32_t *cu_k,
-                                int B, int Tq, int Nk, int H, int max_q_len,
-                                int causal, float sm_scale, void *out,
-                                float *lse, mla_stream_t stream) {
-  const int st = check_prefill(q, k, v, cu_q, cu_k, B, Tq, Nk, H, max_q_len, sm_scale, out, lse);
-  if (st != MLA_OK || Tq == 0 || max_q_len == 0) return st;
-  PrefillArgs a{};
-  a.cu_q = cu_q;
-  a.cu_k = cu_k;
-  a.H = H;
-  a.causal = causal ? 1 : 0;
-  a.scale_log2 = sm_scale * 1.4426950408889634f;
-  a.out = static_cast<__nv_bfloat16 *>(out);
-  a.lse = lse;
-  return launch_prefill<false>(q, k, v, B, Tq, Nk, max_q_len, a, stream);
-}
-
-extern "C" int mla_prefill_attn_window(const void *q, const void *k, const void *v,
-                                       const int32_t *cu_q, const int32_t *cu_k, int B, int Tq,
-                                       int Nk, int H, int max_q_len, int window, int sinks,
-                                       float sm_scale, void *out, float *lse,
-                                       mla_stream_t stream) {
-  if (window < 1 || sinks < 0) return MLA_ERR_INVALID_ARG;
-  const int st = check_prefill(q, k, v, cu_q, cu_k, B, Tq, Nk, H, max_q_len, sm_scale, out, lse);
-  if (st != MLA_OK || Tq == 0 || max_q_len == 0) return st;
-  PrefillArgs a{};
-  a.cu_q = cu_q;
-  a.cu_k = cu_k;
-  a.H = H;
-  a.causal = 1;
-  a.scale_log2 = sm_scale * 1.4426950408889634f;
-  a.out = static_cast<__nv_bfloat16 *>(out);
-  a.lse = lse;
-  // (no request has 2^30 keys: sums with these stay within 32 bits)
-  a.window = window < (1 << 30) ? window : 1 << 30;
-  a.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
-  a.q = static_cast<const __nv_bfloat16 *>(q);
-  a.k = static_cast<const __nv_bfloat16 *>(k);
-  a.v = static_cast<const __nv_bfloat16 *>(v);
-  return launch_prefill<true>(q, k, v, B, Tq, Nk, max_q_len, a, stream);
 }
