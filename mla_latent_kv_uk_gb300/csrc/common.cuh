@@ -68,4 +68,9 @@ __device__ __forceinline__ void raise_error(int *err, int bits) {
   if (err) atomicOr(err, bits);
 }
 
+// The lowest n of 64 bits (none for n <= 0).
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
+}
+
 }  // namespace mla

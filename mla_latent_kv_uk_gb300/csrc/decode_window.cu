@@ -817,9 +817,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if constexpr (FP8) tmem_ld_x64(s_at, reinterpret_cast<uint32_t *>(x));
         else tmem_ld_x32(s_at, reinterpret_cast<uint32_t *>(x));
         if (masked) {
-          const int e = p - key0, a = wlo - key0, z = args.sinks - key0;
+          const uint64_t seen =
+              low_bits(p - key0 + 1) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0));
 #pragma unroll
-          for (int k = 0; k < F::kMine; ++k) x[k] = k <= e && (k >= a || k < z) ? x[k] : -INFINITY;
+          for (int k = 0; k < F::kMine; ++k) x[k] = seen & (uint64_t(1) << k) ? x[k] : -INFINITY;
         }
         float top = -INFINITY;
 #pragma unroll

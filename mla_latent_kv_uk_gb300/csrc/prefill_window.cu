@@ -16,7 +16,7 @@
 //     P_g(t) V in the same columns, so a softmax's latency is on the path
 //     twice a tile;
 //   * query tile B leaves out the key tile that only A's window still holds;
-//   * results leave in 32-byte stores, whole sectors.
+//   * results leave 64 bytes of a row at a time.
 // The MMA warp runs converged with one elected lane (descriptors stay in
 // uniform registers).
 //
@@ -43,6 +43,7 @@ constexpr int kDq = 192, kDv = 128;
 constexpr int kBox = 128 * 128;                  // 128 rows x 64 bf16
 constexpr int kQBytes = 3 * kBox, kKBytes = 3 * kBox, kVBytes = 2 * kBox;
 constexpr int kKStages = 2;
+constexpr int kAhead = 4;                        // key tiles fetched into L2 ahead of their loads
 constexpr int kOffK = kQT * kQBytes;
 constexpr int kOffV = kOffK + kKStages * kKBytes;
 constexpr int kOffX = kOffV + kVBytes;           // [2][256] row maxima, then sums
@@ -60,7 +61,6 @@ struct Args {
   float scale_log2;
   __nv_bfloat16 *out;
   float *lse;
-  int wide;                                      // out starts on 32 bytes
   const __nv_bfloat16 *q, *k, *v;
   int *err;
 };
@@ -106,6 +106,10 @@ struct Item {
   __device__ __forceinline__ bool takes(int g, int t) const { return t < nt[g] && t != skip[g]; }
 };
 
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z) : "memory");
+}
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -220,6 +224,30 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
     if (lane == 0) {
       bool ok = true;
       int kc = 0, n = 0;                       // K tiles, items with tiles so far
+      // Keys and values of the tiles ahead, the next item's too, go to L2: the
+      // single V tile is loaded while its products wait, which hides the way
+      // from L2 but not the one from DRAM.
+      Item nx;
+      int ni = blockIdx.x, nt = 0, fetched = 0;
+      bool open = false;
+      auto fetch = [&]() {
+        while (!open) {
+          if (ni >= args.items) return;
+          open = nx.load(args, ni) && nx.ntiles > 0;
+          nt = 0;
+          if (!open) ni += gridDim.x;
+        }
+        const int row = nx.k0 + nx.tile(nt) * kBN;
+        if (fetched > 0) {                     // (the very first tile is loaded at once)
+          for (int d = 0; d < 3; ++d) prefetch_3d(&tm_k, 64 * d, nx.h, row);
+          for (int d = 0; d < 2; ++d) prefetch_3d(&tm_v, 64 * d, nx.h, row);
+        }
+        ++fetched;
+        if (++nt == nx.ntiles) {
+          open = false;
+          ni += gridDim.x;
+        }
+      };
       for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
         Item it;
         if (!it.load(args, i) || it.ntiles == 0) continue;
@@ -239,6 +267,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
           for (int d = 0; d < 3; ++d)
             tma_load_3d(sm_k + s * kKBytes + d * kBox, &tm_k, &k_full[s], 64 * d, it.h,
                         it.k0 + it.tile(t) * kBN);
+          for (int e = kc == 0 ? -kAhead : 0; e <= 0; ++e) fetch();
         }
       }
       if (*abort_flag) {
@@ -387,12 +416,16 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
         // 32 scores at a time, read once for the maximum and once for the
         // exponentials: 64 at once would not fit the 96 registers that 20
         // warps have
+        // (a bit for each of the 64 keys that this query sees: three compares
+        // for each score made a masked tile cost twice an unmasked one)
+        const uint64_t seen = masked ? low_bits(lim - key0) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0))
+                                     : ~uint64_t(0);
         auto load = [&](int h, float *x) {
           tmem_ld_x32(lane_base + col_s + 32 * h, reinterpret_cast<uint32_t *>(x));
           if (masked) {
-            const int e = lim - key0 - 32 * h, a = wlo - key0 - 32 * h, z = args.sinks - key0 - 32 * h;
+            const uint32_t w = static_cast<uint32_t>(seen >> (32 * h));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = k < e && (k >= a || k < z) ? x[k] : -INFINITY;
+            for (int k = 0; k < 32; ++k) x[k] = w & (1u << k) ? x[k] : -INFINITY;
           }
         };
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -497,24 +530,36 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
           for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(row[k]);
         }
         __syncwarp();
-        if (row_ok) {
-          __nv_bfloat16 *dst = args.out + orow * kDv + col;
-          auto f = [&](int k) { return __uint_as_float(o[k]) * inv; };
+        // four lanes turn their rows' four 16-byte chunks round, so that a
+        // store covers 64 bytes of eight rows and not 16 of 32 (which took
+        // 4000 cycles an item)
+        uint4 w[4];
+        auto f = [&](int k) { return __uint_as_float(o[k]) * inv; };
 #pragma unroll
-          for (int k = 0; k < 32; k += 16) {
-            uint32_t w[8];
+        for (int ch = 0; ch < 4; ++ch)
+          w[ch] = make_uint4(bf16x2_rn(f(8 * ch), f(8 * ch + 1)), bf16x2_rn(f(8 * ch + 2), f(8 * ch + 3)),
+                             bf16x2_rn(f(8 * ch + 4), f(8 * ch + 5)), bf16x2_rn(f(8 * ch + 6), f(8 * ch + 7)));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = bf16x2_rn(f(k + 2 * e), f(k + 2 * e + 1));
-            if (args.wide) {
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + k),
-                           "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
-                           "r"(w[6]), "r"(w[7]) : "memory");
-            } else {
-              reinterpret_cast<uint4 *>(dst + k)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4 *>(dst + k)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+        for (int s = 1; s < 4; s <<= 1) {
+          const bool up = lane & s;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            if (ch & s) continue;
+            uint4 give = up ? w[ch] : w[ch | s];
+            give.x = __shfl_xor_sync(0xffffffffu, give.x, s);
+            give.y = __shfl_xor_sync(0xffffffffu, give.y, s);
+            give.z = __shfl_xor_sync(0xffffffffu, give.z, s);
+            give.w = __shfl_xor_sync(0xffffffffu, give.w, s);
+            if (up) w[ch] = give;
+            else w[ch | s] = give;
           }
         }
+        const int r0 = quarter * 32 + (lane & ~3);
+        __nv_bfloat16 *dst = args.out + ((static_cast<int64_t>(it.q0) + it.row0 + g * kBM + r0) * args.H + it.h) * kDv +
+                             col + 8 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (r0 + k < rows) *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(k) * args.H * kDv) = w[k];
       }
       if (row_ok && sub == 0)
         args.lse[orow] = empty ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
@@ -577,7 +622,6 @@ extern "C" int mla_prefill_attn_window(const void *q, const void *k, const void 
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.lse = lse;
-  a.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.k = static_cast<const __nv_bfloat16 *>(k);
   a.v = static_cast<const __nv_bfloat16 *>(v);
