@@ -13,13 +13,22 @@
 // Blocks of the cache: a block's new scale depends on all its new rows, and
 // its old rows may have to follow it, so one CTA owns a block: that of the
 // block's first token in the call.  It finds the other members by reading
-// the slot list; CTAs of other members leave at once, most of them on seeing
-// that the token before them has the same block.
+// the slot list; most tokens are passed over on seeing that the token before
+// them has the same block.
+//
+// What bounds it: a step (32 tokens, 128 heads: 1 MB) is one chain of loads
+// (slots, rows), arithmetic and stores, 4.2 us with the launch.  A chunk moves
+// its queries, read and written: 63 MB in 15.6 us, 4.1 TB/s of the 6.8 that a
+// copy reaches, the first 3 us of which look at slots and fill the memory
+// pipes.  Measured on the way there: a CTA for each token, that looks at the
+// slots and leaves, 18.5 us; rows read again for their codes instead of kept,
+// 15.8; three CTAs to an SM in 40 registers, 16.0 (spilled rows).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <climits>
 #include <cmath>
 
 #include "common.cuh"
@@ -28,10 +37,15 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kHeadsPerCta = 128;   // query heads that a CTA rotates: four 16-byte chunks a thread
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kQueryRows = 256;     // (token, head) rows that a CTA rotates: four 16-byte chunks a thread
+constexpr int kMinHeadShift = 4, kMaxHeadShift = 7, kMaxTokens = kQueryRows >> kMinHeadShift;
 constexpr int kPairs = kRope / 2;
 constexpr int kMinExp = -100;
+// CTAs that look for blocks (under two to an SM): one for each token up to
+// these, then as many tokens to a CTA as that takes
+constexpr int kAppendCtas = 256, kMaxPerCta = 64;
+constexpr int kAhead = 4;           // slots that a thread has on their way
 
 // theta_i / 2pi as a fraction of 2^64
 struct Turns {
@@ -52,6 +66,9 @@ struct AppendArgs {
   float *scales;
   int sb_shift;                     // log2(scale_block)
   int64_t num_slots;
+  unsigned append_ctas;             // CTAs for the cache rows, per_cta tokens each
+  int per_cta;
+  int groups, head_shift;           // query items: 2^head_shift heads of a few tokens
   int *err;
 };
 
@@ -70,19 +87,25 @@ __device__ __forceinline__ uint32_t rot_pair(float a, float b, float c, float s)
   return sm100::bf16x2_rn(fmaf(a, c, -(b * s)), fmaf(a, s, b * c));
 }
 
-// largest |x| of a pair of bf16 values that is finite
-__device__ __forceinline__ float finite_max(float m, uint32_t w) {
-  const float a = fabsf(bf_lo(w)), b = fabsf(bf_hi(w));
-  if (a < INFINITY) m = fmaxf(m, a);
-  if (b < INFINITY) m = fmaxf(m, b);
-  return m;
+// Maxima of |x| over the finite values of both halves of bf16 words, as 16-bit
+// integers 0x80 above their bits: that makes infinity and NaN negative.
+constexpr uint32_t kMaxStart = 0x00800080u;
+__device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t w) {
+  return __vmaxs2(m, (w & 0x7FFF7FFFu) + kMaxStart);
 }
 
-// two bf16 values -> two e4m3 codes of value / scale (a caller's scale may be
-// no power of two, so this divides)
-__device__ __forceinline__ uint32_t codes2(uint32_t w, float scale) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(bf_lo(w) / scale, bf_hi(w) / scale), __NV_SATFINITE,
-                                  __NV_E4M3);
+// two bf16 values -> two e4m3 codes of value / scale.  inv: 1 / scale where
+// that is exact and so is the same; a caller's scale may be no power of two
+__device__ __forceinline__ uint32_t codes2(uint32_t w, float scale, float inv) {
+  float2 f = make_float2(bf_lo(w), bf_hi(w));
+  if (inv != 0.f) {
+    f.x *= inv;
+    f.y *= inv;
+  } else {
+    f.x /= scale;
+    f.y /= scale;
+  }
+  return __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
 }
 
 // four e4m3 codes -> the codes of value * ratio
@@ -108,16 +131,20 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// One warp: token t's k_pe, rotated and stored to k_out; lane i returns its
-// pair i as (a, b) in the low and high half of the word.
-__device__ __forceinline__ uint32_t rotate_k(const AppendArgs &p, const Turns &turns, int t, int lane) {
+// Token t's k_pe as one warp holds it: lane i has pair i as (a, b) in the low
+// and high half of a word.
+__device__ __forceinline__ uint32_t load_k(const AppendArgs &p, int t, int lane) {
   const uint16_t *k = reinterpret_cast<const uint16_t *>(p.k_pe + t * p.k_st);
+  if (!p.half_layout) return reinterpret_cast<const uint32_t *>(k)[lane];
+  return k[lane] | (static_cast<uint32_t>(k[lane + kPairs]) << 16);
+}
+
+// Rotates it by the token's position and stores it to k_out; returns the pairs.
+__device__ __forceinline__ uint32_t store_k(const AppendArgs &p, unsigned long long per_pos, int t,
+                                            int pos, uint32_t w, int lane) {
   uint16_t *o = reinterpret_cast<uint16_t *>(p.k_out + t * p.ko_st);
-  uint32_t w;
-  if (!p.half_layout) w = reinterpret_cast<const uint32_t *>(k)[lane];
-  else w = k[lane] | (static_cast<uint32_t>(k[lane + kPairs]) << 16);
   float s, c;
-  turn(p.positions[t], turns.per_pos[lane], s, c);
+  turn(pos, per_pos, s, c);
   w = rot_pair(bf_lo(w), bf_hi(w), c, s);
   __syncwarp();   // in place: every lane has read its pair
   if (!p.half_layout) {
@@ -129,104 +156,127 @@ __device__ __forceinline__ uint32_t rotate_k(const AppendArgs &p, const Turns &t
   return w;
 }
 
-// kRows: rows of a block that one warp keeps (scale_block / 8)
+__device__ __forceinline__ void rotate_k(const AppendArgs &p, unsigned long long per_pos, int t,
+                                         int lane) {
+  store_k(p, per_pos, t, p.positions[t], load_k(p, t, lane), lane);
+}
+
+// The slots of tokens u, u + kThreads, ..
+__device__ __forceinline__ void load_slots(const AppendArgs &p, int64_t u, int (&s)[kAhead]) {
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i, u += kThreads) s[i] = u < p.T ? __ldg(p.slots + u) : -1;
+}
+
+// The block g of token t, whose token before is in another block.  A warp keeps
+// its kRows rows in registers from the maximum to the store: every load of the
+// block is on its way at once, and with the queries' traffic beside it a load
+// takes microseconds.  ahead: the first kAhead slots of this thread.
 template <int kRows>
-__device__ void append_block(const AppendArgs &p, const Turns &turns, int t) {
+__device__ __forceinline__ void append_block(const AppendArgs &p, unsigned long long per_pos, int t,
+                                             int g, const int (&ahead)[kAhead]) {
   constexpr int kBlock = kRows * kWarps;
   __shared__ int row_t[kBlock];       // the token that a row gets, or -1
   __shared__ int first, members;
   __shared__ uint32_t amax_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t slot = p.slots[t];
-  if (slot < 0 || slot >= p.num_slots) {   // nothing to store
-    if (warp == 0) rotate_k(p, turns, t, lane);
-    if (tid == 0 && slot >= p.num_slots) raise_error(p.err, MLA_DEVERR_BLOCK_ID);
-    return;
-  }
-  const int g = static_cast<int>(slot >> p.sb_shift);
   auto same = [&](int s) { return s >= 0 && s < p.num_slots && (s >> p.sb_shift) == g; };
-  if (t > 0 && same(p.slots[t - 1])) return;
   if (tid < kBlock) row_t[tid] = -1;
   if (tid == 0) {
     first = t;
     members = 0;
     amax_s = 0;
   }
+  const float held = p.scales[g];
   __syncthreads();
-  for (int u = tid; u < p.T; u += kThreads) {
-    const int s = p.slots[u];
-    if (same(s)) {
+  int s[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) s[i] = ahead[i];
+  for (int64_t u0 = tid;;) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!same(s[i])) continue;
+      const int u = static_cast<int>(u0) + i * kThreads;
       if (u < t) first = 0;   // any member before t: its CTA, or another's, owns the block
-      atomicMax(&row_t[s & (kBlock - 1)], u);
+      atomicMax(&row_t[s[i] & (kBlock - 1)], u);
       atomicAdd(&members, 1);
     }
+    u0 += kAhead * kThreads;
+    if (u0 >= p.T) break;
+    load_slots(p, u0, s);
   }
   __syncthreads();
   if (first != t) return;
 
-  // new rows: kept in registers from the maximum to the store
   uint4 c[kRows][2];
   uint32_t kp[kRows];
-  int kept = 0;
-  float m = 0.f;
+  int pos[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const int u = row_t[warp + r * kWarps];
     if (u < 0) continue;
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.kv_c + u * p.c_st);
-    c[r][0] = src[lane];
-    c[r][1] = src[lane + 32];
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.kv_c + u * p.c_st) + lane;
+    pos[r] = p.positions[u];
+    kp[r] = load_k(p, u, lane);
+    c[r][0] = __ldg(src);
+    c[r][1] = __ldg(src + 32);
   }
+  int kept = 0;
+  uint32_t m2 = kMaxStart;
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const int u = row_t[warp + r * kWarps];
     if (u < 0) continue;
     ++kept;
-    kp[r] = rotate_k(p, turns, u, lane);
-    m = finite_max(m, kp[r]);
+    kp[r] = store_k(p, per_pos, u, pos[r], kp[r], lane);
+    m2 = finite_max(m2, kp[r]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      m = finite_max(m, c[r][k].x);
-      m = finite_max(m, c[r][k].y);
-      m = finite_max(m, c[r][k].z);
-      m = finite_max(m, c[r][k].w);
+      m2 = finite_max(m2, c[r][k].x);
+      m2 = finite_max(m2, c[r][k].y);
+      m2 = finite_max(m2, c[r][k].z);
+      m2 = finite_max(m2, c[r][k].w);
     }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m2 = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
   if (lane == 0) {
-    atomicMax(&amax_s, __float_as_uint(m));
+    atomicMax(&amax_s, m2 - (kMaxStart & 0xFFFFu));
     atomicSub(&members, kept);
   }
-  __syncthreads();
-  float old = row_t[0] >= 0 ? 0.f : p.scales[g];
-  if (!(old > 0.f) || !(old < INFINITY)) old = 0.f;
-  const float now = fmaxf(old, scale_for(__uint_as_float(amax_s)));
+  __syncthreads();   // and every thread has the old scale
+  const float old = row_t[0] < 0 && held > 0.f && held < INFINITY ? held : 0.f;
+  const float now = fmaxf(old, scale_for(__uint_as_float(amax_s << 16)));
   uint8_t *block = p.cache + static_cast<int64_t>(g) * kBlock * kDqk;
-  __syncthreads();   // every thread has the old scale
   if (tid == 0) p.scales[g] = now;
   const bool grew = old > 0.f && now > old;
-  const float ratio = old / now;
+  const bool exact = (__float_as_uint(now) & 0x7FFFFFu) == 0 && now >= 0x1p-126f && now <= 0x1p126f;
+  const float inv = exact ? 1.f / now : 0.f;
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const int row = warp + r * kWarps;
-    uint8_t *dst = block + static_cast<int64_t>(row) * kDqk;
+    uint8_t *dst = block + row * kDqk;
     if (row_t[row] >= 0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint4 v = c[r][k];
         reinterpret_cast<uint2 *>(dst)[lane + 32 * k] =
-            make_uint2(codes2(v.x, now) | (codes2(v.y, now) << 16), codes2(v.z, now) | (codes2(v.w, now) << 16));
+            make_uint2(codes2(v.x, now, inv) | (codes2(v.y, now, inv) << 16),
+                       codes2(v.z, now, inv) | (codes2(v.w, now, inv) << 16));
       }
-      const uint32_t w = codes2(kp[r], now);
+      const uint32_t w = codes2(kp[r], now, inv);
       if (!p.half_layout) {
         reinterpret_cast<uint16_t *>(dst + kLatent)[lane] = static_cast<uint16_t>(w);
       } else {
         dst[kLatent + lane] = static_cast<uint8_t>(w);
         dst[kLatent + kPairs + lane] = static_cast<uint8_t>(w >> 8);
       }
-    } else if (grew) {
-      uint32_t *d = reinterpret_cast<uint32_t *>(dst);
+    }
+  }
+  if (grew) {
+    const float ratio = old / now;
+#pragma unroll 1
+    for (int row = warp; row < kBlock; row += kWarps) {
+      if (row_t[row] >= 0) continue;
+      uint32_t *d = reinterpret_cast<uint32_t *>(block + row * kDqk);
 #pragma unroll
       for (int k = 0; k < 4; ++k) d[lane + 32 * k] = recode4(d[lane + 32 * k], ratio);
       if (lane < 16) d[lane + 128] = recode4(d[lane + 128], ratio);
@@ -238,79 +288,116 @@ __device__ void append_block(const AppendArgs &p, const Turns &turns, int t) {
       const int u = u0 + lane;
       const int s = u < p.T ? p.slots[u] : -1;
       uint32_t lost = __ballot_sync(0xffffffffu, same(s) && row_t[s & (kBlock - 1)] != u);
-      for (; lost; lost &= lost - 1) rotate_k(p, turns, u0 + __ffs(lost) - 1, lane);
+      for (; lost; lost &= lost - 1) rotate_k(p, per_pos, u0 + __ffs(lost) - 1, lane);
     }
   }
 }
 
-// Grid (T, 1 + head groups): the first CTA of a token takes its cache row,
-// the others rotate 128 heads each.
-__global__ void __launch_bounds__(kThreads)
+// The cache rows of p.per_cta tokens: few CTAs look at the slots, so that those
+// of the queries start at once.
+__device__ __forceinline__ void append_tokens(const AppendArgs &p, const Turns &turns) {
+  __shared__ int slots[kMaxPerCta + 1];
+  const int t0 = blockIdx.x * p.per_cta, n = min(p.per_cta, p.T - t0);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int mine = tid <= n && t0 + tid > 0 ? p.slots[t0 + tid - 1] : -1;
+  int ahead[kAhead];
+  load_slots(p, tid, ahead);
+  const unsigned long long per_pos = turns.per_pos[lane];
+  if (tid <= n) slots[tid] = mine;
+  __syncthreads();
+  auto valid = [&](int s) { return s >= 0 && s < p.num_slots; };
+  for (int i = warp; i < n; i += kWarps) {
+    const int s = slots[i + 1];
+    if (valid(s)) continue;            // nothing to store
+    rotate_k(p, per_pos, t0 + i, lane);
+    if (lane == 0 && s >= 0) raise_error(p.err, MLA_DEVERR_BLOCK_ID);
+  }
+  for (int i = 0; i < n; ++i) {
+    const int s = slots[i + 1], before = slots[i];
+    if (!valid(s)) continue;
+    const int g = s >> p.sb_shift;
+    if (valid(before) && before >> p.sb_shift == g) continue;
+    if (p.sb_shift == 6) append_block<kPage / kWarps>(p, per_pos, t0 + i, g, ahead);
+    else if (p.sb_shift == 5) append_block<32 / kWarps>(p, per_pos, t0 + i, g, ahead);
+    else append_block<16 / kWarps>(p, per_pos, t0 + i, g, ahead);
+    __syncthreads();                   // before the next block's shared words
+  }
+}
+
+// The first CTAs take the cache rows, the others rotate 256 (token, head) rows.
+__global__ void __launch_bounds__(kThreads, 2)
 append_kernel(const __grid_constant__ AppendArgs p, const __grid_constant__ Turns turns) {
-  const int t = blockIdx.x;
-  if (blockIdx.y == 0) {
-    if (p.sb_shift == 6) append_block<8>(p, turns, t);
-    else if (p.sb_shift == 5) append_block<4>(p, turns, t);
-    else append_block<2>(p, turns, t);
+  if (blockIdx.x < p.append_ctas) {
+    append_tokens(p, turns);
     return;
   }
+  const int item = blockIdx.x - p.append_ctas;
+  const int tokens = kQueryRows >> p.head_shift, span = item / p.groups;
+  const int64_t t0 = static_cast<int64_t>(span) * tokens;
+  const int h0 = (item - span * p.groups) << p.head_shift;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(tokens), p.T - t0));
+  const int nh = min(1 << p.head_shift, p.H - h0);
   // every load of the thread goes out before the angles are there
-  __shared__ __align__(16) float cs[kPairs], sn[kPairs];
+  __shared__ __align__(16) float cs[kMaxTokens][kPairs], sn[kMaxTokens][kPairs];
   const int tid = threadIdx.x;
-  const int h0 = (blockIdx.y - 1) * kHeadsPerCta, nh = min(kHeadsPerCta, p.H - h0);
-  const uint8_t *q = p.q_pe + t * p.q_st + h0 * p.q_sh;
-  uint8_t *o = p.q_out + t * p.qo_st + h0 * p.qo_sh;
+  const uint8_t *q = p.q_pe + t0 * p.q_st + h0 * p.q_sh;
+  uint8_t *o = p.q_out + t0 * p.qo_st + h0 * p.qo_sh;
+  auto angles = [&] {
+    const int t = tid / kPairs, i = tid % kPairs;
+    if (t < nt) turn(p.positions[t0 + t], turns.per_pos[i], sn[t][i], cs[t][i]);
+    __syncthreads();
+  };
+  // row r of the item: token r >> head_shift, head r & (2^head_shift - 1)
   if (!p.half_layout) {                // 8 dims: pairs 4ch .. 4ch + 3
-    constexpr int kPer = kHeadsPerCta * 8 / kThreads;
+    constexpr int kPer = kQueryRows * 8 / kThreads;
+    const int ch = tid & 7;
     uint4 v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int h = (tid + i * kThreads) >> 3;
-      if (h < nh) v[i] = reinterpret_cast<const uint4 *>(q + h * p.q_sh)[tid & 7];
+      const int r = (tid + i * kThreads) >> 3, t = r >> p.head_shift, h = r - (t << p.head_shift);
+      if (t < nt && h < nh) v[i] = reinterpret_cast<const uint4 *>(q + t * p.q_st + h * p.q_sh)[ch];
     }
-    if (tid < kPairs) turn(p.positions[t], turns.per_pos[tid], sn[tid], cs[tid]);
-    __syncthreads();
-    const int ch = tid & 7;
-    const float4 c = reinterpret_cast<const float4 *>(cs)[ch], sv = reinterpret_cast<const float4 *>(sn)[ch];
+    angles();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int h = (tid + i * kThreads) >> 3;
-      if (h < nh)
-        reinterpret_cast<uint4 *>(o + h * p.qo_sh)[ch] =
-            make_uint4(rot_pair(bf_lo(v[i].x), bf_hi(v[i].x), c.x, sv.x),
-                       rot_pair(bf_lo(v[i].y), bf_hi(v[i].y), c.y, sv.y),
-                       rot_pair(bf_lo(v[i].z), bf_hi(v[i].z), c.z, sv.z),
-                       rot_pair(bf_lo(v[i].w), bf_hi(v[i].w), c.w, sv.w));
+      const int r = (tid + i * kThreads) >> 3, t = r >> p.head_shift, h = r - (t << p.head_shift);
+      if (t >= nt || h >= nh) continue;
+      const float4 c = reinterpret_cast<const float4 *>(cs[t])[ch], sv = reinterpret_cast<const float4 *>(sn[t])[ch];
+      reinterpret_cast<uint4 *>(o + t * p.qo_st + h * p.qo_sh)[ch] =
+          make_uint4(rot_pair(bf_lo(v[i].x), bf_hi(v[i].x), c.x, sv.x),
+                     rot_pair(bf_lo(v[i].y), bf_hi(v[i].y), c.y, sv.y),
+                     rot_pair(bf_lo(v[i].z), bf_hi(v[i].z), c.z, sv.z),
+                     rot_pair(bf_lo(v[i].w), bf_hi(v[i].w), c.w, sv.w));
     }
   } else {                             // dims 8ch .. and 32 + 8ch ..
-    constexpr int kPer = kHeadsPerCta * 4 / kThreads;
+    constexpr int kPer = kQueryRows * 4 / kThreads;
+    const int ch = tid & 3;
     uint4 va[kPer], vb[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int h = (tid + i * kThreads) >> 2;
-      if (h < nh) {
-        const uint4 *row = reinterpret_cast<const uint4 *>(q + h * p.q_sh);
-        va[i] = row[tid & 3];
-        vb[i] = row[(tid & 3) + 4];
+      const int r = (tid + i * kThreads) >> 2, t = r >> p.head_shift, h = r - (t << p.head_shift);
+      if (t < nt && h < nh) {
+        const uint4 *row = reinterpret_cast<const uint4 *>(q + t * p.q_st + h * p.q_sh);
+        va[i] = row[ch];
+        vb[i] = row[ch + 4];
       }
     }
-    if (tid < kPairs) turn(p.positions[t], turns.per_pos[tid], sn[tid], cs[tid]);
-    __syncthreads();
-    const int ch = tid & 3;
+    angles();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int h = (tid + i * kThreads) >> 2;
-      if (h >= nh) continue;
+      const int r = (tid + i * kThreads) >> 2, t = r >> p.head_shift, h = r - (t << p.head_shift);
+      if (t >= nt || h >= nh) continue;
       uint32_t *a = reinterpret_cast<uint32_t *>(&va[i]), *b = reinterpret_cast<uint32_t *>(&vb[i]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int j = 8 * ch + 2 * k;
-        const uint32_t r0 = rot_pair(bf_lo(a[k]), bf_lo(b[k]), cs[j], sn[j]);
-        const uint32_t r1 = rot_pair(bf_hi(a[k]), bf_hi(b[k]), cs[j + 1], sn[j + 1]);
+        const float2 c = *reinterpret_cast<const float2 *>(&cs[t][8 * ch + 2 * k]);
+        const float2 sv = *reinterpret_cast<const float2 *>(&sn[t][8 * ch + 2 * k]);
+        const uint32_t r0 = rot_pair(bf_lo(a[k]), bf_lo(b[k]), c.x, sv.x);
+        const uint32_t r1 = rot_pair(bf_hi(a[k]), bf_hi(b[k]), c.y, sv.y);
         a[k] = __byte_perm(r0, r1, 0x5410);
         b[k] = __byte_perm(r0, r1, 0x7632);
       }
-      uint4 *dst = reinterpret_cast<uint4 *>(o + h * p.qo_sh);
+      uint4 *dst = reinterpret_cast<uint4 *>(o + t * p.qo_st + h * p.qo_sh);
       dst[ch] = va[i];
       dst[ch + 4] = vb[i];
     }
@@ -349,7 +436,17 @@ extern "C" int mla_rope_cache_append(void *q_pe, int64_t q_stride_t, int64_t q_s
     if (T > 1 && H > 1 && st < (H - 1) * sh + kRope && sh < (T - 1) * st + kRope)
       return MLA_ERR_INVALID_ARG;
   }
+  const int per_cta = min(kMaxPerCta, 1 + (T - 1) / kAppendCtas), append_ctas = 1 + (T - 1) / per_cta;
+  int head_shift = kMinHeadShift;
+  while (head_shift < kMaxHeadShift && (1 << head_shift) < H) ++head_shift;
+  const int tokens = kQueryRows >> head_shift, groups = q_pe ? (H + (1 << head_shift) - 1) >> head_shift : 0;
+  const int64_t ctas = append_ctas + static_cast<int64_t>(1 + (T - 1) / tokens) * groups;
+  if (ctas > INT_MAX) return MLA_ERR_INVALID_ARG;
   AppendArgs p{};
+  p.append_ctas = append_ctas;
+  p.per_cta = per_cta;
+  p.groups = groups;
+  p.head_shift = head_shift;
   p.q_pe = static_cast<const uint8_t *>(q_pe);
   p.k_pe = static_cast<const uint8_t *>(k_pe);
   p.kv_c = static_cast<const uint8_t *>(kv_c);
@@ -383,7 +480,6 @@ extern "C" int mla_rope_cache_append(void *q_pe, int64_t q_stride_t, int64_t q_s
     for (int i = 0; i < bit; ++i) f[bit + i] = f[i] * step;
   }
   for (int i = 0; i < kPairs; ++i) turns.per_pos[i] = static_cast<unsigned long long>(f[i]);
-  const dim3 grid(T, 1 + (q_pe ? (H + kHeadsPerCta - 1) / kHeadsPerCta : 0));
-  append_kernel<<<grid, kThreads, 0, stream>>>(p, turns);
+  append_kernel<<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(p, turns);
   return launch_status();
 }

@@ -137,6 +137,52 @@ def test_append_duplicates_out_of_range_and_special_values(m):
     assert np.array_equal(got_c[~nan], want_c[~nan])
 
 
+@pytest.mark.parametrize("sb", [16, 32, 64])
+@pytest.mark.parametrize("kind", ["random", "runs", "apart"])
+def test_append_many_tokens(m, sb, kind):
+    """Thousands of tokens: several to a CTA, slots taken twice, padding and
+    slots out of range among them, old scales that are no powers of two."""
+    g = synth.generator(7300 + sb)
+    nb, T = 90, 5000
+    codes, scales = _pool(g, nb, sb)
+    scales *= g.uniform(1.0, 2.0, scales.shape).astype(np.float32)
+    if kind == "random":
+        slots = g.integers(-40, nb * 64 + 40, T)
+    elif kind == "runs":                    # ten requests' runs, from anywhere in a page
+        slots = np.concatenate([576 * r + g.integers(0, 70) + np.arange(500) for r in range(10)])
+    else:                                   # neighbours in different blocks, every page twice
+        slots = (np.arange(T) * 64 + np.arange(T) // nb // 2) % (nb * 64)
+    slots = slots.astype(np.int32)
+    pos = g.integers(0, 10 ** 6, T).astype(np.int32)
+    kv = synth.as_bf16(g.standard_normal((T, 576)) * np.exp2(g.integers(-6, 5, (T, 1)))).cuda()
+    k0 = f64(kv[:, 512:].contiguous())
+    _, ko, got_c, got_s, err = _append(m, codes, scales, slots, pos, None, kv, "half")
+    assert err == (1 if kind == "random" else 0)
+    _check_rot(ko, k0, pos, False, "k")
+    want_c, want_s = W.append(codes, scales, _rows(kv[:, :512], ko), slots)
+    assert np.array_equal(got_s, want_s)
+    assert np.array_equal(got_c, want_c)
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("T,H", [(9, 1), (33, 16), (17, 17), (5, 64), (3, 129), (2, 300)])
+def test_append_query_heads(m, layout, T, H):
+    """Head counts on both sides of the groups that a CTA takes; queries whose
+    heads are apart and whose tokens are closer than their heads."""
+    g = synth.generator(7400 + H)
+    kv = synth.as_bf16(g.standard_normal((T, 576))).cuda()
+    pos = g.integers(0, 5000, T).astype(np.int32)
+    for order in ("token", "head"):
+        base = synth.as_bf16(g.standard_normal((T, H, 72) if order == "token" else (H, T, 72))).cuda()
+        view = base if order == "token" else base.transpose(0, 1)
+        q, before = view[:, :, :64], view.clone()
+        want = f64(q.contiguous())
+        qo, _, _, _, err = _append(m, *_pool(g, 2, 64), np.full(T, -1), pos, q, kv.clone(), layout)
+        assert err == 0 and qo is q
+        _check_rot(q, want, pos, layout == "interleaved", f"q {order}")
+        assert torch.equal(view[:, :, 64:], before[:, :, 64:])
+
+
 def test_append_token_by_token_then_read(m):
     """Tokens appended one call at a time, then gathered: every value within
     half an e4m3 step at the block's final scale, plus the half subnormal
