@@ -88,7 +88,6 @@ struct Fmt {
   static constexpr int kMinUnits = (kMinPages + kPages - 1) / kPages;
   static constexpr int kJobCost = kJobPages / kPages;      // in tiles, as all units
   static constexpr int kCols = 128 / kEsz;                 // columns of a 128-byte box row
-  static constexpr int kLatChunks = kLatent / kCols;       // 4 / 8 boxes (the rope: half a one / one)
   static constexpr int kQBytes = 64 * kDqk * kEsz;         // 64 query rows: 36 / 72 KB
   static constexpr int kKRows = kTile / 2;                 // key rows of one CTA
   static constexpr int kKBox = kKRows * 128;
@@ -173,11 +172,10 @@ __device__ __forceinline__ int length_of(int b, const WindowArgs &a, bool tell) 
 }
 
 template <bool FP8>
-__device__ __forceinline__ int units_of(int j, const WindowArgs &a, int &len) {
+__device__ __forceinline__ int tiles_of(int j, const WindowArgs &a, int &len) {
   const int rg = a.RG > 1 ? j / a.B : 0;
   len = length_of(j - rg * a.B, a, blockIdx.x == 0 && rg == 0);
-  const int t = job_of(rg, len, a).tiles(Fmt<FP8>::kPages);
-  return t > 0 ? t + Fmt<FP8>::kJobCost : 0;
+  return job_of(rg, len, a).tiles(Fmt<FP8>::kPages);
 }
 
 struct Seg {
@@ -198,25 +196,59 @@ __device__ __forceinline__ int warp_incl_scan(int x, int lane) {
 // The segments of one CTA pair, found by a whole warp.  Lane k holds the
 // jobs [k*per, (k+1)*per) in sum for the search of a span's first job, and
 // job base + k of the 32 that are being walked.
+//
+// even: where every job can be cut into parts of at most C tiles with no more
+// parts than pairs, each pair has one part of one job instead of C units of
+// what lies end to end: nobody then switches jobs (a second segment ends
+// about 4 us after a first one of the same tiles).  A part is the unit, C = 1.
 template <bool FP8>
 struct Walk {
+  static constexpr int kHeld = 3;   // jobs of a lane that fit (the pairs are fewer than 96)
   int J, per, lane_excl, total, C, span, span_lo, span_hi;
   int base, k, len, units, excl;
+  int even;                         // C of the test, or 0
   bool open;
 
+  __device__ int units_of(int tiles) const {
+    if (even) return (tiles + even - 1) / even;
+    return tiles > 0 ? tiles + Fmt<FP8>::kJobCost : 0;
+  }
   __device__ void init(const WindowArgs &a, int lane) {
     J = a.B * a.RG;
     per = (J + 31) / 32;
-    int sum = 0;
+    even = 0;
+    int sum = 0, held[kHeld];
     len = 0;
-    for (int j = lane * per; j < min(J, (lane + 1) * per); ++j) sum += units_of<FP8>(j, a, len);
-    const int incl = warp_incl_scan(sum, lane);
-    lane_excl = incl - sum;
+    if (per <= kHeld) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        held[i] = i < per && lane * per + i < J ? tiles_of<FP8>(lane * per + i, a, len) : 0;
+        sum += units_of(held[i]);
+      }
+    } else {
+      for (int j = lane * per; j < min(J, (lane + 1) * per); ++j)
+        sum += units_of(tiles_of<FP8>(j, a, len));
+    }
+    total = __reduce_add_sync(0xffffffffu, sum);
+    C = a.forced > 0 ? a.forced : max(Fmt<FP8>::kMinUnits, (total - 1) / a.spans_at_once + 1);
+    if (a.forced == 0 && J <= a.spans_at_once && per <= kHeld) {
+      even = C;
+      int parts = 0;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) parts += units_of(held[i]);
+      const int all = __reduce_add_sync(0xffffffffu, parts);
+      if (all <= a.spans_at_once) {
+        sum = parts;
+        total = all;
+        C = 1;
+      } else {
+        even = 0;
+      }
+    }
+    lane_excl = warp_incl_scan(sum, lane) - sum;
     units = sum;                // (one job a lane: the walk's window is there already)
     excl = lane_excl;
     base = 0;
-    total = __shfl_sync(0xffffffffu, incl, 31);
-    C = a.forced > 0 ? a.forced : max(Fmt<FP8>::kMinUnits, (total - 1) / a.spans_at_once + 1);
     span = blockIdx.x >> 1;
     open = false;
   }
@@ -242,7 +274,7 @@ struct Walk {
     k = 0;
     units = 0;
     len = 0;
-    if (base + lane < J) units = units_of<FP8>(base + lane, a, len);
+    if (base + lane < J) units = units_of(tiles_of<FP8>(base + lane, a, len));
     const int incl = warp_incl_scan(units, lane);
     excl = before + incl - units;
   }
@@ -270,7 +302,7 @@ struct Walk {
         continue;
       }
       ++k;
-      const int first = t0 + Fmt<FP8>::kJobCost, end = t0 + n;
+      const int first = t0 + (even ? 0 : Fmt<FP8>::kJobCost), end = t0 + n;
       const int u0 = max(span_lo, first), u1 = min(span_hi, end);
       if (n == 0 || u1 <= u0) continue;
       s.rg = a.RG > 1 ? j / a.B : 0;
@@ -278,6 +310,12 @@ struct Walk {
       s.len = l;
       s.tile0 = u0 - first;
       s.ntiles = u1 - u0;
+      if (even) {               // part tile0 of n, of sizes that differ by one at most
+        const int tiles = job_of(s.rg, l, a).tiles(Fmt<FP8>::kPages), small = tiles / n,
+                  more = tiles - small * n, i = s.tile0;
+        s.tile0 = i * small + min(i, more);
+        s.ntiles = small + (i < more ? 1 : 0);
+      }
       s.whole = first >= span_lo && end <= span_hi;
       // two partials a span at most: one of a job that began before it, one
       // of a job that goes on behind it
@@ -541,12 +579,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     };
     const uint32_t q_bar = peer_smem(q_full, 0);
     while (ok && (args.solo ? walk.next_solo(args, sg) : walk.next(args, sg, lane))) {
-      if (!(ok = publish(sg))) break;
-      ++ns;
-      if (sg.ntiles == 0) continue;
       const Job job = job_of(sg.rg, sg.len, args);
       Pages pg;
       fetch_blocks(pg, job, sg.b, F::kPages * sg.tile0);
+      if (!(ok = publish(sg))) break;
+      ++ns;
+      if (sg.ntiles == 0) continue;
       // Q, once the last segment's last Q K^T has read it
       if (nq > 0 && !(ok = wait_for(q_empty, (nq - 1) & 1, abort_flag))) break;
       ++nq;
@@ -1048,16 +1086,20 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 // jobs without a key.  Part k of a job whose first span is s0 lies in slot
 // 2 s0 + 1 (k = 0) or 2 (s0 + k).  SPLIT warps share a row and take every
 // SPLIT-th part, joined through shared memory: one request over all pairs
-// has 76 parts a row, which a single warp would read four at a time (the
-// 131072-token request's merge: 28 us with one warp a row).
+// has 76 parts a row, which a single warp would read a few at a time (the
+// 131072-token request's merge: 28 us with one warp a row).  What it costs is
+// latency, so a round's logs and rows are asked for together, the maximum runs
+// along, and the CTAs of a batch are all resident at once (64 registers).
 constexpr int kMergeWarps = 8;
 
 template <typename T, int SPLIT>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeWarps * 32, SPLIT > 1 ? 1 : 4)
 window_merge_kernel(const __grid_constant__ WindowArgs a) {
   constexpr int kRows = kMergeWarps / SPLIT;    // rows of this CTA
+  constexpr int kQuads = sizeof(T);             // 16-byte words of a lane's 16 values
+  constexpr int kRound = (SPLIT > 1 ? 20 : 8) / kQuads;   // parts on their way: 10 / 4 of bf16
   __shared__ float part_o[SPLIT > 1 ? kMergeWarps : 1][kLatent];
-  __shared__ float part_z[kMergeWarps];
+  __shared__ float part_z[kMergeWarps], part_m[kMergeWarps];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % SPLIT;
@@ -1079,37 +1121,51 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   }
   const int s0 = first / C, n = (end - 1) / C - s0 + 1;
   if (n == 1) return;   // written by its pair
-  auto slot_row = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * s0 + 1 : 2 * (s0 + k)) * 128 + rr; };
-  float m = -INFINITY;
-  for (int k = lane; k < n; k += 32) m = fmaxf(m, a.ws_lse[slot_row(k)]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float safe = m == -INFINITY ? 0.f : m;
-  float acc[16], z = 0.f;
+  // lane's values: columns 8 lane .. and 256 + 8 lane ..
+  float acc[16], z = 0.f, m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  for (int k0 = mine; k0 < n; k0 += 4 * SPLIT) {
-    float v[4][16], w[4];
+  for (int k0 = mine; k0 < n; k0 += kRound * SPLIT) {
+    uint4 raw[kRound][kQuads];
+    float w[kRound], top = m;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kRound; ++u) {
       const int k = k0 + u * SPLIT;
       w[u] = -INFINITY;
-      if (k < n) {
-        const int64_t at = slot_row(k);
-        const T *src = static_cast<const T *>(a.ws_o) + at * kLatent;
-        w[u] = __ldg(a.ws_lse + at);
-        load8(src + 8 * lane, v[u]);
-        load8(src + 8 * (lane + 32), v[u] + 8);
-      }
+      if (k >= n) continue;
+      const int64_t at = static_cast<int64_t>(k == 0 ? 2 * s0 + 1 : 2 * (s0 + k)) * 128 + rr;
+      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.ws_o) + at * kLatent);
+      w[u] = __ldg(a.ws_lse + at);
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i)
+        raw[u][i] = __ldg(src + i / (kQuads / 2) * 16 * kQuads + lane * (kQuads / 2) + i % (kQuads / 2));
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (k0 + u * SPLIT < n) {
-        const float wu = expf(w[u] - safe);
-        z += wu;
+    for (int u = 0; u < kRound; ++u) top = fmaxf(top, w[u]);
+    const float safe = top == -INFINITY ? 0.f : top, f = expf(m - safe);
+    m = top;
+    z *= f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = fmaf(wu, v[u][e], acc[e]);
+    for (int e = 0; e < 16; ++e) acc[e] *= f;
+#pragma unroll
+    for (int u = 0; u < kRound; ++u) {
+      if (k0 + u * SPLIT >= n) continue;
+      const float wu = expf(w[u] - safe);
+      z += wu;
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        const uint32_t v[4] = {raw[u][i].x, raw[u][i].y, raw[u][i].z, raw[u][i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (kQuads == 4) {
+            acc[4 * i + e] = fmaf(wu, __uint_as_float(v[e]), acc[4 * i + e]);
+          } else {
+            acc[8 * i + 2 * e] = fmaf(wu, __uint_as_float(v[e] << 16), acc[8 * i + 2 * e]);
+            acc[8 * i + 2 * e + 1] = fmaf(wu, __uint_as_float(v[e] & 0xFFFF0000u), acc[8 * i + 2 * e + 1]);
+          }
+        }
       }
+    }
   }
   if constexpr (SPLIT > 1) {
 #pragma unroll
@@ -1117,32 +1173,41 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
       part_o[warp][8 * lane + e] = acc[e];
       part_o[warp][8 * (lane + 32) + e] = acc[8 + e];
     }
-    if (lane == 0) part_z[warp] = z;
+    if (lane == 0) {
+      part_z[warp] = z;
+      part_m[warp] = m;
+    }
     __syncthreads();
+    if (!row_ok) return;
     // 512 / SPLIT columns a warp, in the warps' order
     constexpr int kCols = kLatent / SPLIT;
+    float f[SPLIT];
+#pragma unroll
+    for (int w = 0; w < SPLIT; ++w) m = fmaxf(m, part_m[warp - mine + w]);
+    const float safe = m == -INFINITY ? 0.f : m;
     z = 0.f;
 #pragma unroll
-    for (int w = 0; w < SPLIT; ++w) z += part_z[warp - mine + w];
+    for (int w = 0; w < SPLIT; ++w) {
+      f[w] = expf(part_m[warp - mine + w] - safe);
+      z = fmaf(part_z[warp - mine + w], f[w], z);
+    }
     const float inv = z == 0.f ? 0.f : 1.f / z;
-    if (!row_ok) return;
 #pragma unroll
     for (int c = lane; c < kCols; c += 32) {
       float x = 0.f;
 #pragma unroll
-      for (int w = 0; w < SPLIT; ++w) x += part_o[warp - mine + w][mine * kCols + c];
+      for (int w = 0; w < SPLIT; ++w) x = fmaf(part_o[warp - mine + w][mine * kCols + c], f[w], x);
       if constexpr (sizeof(T) == 4) out[mine * kCols + c] = x * inv;
       else out[mine * kCols + c] = __float2bfloat16_rn(x * inv);
     }
-    if (mine == 0 && lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(z);
   } else {
     const float inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] *= inv;
     store8(out + 8 * lane, acc);
     store8(out + 8 * (lane + 32), acc + 8);
-    if (lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(z);
   }
+  if (mine == 0 && lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(z);
 }
 
 template <typename T, int SPLIT>
