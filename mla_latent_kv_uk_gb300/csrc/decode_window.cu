@@ -52,6 +52,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <climits>
 #include <mutex>
 
 #include "common.cuh"
@@ -66,7 +67,7 @@ using namespace sm100;
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;              // warps 4..11
 constexpr int kMinPages = 6;               // smallest automatic span, in pages
-constexpr int kJobPages = 4;               // what switching to a job costs, in pages
+constexpr int kJobPages = 6;               // what switching to a job costs, in pages
 // Jobs that cannot have more pages than this are not cut: each is one pair's
 // from end to end, written directly, and no merge kernel follows.
 constexpr int kSoloPages = 6;
@@ -128,11 +129,14 @@ struct WindowArgs {
   float scale_log2;             // sm_scale * log2(e) * q_scale
   const int32_t *block_table, *seq_lens;
   int B, q_len, H, max_blocks, num_blocks, window, sinks;
-  int RG, forced, spans_at_once, solo;
+  int RG, forced, solo;
+  int groups, group_jobs;       // row groups planned apart (RG or 1), jobs of each
+  int spans_at_once;            // pairs of a group
+  int group_spans;              // most spans of a group
   void *out;
   int out_f32;
   float *lse;
-  int *ws_head;                 // [0] C; then per job {first unit, end unit}
+  int *ws_head;                 // C of each group; then per job {first unit, end unit}
   void *ws_o;                   // [slots, 128, 512] of the output's type
   float *ws_lse;                // [slots, 128]
   int *err;
@@ -204,9 +208,10 @@ __device__ __forceinline__ int warp_incl_scan(int x, int lane) {
 template <bool FP8>
 struct Walk {
   static constexpr int kHeld = 3;   // jobs of a lane that fit (the pairs are fewer than 96)
-  int J, per, lane_excl, total, C, span, span_lo, span_hi;
+  int J, job0, per, lane_excl, total, C, span, span_lo, span_hi;
   int base, k, len, units, excl;
   int even;                         // C of the test, or 0
+  int slot0;
   bool open;
 
   __device__ int units_of(int tiles) const {
@@ -214,7 +219,11 @@ struct Walk {
     return tiles > 0 ? tiles + Fmt<FP8>::kJobCost : 0;
   }
   __device__ void init(const WindowArgs &a, int lane) {
-    J = a.B * a.RG;
+    const int pair = blockIdx.x >> 1, group = pair / a.spans_at_once;
+    J = group < a.groups ? a.group_jobs : 0;
+    job0 = group * J;
+    slot0 = group * a.group_spans;
+    span = pair - group * a.spans_at_once;
     per = (J + 31) / 32;
     even = 0;
     int sum = 0, held[kHeld];
@@ -222,12 +231,12 @@ struct Walk {
     if (per <= kHeld) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        held[i] = i < per && lane * per + i < J ? tiles_of<FP8>(lane * per + i, a, len) : 0;
+        held[i] = i < per && lane * per + i < J ? tiles_of<FP8>(job0 + lane * per + i, a, len) : 0;
         sum += units_of(held[i]);
       }
     } else {
       for (int j = lane * per; j < min(J, (lane + 1) * per); ++j)
-        sum += units_of(tiles_of<FP8>(j, a, len));
+        sum += units_of(tiles_of<FP8>(job0 + j, a, len));
     }
     total = __reduce_add_sync(0xffffffffu, sum);
     C = a.forced > 0 ? a.forced : max(Fmt<FP8>::kMinUnits, (total - 1) / a.spans_at_once + 1);
@@ -249,8 +258,8 @@ struct Walk {
     units = sum;                // (one job a lane: the walk's window is there already)
     excl = lane_excl;
     base = 0;
-    span = blockIdx.x >> 1;
     open = false;
+    if (span == 0 && J > 0 && (blockIdx.x & 1) == 0 && lane == 0) a.ws_head[group] = C;
   }
   __device__ void init_solo(const WindowArgs &a) {
     J = a.B * a.RG;
@@ -274,7 +283,7 @@ struct Walk {
     k = 0;
     units = 0;
     len = 0;
-    if (base + lane < J) units = units_of(tiles_of<FP8>(base + lane, a, len));
+    if (base + lane < J) units = units_of(tiles_of<FP8>(job0 + base + lane, a, len));
     const int incl = warp_incl_scan(units, lane);
     excl = before + incl - units;
   }
@@ -292,11 +301,11 @@ struct Walk {
         open = true;
       }
       if (k == 32) load(a, base + 32, __shfl_sync(0xffffffffu, excl + units, 31), lane);
-      const int j = base + k;
+      const int j = job0 + base + k;
       const int t0 = __shfl_sync(0xffffffffu, excl, k & 31);
       const int n = __shfl_sync(0xffffffffu, units, k & 31);
       const int l = __shfl_sync(0xffffffffu, len, k & 31);
-      if (j >= J || t0 >= span_hi) {
+      if (base + k >= J || t0 >= span_hi) {
         span += a.spans_at_once;
         open = false;
         continue;
@@ -319,10 +328,10 @@ struct Walk {
       s.whole = first >= span_lo && end <= span_hi;
       // two partials a span at most: one of a job that began before it, one
       // of a job that goes on behind it
-      s.slot = 2 * span + (first >= span_lo ? 1 : 0);
+      s.slot = 2 * (slot0 + span) + (first >= span_lo ? 1 : 0);
       if (first >= span_lo && (blockIdx.x & 1) == 0 && lane == 0) {
-        a.ws_head[2 + 2 * j] = first;
-        a.ws_head[3 + 2 * j] = end;
+        a.ws_head[a.groups + 2 * j] = first;
+        a.ws_head[a.groups + 2 * j + 1] = end;
       }
       return true;
     }
@@ -561,7 +570,6 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       walk.init_solo(args);
     } else {
       walk.init(args, lane);
-      if (blockIdx.x == 0 && lane == 0) args.ws_head[0] = walk.C;
     }
     Seg sg;
     int ns = 0, nq = 0, kc = 0;             // segments, queries, K slots so far
@@ -1110,7 +1118,8 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   if (SPLIT == 1 && !row_ok) return;
   const int64_t row = static_cast<int64_t>(b) * R + rg * 128 + rr;
   T *out = static_cast<T *>(a.out) + row * kLatent;
-  const int C = a.ws_head[0], first = a.ws_head[2 + 2 * j], end = a.ws_head[3 + 2 * j];
+  const int group = j / a.group_jobs;
+  const int C = a.ws_head[group], first = a.ws_head[a.groups + 2 * j], end = a.ws_head[a.groups + 2 * j + 1];
   if (job_of(rg, length_of(b, a, false), a).pages == 0) {   // (the words above hold nothing)
     if (mine == 0 && row_ok) {
       const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -1119,7 +1128,7 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
     }
     return;
   }
-  const int s0 = first / C, n = (end - 1) / C - s0 + 1;
+  const int s0 = first / C + group * a.group_spans, n = (end - 1) / C - first / C + 1;
   if (n == 1) return;   // written by its pair
   // lane's values: columns 8 lane .. and 256 + 8 lane ..
   float acc[16], z = 0.f, m = -INFINITY;
@@ -1273,7 +1282,9 @@ bool shape_ok(int B, int q_len, int H) {
 
 struct WsLayout {
   size_t o_off, lse_off, total;
-  bool solo;
+  int groups;
+  int64_t group_spans;
+  bool solo, fits;              // fits: the units of all jobs count in 32 bits
 };
 
 WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sinks,
@@ -1287,14 +1298,21 @@ WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sin
                                 (static_cast<int64_t>(sinks) + kPage - 1) / kPage);
   WsLayout w{};
   w.solo = split_tiles == 0 && pages <= kSoloPages;
+  w.fits = J * (pages + kJobPages) <= INT_MAX;
+  w.groups = 1;
   if (w.solo) return w;   // nothing to keep
+  // Row groups of a request read the same pages.  Planned apart, each over its
+  // share of the pairs, they do so at the same time, and all but one read from
+  // L2 - unless that leaves more than a sixteenth of the pairs idle.
+  if (RG <= pairs && pairs / RG * RG * 16 >= static_cast<int64_t>(pairs) * 15) w.groups = static_cast<int>(RG);
   // (a forced split counts tiles: the smaller ones, of one page, make more)
-  const int64_t spans =
-      split_tiles > 0 ? (J * (pages + kJobPages) + split_tiles - 1) / split_tiles : pairs;
+  w.group_spans = split_tiles > 0 ? (J / w.groups * (pages + kJobPages) + split_tiles - 1) / split_tiles
+                                  : pairs / w.groups;
+  const size_t slots = static_cast<size_t>(2 * w.groups) * w.group_spans;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  w.o_off = up((2 + 2 * static_cast<size_t>(J)) * sizeof(int));
-  w.lse_off = w.o_off + static_cast<size_t>(2 * spans) * 128 * kLatent * sizeof(float);
-  w.total = w.lse_off + static_cast<size_t>(2 * spans) * 128 * sizeof(float);
+  w.o_off = up((w.groups + 2 * static_cast<size_t>(J)) * sizeof(int));
+  w.lse_off = w.o_off + slots * 128 * kLatent * sizeof(float);
+  w.total = w.lse_off + slots * 128 * sizeof(float);
   return w;
 }
 
@@ -1362,6 +1380,7 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   const int pairs = pairs_for_device();
   if (pairs == 0) return MLA_ERR_CUDA;
   const WsLayout w = ws_layout(B, q_len, H, max_blocks * kPage, window, sinks, split_tiles, pairs);
+  if (!w.fits) return MLA_ERR_INVALID_ARG;
   if (!w.solo && (!workspace || ws_bytes < w.total)) return MLA_ERR_WORKSPACE;
   WindowArgs a{};
   a.err = device_error_word();
@@ -1384,7 +1403,10 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.forced = split_tiles;
   a.solo = w.solo;
   const int64_t jobs = static_cast<int64_t>(B) * a.RG;
-  a.spans_at_once = w.solo ? static_cast<int>(std::min<int64_t>(pairs, jobs)) : pairs;
+  a.groups = w.groups;
+  a.group_jobs = static_cast<int>(jobs / w.groups);
+  a.group_spans = static_cast<int>(w.group_spans);
+  a.spans_at_once = w.solo ? static_cast<int>(std::min<int64_t>(pairs, jobs)) : pairs / w.groups;
   a.out = out;
   a.out_f32 = out_dtype == MLA_F32;
   a.lse = lse;
@@ -1392,8 +1414,8 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.ws_head = reinterpret_cast<int *>(ws);
   a.ws_o = ws + w.o_off;
   a.ws_lse = reinterpret_cast<float *>(ws + w.lse_off);
-  const int st = fp8 ? launch_pairs<true>(q, kv_cache, a.spans_at_once, a, stream)
-                     : launch_pairs<false>(q, kv_cache, a.spans_at_once, a, stream);
+  const int st = fp8 ? launch_pairs<true>(q, kv_cache, a.spans_at_once * w.groups, a, stream)
+                     : launch_pairs<false>(q, kv_cache, a.spans_at_once * w.groups, a, stream);
   if (st != MLA_OK || w.solo) return st;
   // a job has about pairs / jobs parts: above eight, a CTA's warps share a row
   const bool many = jobs * 8 < pairs;
@@ -1416,7 +1438,9 @@ extern "C" int mla_decode_window_workspace_size(int B, int q_len, int H, int max
     return MLA_ERR_INVALID_ARG;
   // (without a device: what an upper bound of pairs needs)
   const int pairs = pairs_for_device();
-  *bytes = ws_layout(B, q_len, H, max_seq_len, window, sinks, split_tiles, pairs ? pairs : 128).total;
+  const WsLayout w = ws_layout(B, q_len, H, max_seq_len, window, sinks, split_tiles, pairs ? pairs : 128);
+  if (!w.fits) return MLA_ERR_INVALID_ARG;
+  *bytes = w.total;
   return MLA_OK;
 }
 

@@ -155,6 +155,33 @@ def test_long_rows_split_over_the_device(m, fmt):
     c.check(out, lse, f"{fmt} long")
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "s32"])
+@pytest.mark.parametrize("lens,q_len,H,window,sinks,split", [
+    ([900, 3, 0, 1700, 650, 64, 2, 1100, 40, 500, 777, 1300], 3, 128, 700, 5, 0),   # three row groups
+    ([2600, 1, 333], 4, 160, 0, 0, 0),                                          # five
+    ([2600, 1, 333], 4, 160, 0, 0, 4),
+    ([700, 60], 20, 256, 300, 4, 0),          # forty: too many to plan each apart
+])
+def test_row_groups(m, fmt, lens, q_len, H, window, sinks, split):
+    """More query rows than a pair takes at once, cut and uncut."""
+    c = Case(fmt, lens, q_len, H, window, sinks, seed=40 + q_len)
+    out, lse = c.run(m, split_tiles=split)
+    assert m.mla_get_device_error() == 0
+    c.check(out, lse, f"{fmt} {lens} x {q_len * H} rows")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_even_parts(m, fmt):
+    """Fewer requests than CTA pairs, of lengths alike and not: cut into even
+    parts or end to end, the same rows."""
+    for n, lens in enumerate(([1100] * 20, [1100 + 7 * i for i in range(30)], [640] * 70,
+                              [5000, 0, 1, 64] + [390] * 30)):
+        c = Case(fmt, lens, 1, 16, 0, 0, seed=30 + n)
+        out, lse = c.run(m)
+        assert m.mla_get_device_error() == 0
+        c.check(out, lse, f"{fmt} {n}")
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "s16"])
 def test_many_requests(m, fmt):
     lens = (np.arange(300) * 37) % 180
