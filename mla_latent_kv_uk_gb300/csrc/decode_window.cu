@@ -46,6 +46,14 @@
 // (no plan kernel).  A job that is cut leaves partials in the workspace,
 // which a merge kernel combines: at most two per span, whatever the number
 // of jobs.
+//
+// What bounds it now (each key row takes 128 x 1088 x 2 operations a row group):
+// 64 e4m3 requests of up to 16384 tokens 92 us, at 1.6 of the 1.9 PFLOP/s that
+// a bf16 product reaches, near the 1632 cycles of a tile's MMAs; 128 bf16
+// requests of two tokens and a window of 4096 146 us, 1.15 PFLOP/s, where Q K^T
+// of 64 keys takes as long as one of 128; one e4m3 request of 131072 tokens
+// 34.5 us, the smallest calls 8.8: 3 us until the first keys are there, 4 from
+// the last scores to the results, and 3 for the merge where there is one.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -66,10 +74,15 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;              // warps 4..11
-constexpr int kMinPages = 6;               // smallest automatic span, in pages
-constexpr int kJobPages = 6;               // what switching to a job costs, in pages
+constexpr int kMinPages = 6;               // smallest automatic span, in pages (4 and 8 measure the same)
+// What switching to a job costs, in pages: with 4 / 6 / 8 of them the mixed
+// e4m3 batch (64 requests) takes 93.6 / 91.2 / 90.5 us, the speculative bf16
+// batch (128 requests, two row groups each) 145.8 / 146.2 / 148.4.
+constexpr int kJobPages = 6;
 // Jobs that cannot have more pages than this are not cut: each is one pair's
-// from end to end, written directly, and no merge kernel follows.
+// from end to end, written directly, and no merge kernel follows.  Two e4m3
+// requests of 130 tokens: 8.0 us, cut 10.3; a window of 128: 8.8, cut 11.5; but
+// 32 requests of 18 pages: 24.8, cut 22.4.
 constexpr int kSoloPages = 6;
 constexpr int kSegSlots = 4;
 constexpr uint32_t kColO = 0, kColS = 256;   // O [0,256), then the S tiles
@@ -78,8 +91,10 @@ constexpr int kSBufs = 4;                    // Q K^T runs two tiles ahead of P 
 // What differs between the formats.  K and V come through rings of slots.
 // The bf16 tile is one page: its query takes 72 KB, and the other 152 KB then
 // hold two tiles of keys and values, so that a tile's values are on their way
-// while the last one's are read (with two-page tiles, one of each, the
-// speculative batch took 162 us).
+// while the last one's are read.  (A two-page tile runs Q K^T at twice the
+// rate, but there is room for one only, in slots that wait 2500 cycles for
+// their next load: the speculative batch took 140 us instead of 146, a window
+// of 128 10.3 instead of 8.8, the batch of 32 the same.)
 template <bool FP8>
 struct Fmt {
   static constexpr int kEsz = FP8 ? 1 : 2;
@@ -1092,20 +1107,22 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 
 // Combines the partials of the jobs that were cut, and writes the rows of
 // jobs without a key.  Part k of a job whose first span is s0 lies in slot
-// 2 s0 + 1 (k = 0) or 2 (s0 + k).  SPLIT warps share a row and take every
-// SPLIT-th part, joined through shared memory: one request over all pairs
-// has 76 parts a row, which a single warp would read a few at a time (the
-// 131072-token request's merge: 28 us with one warp a row).  What it costs is
-// latency, so a round's logs and rows are asked for together, the maximum runs
-// along, and the CTAs of a batch are all resident at once (64 registers).
+// 2 s0 + 1 (k = 0) or 2 (s0 + k).  What it costs is latency, so a round's logs
+// and rows are asked for together, the maximum runs along, and the CTAs are all
+// resident at once (64 registers where there are most of them).  SPLIT warps
+// share a row and take every SPLIT-th part, joined through shared memory.
+// Decode and merge over 65536 tokens (e4m3, 128 heads), 1 / 4 / 8 warps a row:
+// 1 request (76 parts a row) 49.4 / 23.5 / 20.2 us, 4 requests (19 parts)
+// 26.6 / 19.8 / 26.5, 8 requests (9) 22.5 / 22.8 / 34.1.
 constexpr int kMergeWarps = 8;
 
 template <typename T, int SPLIT>
-__global__ void __launch_bounds__(kMergeWarps * 32, SPLIT > 1 ? 1 : 4)
+__global__ void __launch_bounds__(kMergeWarps * 32, SPLIT == 8 ? 1 : SPLIT == 4 ? 2 : 4)
 window_merge_kernel(const __grid_constant__ WindowArgs a) {
   constexpr int kRows = kMergeWarps / SPLIT;    // rows of this CTA
   constexpr int kQuads = sizeof(T);             // 16-byte words of a lane's 16 values
-  constexpr int kRound = (SPLIT > 1 ? 20 : 8) / kQuads;   // parts on their way: 10 / 4 of bf16
+  // parts on their way: of bf16 10 / 6 / 4
+  constexpr int kRound = (SPLIT == 8 ? 20 : SPLIT == 4 ? 12 : 8) / kQuads;
   __shared__ float part_o[SPLIT > 1 ? kMergeWarps : 1][kLatent];
   __shared__ float part_z[kMergeWarps], part_m[kMergeWarps];
   grid_dep_wait();
@@ -1225,6 +1242,13 @@ cudaError_t launch_merge(const WindowArgs &a, mla_stream_t stream) {
   const int rows = std::min(128, a.q_len * a.H);
   return launch_pdl(window_merge_kernel<T, SPLIT>, dim3(a.B * a.RG, (rows + kRows - 1) / kRows),
                     dim3(kMergeWarps * 32), 0, stream, a);
+}
+
+template <typename T>
+cudaError_t merge(int64_t parts, const WindowArgs &a, mla_stream_t stream) {
+  return parts > 40   ? launch_merge<T, 8>(a, stream)
+         : parts > 10 ? launch_merge<T, 4>(a, stream)
+                      : launch_merge<T, 1>(a, stream);
 }
 
 // ------------------------------------------------------------------- host
@@ -1417,11 +1441,8 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   const int st = fp8 ? launch_pairs<true>(q, kv_cache, a.spans_at_once * w.groups, a, stream)
                      : launch_pairs<false>(q, kv_cache, a.spans_at_once * w.groups, a, stream);
   if (st != MLA_OK || w.solo) return st;
-  // a job has about pairs / jobs parts: above eight, a CTA's warps share a row
-  const bool many = jobs * 8 < pairs;
-  const cudaError_t e = a.out_f32 ? (many ? launch_merge<float, 8>(a, stream) : launch_merge<float, 1>(a, stream))
-                                  : (many ? launch_merge<__nv_bfloat16, 8>(a, stream)
-                                          : launch_merge<__nv_bfloat16, 1>(a, stream));
+  const int64_t parts = pairs / jobs;   // of a job, about
+  const cudaError_t e = a.out_f32 ? merge<float>(parts, a, stream) : merge<__nv_bfloat16>(parts, a, stream);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
