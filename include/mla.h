@@ -357,7 +357,8 @@ int mla_prefill_attn(const void *q, const void *k, const void *v,
  *   kv_scales[s/64, (s%64)/scale_block] * e4m3(kv_cache[s, c])
  * (s = block*64 + offset).  No calibration is needed: mla_rope_cache_append
  * finds the scales, mla_decode_paged_scaled and mla_gather_cache_scaled
- * read them.  Scales are >= 0 and finite.
+ * read them.  Scales are >= 0 and at most 2^120; 0 stands for rows of zeros
+ * (the decode takes 2^-100 for anything below it).
  *
  * Append: mla_rope_cache_write for this cache.  For each new token t < T
  *   q_out[t,h,:] = R(positions[t]) q_pe[t,h,:]      (h < H)
@@ -374,7 +375,8 @@ int mla_prefill_attn(const void *q, const void *k, const void *v,
  * e4m3 normal range are rounded).  Rounding is to nearest even, infinities
  * saturate, NaN stays NaN.  Rows of blocks that the call does not write to
  * keep their bits.  Tokens of a block may stand anywhere in the call; where
- * a slot comes up twice the later token's row stays.  A negative slot is
+ * a slot comes up twice the later token's row stays.  Calls that write to the
+ * same block follow one another on a stream.  A negative slot is
  * padding: its q and k are rotated and nothing is stored; a slot >=
  * num_blocks*64 does the same and sets MLA_DEVERR_BLOCK_ID.
  *
@@ -384,7 +386,8 @@ int mla_prefill_attn(const void *q, const void *k, const void *v,
  * 8, so slices of one projection's output are read in place).  q_out
  * [T,H,64], k_out [T,64] contiguous, or NULL: rotated in place.  positions,
  * slot_mapping [T] int32.  1 < rope_base < inf, 1 <= H <= 4096 with a
- * query, num_blocks < 2^25.  T == 0 is a no-op. */
+ * query, num_blocks < 2^25; T * ceil(H / 128) < 2^31 - 256.  T == 0 is a
+ * no-op. */
 int mla_rope_cache_append(void *q_pe, int64_t q_stride_t, int64_t q_stride_h,
                           void *k_pe, int64_t k_stride, const void *kv_c,
                           int64_t c_stride, const int32_t *positions,
@@ -423,7 +426,9 @@ int mla_gather_cache_scaled(const void *kv_cache, const float *kv_scales,
  * before it is read (calls on different streams need workspaces of their
  * own); 0 bytes, and workspace may be NULL, where no request can have more
  * than a few tiles.  split_tiles as in mla_decode_paged, in tiles of 128
- * (e4m3) or 64 (bf16) tokens.  Limits as there. */
+ * (e4m3) or 64 (bf16) tokens.  Limits as there; k_scale of an e4m3 cache from
+ * 2^-100 to 2^120; B * ceil(q_len * H / 128) * (pages + 6) < 2^31, with pages
+ * the most that a request can have (max_blocks, or window + sinks in pages). */
 int mla_decode_window_workspace_size(int B, int q_len, int H, int max_seq_len,
                                      int window, int sinks, int split_tiles,
                                      size_t *bytes);
@@ -453,7 +458,9 @@ int mla_decode_paged_scaled(const void *q, float q_scale, const void *kv_cache,
  *   j <= p and (j > p - window or j < sinks),     window >= 1, sinks >= 0.
  * The window is the same whether the keys before the queries are new tokens
  * or gathered context, so one call attends to both.  What a query does not
- * see does not reach its row, NaN and infinities included.
+ * see does not reach its row, NaN and infinities included, in rows behind
+ * cu_k[B] too (a NaN or infinite value that queries of its key tile do not
+ * see costs them a second look at their keys).
  * B * H * ceil(max_q_len / 256) < 2^31 - 1024. */
 int mla_prefill_attn_window(const void *q, const void *k, const void *v,
                             const int32_t *cu_q, const int32_t *cu_k, int B,

@@ -369,6 +369,7 @@ def mla_rope_cache_write(q_pe, k_pe, kv_c, positions, slot_mapping, kv_cache, *,
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _Tensor = torch.Tensor
+_INT_MAX = 0x7FFFFFFF   # a window or sinks beyond it are all the same (and would wrap)
 
 
 def _current_device(t, name):
@@ -458,7 +459,7 @@ def mla_rope_cache_append(q_pe, k_pe, kv_c, positions, slot_mapping, kv_cache, k
         if k_out.shape != k_pe.shape:
             raise ValueError("k_out must have k_pe's shape")
     _check("mla_rope_cache_append", lib.mla_rope_cache_append(
-        q, qt, qh, k, k_pe.stride(0), c, kv_c.stride(0), pos, slots, T, H, rope_base,
+        q, qt, qh, k, k_pe.stride(0), c, kv_c.stride(0), pos, slots, T, H, float(rope_base),
         _ROPE_LAYOUT[layout], qo, ko, cache, scales, sb, num_blocks, _raw_stream(dev)))
     return (q_pe if q_out is None else q_out), (k_pe if k_out is None else k_out)
 
@@ -481,6 +482,7 @@ def mla_gather_cache_scaled(kv_cache, kv_scales, block_table, seq_lens, cu_out, 
         if seq_starts.numel() != B:
             raise ValueError("seq_starts must be [B]")
     scales, sb = _scales_at(kv_scales, num_blocks, dev)
+    total_rows = int(total_rows)
     if out is None:
         out = torch.empty((total_rows, 576), dtype=torch.bfloat16, device=kv_cache.device)
         to = out.data_ptr()
@@ -498,7 +500,8 @@ def mla_decode_window_workspace_size(B, q_len, H, max_seq_len, window=0, sinks=0
                                      split_tiles=0) -> int:
     n = _sz(0)
     _check("mla_decode_window_workspace_size", lib.mla_decode_window_workspace_size(
-        B, q_len, H, max_seq_len, int(window), int(sinks), int(split_tiles), ctypes.byref(n)))
+        B, q_len, H, max_seq_len, min(int(window), _INT_MAX), min(int(sinks), _INT_MAX),
+        int(split_tiles), ctypes.byref(n)))
     return n.value
 
 
@@ -525,6 +528,7 @@ def _decode_window(q, kv_cache, block_table, seq_lens, window, sinks, split_tile
     b, max_blocks = block_table.shape
     if D != 576 or page != 64 or row != 576 or b != B or seq_lens.numel() != B:
         raise ValueError("decode shapes")
+    window, sinks, split_tiles = min(int(window), _INT_MAX), min(int(sinks), _INT_MAX), int(split_tiles)
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype {out_dtype} is neither bf16 nor fp32")
     if out is None:
@@ -549,7 +553,7 @@ def _decode_window(q, kv_cache, block_table, seq_lens, window, sinks, split_tile
             ws_at = workspace.data_ptr()
     else:
         ws_at, n = _at(workspace, "workspace", torch.uint8, 1, dev), workspace.numel()
-    tail = (split_tiles, out_at, _DTYPE_CODE[out_dtype], lse_at, ws_at, n, _raw_stream(dev))
+    tail = (window, sinks, split_tiles, out_at, _DTYPE_CODE[out_dtype], lse_at, ws_at, n, _raw_stream(dev))
     return out, lse, dev, q_at, cache, (table, lens, B, q_len, H, max_blocks, num_blocks), tail
 
 
@@ -562,7 +566,7 @@ def mla_decode_paged_window(q, kv_cache, block_table, seq_lens, *, sm_scale, win
         q, kv_cache, block_table, seq_lens, window, sinks, split_tiles, out_dtype, out, lse, workspace)
     code = _DTYPE_CODE[q.dtype]
     _check("mla_decode_paged_window", lib.mla_decode_paged_window(
-        q_at, code, q_scale, cache, code, k_scale, *shape, sm_scale, window, sinks, *tail))
+        q_at, code, float(q_scale), cache, code, float(k_scale), *shape, float(sm_scale), *tail))
     return out, lse
 
 
@@ -577,7 +581,7 @@ def mla_decode_paged_scaled(q, kv_cache, kv_scales, block_table, seq_lens, *, sm
         raise TypeError(f"q: dtype {q.dtype} is not torch.float8_e4m3fn")
     scales, sb = _scales_at(kv_scales, shape[6], dev)
     _check("mla_decode_paged_scaled", lib.mla_decode_paged_scaled(
-        q_at, q_scale, cache, scales, sb, *shape, sm_scale, window, sinks, *tail))
+        q_at, float(q_scale), cache, scales, sb, *shape, float(sm_scale), *tail))
     return out, lse
 
 
@@ -610,8 +614,8 @@ def mla_prefill_attn_window(q, k, v, cu_q, cu_k, max_q_len, *, window, sinks=0, 
         if lse.shape != (Tq, H):
             raise ValueError("lse must be [Tq, H]")
     _check("mla_prefill_attn_window", lib.mla_prefill_attn_window(
-        q_at, k_at, v_at, cq, ck, B, Tq, Nk, H, max_q_len, window, sinks, sm_scale, out_at, lse_at,
-        _raw_stream(dev)))
+        q_at, k_at, v_at, cq, ck, B, Tq, Nk, H, int(max_q_len), min(int(window), _INT_MAX),
+        min(int(sinks), _INT_MAX), float(sm_scale), out_at, lse_at, _raw_stream(dev)))
     return out, lse
 
 

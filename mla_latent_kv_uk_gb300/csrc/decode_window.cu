@@ -1356,6 +1356,8 @@ int check_window(const void *q, int q_dtype, float q_scale, const void *kv_cache
   if (kv_dtype == MLA_E4M3 && (!(q_scale > 0.f) || !(q_scale < INFINITY) || !(k_scale > 0.f) ||
                                !(k_scale < INFINITY)))
     return MLA_ERR_INVALID_ARG;
+  // (the kernel takes scales from 2^-100 to 2^120)
+  if (kv_dtype == MLA_E4M3 && (k_scale < 0x1p-100f || k_scale > 0x1p120f)) return MLA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out)) return MLA_ERR_INVALID_ARG;
   return MLA_OK;
 }

@@ -22,8 +22,10 @@
 //
 // Masked keys and values that are not finite: a product over a tile multiplies
 // every value row, also by 0, so a NaN that a query does not see would reach
-// its row.  A row whose columns come out not finite although its scores are is
-// computed again from the definition; rows without such values pay one test.
+// its row.  Values behind the request's last key (padding, which may hold
+// anything) are cleared in shared memory; a row whose columns come out not
+// finite although its scores are is computed again from the definition, by its
+// warp.  Rows without such values pay one test.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -145,24 +147,51 @@ __device__ __forceinline__ bool named_and(uint32_t id, bool v) {
   return r != 0;
 }
 
-// 32 output columns of one query from the definition: p = 2^(s - m) over the
-// keys [0, sinks) and [lo, lim).
+// 32 output columns of one query from the definition, by a whole warp: p =
+// 2^(s - m) over the keys [0, sinks) and [lo, lim), a key per lane at a time.
+// (The others wait for at most a second: a long row has to be done by then.)
 __device__ __noinline__ void row_again(const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                                        const __nv_bfloat16 *v, int64_t k_stride, int64_t v_stride,
                                        int sinks, int lo, int lim, float scale_log2, float m,
                                        float *o) {
-  for (int e = 0; e < 32; ++e) o[e] = 0.f;
-  for (int j = 0; j < lim; ++j) {
-    if (j >= sinks && j < lo) {
-      j = lo - 1;
-      continue;
+  const int lane = lane_id();
+  auto fma8 = [](uint4 a, uint4 b, float s) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s);
+      s = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), s);
     }
+    return s;
+  };
+#pragma unroll
+  for (int e = 0; e < 32; ++e) o[e] = 0.f;
+  for (int j0 = 0; j0 < lim; j0 += 32) {
+    if (j0 >= sinks && j0 + 32 <= lo) j0 = lo & ~31;
+    const int j = j0 + lane;
+    if (j >= lim || (j >= sinks && j < lo)) continue;
+    const uint4 *kr = reinterpret_cast<const uint4 *>(k + j * k_stride);
+    const uint4 *qr = reinterpret_cast<const uint4 *>(q), *vr = reinterpret_cast<const uint4 *>(v + j * v_stride);
     float s = 0.f;
-    for (int d = 0; d < kDq; ++d)
-      s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[j * k_stride + d]), s);
+#pragma unroll 4
+    for (int d = 0; d < kDq / 8; ++d) s = fma8(__ldg(qr + d), __ldg(kr + d), s);
     const float p = ex2(fmaf(s, scale_log2, -m));
-    for (int e = 0; e < 32; ++e) o[e] = fmaf(p, __bfloat162float(v[j * v_stride + e]), o[e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint4 u = __ldg(vr + e);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[8 * e + 2 * i] = fmaf(p, __uint_as_float(w[i] << 16), o[8 * e + 2 * i]);
+        o[8 * e + 2 * i + 1] = fmaf(p, __uint_as_float(w[i] & 0xFFFF0000u), o[8 * e + 2 * i + 1]);
+      }
+    }
   }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+#pragma unroll
+    for (int x = 16; x; x >>= 1) o[e] += __shfl_xor_sync(0xffffffffu, o[e], x);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -393,11 +422,13 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
       return *its;
     };
     auto all_ok = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
-    int c = 0;                                   // tiles of query tile g so far
+    int c = 0, vc = 0;                           // tiles of query tile g, V tiles so far
     bool ok = true;
     for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
       Item it;
       if (!it.load(args, i)) continue;
+      const int vc0 = vc;
+      vc += it.ntiles;
       // (selects: an index would put the arrays into local memory)
       const int nt = g ? it.nt[1] : it.nt[0], skip = g ? it.skip[1] : -1;
       const int rows = g ? it.rows[1] : it.rows[0];
@@ -487,6 +518,15 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
             tmem_st_x32(lane_base + col_o + o0, o);
           }
         }
+        const int inside = it.nk - it.tile(t) * kBN;   // rows of the tile that are this request's
+        if (inside < kBN && (g == 0 || !it.takes(0, t))) {   // (the first of the two to use it)
+          // (its scores being there, the V tiles before it are: no parity is mistaken)
+          if (!(ok = all_ok(wait_for(v_full, (vc0 + t) & 1, abort_flag)))) break;
+          for (int u = ((warp - 4) & 7) * 32 + lane; u < (kBN - inside) * 16; u += 256)
+            *reinterpret_cast<uint4 *>(sm_v + (u & 8 ? kBox : 0) + (inside + (u >> 4)) * 128 + (u & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[g]);
@@ -520,14 +560,19 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         const int col = 64 * sub + o0;
         // (a row whose own scores are not finite, l NaN, stays NaN)
-        if (row_ok && l > 0.f && nan != 0.f) {
+        for (uint32_t again = __ballot_sync(0xffffffffu, row_ok && l > 0.f && nan != 0.f); again;
+             again &= again - 1) {
+          const int from = __ffs(again) - 1;
           float row[32];
           const int64_t ks = static_cast<int64_t>(args.H) * kDq, vs = static_cast<int64_t>(args.H) * kDv;
-          const int h = static_cast<int>(orow % args.H), b = i / args.nqp / args.H;
+          const int64_t at = __shfl_sync(0xffffffffu, orow, from);
+          const int h = static_cast<int>(at % args.H), b = i / args.nqp / args.H;
           const int64_t k0 = __ldg(args.cu_k + b);   // (not kept in a register for this)
-          row_again(args.q + orow * kDq, args.k + k0 * ks + h * kDq, args.v + k0 * vs + h * kDv + col,
-                    ks, vs, args.sinks, wlo, lim, args.scale_log2, m, row);
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(row[k]);
+          row_again(args.q + at * kDq, args.k + k0 * ks + h * kDq, args.v + k0 * vs + h * kDv + col, ks, vs,
+                    args.sinks, __shfl_sync(0xffffffffu, wlo, from), __shfl_sync(0xffffffffu, lim, from),
+                    args.scale_log2, __shfl_sync(0xffffffffu, m, from), row);
+          if (lane == from)
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(row[k]);
         }
         __syncwarp();
         // four lanes turn their rows' four 16-byte chunks round, so that a

@@ -236,6 +236,54 @@ def test_gather_scaled(m, sb):
     assert not out[249].any()
 
 
+def test_captured_step(m):
+    """A decode step (append, then attention over the cache) captured on a
+    stream of its own and replayed for the next tokens gives what eager calls
+    give, scales and all."""
+    g = synth.generator(7700)
+    B, H, nb, sb = 3, 32, 40, 32
+    bt = _i32(g.permutation(nb - 1)[:B * 12].reshape(B, 12))
+    codes, scales = _pool(g, nb, sb)
+    base = np.array([500, 63, 130], np.int32)
+    steps = [(synth.as_bf16(g.standard_normal((B, 576)) * 2.0 ** i).cuda(),
+              synth.as_bf16(g.standard_normal((B, H, 64))).cuda(),
+              synth.as_e4m3(g.standard_normal((B, 1, H, 576)).astype(np.float32)).cuda()) for i in range(4)]
+
+    def state():
+        return (torch.from_numpy(codes).cuda().view(torch.float8_e4m3fn), torch.from_numpy(scales).cuda(),
+                steps[0][0].clone(), steps[0][1].clone(), steps[0][2].clone(), _i32(base))
+
+    def step(cache, sc, kv, q_pe, q, pos):
+        p = pos.long()
+        slots = (bt.long().gather(1, (p // 64)[:, None])[:, 0] * 64 + p % 64).int()
+        m.mla_rope_cache_append(q_pe, kv[:, 512:], kv[:, :512], pos, slots, cache, sc)
+        return m.mla_decode_paged_scaled(q, cache, sc, bt, pos + 1, sm_scale=0.05, window=200, sinks=3)
+
+    eager, got = state(), state()
+    want = []
+    for i, (kv, q_pe, q) in enumerate(steps):
+        for t, x in zip(eager[2:5], (kv, q_pe, q)):
+            t.copy_(x)
+        eager[5].copy_(_i32(base + i))
+        want.append([t.clone() for t in step(*eager)])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*state())                      # warm-up on tensors of its own
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out, lse = step(*got)
+        for i, (kv, q_pe, q) in enumerate(steps):
+            for t, x in zip(got[2:5], (kv, q_pe, q)):
+                t.copy_(x)
+            got[5].copy_(_i32(base + i))
+            graph.replay()
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got[0].view(torch.uint8), eager[0].view(torch.uint8)) and torch.equal(got[1], eager[1])
+    assert m.mla_get_device_error() == 0
+
+
 def test_step_over_a_scaled_cache(m):
     """One serving step as it is used: a prompt's chunk is appended, its
     context gathered, expanded and attended to with a window; then a decode

@@ -129,6 +129,42 @@ def test_next_requests_nan_stays_away(m):
     assert torch.isnan(out[60:]).all()
 
 
+def test_padding_behind_the_keys(m):
+    """Rows behind the last request hold NaN, as a reused buffer may: the last
+    tile's values of many keys, one query tile and two."""
+    for nq, nk, window in ((300, 2999, 2500), (100, 1201, 40), (1, 77, 1000)):
+        q, k, v, cu_q, cu_k = _inputs(80 + nq, [nq], [nk], 2)
+        pad = torch.full((200, 2, 192), float("nan"), dtype=torch.bfloat16)
+        kb, vb = torch.cat([k, pad]), torch.cat([v, pad[:, :, :128]])
+        out, lse = m.mla_prefill_attn_window(q.cuda(), kb.cuda(), vb.cuda(), _i32(cu_q), _i32(cu_k), nq,
+                                             window=window, sinks=5, sm_scale=SCALE)
+        want = m.mla_prefill_attn_window(q.cuda(), k.cuda(), v.cuda(), _i32(cu_q), _i32(cu_k), nq,
+                                         window=window, sinks=5, sm_scale=SCALE)
+        assert m.mla_get_device_error() == 0
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])   # (no row was computed anew)
+
+
+def test_nan_of_a_later_token_in_a_long_window(m):
+    """The last token's values are NaN: the rows before it, computed anew from
+    their 5000 keys, are right, and so is the error word."""
+    q, k, v, cu_q, cu_k = _inputs(81, [140], [6000], 2)
+    vb = v.clone()
+    vb[5999] = float("nan")
+    out, lse = m.mla_prefill_attn_window(q.cuda(), k.cuda(), vb.cuda(), _i32(cu_q), _i32(cu_k), np.int64(140),
+                                         window=np.int64(5000), sinks=7, sm_scale=np.float32(SCALE))
+    assert m.mla_get_device_error() == 0
+    assert torch.isnan(out[139]).all()
+    _check(out, lse, q, k, v, cu_q, cu_k, 5000, 7, "NaN behind", rows=np.arange(140) < 139)
+
+
+def test_a_window_beyond_32_bits(m):
+    q, k, v, cu_q, cu_k = _inputs(82, [30], [90], 1)
+    a = (q.cuda(), k.cuda(), v.cuda(), _i32(cu_q), _i32(cu_k), 30)
+    far = m.mla_prefill_attn_window(*a, window=2 ** 32 + 5, sinks=0, sm_scale=SCALE)
+    want = m.mla_prefill_attn_window(*a, window=90, sinks=0, sm_scale=SCALE)
+    assert torch.equal(far[0], want[0]) and torch.equal(far[1], want[1])
+
+
 def test_graph_replay(m):
     q, k, v, cu_q, cu_k = _inputs(79, [100, 40], [300, 40], 2)
     a = [q.cuda(), k.cuda(), v.cuda(), _i32(cu_q), _i32(cu_k), 100]

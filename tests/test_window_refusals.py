@@ -71,7 +71,7 @@ BAD_DECODE = [
 
 @pytest.mark.parametrize("bad", BAD_DECODE + [
     dict(qd=1), dict(kd=1), dict(qd=2, kd=2), dict(qd=1, kd=1, qs=0.0), dict(qd=1, kd=1, ks=-1.0),
-    dict(qd=1, kd=1, ks=float("nan"))])
+    dict(qd=1, kd=1, ks=float("nan")), dict(qd=1, kd=1, ks=2.0 ** -101), dict(qd=1, kd=1, ks=2.0 ** 121)])
 def test_decode_window(L, bad):
     assert L.mla_decode_paged_window(*_change(DECODE, **bad)) == INVALID
 
@@ -83,6 +83,18 @@ SCALED = dict(q=A, qs=1.0, kv=A, scales=A, sb=64, bt=A, lens=A, B=2, q_len=1, H=
 @pytest.mark.parametrize("bad", BAD_DECODE + [dict(scales=P(0)), dict(sb=0), dict(sb=24), dict(qs=0.0)])
 def test_decode_scaled(L, bad):
     assert L.mla_decode_paged_scaled(*_change(SCALED, **bad)) == INVALID
+
+
+@pytest.mark.gpu
+def test_decode_units_beyond_32_bits(L):
+    """(The grid depends on the device.)  Refused before any launch, as its
+    workspace's size is."""
+    many = dict(B=1024, q_len=64, H=128, mb=1 << 16, window=0)
+    assert L.mla_decode_paged_window(*_change(DECODE, **many)) == INVALID
+    assert L.mla_decode_paged_scaled(*_change(SCALED, **many)) == INVALID
+    n = ctypes.c_size_t(0)
+    assert L.mla_decode_window_workspace_size(1024, 64, 128, 1 << 22, 0, 0, 0, ctypes.byref(n)) == INVALID
+    assert L.mla_decode_window_workspace_size(1024, 64, 128, 1 << 22, 128, 0, 1, ctypes.byref(n)) == OK
 
 
 @pytest.mark.gpu
