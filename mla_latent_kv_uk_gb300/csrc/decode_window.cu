@@ -45,7 +45,11 @@
 // [pC, (p+1)C).  Each CTA works the plan out for itself from the lengths
 // (no plan kernel).  A job that is cut leaves partials in the workspace,
 // which a merge kernel combines: at most two per span, whatever the number
-// of jobs.
+// of jobs.  Partials for a bf16 output are fp16 with a unit for every row and
+// 128 columns: off by 2^-11 of themselves, or 2^-39 of the largest of these,
+// which adds nothing to the output's own rounding (bf16 partials took a batch's
+// error from 2.3e-3 to 2.7e-3 of its rms; fp32 ones are twice the bytes, 2 to 5
+// us of a merge).
 //
 // What bounds it now (each key row takes 128 x 1088 x 2 operations a row group):
 // 64 e4m3 requests of up to 16384 tokens 92 us, at 1.6 of the 1.9 PFLOP/s that
@@ -62,6 +66,7 @@
 #include <algorithm>
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "merge_row.cuh"
@@ -152,8 +157,9 @@ struct WindowArgs {
   int out_f32;
   float *lse;
   int *ws_head;                 // C of each group; then per job {first unit, end unit}
-  void *ws_o;                   // [slots, 128, 512] of the output's type
+  void *ws_o;                   // [slots, 128, 512] fp32, or fp16 for a bf16 output
   float *ws_lse;                // [slots, 128]
+  float *ws_unit;               // [slots, 128, 2, 2] fp16: what 1 stands for, by 128 columns (1, 3; 2, 4)
   int *err;
 };
 
@@ -1053,34 +1059,61 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const float v = empty ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
         (sg.whole ? args.lse : args.ws_lse)[at + r] = v;
       }
+      uint32_t all[128];
+      tmem_ld_x64(lane_base + kColO + 128 * group, all);
+      tmem_ld_x64(lane_base + kColO + 128 * group + 64, all + 64);
+      tc_fence_before();   // (O has been read: the next segment's P V may begin)
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(o_bar);
+      const bool fp16 = !sg.whole && !args.out_f32;
+      float factor = inv;
+      if (fp16) {
+        // the largest finite |O| to [2^14, 2^15)
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 128; k += 2)
+          top = fmax3(top, fabsf(__uint_as_float(all[k])), fabsf(__uint_as_float(all[k + 1])));
+        if (top == INFINITY) {
+          top = 0.f;
+#pragma unroll
+          for (int k = 0; k < 128; ++k) {
+            const float a = fabsf(__uint_as_float(all[k]));
+            if (a < INFINITY) top = fmaxf(top, a);
+          }
+        }
+        const uint32_t exp = max(__float_as_uint(top) >> 23, 15u);
+        factor = __uint_as_float((268u - exp) << 23);
+        if (r < nrows)
+          args.ws_unit[4 * (at + r) + 2 * group + half] = __uint_as_float((exp - 14u) << 23) * inv;
+      }
       // pieces of 64 bytes a row, staged through 2 KB of this warp's own in its
       // group's P tile (in its row block, which the pair writes again behind
       // its next barrier), so that stores cover whole sectors
       uint4 *buf = reinterpret_cast<uint4 *>(sm_p + group * F::kPBytes + block * 4096 + half * 2048);
       static_assert(F::kPBytes >= 4 * 2048, "staging");
-      uint32_t all[128];
-      tmem_ld_x64(lane_base + kColO + 128 * group, all);
-      tmem_ld_x64(lane_base + kColO + 128 * group + 64, all + 64);
+      // (a body for each type of element: 0 bf16, 1 fp16, 2 fp32)
+      auto write = [&](auto type) {
+        constexpr int kType = decltype(type)::value, kPer = kType == 2 ? 16 : 32;   // values of a piece
+        auto pack = [&](int k) -> uint32_t {
+          const float x = __uint_as_float(all[k]) * factor;
+          if constexpr (kType == 2) return __float_as_uint(x);
+          const float y = __uint_as_float(all[k + 1]) * factor;
+          if constexpr (kType == 0) return bf16x2_rn(x, y);
+          const __half2 h = __floats2half2_rn(x, y);
+          return *reinterpret_cast<const uint32_t *>(&h);
+        };
 #pragma unroll
-      for (int q = 0; q < 128; q += 32) {
-        auto f = [&](int k) { return __uint_as_float(all[q + k]) * inv; };
-#pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {     // one (bf16) or two (fp32) pieces
-          if (!args.out_f32 && pc == 1) break;
+        for (int q = 0; q < 128; q += kPer) {
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int e = 16 * pc + 4 * k;
+            constexpr int kStep = kPer / 16;
+            const int e = q + 4 * kStep * k;
             buf[lane * 4 + (k ^ ((lane >> 1) & 3))] =
-                args.out_f32 ? make_uint4(__float_as_uint(f(e)), __float_as_uint(f(e + 1)),
-                                          __float_as_uint(f(e + 2)), __float_as_uint(f(e + 3)))
-                             : make_uint4(bf16x2_rn(f(8 * k), f(8 * k + 1)),
-                                          bf16x2_rn(f(8 * k + 2), f(8 * k + 3)),
-                                          bf16x2_rn(f(8 * k + 4), f(8 * k + 5)),
-                                          bf16x2_rn(f(8 * k + 6), f(8 * k + 7)));
+                make_uint4(pack(e), pack(e + kStep), pack(e + 2 * kStep), pack(e + 3 * kStep));
           }
           __syncwarp();
-          uint8_t *dst = dst0 + static_cast<int64_t>(q + 16 * pc) * esz;
+          uint8_t *dst = dst0 + static_cast<int64_t>(q) * (64 / kPer);
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
             const int row = it * 8 + (lane >> 2), ch = lane & 3;
@@ -1089,10 +1122,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
               reinterpret_cast<uint4 *>(dst + rr * rstride)[ch] = buf[row * 4 + (ch ^ ((row >> 1) & 3))];
           }
         }
-      }
-      tc_fence_before();   // (O has been read: the next segment's P V may begin)
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(o_bar);
+      };
+      if (args.out_f32) write(std::integral_constant<int, 2>{});
+      else if (fp16) write(std::integral_constant<int, 1>{});
+      else write(std::integral_constant<int, 0>{});
     }
     if (!told) named_and(1 + 2 * group + block, 64, ok && !*abort_flag);
   }
@@ -1121,8 +1154,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, SPLIT == 8 ? 1 : SPLIT == 4 
 window_merge_kernel(const __grid_constant__ WindowArgs a) {
   constexpr int kRows = kMergeWarps / SPLIT;    // rows of this CTA
   constexpr int kQuads = sizeof(T);             // 16-byte words of a lane's 16 values
-  // parts on their way: of bf16 10 / 6 / 4
-  constexpr int kRound = (SPLIT == 8 ? 20 : SPLIT == 4 ? 12 : 8) / kQuads;
+  // parts on their way: of fp16 10 / 6 / 2 (one warp a row: 4 of them, in spilled
+  // registers, took 1 us more)
+  constexpr int kRound = (SPLIT == 8 ? 20 : SPLIT == 4 ? 12 : 4) / kQuads;
   __shared__ float part_o[SPLIT > 1 ? kMergeWarps : 1][kLatent];
   __shared__ float part_z[kMergeWarps], part_m[kMergeWarps];
   grid_dep_wait();
@@ -1154,6 +1188,7 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   for (int k0 = mine; k0 < n; k0 += kRound * SPLIT) {
     uint4 raw[kRound][kQuads];
     float w[kRound], top = m;
+    float2 unit[kRound];                        // (of fp16) by the lane's two runs of columns
 #pragma unroll
     for (int u = 0; u < kRound; ++u) {
       const int k = k0 + u * SPLIT;
@@ -1162,6 +1197,7 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
       const int64_t at = static_cast<int64_t>(k == 0 ? 2 * s0 + 1 : 2 * (s0 + k)) * 128 + rr;
       const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.ws_o) + at * kLatent);
       w[u] = __ldg(a.ws_lse + at);
+      if constexpr (kQuads == 2) unit[u] = __ldg(reinterpret_cast<const float2 *>(a.ws_unit) + 2 * at + (lane >> 4));
 #pragma unroll
       for (int i = 0; i < kQuads; ++i)
         raw[u][i] = __ldg(src + i / (kQuads / 2) * 16 * kQuads + lane * (kQuads / 2) + i % (kQuads / 2));
@@ -1186,8 +1222,10 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
           if constexpr (kQuads == 4) {
             acc[4 * i + e] = fmaf(wu, __uint_as_float(v[e]), acc[4 * i + e]);
           } else {
-            acc[8 * i + 2 * e] = fmaf(wu, __uint_as_float(v[e] << 16), acc[8 * i + 2 * e]);
-            acc[8 * i + 2 * e + 1] = fmaf(wu, __uint_as_float(v[e] & 0xFFFF0000u), acc[8 * i + 2 * e + 1]);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[e]));
+            const float wf = wu * (i ? unit[u].y : unit[u].x);
+            acc[8 * i + 2 * e] = fmaf(wf, f.x, acc[8 * i + 2 * e]);
+            acc[8 * i + 2 * e + 1] = fmaf(wf, f.y, acc[8 * i + 2 * e + 1]);
           }
         }
       }
@@ -1305,7 +1343,7 @@ bool shape_ok(int B, int q_len, int H) {
 }
 
 struct WsLayout {
-  size_t o_off, lse_off, total;
+  size_t o_off, lse_off, unit_off, total;
   int groups;
   int64_t group_spans;
   bool solo, fits;              // fits: the units of all jobs count in 32 bits
@@ -1336,7 +1374,8 @@ WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sin
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   w.o_off = up((w.groups + 2 * static_cast<size_t>(J)) * sizeof(int));
   w.lse_off = w.o_off + slots * 128 * kLatent * sizeof(float);
-  w.total = w.lse_off + slots * 128 * sizeof(float);
+  w.unit_off = w.lse_off + slots * 128 * sizeof(float);
+  w.total = w.unit_off + slots * 128 * 4 * sizeof(float);
   return w;
 }
 
@@ -1440,6 +1479,7 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.ws_head = reinterpret_cast<int *>(ws);
   a.ws_o = ws + w.o_off;
   a.ws_lse = reinterpret_cast<float *>(ws + w.lse_off);
+  a.ws_unit = reinterpret_cast<float *>(ws + w.unit_off);
   const int st = fp8 ? launch_pairs<true>(q, kv_cache, a.spans_at_once * w.groups, a, stream)
                      : launch_pairs<false>(q, kv_cache, a.spans_at_once * w.groups, a, stream);
   if (st != MLA_OK || w.solo) return st;

@@ -182,6 +182,28 @@ def test_even_parts(m, fmt):
         c.check(out, lse, f"{fmt} {n}")
 
 
+def test_partials_of_any_magnitude(m):
+    """Values from 2^-90 to 2^90 by runs of 64 columns, cut, rounded to 16 bits
+    and merged: every column as good as its own values allow."""
+    c = Case("bf16", [1300], 1, 16, 0, 0, seed=65)
+    e = np.repeat([-90, 60, 0, 20, -30, -20, -60, 5, 0], 64).astype(np.float64)
+    c.cache = (c.cache.double() * torch.from_numpy(np.exp2(e))).bfloat16()
+    c.q[..., :512] = 0                      # (scores by the last 64 columns)
+    rows = f64(c.cache)[c.bt[0, np.arange(1300) // 64], np.arange(1300) % 64][:, :512]
+    most = torch.from_numpy(np.abs(rows).max(axis=0)).cuda()
+    run = most.view(4, 128).amax(dim=1, keepdim=True).expand(4, 128).reshape(512)
+    want, want_l = c.run(m, out_dtype=torch.float32)
+    assert bool((want.abs() > 0).all())
+    for kw in (dict(), dict(split_tiles=3)):
+        out, lse = c.run(m, **kw)
+        # the output's rounding 2^-8; with weights that sum to 1, the bf16
+        # probabilities of either call 2^-8 of the column's largest value, the
+        # fp16 partials 2^-11 of it or 2^-39 of the largest of 128 columns
+        bound = want.double().abs() * 2.0 ** -8 + most * (2.0 ** -7 + 2.0 ** -10) + run * 2.0 ** -38
+        assert bool(((out.double() - want.double()).abs() <= bound).all())
+        assert float((lse - want_l).abs().max()) <= 1e-4
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "s16"])
 def test_many_requests(m, fmt):
     lens = (np.arange(300) * 37) % 180
