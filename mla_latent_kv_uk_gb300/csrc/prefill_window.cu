@@ -20,6 +20,12 @@
 // The MMA warp runs converged with one elected lane (descriptors stay in
 // uniform registers).
 //
+// What bounds it: 4 x 512 queries over 8192 keys, 128 heads, a window of 1024
+// take 197 us, 0.87 PFLOP/s of visible pairs (1.15 of the tiles, which are
+// partly masked) of the 1.9 that a product reaches.  The tensor pipe is busy half
+// of the time; the softmax between S and P and about 4000 cycles at an item's
+// end are the rest.
+//
 // Masked keys and values that are not finite: a product over a tile multiplies
 // every value row, also by 0, so a NaN that a query does not see would reach
 // its row.  Values behind the request's last key (padding, which may hold
