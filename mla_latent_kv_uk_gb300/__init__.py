@@ -11,7 +11,7 @@ Importing this module raises ImportError if the library has not been built
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 
 import torch
@@ -96,6 +96,25 @@ class MlaError(RuntimeError):
 def _check(fn, status):
     if status != 0:
         raise MlaError(fn, status)
+
+
+def _load_binding():
+    """The compiled module, which gets the entries' addresses from here: there
+    is one library, this process's."""
+    path = _build.binding_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build the CUDA library first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')")
+    spec = importlib.util.spec_from_file_location("_mla_binding", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(_check, *(ctypes.cast(getattr(lib, name), _p).value for name in (
+        "mla_rope_cache_append", "mla_gather_cache_scaled", "mla_decode_window_workspace_size",
+        "mla_decode_paged_window", "mla_decode_paged_scaled", "mla_prefill_attn_window")))
+    return mod
+
+
+_binding = _load_binding()
 
 
 def _stream():
@@ -363,64 +382,9 @@ def mla_rope_cache_write(q_pe, k_pe, kv_c, positions, slot_mapping, kv_cache, *,
         float(k_scale), kv_cache.shape[0], _stream()))
 
 
-# The calls below take microseconds on the device, so their host side is kept
-# short: one look at each tensor that also gives its address (ctypes takes
-# plain integers for pointers), the raw stream handle, and cached sizes.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_Tensor = torch.Tensor
-_INT_MAX = 0x7FFFFFFF   # a window or sinks beyond it are all the same (and would wrap)
-
-
-def _current_device(t, name):
-    """Index of the current device, which the first tensor has to be on."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return dev
-
-
-def _at(t, name, dtype, dims, dev):
-    """Address of a contiguous tensor of this dtype, rank and device."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
-    if t.dim() != dims:
-        raise ValueError(f"{name}: expected {dims} dims, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows_at(t, name, dims, dev):
-    """Address of a bf16 tensor whose last dim is contiguous; the others may be strided."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: dtype {t.dtype} is not torch.bfloat16")
-    if t.dim() != dims:
-        raise ValueError(f"{name}: expected {dims} dims, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.numel():
-        raise ValueError(f"{name}: the last dim must be contiguous")
-    return t.data_ptr()
-
-
-def _scales_at(kv_scales, num_blocks, dev):
-    """Address of kv_scales [num_blocks, 64 / scale_block], and scale_block."""
-    at = _at(kv_scales, "kv_scales", torch.float32, 2, dev)
-    n, per = kv_scales.shape
-    if n != num_blocks or per not in (1, 2, 4):
-        raise ValueError("kv_scales must be [num_blocks, 64 / scale_block], scale_block 16, 32 or 64")
-    return at, 64 // per
+# The calls below take microseconds on the device: their tensors are checked and
+# their results allocated by a compiled module (csrc/binding.cpp), to which a
+# None is a result to allocate.
 
 
 def mla_rope_cache_append(q_pe, k_pe, kv_c, positions, slot_mapping, kv_cache, kv_scales, *,
@@ -431,130 +395,24 @@ def mla_rope_cache_append(q_pe, k_pe, kv_c, positions, slot_mapping, kv_cache, k
     e4m3, kv_scales [num_blocks, 64/scale_block] fp32, both updated.  q_pe, k_pe
     and kv_c may be strided (slices of one projection): strides and offsets of
     8 elements.  Returns (q_out, k_out)."""
-    dev = _current_device(k_pe, "k_pe")
-    k, c = _rows_at(k_pe, "k_pe", 2, dev), _rows_at(kv_c, "kv_c", 2, dev)
-    pos = _at(positions, "positions", torch.int32, 1, dev)
-    slots = _at(slot_mapping, "slot_mapping", torch.int32, 1, dev)
-    cache = _at(kv_cache, "kv_cache", torch.float8_e4m3fn, 3, dev)
-    T, width = k_pe.shape
-    num_blocks, page, row = kv_cache.shape
-    q = qo = ko = None
-    H = qt = qh = 0
-    if q_pe is not None:
-        q = _rows_at(q_pe, "q_pe", 3, dev)
-        n, H, qw = q_pe.shape
-        if n != T or qw != 64:
-            raise ValueError("q_pe must be [T, H, 64]")
-        qt, qh, _ = q_pe.stride()
-    if (width != 64 or kv_c.shape != (T, 512) or positions.numel() != T
-            or slot_mapping.numel() != T or page != 64 or row != 576):
-        raise ValueError("rope / cache-append shapes")
-    scales, sb = _scales_at(kv_scales, num_blocks, dev)
-    if q_out is not None:
-        qo = _at(q_out, "q_out", torch.bfloat16, 3, dev)
-        if q_pe is None or q_out.shape != q_pe.shape:
-            raise ValueError("q_out must have q_pe's shape")
-    if k_out is not None:
-        ko = _at(k_out, "k_out", torch.bfloat16, 2, dev)
-        if k_out.shape != k_pe.shape:
-            raise ValueError("k_out must have k_pe's shape")
-    _check("mla_rope_cache_append", lib.mla_rope_cache_append(
-        q, qt, qh, k, k_pe.stride(0), c, kv_c.stride(0), pos, slots, T, H, float(rope_base),
-        _ROPE_LAYOUT[layout], qo, ko, cache, scales, sb, num_blocks, _raw_stream(dev)))
+    _binding.append(q_pe, k_pe, kv_c, positions, slot_mapping, kv_cache, kv_scales, rope_base,
+                    _ROPE_LAYOUT[layout], q_out, k_out)
     return (q_pe if q_out is None else q_out), (k_pe if k_out is None else k_out)
 
 
 def mla_gather_cache_scaled(kv_cache, kv_scales, block_table, seq_lens, cu_out, total_rows, *,
                             seq_starts=None, out=None):
     """mla_gather_cache out of a block-scaled e4m3 cache, as bf16 rows [total_rows, 576]."""
-    dev = _current_device(kv_cache, "kv_cache")
-    cache = _at(kv_cache, "kv_cache", torch.float8_e4m3fn, 3, dev)
-    table = _at(block_table, "block_table", torch.int32, 2, dev)
-    lens = _at(seq_lens, "seq_lens", torch.int32, 1, dev)
-    cu = _at(cu_out, "cu_out", torch.int32, 1, dev)
-    B, max_blocks = block_table.shape
-    num_blocks, page, row = kv_cache.shape
-    if page != 64 or row != 576 or seq_lens.numel() != B or cu_out.numel() != B + 1:
-        raise ValueError("gather shapes")
-    starts = None
-    if seq_starts is not None:
-        starts = _at(seq_starts, "seq_starts", torch.int32, 1, dev)
-        if seq_starts.numel() != B:
-            raise ValueError("seq_starts must be [B]")
-    scales, sb = _scales_at(kv_scales, num_blocks, dev)
-    total_rows = int(total_rows)
-    if out is None:
-        out = torch.empty((total_rows, 576), dtype=torch.bfloat16, device=kv_cache.device)
-        to = out.data_ptr()
-    else:
-        to = _at(out, "out", torch.bfloat16, 2, dev)
-        if out.shape != (total_rows, 576):
-            raise ValueError("out must be [total_rows, 576]")
-    _check("mla_gather_cache_scaled", lib.mla_gather_cache_scaled(
-        cache, scales, sb, table, lens, starts, cu, B, max_blocks, num_blocks, total_rows, to,
-        _raw_stream(dev)))
-    return out
+    return _binding.gather(kv_cache, kv_scales, block_table, seq_lens, cu_out, total_rows, seq_starts, out)
 
 
 def mla_decode_window_workspace_size(B, q_len, H, max_seq_len, window=0, sinks=0,
                                      split_tiles=0) -> int:
     n = _sz(0)
     _check("mla_decode_window_workspace_size", lib.mla_decode_window_workspace_size(
-        B, q_len, H, max_seq_len, min(int(window), _INT_MAX), min(int(sinks), _INT_MAX),
+        B, q_len, H, max_seq_len, min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF),
         int(split_tiles), ctypes.byref(n)))
     return n.value
-
-
-@functools.lru_cache(maxsize=1024)
-def _window_workspace(dev, *shape):
-    """(The size depends on the device's SMs, so the device is part of the key.)"""
-    return mla_decode_window_workspace_size(*shape)
-
-
-def _decode_window(q, kv_cache, block_table, seq_lens, window, sinks, split_tiles, out_dtype, out,
-                   lse, workspace):
-    """Checks and allocations that the two windowed decodes share: the outputs and the
-    arguments from the device and the query's address on."""
-    dev = _current_device(q, "q")
-    dtype = q.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float8_e4m3fn:
-        raise TypeError(f"q: dtype {dtype} is neither bf16 nor e4m3")
-    q_at = _at(q, "q", dtype, 4, dev)
-    cache = _at(kv_cache, "kv_cache", dtype, 3, dev)
-    table = _at(block_table, "block_table", torch.int32, 2, dev)
-    lens = _at(seq_lens, "seq_lens", torch.int32, 1, dev)
-    B, q_len, H, D = q.shape
-    num_blocks, page, row = kv_cache.shape
-    b, max_blocks = block_table.shape
-    if D != 576 or page != 64 or row != 576 or b != B or seq_lens.numel() != B:
-        raise ValueError("decode shapes")
-    window, sinks, split_tiles = min(int(window), _INT_MAX), min(int(sinks), _INT_MAX), int(split_tiles)
-    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
-        raise TypeError(f"out_dtype {out_dtype} is neither bf16 nor fp32")
-    if out is None:
-        out = torch.empty((B, q_len, H, 512), dtype=out_dtype, device=q.device)
-        out_at = out.data_ptr()
-    else:
-        out_at = _at(out, "out", out_dtype, 4, dev)
-        if out.shape != (B, q_len, H, 512):
-            raise ValueError("out must be [B, q_len, H, 512]")
-    if lse is None:
-        lse = torch.empty((B, q_len, H), dtype=torch.float32, device=q.device)
-        lse_at = lse.data_ptr()
-    else:
-        lse_at = _at(lse, "lse", torch.float32, 3, dev)
-        if lse.shape != (B, q_len, H):
-            raise ValueError("lse must be [B, q_len, H]")
-    ws_at, n = None, 0
-    if workspace is None:
-        n = _window_workspace(dev, B, q_len, H, max_blocks * 64, window, sinks, split_tiles)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-            ws_at = workspace.data_ptr()
-    else:
-        ws_at, n = _at(workspace, "workspace", torch.uint8, 1, dev), workspace.numel()
-    tail = (window, sinks, split_tiles, out_at, _DTYPE_CODE[out_dtype], lse_at, ws_at, n, _raw_stream(dev))
-    return out, lse, dev, q_at, cache, (table, lens, B, q_len, H, max_blocks, num_blocks), tail
 
 
 def mla_decode_paged_window(q, kv_cache, block_table, seq_lens, *, sm_scale, window, sinks=0,
@@ -562,12 +420,8 @@ def mla_decode_paged_window(q, kv_cache, block_table, seq_lens, *, sm_scale, win
                             out=None, lse=None, workspace=None):
     """mla_decode_paged (causal) where a query at position p sees the keys
     j > p - window and the first `sinks` (window 0: every earlier key)."""
-    out, lse, _, q_at, cache, shape, tail = _decode_window(
-        q, kv_cache, block_table, seq_lens, window, sinks, split_tiles, out_dtype, out, lse, workspace)
-    code = _DTYPE_CODE[q.dtype]
-    _check("mla_decode_paged_window", lib.mla_decode_paged_window(
-        q_at, code, float(q_scale), cache, code, float(k_scale), *shape, float(sm_scale), *tail))
-    return out, lse
+    return _binding.decode(q, kv_cache, None, block_table, seq_lens, sm_scale, q_scale, k_scale, window,
+                           sinks, split_tiles, out_dtype, out, lse, workspace)
 
 
 def mla_decode_paged_scaled(q, kv_cache, kv_scales, block_table, seq_lens, *, sm_scale,
@@ -575,48 +429,17 @@ def mla_decode_paged_scaled(q, kv_cache, kv_scales, block_table, seq_lens, *, sm
                             out_dtype=torch.bfloat16, out=None, lse=None, workspace=None):
     """mla_decode_paged_window over a block-scaled e4m3 cache (q e4m3,
     kv_scales [num_blocks, 64/scale_block] fp32)."""
-    out, lse, dev, q_at, cache, shape, tail = _decode_window(
-        q, kv_cache, block_table, seq_lens, window, sinks, split_tiles, out_dtype, out, lse, workspace)
-    if q.dtype is not torch.float8_e4m3fn:
-        raise TypeError(f"q: dtype {q.dtype} is not torch.float8_e4m3fn")
-    scales, sb = _scales_at(kv_scales, shape[6], dev)
-    _check("mla_decode_paged_scaled", lib.mla_decode_paged_scaled(
-        q_at, float(q_scale), cache, scales, sb, *shape, float(sm_scale), *tail))
-    return out, lse
+    if kv_scales is None:
+        raise TypeError("kv_scales must be a tensor")
+    return _binding.decode(q, kv_cache, kv_scales, block_table, seq_lens, sm_scale, q_scale, 1.0, window,
+                           sinks, split_tiles, out_dtype, out, lse, workspace)
 
 
 def mla_prefill_attn_window(q, k, v, cu_q, cu_k, max_q_len, *, window, sinks=0, sm_scale, out=None,
                             lse=None):
     """mla_prefill_attn (causal) where a query at position p of its request sees
     the keys j > p - window and the first `sinks`."""
-    dev = _current_device(q, "q")
-    q_at = _at(q, "q", torch.bfloat16, 3, dev)
-    k_at = _at(k, "k", torch.bfloat16, 3, dev)
-    v_at = _at(v, "v", torch.bfloat16, 3, dev)
-    cq, ck = _at(cu_q, "cu_q", torch.int32, 1, dev), _at(cu_k, "cu_k", torch.int32, 1, dev)
-    Tq, H, dq = q.shape
-    Nk = k.shape[0]
-    B = cu_q.numel() - 1
-    if dq != 192 or k.shape != (Nk, H, 192) or v.shape != (Nk, H, 128) or cu_k.numel() != B + 1:
-        raise ValueError("prefill shapes")
-    if out is None:
-        out = torch.empty((Tq, H, 128), dtype=torch.bfloat16, device=q.device)
-        out_at = out.data_ptr()
-    else:
-        out_at = _at(out, "out", torch.bfloat16, 3, dev)
-        if out.shape != (Tq, H, 128):
-            raise ValueError("out must be [Tq, H, 128]")
-    if lse is None:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-        lse_at = lse.data_ptr()
-    else:
-        lse_at = _at(lse, "lse", torch.float32, 2, dev)
-        if lse.shape != (Tq, H):
-            raise ValueError("lse must be [Tq, H]")
-    _check("mla_prefill_attn_window", lib.mla_prefill_attn_window(
-        q_at, k_at, v_at, cq, ck, B, Tq, Nk, H, int(max_q_len), min(int(window), _INT_MAX),
-        min(int(sinks), _INT_MAX), float(sm_scale), out_at, lse_at, _raw_stream(dev)))
-    return out, lse
+    return _binding.prefill(q, k, v, cu_q, cu_k, max_q_len, window, sinks, sm_scale, out, lse)
 
 
 def mla_stage_copy(dst, src):

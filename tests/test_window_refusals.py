@@ -132,3 +132,91 @@ def test_prefill_window(L, bad):
 
 def test_prefill_window_no_queries(L):
     assert L.mla_prefill_attn_window(*_change(PREFILL, Tq=0, q=P(0))) == OK
+
+
+# ------------------------------------------------- the Python calls' checks
+def _calls(m, dev):
+    """One good set of arguments for each call, by name."""
+    def z(*s, dtype=torch.int32):
+        return torch.zeros(s, dtype=torch.uint8 if dtype is E4M3 else dtype, device=dev).view(dtype)
+
+    E4M3, BF = torch.float8_e4m3fn, torch.bfloat16
+    cache, scales = z(3, 64, 576, dtype=E4M3), torch.ones((3, 2), device=dev)
+    table, lens = z(2, 1), z(2)
+    return {
+        m.mla_rope_cache_append: dict(q_pe=z(4, 2, 64, dtype=BF), k_pe=z(4, 64, dtype=BF), kv_c=z(4, 512, dtype=BF),
+                                      positions=z(4), slot_mapping=z(4), kv_cache=cache, kv_scales=scales,
+                                      q_out=z(4, 2, 64, dtype=BF), k_out=z(4, 64, dtype=BF)),
+        m.mla_gather_cache_scaled: dict(kv_cache=cache, kv_scales=scales, block_table=table, seq_lens=lens,
+                                        cu_out=z(3), total_rows=0, seq_starts=z(2), out=z(0, 576, dtype=BF)),
+        m.mla_decode_paged_window: dict(q=z(2, 1, 4, 576, dtype=E4M3), kv_cache=cache, block_table=table,
+                                        seq_lens=lens, sm_scale=1.0, window=0, out=z(2, 1, 4, 512, dtype=BF),
+                                        lse=z(2, 1, 4, dtype=torch.float32)),
+        m.mla_decode_paged_scaled: dict(q=z(2, 1, 4, 576, dtype=E4M3), kv_cache=cache, kv_scales=scales,
+                                        block_table=table, seq_lens=lens, sm_scale=1.0,
+                                        out=z(2, 1, 4, 512, dtype=BF), lse=z(2, 1, 4, dtype=torch.float32)),
+        m.mla_prefill_attn_window: dict(q=z(4, 2, 192, dtype=BF), k=z(4, 2, 192, dtype=BF), v=z(4, 2, 128, dtype=BF),
+                                        cu_q=z(2), cu_k=z(2), max_q_len=0, window=8, sm_scale=1.0,
+                                        out=z(4, 2, 128, dtype=BF), lse=z(4, 2, dtype=torch.float32)),
+    }
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mla_latent_kv_uk_gb300 as mod
+    return mod
+
+
+def test_tensors_of_the_host_and_other_things(m):
+    for call, kw in _calls(m, "cpu").items():
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call(**kw)
+        with pytest.raises(TypeError, match="must be a tensor"):
+            call(**{**kw, **{k: 3 for k in ("k_pe", "kv_cache", "q") if k in kw}})
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(KeyError):
+        m.mla_rope_cache_append(**_calls(m, "cpu")[m.mla_rope_cache_append], layout="neither")
+
+
+@pytest.mark.gpu
+def test_python_checks(m):
+    """Every tensor in turn of another type, rank, device and stride, and of
+    another length; numbers that are none."""
+    for call, kw in _calls(m, "cuda").items():
+        call(**kw)                              # as it stands it is taken
+        for name, t in kw.items():
+            if not isinstance(t, torch.Tensor):
+                with pytest.raises(TypeError):
+                    call(**{**kw, name: "x"})
+                continue
+            for bad, errors in ((t.unsqueeze(0), ValueError), (t.cpu(), ValueError),
+                                (torch.zeros(t.shape, dtype=torch.float64, device="cuda"), TypeError),
+                                ([1], TypeError)):
+                with pytest.raises(errors):
+                    call(**{**kw, name: bad})
+            if t.numel() > 1:
+                wide = torch.zeros((*t.shape, 2), dtype=torch.uint8 if t.dtype == torch.float8_e4m3fn else t.dtype,
+                                   device="cuda").view(t.dtype)[..., 0]
+                with pytest.raises(ValueError):
+                    call(**{**kw, name: wide})
+            if t.numel() and (name != "kv_cache" or "kv_scales" in kw):    # (else any number of blocks will do)
+                with pytest.raises((ValueError, TypeError)):
+                    call(**{**kw, name: t[:-1]})
+        with pytest.raises(ValueError):
+            call(**{**kw, **({"total_rows": 2 ** 40} if "total_rows" in kw else
+                             {"max_q_len": -2 ** 40} if "max_q_len" in kw else
+                             {"split_tiles": 2 ** 31} if "sm_scale" in kw else {"kv_scales": kw["kv_scales"][:, :0]})})
+    assert m.mla_get_device_error() in (0, 1)   # (the tables' zeros are block 0)
+
+
+@pytest.mark.gpu
+def test_status_becomes_the_librarys_error(m):
+    kw = _calls(m, "cuda")[m.mla_prefill_attn_window]
+    with pytest.raises(m.MlaError) as e:
+        m.mla_prefill_attn_window(**{**kw, "window": 0})
+    assert e.value.status == INVALID and "mla_prefill_attn_window" in str(e.value)
+    kw = _calls(m, "cuda")[m.mla_decode_paged_window]
+    with pytest.raises(m.MlaError) as e:
+        m.mla_decode_paged_window(**{**kw, "split_tiles": 1, "workspace": torch.zeros(8, dtype=torch.uint8, device="cuda")})
+    assert e.value.status == WORKSPACE
