@@ -10,8 +10,9 @@
 // that hold a sink or a key of the window are loaded, so an item has few of
 // them (a window of 1024: eleven) and what comes before its first product and
 // after its last one counts as much as the products.  Hence
-//   * the CTAs are persistent, one per SM: the loads of the next item's keys
-//     and the barriers, tensor memory and descriptors are there already;
+//   * the CTAs are persistent, one per SM: the barriers, tensor memory and
+//     descriptors are there already, and the next item's query and keys load
+//     while the last results are written;
 //   * two threads share a query row (64 keys each): S_g(t + 1) follows
 //     P_g(t) V in the same columns, so a softmax's latency is on the path
 //     twice a tile;
@@ -21,10 +22,15 @@
 // uniform registers).
 //
 // What bounds it: 4 x 512 queries over 8192 keys, 128 heads, a window of 1024
-// take 192 us, 0.90 PFLOP/s of visible pairs (1.15 of the tiles, which are
-// partly masked) of the 1.9 that a product reaches.  The tensor pipe is busy half
-// of the time; the softmax between S and P and about 4000 cycles at an item's
-// end are the rest.
+// take 188 us, 0.92 PFLOP/s of visible pairs (1.15 of the tiles, which are
+// partly masked) of the 1.9 that a product reaches.  A key tile of both query
+// tiles takes 3650 cycles where its MMAs take 2560: S, softmax, P and O follow
+// one another, and tensor memory is full, so no S runs ahead.  About 10000 of an
+// item's 50000 cycles pass between its last product and the next item's second
+// tile: the results, the query's load, and a first tile without anything beside
+// it.  Tried: results by warps of their own (80 registers for the softmax: 232
+// us), fewer MMA steps for the sinks' tile (196), the next item's query or keys
+// fetched into L2 ahead (196, 188), a barrier for either query tile (188).
 //
 // Masked keys and values that are not finite: a product over a tile multiplies
 // every value row, also by 0, so a NaN that a query does not see would reach
@@ -51,7 +57,6 @@ constexpr int kDq = 192, kDv = 128;
 constexpr int kBox = 128 * 128;                  // 128 rows x 64 bf16
 constexpr int kQBytes = 3 * kBox, kKBytes = 3 * kBox, kVBytes = 2 * kBox;
 constexpr int kKStages = 2;
-constexpr int kAhead = 4;                        // key tiles fetched into L2 ahead of their loads
 constexpr int kOffK = kQT * kQBytes;
 constexpr int kOffV = kOffK + kKStages * kKBytes;
 constexpr int kOffX = kOffV + kVBytes;           // [2][256] row maxima, then sums
@@ -114,10 +119,6 @@ struct Item {
   __device__ __forceinline__ bool takes(int g, int t) const { return t < nt[g] && t != skip[g]; }
 };
 
-__device__ __forceinline__ void prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z) : "memory");
-}
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -259,30 +260,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
     if (lane == 0) {
       bool ok = true;
       int kc = 0, n = 0;                       // K tiles, items with tiles so far
-      // Keys and values of the tiles ahead, the next item's too, go to L2: the
-      // single V tile is loaded while its products wait, which hides the way
-      // from L2 but not the one from DRAM.
-      Item nx;
-      int ni = blockIdx.x, nt = 0, fetched = 0;
-      bool open = false;
-      auto fetch = [&]() {
-        while (!open) {
-          if (ni >= args.items) return;
-          open = nx.load(args, ni) && nx.ntiles > 0;
-          nt = 0;
-          if (!open) ni += gridDim.x;
-        }
-        const int row = nx.k0 + nx.tile(nt) * kBN;
-        if (fetched > 0) {                     // (the very first tile is loaded at once)
-          for (int d = 0; d < 3; ++d) prefetch_3d(&tm_k, 64 * d, nx.h, row);
-          for (int d = 0; d < 2; ++d) prefetch_3d(&tm_v, 64 * d, nx.h, row);
-        }
-        ++fetched;
-        if (++nt == nx.ntiles) {
-          open = false;
-          ni += gridDim.x;
-        }
-      };
       for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
         Item it;
         if (!it.load(args, i) || it.ntiles == 0) continue;
@@ -302,7 +279,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
           for (int d = 0; d < 3; ++d)
             tma_load_3d(sm_k + s * kKBytes + d * kBox, &tm_k, &k_full[s], 64 * d, it.h,
                         it.k0 + it.tile(t) * kBN);
-          for (int e = kc == 0 ? -kAhead : 0; e <= 0; ++e) fetch();
         }
       }
       if (*abort_flag) {
@@ -467,7 +443,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
         };
         // 32 rows by 32 keys that nobody sees need no exponentials: 6 of 16 of
         // the tiles on the diagonal and at the window's edge, 15 of a few sinks'
-        // (196 us without)
         const bool none[2] = {!__any_sync(0xffffffffu, static_cast<uint32_t>(seen) != 0),
                               !__any_sync(0xffffffffu, static_cast<uint32_t>(seen >> 32) != 0)};
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -570,12 +545,16 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
       for (int o0 = 0; o0 < 64; o0 += 32) {
         uint32_t o[32];
         if (any) tmem_ld_x32(lane_base + col_o + o0, o);
-        float nan = 0.f;   // NaN if a column is not finite
+        if (__any_sync(0xffffffffu, empty)) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          if (empty) o[k] = 0;
-          nan = fmaf(__uint_as_float(o[k]), 0.f, nan);
+          for (int k = 0; k < 32; ++k)
+            if (empty) o[k] = 0;
         }
+        float nan = 0.f, nan2 = 0.f;   // NaN if a column is not finite
+#pragma unroll
+        for (int k = 0; k < 32; k += 2)
+          fma_f32x2(nan, nan2, __uint_as_float(o[k]), __uint_as_float(o[k + 1]), 0.f, 0.f, nan, nan2);
+        nan += nan2;
         const int col = 64 * sub + o0;
         // (a row whose own scores are not finite, l NaN, stays NaN)
         for (uint32_t again = __ballot_sync(0xffffffffu, row_ok && l > 0.f && nan != 0.f); again;
@@ -597,11 +576,14 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
         // store covers 64 bytes of eight rows and not 16 of 32 (which took
         // 4000 cycles an item)
         uint4 w[4];
-        auto f = [&](int k) { return __uint_as_float(o[k]) * inv; };
+        auto f = [&](int k) {
+          float a, b;
+          fma_f32x2(a, b, __uint_as_float(o[k]), __uint_as_float(o[k + 1]), inv, inv, -0.f, -0.f);
+          return bf16x2_rn(a, b);
+        };
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
-          w[ch] = make_uint4(bf16x2_rn(f(8 * ch), f(8 * ch + 1)), bf16x2_rn(f(8 * ch + 2), f(8 * ch + 3)),
-                             bf16x2_rn(f(8 * ch + 4), f(8 * ch + 5)), bf16x2_rn(f(8 * ch + 6), f(8 * ch + 7)));
+          w[ch] = make_uint4(f(8 * ch), f(8 * ch + 2), f(8 * ch + 4), f(8 * ch + 6));
 #pragma unroll
         for (int s = 1; s < 4; s <<= 1) {
           const bool up = lane & s;
