@@ -17,8 +17,8 @@
 // them has the same block.
 //
 // What bounds it: a step (32 tokens, 128 heads: 1 MB) is one chain of loads
-// (slots, rows), arithmetic and stores, 4.2 us with the launch.  A chunk moves
-// its queries, read and written: 63 MB in 15.6 us, 4.1 TB/s of the 6.8 that a
+// (slots, rows), arithmetic and stores, 4.0 us with the launch.  A chunk moves
+// its queries, read and written: 63 MB in 15.3 us, 4.1 TB/s of the 6.8 that a
 // copy reaches, the first 3 us of which look at slots and fill the memory
 // pipes.  Measured on the way there: a CTA for each token, that looks at the
 // slots and leaves, 18.5 us; rows read again for their codes instead of kept,
@@ -327,6 +327,8 @@ __device__ __forceinline__ void append_tokens(const AppendArgs &p, const Turns &
 // The first CTAs take the cache rows, the others rotate 256 (token, head) rows.
 __global__ void __launch_bounds__(kThreads, 2)
 append_kernel(const __grid_constant__ AppendArgs p, const __grid_constant__ Turns turns) {
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
   if (blockIdx.x < p.append_ctas) {
     append_tokens(p, turns);
     return;
@@ -480,6 +482,8 @@ extern "C" int mla_rope_cache_append(void *q_pe, int64_t q_stride_t, int64_t q_s
     for (int i = 0; i < bit; ++i) f[bit + i] = f[i] * step;
   }
   for (int i = 0; i < kPairs; ++i) turns.per_pos[i] = static_cast<unsigned long long>(f[i]);
-  append_kernel<<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(p, turns);
-  return launch_status();
+  return launch_pdl(append_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, stream, p, turns) ==
+                 cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }

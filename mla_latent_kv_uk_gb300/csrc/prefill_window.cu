@@ -254,6 +254,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+  grid_dep_launch();
 
   if (warp == 0) {
     // ------------------------------------------------------ Q and K
@@ -675,6 +677,8 @@ extern "C" int mla_prefill_attn_window(const void *q, const void *k, const void 
                                       kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
   const int grid = std::min(sms, a.items);
-  prefill_window_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, a);
-  return launch_status();
+  return launch_pdl(prefill_window_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, tq, tk, tv, a) ==
+                 cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }
