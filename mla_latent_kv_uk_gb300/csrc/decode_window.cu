@@ -908,12 +908,17 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             break;
           old = x_ref[64 * (group ^ 1) + r];
         }
-        const bool move = top > old + kLazy || (old == -INFINITY && top > -INFINITY);
+        // Where one of the warp's rows has to move, all that can do so: the pass
+        // over O is paid for, and the next one is further off.  (The row's other
+        // thread, in a warp of the same rows, decides alike.)
+        const bool must = top > old + kLazy || (old == -INFINITY && top > -INFINITY);
+        const bool moves = __any_sync(0xffffffffu, must);
+        const bool move = moves && top - F::kTop > old;
         const float now = move ? top - F::kTop : old;
         if (half == 0) x_ref[64 * group + r] = now;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ref_there[2 * group + block]);
-        const bool rescale = t > 0 && __any_sync(0xffffffffu, move);
+        const bool rescale = t > 0 && moves;
         const float f = move ? (old == -INFINITY ? 0.f : ex2(old - now)) : 1.f;
         if (ref != now && l != 0.f) l *= ex2(ref - now);
         ref = now;
