@@ -38,7 +38,7 @@
 // 1 issues the MMAs (leader CTA), 2 loads V, 4..11 turn scores into
 // probabilities (two groups taking the tiles in turn, one row and half of the
 // tile's keys per thread) and write the results.  Lazy rescaling: O is rescaled when a row's reference would
-// be exceeded by more than 2^8.
+// be exceeded by more than 2^kLazy.
 //
 // Split: every row group of a request is a job of its list's tiles plus
 // kJobCost units for the switch; jobs lie end to end and pair p takes units
@@ -139,8 +139,9 @@ struct Fmt {
   static_assert(kKSlotBytes % 1024 == 0 && kQBytes % 1024 == 0 && kKBox % 1024 == 0, "swizzled tiles");
   // p' of a row's largest key after the reference moved, as a power of two
   static constexpr float kTop = FP8 ? 5.f : 0.f;
+  // p' is at most 2^kLazy before it moves again: e4m3 holds 448 > 2^8.75
+  static constexpr float kLazy = FP8 ? 8.75f : 16.f;
 };
-constexpr float kLazy = 8.f;              // p' is at most 2^kLazy
 
 struct WindowArgs {
   const float *scales;          // nullptr: k_scale
@@ -911,7 +912,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         // Where one of the warp's rows has to move, all that can do so: the pass
         // over O is paid for, and the next one is further off.  (The row's other
         // thread, in a warp of the same rows, decides alike.)
-        const bool must = top > old + kLazy || (old == -INFINITY && top > -INFINITY);
+        const bool must = top > old + F::kLazy || (old == -INFINITY && top > -INFINITY);
         const bool moves = __any_sync(0xffffffffu, must);
         const bool move = moves && top - F::kTop > old;
         const float now = move ? top - F::kTop : old;
