@@ -4,8 +4,8 @@
 // Rows and keys.  The q_len * H query rows of a request (query token outer,
 // head inner) all attend to the same latent rows, so they are taken in groups
 // of 128: per tile of T keys (e4m3: 128, bf16: 64) S = Q K^T is a dense
-// [128 x T x 576] product and O += P V a [128 x 512 x T] one.  A request's keys are a list of
-// 64-token pages, the sinks' pages and then those from the window's first key
+// [128 x T x 576] product and O += P V a [128 x 512 x T] one.  A request's keys
+// are a list of 64-token pages, the sinks' pages and then those from the window's first key
 // to the last query; only the list's pages are loaded.  Each row masks the
 // keys that it does not see.
 //
@@ -37,8 +37,8 @@
 // Warps: 0 walks the split plan, publishes the segments and loads Q and K,
 // 1 issues the MMAs (leader CTA), 2 loads V, 4..11 turn scores into
 // probabilities (two groups taking the tiles in turn, one row and half of the
-// tile's keys per thread) and write the results.  Lazy rescaling: O is rescaled when a row's reference would
-// be exceeded by more than 2^kLazy.
+// tile's keys per thread) and write the results.  Lazy rescaling: O is rescaled
+// when a row's reference would be exceeded by more than 2^kLazy.
 //
 // Split: every row group of a request is a job of its list's tiles plus
 // kJobCost units for the switch; jobs lie end to end and pair p takes units
@@ -52,7 +52,7 @@
 // us of a merge).
 //
 // What bounds it now (each key row takes 128 x 1088 x 2 operations a row group):
-// 64 e4m3 requests of up to 16384 tokens 92 us, at 1.6 of the 1.9 PFLOP/s that
+// 64 e4m3 requests of up to 16384 tokens 90 us, at 1.65 of the 1.9 PFLOP/s that
 // a bf16 product reaches, near the 1632 cycles of a tile's MMAs; 128 bf16
 // requests of two tokens and a window of 4096 146 us, 1.15 PFLOP/s, where Q K^T
 // of 64 keys takes as long as one of 128; one e4m3 request of 131072 tokens

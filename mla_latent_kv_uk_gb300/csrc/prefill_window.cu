@@ -22,7 +22,7 @@
 // uniform registers).
 //
 // What bounds it: 4 x 512 queries over 8192 keys, 128 heads, a window of 1024
-// take 188 us, 0.92 PFLOP/s of visible pairs (1.15 of the tiles, which are
+// take 187 us, 0.92 PFLOP/s of visible pairs (1.15 of the tiles, which are
 // partly masked) of the 1.9 that a product reaches.  A key tile of both query
 // tiles takes 3650 cycles where its MMAs take 2560: S, softmax, P and O follow
 // one another, and tensor memory is full, so no S runs ahead.  About 10000 of an
@@ -64,7 +64,7 @@ constexpr int kOffBars = kOffX + 2 * 256 * 4;
 constexpr int kSmemBytes = kOffBars + 256;
 constexpr int kSoftWarps = 16;
 constexpr int kThreads = (4 + kSoftWarps) * 32;
-constexpr float kLazy = 8.f;                     // O follows a maximum that grew by more than 2^8
+constexpr float kLazy = 16.f;                    // O follows a maximum that grew by more than 2^16
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct Args {
