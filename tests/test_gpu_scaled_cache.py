@@ -284,6 +284,56 @@ def test_captured_step(m):
     assert m.mla_get_device_error() == 0
 
 
+def test_calls_close_behind_one_another(m):
+    """Append, gather, prefill and decode on the same cache, twenty times over
+    without a wait between them (each starts while the one before drains), give
+    bit for bit what they give with a wait behind each call."""
+    g = synth.generator(7800)
+    B, H, sb, window, sinks, nb, new = 4, 16, 16, 150, 3, 60, 37
+    bt = g.permutation(nb - 1)[:B * 14].reshape(B, 14).astype(np.int32)
+    w = synth.as_bf16(g.standard_normal((H * 256, 512)) * 0.05).cuda()
+    steps = []
+    for i in range(20):
+        lens = np.full(B, (i + 1) * new) + np.arange(B)
+        slots = np.concatenate([bt[b, np.arange(n - new, n) // 64] * 64 + np.arange(n - new, n) % 64
+                                for b, n in enumerate(lens)])
+        kv = synth.as_bf16(g.standard_normal((B * new, 576)) * 2.0 ** (i % 5)).cuda()
+        q = synth.as_bf16(g.standard_normal((B * new, H, 192))).cuda()
+        q1 = synth.as_e4m3(g.standard_normal((B, 1, H, 576)).astype(np.float32)).cuda()
+        steps.append((kv, q, q1, _i32(lens), _i32(slots), _i32(np.arange(B * new)),
+                      _i32(np.concatenate([[0], np.cumsum(lens)])), int(lens.sum()),
+                      _i32(np.arange(B + 1) * new)))
+    table = _i32(bt)
+
+    def run(wait):
+        cache = torch.zeros((nb, 64, 576), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        sc = torch.zeros((nb, 64 // sb), device="cuda")
+        got = []
+        for kv0, q0, q1, lens, slots, pos, cu_k, total, cu_q in steps:
+            kv, q = kv0.clone(), q0.clone()
+            torch.cuda.synchronize()
+            m.mla_rope_cache_append(q[:, :, 128:], kv[:, 512:], kv[:, :512], pos, slots, cache, sc)
+            wait()
+            rows = m.mla_gather_cache_scaled(cache, sc, table, lens, cu_k, total)
+            wait()
+            K, V = m.mla_expand_kv(rows, w, H)
+            wait()
+            a = m.mla_prefill_attn_window(q, K, V, cu_q, cu_k, new, window=window, sinks=sinks, sm_scale=0.07)
+            wait()
+            b = m.mla_decode_paged_scaled(q1, cache, sc, table, lens, sm_scale=0.01, window=0)
+            wait()
+            c = m.mla_decode_paged_scaled(q1, cache, sc, table, lens, sm_scale=0.01, window=window, sinks=sinks)
+            wait()
+            got += [rows, q, *a, *b, *c]
+        torch.cuda.synchronize()
+        return got + [cache.view(torch.uint8), sc]
+
+    want, got = run(torch.cuda.synchronize), run(lambda: None)
+    assert m.mla_get_device_error() == 0
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+
+
 def test_step_over_a_scaled_cache(m):
     """One serving step as it is used: a prompt's chunk is appended, its
     context gathered, expanded and attended to with a window; then a decode
