@@ -5,9 +5,9 @@
 // head inner) all attend to the same latent rows, so they are taken in groups
 // of 128: per tile of T keys (e4m3: 128, bf16: 64) S = Q K^T is a dense
 // [128 x T x 576] product and O += P V a [128 x 512 x T] one.  A request's keys
-// are a list of 64-token pages, the sinks' pages and then those from the window's first key
-// to the last query; only the list's pages are loaded.  Each row masks the
-// keys that it does not see.
+// are a list of 64-token pages, the sinks' pages and then those from the
+// window's first key to the last query; only the list's pages are loaded.  Each
+// row masks the keys that it does not see.
 //
 // CTA pairs.  The fp32 output of 128 rows x 512 columns would fill one SM's
 // tensor memory, so two CTAs of a cluster run each product as one
@@ -493,11 +493,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   uint64_t *seg_empty = seg_full + kSegSlots; // [kSegSlots]
   uint64_t *ref_there = seg_empty + kSegSlots;   // [2 groups][2 row blocks]
   uint64_t *sum_there = ref_there + 4;        // [2 row blocks]
-  uint64_t *o_free = sum_there + 2;           // leader: the last segment's O has been read
+  uint64_t *l_read = sum_there + 2;           // [2 row blocks] bf16: the sums in x_max have been read
+  uint64_t *o_free = l_read + 2;           // leader: the last segment's O has been read
   uint64_t *drain = o_free + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((2 * (F::kKSlots + F::kVSlots) + kSBufs + 4 + 2 + 2 * kSegSlots + 8) * 8 + 8 <= F::kBarBytes,
+  static_assert((2 * (F::kKSlots + F::kVSlots) + kSBufs + 4 + 2 + 2 * kSegSlots + 10) * 8 + 8 <= F::kBarBytes,
                 "barriers");
   static_assert(sizeof(Seg) <= 32, "segment slot");
 
@@ -529,7 +530,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       mbar_init(&seg_empty[s], kSoftWarps + (rank == 0 ? 2 : 1));   // V, softmax, the leader's MMAs
     }
     for (int s = 0; s < 4; ++s) mbar_init(&ref_there[s], 2);   // the two warps of a row block
-    for (int s = 0; s < 2; ++s) mbar_init(&sum_there[s], 4);   // its four, of both groups
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sum_there[s], 4);            // its four, of both groups
+      mbar_init(&l_read[s], 1);
+    }
     mbar_init(o_free, 2 * kSoftWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -853,7 +857,13 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       load_scales(load_blk(t_first), sc);
       const int uc0 = uc;
       uc += sg.ntiles;
-      float ref = -INFINITY, l = 0.f;                   // l in units of 2^ref
+      // sums in units of 2^ref: of the probabilities for the logarithm and (bf16)
+      // of their rounded values for the results, where a large one's rounding
+      // then is in the numerator and the denominator (16 rows of 132 keys: 2.1e-3
+      // of the output's rms against 64 bits, 1.7e-3 of it the output's own
+      // rounding; divided by the unrounded sum 2.3e-3, of one set in seven more
+      // than 2.5e-3)
+      float ref = -INFINITY, l = 0.f, lr = 0.f;
       for (int t = t_first; t < sg.ntiles; t += 2) {
         const int u = uc0 + t, half_u = u >> 1;         // (group u & 1)
         load_scales(blk_next, sc_next);
@@ -901,6 +911,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           }
           top = fmaxf(top, fmaf(fmaxf(m0, m1), c[g], lg[g]));
         }
+        if (!FP8 && t <= 1 && segs > 0 &&
+            !(ok = all_ok(wait_for(&l_read[block], (segs - 1) & 1, abort_flag))))
+          break;
         if (!(ok = pair_max(top))) break;
         // the reference that the tile before left, and what this one makes of it
         float old = -INFINITY;
@@ -921,21 +934,31 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (lane == 0) mbar_arrive(&ref_there[2 * group + block]);
         const bool rescale = t > 0 && moves;
         const float f = move ? (old == -INFINITY ? 0.f : ex2(old - now)) : 1.f;
-        if (ref != now && l != 0.f) l *= ex2(ref - now);
+        if (ref != now && l != 0.f) {
+          const float by = ex2(ref - now);
+          l *= by;
+          lr *= by;
+        }
         ref = now;
         const float base = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
         for (int g = 0; g < kBlocks; ++g) {
           const float d = lg[g] - base;
-          float s0 = 0.f, s1 = 0.f;
+          float s0 = 0.f, s1 = 0.f, r0 = 0.f, r1 = 0.f;
 #pragma unroll
           for (int k = kRun * g; k < kRun * g + kRun; k += 2) {
             fma_f32x2(x[k], x[k + 1], x[k], x[k + 1], c[g], c[g], d, d);
             x[k] = ex2(x[k]);
             x[k + 1] = ex2(x[k + 1]);
             add_f32x2(s0, s1, s0, s1, x[k], x[k + 1]);
+            if constexpr (!FP8) {
+              const uint32_t pk = bf16x2_rn(x[k], x[k + 1]);
+              x[k] = __uint_as_float(pk);               // (both: stored as they are)
+              add_f32x2(r0, r1, r0, r1, __uint_as_float(pk << 16), __uint_as_float(pk & 0xFFFF0000u));
+            }
           }
           l = fmaf(s0 + s1, sc[g], l);
+          lr += r0 + r1;
         }
         // P goes where the P V of this group's last tile read
         if (u >= 2 && !(ok = all_ok(wait_for(&pv_done[group], (half_u - 1) & 1, abort_flag)))) break;
@@ -963,8 +986,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             row[(4 * half + q) ^ (r & 7)] =
-                make_uint4(bf16x2_rn(x[8 * q], x[8 * q + 1]), bf16x2_rn(x[8 * q + 2], x[8 * q + 3]),
-                           bf16x2_rn(x[8 * q + 4], x[8 * q + 5]), bf16x2_rn(x[8 * q + 6], x[8 * q + 7]));
+                make_uint4(__float_as_uint(x[8 * q]), __float_as_uint(x[8 * q + 2]),
+                           __float_as_uint(x[8 * q + 4]), __float_as_uint(x[8 * q + 6]));
         }
         if (rescale) {
           // O follows the reference, now that the last P V is done
@@ -1044,16 +1067,28 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         break;
       tc_fence_after();
       const float end_ref = x_ref[64 * lg_last + r];
-      if (l != 0.f) l *= ex2(ref - end_ref);
+      if (l != 0.f) {
+        const float by = ex2(ref - end_ref);
+        l *= by;
+        lr *= by;
+      }
       ref = end_ref;
-      x_sum[128 * group + 64 * half + r] = l;
+      // (of x_max the row's four have taken the last maximum)
+      x_sum[128 * group + 64 * half + r] = FP8 ? l : lr;
+      if (!FP8) x_max[64 * half + r] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sum_there[block]);
       if (!(ok = all_ok(wait_for(&sum_there[block], segs & 1, abort_flag)))) break;
       ++segs;
-      l = (x_sum[r] + x_sum[64 + r]) + (x_sum[128 + r] + x_sum[192 + r]);
-      const bool empty = l == 0.f;
-      const float inv = empty ? 0.f : 1.f / l;
+      auto total = [&](const float *x) { return (x[r] + x[64 + r]) + (x[128 + r] + x[192 + r]); };
+      const float sum = total(x_sum);
+      const bool empty = sum == 0.f;
+      const float inv = empty ? 0.f : 1.f / sum;
+      if (half + group == 0) {
+        l = FP8 ? sum : total(xchg);
+        __syncwarp();
+        if (!FP8 && lane == 0) mbar_arrive(&l_read[block]);
+      }
       const int64_t row0 = static_cast<int64_t>(sg.b) * R + sg.rg * 128 + 64 * rank;
       const int64_t at = sg.whole ? row0 : static_cast<int64_t>(sg.slot) * 128 + 64 * rank;
       const int nrows = min(64, R - sg.rg * 128 - 64 * rank);
