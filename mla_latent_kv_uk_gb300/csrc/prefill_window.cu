@@ -22,7 +22,7 @@
 // uniform registers).
 //
 // What bounds it: 4 x 512 queries over 8192 keys, 128 heads, a window of 1024
-// take 187 us, 0.92 PFLOP/s of visible pairs (1.15 of the tiles, which are
+// take 184 us, 0.94 PFLOP/s of visible pairs (1.15 of the tiles, which are
 // partly masked) of the 1.9 that a product reaches.  A key tile of both query
 // tiles takes 3650 cycles where its MMAs take 2560: S, softmax, P and O follow
 // one another, and tensor memory is full, so no S runs ahead.  About 10000 of an
@@ -420,7 +420,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
       const int q = it.row0 + g * kBM + r;       // query of the request
       const int lim = min(it.nk, q + it.nk - it.nq + 1);
       const int wlo = lim - args.window;         // the window's first key
-      float m = -INFINITY, l = 0.f;
+      // sums of the probabilities, for the logarithm, and of their rounded values,
+      // for the results: a large one's rounding is then in both parts of the quotient
+      // (which counts where few keys have most of the weight)
+      float m = -INFINITY, l = 0.f, lr = 0.f;
       bool any = false;
       for (int t = 0; t < nt; ++t) {
         if (t == skip) continue;
@@ -469,11 +472,11 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
           f = m == -INFINITY ? 0.f : ex2(m - top);
           m = top;
           l *= f;
+          lr *= f;
         }
         const bool rescale = any && __any_sync(0xffffffffu, move);
         const float nm = m == -INFINITY ? 0.f : -m, sc = args.scale_log2;
-        // the row sum is of the unrounded probabilities
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        float ps[4] = {0.f, 0.f, 0.f, 0.f}, pr[2] = {0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[16];   // over scores that this thread has read: of the first half, then of both
@@ -495,10 +498,15 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
             add_f32x2(ps[2], ps[3], ps[2], ps[3], x[k + 2], x[k + 3]);
           }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) pk[k] = bf16x2_rn(x[2 * k], x[2 * k + 1]);
+          for (int k = 0; k < 16; ++k) {
+            pk[k] = bf16x2_rn(x[2 * k], x[2 * k + 1]);
+            add_f32x2(pr[0], pr[1], pr[0], pr[1], __uint_as_float(pk[k] << 16),
+                      __uint_as_float(pk[k] & 0xFFFF0000u));
+          }
           tmem_st_x16(lane_base + col_s + 16 * h, pk);
         }
         l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        lr += pr[0] + pr[1];
         if (rescale) {
           // O follows the maximum, now that the last P V is done (64 columns
           // for either thread of the row)
@@ -533,16 +541,20 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
       tc_fence_after();
       {
         const float other = exchange(l);
+        if (!told) {
+          l += other;
+          named_and(bar_id, true);               // (taken: the other sum goes the same way)
+          lr += exchange(lr);
+        }
         if (told) {
           ok = false;
           break;
         }
-        l += other;
       }
       const bool row_ok = r < rows;
       const int64_t orow = static_cast<int64_t>(it.q0 + q) * args.H + it.h;
       const bool empty = l == 0.f;
-      const float inv = empty ? 0.f : 1.f / l;
+      const float inv = empty ? 0.f : 1.f / lr;
 #pragma unroll 1
       for (int o0 = 0; o0 < 64; o0 += 32) {
         uint32_t o[32];
@@ -570,8 +582,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
           row_again(args.q + at * kDq, args.k + k0 * ks + h * kDq, args.v + k0 * vs + h * kDv + col, ks, vs,
                     args.sinks, __shfl_sync(0xffffffffu, wlo, from), __shfl_sync(0xffffffffu, lim, from),
                     args.scale_log2, __shfl_sync(0xffffffffu, m, from), row);
-          if (lane == from)
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(row[k]);
+          if (lane == from)                    // (of unrounded probabilities)
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(row[k] * (lr / l));
         }
         __syncwarp();
         // four lanes turn their rows' four 16-byte chunks round, so that a
