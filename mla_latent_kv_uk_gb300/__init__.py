@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function below checks tensor devices,
 dtypes and shapes, allocates outputs with torch when the caller passes none,
-and calls the C entry point of the same name on torch's current CUDA stream.
+and calls the C entry point of the same name on torch's current CUDA stream
+(the window, sink and block-scaled-cache calls through a compiled module).
 All arithmetic runs in the library's CUDA kernels; there is no fallback.
 Importing this module raises ImportError if the library has not been built
 (``python -c "import __graft_entry__ as g; g.build()"``).
