@@ -147,7 +147,7 @@ struct WindowArgs {
   const float *scales;          // nullptr: k_scale
   int sb_shift;                 // log2(tokens per scale)
   float k_scale;                // cache value of code 1 (bf16: 1)
-  float scale_log2;             // sm_scale * log2(e) * q_scale
+  float scale_log2, scale_pre;  // sm_scale * log2(e) * q_scale as a product, so that it is in range
   const int32_t *block_table, *seq_lens;
   int B, q_len, H, max_blocks, num_blocks, window, sinks;
   int RG, forced, solo;
@@ -883,7 +883,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         for (int g = 0; g < kBlocks; ++g) {
           // (a scale of 0 stands for zeros: so does the smallest one)
           const float sigma = fminf(fmaxf(sc[g], 0x1p-100f), 0x1p120f);
-          c[g] = sigma * args.scale_log2;
+          // (at least 2^-126, which makes any score 0 as well as less does: masked
+          // scores of -inf times 0 would be NaN)
+          c[g] = fminf(fmaxf(sigma * args.scale_pre * args.scale_log2, 0x1p-126f), 0x1.fffffep127f);
           lg[g] = FP8 ? log2f(sigma) : 0.f;
           sc[g] = FP8 ? 1.f / sigma : 1.f;
         }
@@ -1494,7 +1496,10 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.scales = scales;
   a.sb_shift = sb_shift;
   a.k_scale = fp8 ? k_scale : 1.f;
-  a.scale_log2 = sm_scale * 1.4426950408889634f * (fp8 ? q_scale : 1.f);
+  // times a scale of 2^-100 to 2^120 the factor may be in range where it is not by itself
+  const double scale = static_cast<double>(sm_scale) * 1.4426950408889634 * (fp8 ? q_scale : 1.f);
+  a.scale_pre = scale < 0x1p-60 ? 0x1p-100f : scale > 0x1p100 ? 0x1p100f : 1.f;
+  a.scale_log2 = static_cast<float>(scale / a.scale_pre);
   a.block_table = block_table;
   a.seq_lens = seq_lens;
   a.B = B;
