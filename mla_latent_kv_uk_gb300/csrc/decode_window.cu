@@ -31,8 +31,11 @@
 // log2(e) * q_scale, the scores in the log2 domain are sigma * c * raw, and
 // P' = sigma * 2^(s - m) = 2^(raw * (sigma c) + log2 sigma - m) goes against
 // the raw codes of V: one FMA and one exponential per score whatever the
-// scales.  m follows the largest s + log2 sigma; the normaliser is
-// sum P' / sigma, summed per block before the division.
+// scales.  m follows the largest s + log2 sigma.  The normaliser has a unit of
+// its own, n = the largest s of the thread's keys so far: sum 2^(s - n) is the
+// sum over the blocks of 2^(m - log2 sigma - n) sum P'.  Where the keys with
+// the weight have a scale 2^100 below those that m follows, P' would vanish in
+// fp32 and their scores are taken again from tensor memory.
 //
 // Warps: 0 walks the split plan, publishes the segments and loads Q and K,
 // 1 issues the MMAs (leader CTA), 2 loads V, 4..11 turn scores into
@@ -130,8 +133,9 @@ struct Fmt {
   static constexpr int kOffK = kOffQ + kQBytes;
   static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVSlotBytes;
-  static constexpr int kOffX = kOffP + kPBufs * kPBytes;   // [2][128] maxima, [2][64] references, [256] sums
-  static constexpr int kOffSeg = kOffX + (256 + 128 + 256) * 4;
+  // [2][128] maxima, [2][64] references, [256] sums, e4m3: [256] units of the sums
+  static constexpr int kOffX = kOffP + kPBufs * kPBytes;
+  static constexpr int kOffSeg = kOffX + (256 + 128 + 256 + (FP8 ? 256 : 0)) * 4;
   static constexpr int kOffBars = kOffSeg + kSegSlots * 32;
   static constexpr int kBarBytes = 384;
   static constexpr int kSmem = kOffBars + kBarBytes;
@@ -464,6 +468,24 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint3
   const __half2 rest = __hsub2(p, *reinterpret_cast<const __half2 *>(&back));
   hi = h;
   lo = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+}
+
+// sum 2^(s - n) over the seen keys of the blocks whose P' is 2^-95 of that or less
+// (of the others none of 2^-31 of the sum vanishes), by a whole warp; apart, as the
+// kernel is 2 % slower with it in its loop.
+__device__ __noinline__ float far_sum(uint32_t scores, uint64_t seen, float4 c, float4 lg, float base, float n) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g, seen >>= 16) {
+    const uint32_t take = base - lg.x - n > 95.f ? static_cast<uint32_t>(seen) : 0;
+    float x[16];
+    tmem_ld_x16(scores + 16 * g, reinterpret_cast<uint32_t *>(x));
+#pragma unroll
+    for (int k = 0; k < 16; ++k) sum += take & (1u << k) ? ex2(fmaf(x[k], c.x, -n)) : 0.f;
+    c = make_float4(c.y, c.z, c.w, c.x);
+    lg = make_float4(lg.y, lg.z, lg.w, lg.x);
+  }
+  return sum;
 }
 
 template <bool FP8>
@@ -801,7 +823,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     const uint32_t lane_base = tmem + ((quarter * 32u) << 16);
     const uint32_t p_bar[2] = {peer_smem(&p_full[0], 0), peer_smem(&p_full[1], 0)};
     const uint32_t o_bar = peer_smem(o_free, 0);
-    float *x_max = xchg + 128 * group, *x_ref = xchg + 256, *x_sum = xchg + 384;
+    float *x_max = xchg + 128 * group, *x_ref = xchg + 256, *x_sum = xchg + 384, *x_unit = xchg + 640;
     // The hardware barrier of the two warps has no limit, so neither may leave
     // the other in it: it takes along whether all is well, a warp whose wait
     // ran out goes through it once more before it leaves, and the other leaves
@@ -857,13 +879,13 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       load_scales(load_blk(t_first), sc);
       const int uc0 = uc;
       uc += sg.ntiles;
-      // sums in units of 2^ref: of the probabilities for the logarithm and (bf16)
-      // of their rounded values for the results, where a large one's rounding
-      // then is in the numerator and the denominator (16 rows of 132 keys: 2.1e-3
-      // of the output's rms against 64 bits, 1.7e-3 of it the output's own
-      // rounding; divided by the unrounded sum 2.3e-3, of one set in seven more
-      // than 2.5e-3)
-      float ref = -INFINITY, l = 0.f, lr = 0.f;
+      // e4m3: the sum in units of 2^ln.  bf16: sums in units of 2^ref, of the
+      // probabilities for the logarithm and of their rounded values for the
+      // results, where a large one's rounding then is in the numerator and the
+      // denominator (16 rows of 132 keys: 2.1e-3 of the output's rms against 64
+      // bits, 1.7e-3 of it the output's own rounding; divided by the unrounded sum
+      // 2.3e-3, of one set in seven more than 2.5e-3)
+      float ref = -INFINITY, l = 0.f, lr = 0.f, ln = -INFINITY;
       for (int t = t_first; t < sg.ntiles; t += 2) {
         const int u = uc0 + t, half_u = u >> 1;         // (group u & 1)
         load_scales(blk_next, sc_next);
@@ -887,7 +909,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           // scores of -inf times 0 would be NaN)
           c[g] = fminf(fmaxf(sigma * args.scale_pre * args.scale_log2, 0x1p-126f), 0x1.fffffep127f);
           lg[g] = FP8 ? log2f(sigma) : 0.f;
-          sc[g] = FP8 ? 1.f / sigma : 1.f;
+        }
+        float lg_min = lg[0], lg_max = lg[0];
+#pragma unroll
+        for (int g = 1; g < kBlocks; ++g) {
+          lg_min = fminf(lg_min, lg[g]);
+          lg_max = fmaxf(lg_max, lg[g]);
         }
         constexpr int kRun = F::kMine / kBlocks;        // keys of one scale: 16 / 32
         if (!(ok = all_ok(wait_for(&s_full[u % kSBufs], (u / kSBufs) & 1, abort_flag)))) break;
@@ -896,13 +923,15 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const uint32_t s_at = lane_base + kColS + F::kTile / 2 * (u % kSBufs);
         if constexpr (FP8) tmem_ld_x64(s_at, reinterpret_cast<uint32_t *>(x));
         else tmem_ld_x32(s_at, reinterpret_cast<uint32_t *>(x));
+        auto seen_keys = [&] {
+          return low_bits(p - key0 + 1) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0));
+        };
         if (masked) {
-          const uint64_t seen =
-              low_bits(p - key0 + 1) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0));
+          const uint64_t seen = seen_keys();
 #pragma unroll
           for (int k = 0; k < F::kMine; ++k) x[k] = seen & (uint64_t(1) << k) ? x[k] : -INFINITY;
         }
-        float top = -INFINITY;
+        float top = -INFINITY, raw[kBlocks];            // largest s + log2 sigma; of a block's scores
 #pragma unroll
         for (int g = 0; g < kBlocks; ++g) {
           float m0 = -INFINITY, m1 = -INFINITY;
@@ -911,8 +940,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             m0 = fmax3(m0, x[kRun * g + k], x[kRun * g + k + 1]);
             m1 = fmax3(m1, x[kRun * g + k + 2], x[kRun * g + k + 3]);
           }
-          top = fmaxf(top, fmaf(fmaxf(m0, m1), c[g], lg[g]));
+          raw[g] = fmaxf(m0, m1);
+          top = fmaxf(top, fmaf(raw[g], c[g], lg[g]));
         }
+        const float high_low = fmaxf(ln, top - lg_max);   // the largest s is no less
         if (!FP8 && t <= 1 && segs > 0 &&
             !(ok = all_ok(wait_for(&l_read[block], (segs - 1) & 1, abort_flag))))
           break;
@@ -936,13 +967,16 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (lane == 0) mbar_arrive(&ref_there[2 * group + block]);
         const bool rescale = t > 0 && moves;
         const float f = move ? (old == -INFINITY ? 0.f : ex2(old - now)) : 1.f;
-        if (ref != now && l != 0.f) {
+        if (!FP8 && ref != now && l != 0.f) {
           const float by = ex2(ref - now);
           l *= by;
           lr *= by;
         }
         ref = now;
+        float part[kBlocks], rest = 0.f;                // (the sum waits until the probabilities are handed over)
         const float base = ref == -INFINITY ? 0.f : ref;
+        // a P' that is 2^-95 of its 2^(s - n) or less, below
+        const bool again = FP8 && __any_sync(0xffffffffu, high_low > -INFINITY && base - lg_min - high_low > 95.f);
 #pragma unroll
         for (int g = 0; g < kBlocks; ++g) {
           const float d = lg[g] - base;
@@ -959,8 +993,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
               add_f32x2(r0, r1, r0, r1, __uint_as_float(pk << 16), __uint_as_float(pk & 0xFFFF0000u));
             }
           }
-          l = fmaf(s0 + s1, sc[g], l);
-          lr += r0 + r1;
+          if constexpr (FP8) {
+            part[g] = s0 + s1;
+          } else {
+            l += s0 + s1;
+            lr += r0 + r1;
+          }
         }
         // P goes where the P V of this group's last tile read
         if (u >= 2 && !(ok = all_ok(wait_for(&pv_done[group], (half_u - 1) & 1, abort_flag)))) break;
@@ -990,6 +1028,17 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             row[(4 * half + q) ^ (r & 7)] =
                 make_uint4(__float_as_uint(x[8 * q]), __float_as_uint(x[8 * q + 2]),
                            __float_as_uint(x[8 * q + 4]), __float_as_uint(x[8 * q + 6]));
+        }
+        auto next_unit = [&] {
+          float n = ln;
+#pragma unroll
+          for (int g = 0; g < kBlocks; ++g) n = fmaxf(n, raw[g] * c[g]);
+          return n;
+        };
+        if constexpr (FP8) {
+          if (again)
+            rest = far_sum(s_at, masked ? seen_keys() : ~uint64_t(0), make_float4(c[0], c[1], c[2], c[3]),
+                           make_float4(lg[0], lg[1], lg[2], lg[3]), base, next_unit());
         }
         if (rescale) {
           // O follows the reference, now that the last P V is done
@@ -1058,6 +1107,16 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(p_bar[group]);
+        if constexpr (FP8) {
+          const float n = next_unit();
+          l = fmaf(l, ln == n ? 1.f : ex2(ln - n), rest);
+          ln = n;
+#pragma unroll
+          for (int g = 0; g < kBlocks; ++g) {
+            const float e = base - lg[g] - (n == -INFINITY ? 0.f : n);
+            l = fmaf(part[g], e > 95.f ? 0.f : ex2(e), l);
+          }
+        }
 #pragma unroll
         for (int g = 0; g < kBlocks; ++g) sc[g] = sc_next[g];
       }
@@ -1069,12 +1128,13 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         break;
       tc_fence_after();
       const float end_ref = x_ref[64 * lg_last + r];
-      if (l != 0.f) {
+      if (!FP8 && l != 0.f) {
         const float by = ex2(ref - end_ref);
         l *= by;
         lr *= by;
       }
       ref = end_ref;
+      if constexpr (FP8) x_unit[128 * group + 64 * half + r] = ln;
       // (of x_max the row's four have taken the last maximum)
       x_sum[128 * group + 64 * half + r] = FP8 ? l : lr;
       if (!FP8) x_max[64 * half + r] = l;
@@ -1083,9 +1143,18 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       if (!(ok = all_ok(wait_for(&sum_there[block], segs & 1, abort_flag)))) break;
       ++segs;
       auto total = [&](const float *x) { return (x[r] + x[64 + r]) + (x[128 + r] + x[192 + r]); };
-      const float sum = total(x_sum);
+      float sum, unit = ref;                            // (the logarithm's, too)
+      if constexpr (FP8) {
+        unit = fmaxf(fmaxf(x_unit[r], x_unit[64 + r]), fmaxf(x_unit[128 + r], x_unit[192 + r]));
+        if (unit == -INFINITY) unit = 0.f;
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 256; k += 64) sum = fmaf(x_sum[k + r], ex2(x_unit[k + r] - unit), sum);
+      } else {
+        sum = total(x_sum);
+      }
       const bool empty = sum == 0.f;
-      const float inv = empty ? 0.f : 1.f / sum;
+      const float inv = empty ? 0.f : FP8 ? ex2(ref - unit) / sum : 1.f / sum;
       if (half + group == 0) {
         l = FP8 ? sum : total(xchg);
         __syncwarp();
@@ -1099,7 +1168,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                       (at * kLatent + 256 * half + 128 * group) * esz;
       const int64_t rstride = static_cast<int64_t>(kLatent) * esz;
       if (half + group == 0 && r < nrows) {
-        const float v = empty ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
+        const float v = empty ? -INFINITY : (unit + log2f(l)) * 0.69314718055994531f;
         (sg.whole ? args.lse : args.ws_lse)[at + r] = v;
       }
       uint32_t all[128];

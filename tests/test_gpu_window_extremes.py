@@ -8,7 +8,7 @@ import torch
 import synth
 from oracle import window as W
 from tests._helpers import f64
-from tests.test_gpu_window_decode import Case
+from tests.test_gpu_window_decode import Case, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,29 @@ def test_factors_that_only_together_are_in_range(m, q_scale, k_scale):
     assert float((lse - base_l).abs().max()) <= 2.0 ** -13
     most = float(base.abs().max())
     assert float((out.double() / k_scale - base.double()).abs().max()) <= 2.0 ** -6 * most
+
+
+@pytest.mark.parametrize("far", [2.0 ** 30, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("split", [0, 1])
+def test_blocks_whose_scales_are_far_apart(m, far, split):
+    """Blocks of tiny rows (2^-100 a unit) beside blocks of `far`: equal scores,
+    so equal weights, and the output is the mean."""
+    g = synth.generator(210)
+    n, H = 300, 16
+    nb = 6
+    bt = g.permutation(nb).astype(np.int32)[None, :5]
+    scales = np.where(g.random((nb, 4)) < 0.5, far, 2.0 ** -100).astype(np.float32)
+    codes = g.integers(0, 127, (nb, 64, 576)).astype(np.uint8)
+    codes[..., 512:] = 0
+    q = np.zeros((1, 1, H, 576), np.float32)
+    q[..., 512:] = g.standard_normal((H, 64))         # (of scores 0: the keys' last columns are)
+    q8 = synth.as_e4m3(q)
+    c64 = W.scaled_values(codes, scales)
+    out, lse = m.mla_decode_paged_scaled(
+        q8.cuda(), torch.from_numpy(codes).cuda().view(torch.float8_e4m3fn), torch.from_numpy(scales).cuda(),
+        _i32(bt), _i32([n]), sm_scale=0.1, out_dtype=torch.float32, split_tiles=split)
+    assert m.mla_get_device_error() == 0
+    ref, ref_l = W.window_decode(f64(q8), c64, bt, np.array([n]), 0.1, 0, 0)
+    assert np.abs(lse.cpu().numpy() - ref_l).max() <= 1e-4
+    # probabilities off by 2^-8 of themselves
+    assert np.abs(f64(out) - ref).max() <= 2.0 ** -7 * np.abs(ref).max()
