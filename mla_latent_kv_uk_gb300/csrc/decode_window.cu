@@ -22,10 +22,19 @@
 // at N = 256 (P V: 16 per tile in either format).
 //
 // e4m3 probabilities.  P as one e4m3 value would be off by up to 2^-4 and the
-// output with it; P is held as the sum of two e4m3 values, hi = e4m3(p) and
-// lo = e4m3(p - hi), at twice the P V steps: off by at most 2^-8 p, as bf16,
-// or by half a subnormal step (2^-10) where p < 2^-2 and the row's largest p
-// is at least 2^5.
+// output with it; P is held as the sum of two values, hi = e4m3(p) and lo =
+// e5m2(p - hi), at twice the P V steps: off by at most 2^-8 p where p is 2^-6 or
+// more, by 2^-14 (and 2^-3 p) below, and by all of it below 2^-17.  So that
+// thousands of small p do not lose a part of their weight together behind a row's
+// few large ones (a sink 10 nats above 16384 keys of one score: 34 % of their
+// weight with lo = e4m3), a row's reference also follows its tiles down: where a
+// tile's largest p falls below 2^-6, to 1, with O (fp32) scaled up; at most 2^16
+// below the highest, so 2^-21 of the row's largest p and more are held like that.
+// What a row loses is then 2^-8 of its weights and, in a tile, what is below
+// 2^-11 of the tile's largest: it does not grow with the number of keys.
+// (e4m3 for both: half the error on rows whose scores are alike, 7e-4 instead of
+// 1.3e-3 of an output's rms where its own rounding is 1.7e-3.  e5m2 for both
+// has the range without the steps down, at 2.3e-3.)
 //
 // Block scales.  With sigma the scale of a key's block and c = sm_scale *
 // log2(e) * q_scale, the scores in the log2 domain are sigma * c * raw, and
@@ -41,7 +50,8 @@
 // 1 issues the MMAs (leader CTA), 2 loads V, 4..11 turn scores into
 // probabilities (two groups taking the tiles in turn, one row and half of the
 // tile's keys per thread) and write the results.  Lazy rescaling: O is rescaled
-// when a row's reference would be exceeded by more than 2^kLazy.
+// when a row's reference would be exceeded by more than 2^kLazy (e4m3: or a tile's
+// largest p is below 2^kLow).
 //
 // Split: every row group of a request is a job of its list's tiles plus
 // kJobCost units for the switch; jobs lie end to end and pair p takes units
@@ -145,6 +155,10 @@ struct Fmt {
   static constexpr float kTop = FP8 ? 5.f : 0.f;
   // p' is at most 2^kLazy before it moves again: e4m3 holds 448 > 2^8.75
   static constexpr float kLazy = FP8 ? 8.75f : 16.f;
+  // e4m3: p' of a tile's largest key at which the reference follows it down, at
+  // most kDepth below the highest one (-3 in place of -6: on 16384 keys of a
+  // deviation of 3 nats 57 passes over O in 128 tiles and not 21, and no less error)
+  static constexpr float kLow = -6.f, kDepth = 16.f;
 };
 
 struct WindowArgs {
@@ -459,15 +473,15 @@ __device__ __forceinline__ bool named_and(uint32_t id, uint32_t count, bool v) {
   return r != 0;
 }
 
-// Probabilities (a, b) as two pairs of e4m3 codes, hi and lo.
-__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint32_t &lo) {
+// Probabilities (a, b) as pairs of e4m3 codes, hi, and of e5m2 codes, lo.
+__device__ __forceinline__ void split_fp8(float a, float b, uint32_t &hi, uint32_t &lo) {
   const __half2 p = __floats2half2_rn(a, b);
   const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
   const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
   // exact: both are multiples of p's last place (or of 2^-24)
   const __half2 rest = __hsub2(p, *reinterpret_cast<const __half2 *>(&back));
   hi = h;
-  lo = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+  lo = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E5M2);
 }
 
 // sum 2^(s - n) over the seen keys of the blocks whose P' is 2^-95 of that or less
@@ -722,6 +736,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                     : idesc_bf16(128, F::kTile, false, false);
       const uint32_t idesc_pv = FP8 ? idesc_e4m3(128, 256, false, true)
                                     : idesc_bf16(128, 256, false, true);
+      const uint32_t idesc_lo = idesc_pv | kIdescA_e5m2;
       const uint32_t me = elect_one();
       const uint32_t qd = desc_lo(sm_q, 16);
       auto wait = [&](uint64_t *bar, int phase) -> bool {
@@ -772,7 +787,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                             first && step == 0 ? 0u : 1u, me);
               if constexpr (FP8)
                 pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa + 512), bd,
-                              idesc_pv, 1, me);
+                              idesc_lo, 1, me);
             }
             if (j == 1) pair_commit(&v_empty[s], me);
           }
@@ -886,6 +901,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       // bits, 1.7e-3 of it the output's own rounding; divided by the unrounded sum
       // 2.3e-3, of one set in seven more than 2.5e-3)
       float ref = -INFINITY, l = 0.f, lr = 0.f, ln = -INFINITY;
+      float highest = -INFINITY;                        // reference so far
       for (int t = t_first; t < sg.ntiles; t += 2) {
         const int u = uc0 + t, half_u = u >> 1;         // (group u & 1)
         load_scales(blk_next, sc_next);
@@ -948,6 +964,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             !(ok = all_ok(wait_for(&l_read[block], (segs - 1) & 1, abort_flag))))
           break;
         if (!(ok = pair_max(top))) break;
+        // a reference above this goes down (none, where the row sees no key of the tile)
+        const float above = top > -INFINITY ? fmaxf(top - F::kLow, highest - F::kDepth) : INFINITY;
         // the reference that the tile before left, and what this one makes of it
         float old = -INFINITY;
         if (t > 0) {
@@ -955,13 +973,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             break;
           old = x_ref[64 * (group ^ 1) + r];
         }
-        // Where one of the warp's rows has to move, all that can do so: the pass
-        // over O is paid for, and the next one is further off.  (The row's other
-        // thread, in a warp of the same rows, decides alike.)
-        const bool must = top > old + F::kLazy || (old == -INFINITY && top > -INFINITY);
-        const bool moves = __any_sync(0xffffffffu, must);
-        const bool move = moves && top - F::kTop > old;
-        const float now = move ? top - F::kTop : old;
+        // Where one of the warp's rows has to move, all that can go up do so: the
+        // pass over O is paid for, and the next one is further off.  (The row's
+        // other thread, in a warp of the same rows, decides alike.)
+        const bool down = FP8 && old > above;
+        const bool moves = __any_sync(0xffffffffu, top - F::kLazy > old || down);
+        const bool up = moves && top - F::kTop > old, move = up || down;
+        float now = up ? top - F::kTop : old;
+        if (down) now = fmaxf(top, fmaxf(highest, old) - F::kDepth);
         if (half == 0) x_ref[64 * group + r] = now;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ref_there[2 * group + block]);
@@ -973,6 +992,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           lr *= by;
         }
         ref = now;
+        if constexpr (FP8) highest = fmaxf(highest, fmaxf(old, now));
         float part[kBlocks], rest = 0.f;                // (the sum waits until the probabilities are handed over)
         const float base = ref == -INFINITY ? 0.f : ref;
         // a P' that is 2^-95 of its 2^(s - n) or less, below
@@ -1012,8 +1032,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t h0, h1, l0, l1;
-              split_e4m3(x[16 * q + 4 * k], x[16 * q + 4 * k + 1], h0, l0);
-              split_e4m3(x[16 * q + 4 * k + 2], x[16 * q + 4 * k + 3], h1, l1);
+              split_fp8(x[16 * q + 4 * k], x[16 * q + 4 * k + 1], h0, l0);
+              split_fp8(x[16 * q + 4 * k + 2], x[16 * q + 4 * k + 3], h1, l1);
               h[k] = h0 | (h1 << 16);
               w[k] = l0 | (l1 << 16);
             }

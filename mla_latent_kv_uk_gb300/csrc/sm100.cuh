@@ -353,6 +353,9 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn,
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Added to an e4m3 descriptor: A is e5m2 (kind::f8f6f4 takes a type for either).
+constexpr uint32_t kIdescA_e5m2 = 1u << 7;
+
 // TMEM -> registers, 32 lanes x 32 bit, N consecutive columns per thread;
 // the load and its completion wait are one asm block, so no use of the
 // registers can be scheduled before the data has arrived.

@@ -7,7 +7,7 @@ import torch
 
 import synth
 from oracle import window as W
-from tests._helpers import f64
+from tests._helpers import AttnTerms, check_attention, f64, row_terms
 from tests.test_gpu_window_decode import Case, _i32
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +87,114 @@ def test_blocks_whose_scales_are_far_apart(m, far, split):
     assert np.abs(lse.cpu().numpy() - ref_l).max() <= 1e-4
     # probabilities off by 2^-8 of themselves
     assert np.abs(f64(out) - ref).max() <= 2.0 ** -7 * np.abs(ref).max()
+
+
+def _scaled(g, values, scales, bt):
+    """A block-scaled pool of `values` [n, 576] at positions 0.. of one request."""
+    n, sb = len(values), 64 // scales.shape[1]
+    pages = -(-n // 64)
+    x = np.zeros((scales.shape[0] * 64, 576), np.float32)
+    at = bt[0, np.arange(n) // 64] * 64 + np.arange(n) % 64
+    s = scales.reshape(-1)[at // sb].astype(np.float64)
+    x[at] = values / s[:, None]
+    codes = synth.as_e4m3(x.reshape(-1, 64, 576))
+    exact = W.scaled_values(codes.view(torch.uint8).numpy(), scales)
+    assert pages <= bt.shape[1]
+    return codes, exact
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "s16", "s64"])
+@pytest.mark.parametrize("n,window,sinks,split,sink_value", [
+    (4096, 0, 0, 0, 1.0), (4096, 0, 0, 64, 1.0), (4096, 0, 0, 64, 0.0), (16384, 0, 0, 1 << 20, 1.0),
+    (16384, 0, 0, 1 << 20, 30.0), (65536, 0, 0, 1 << 20, 1.0), (65536, 0, 0, 0, 30.0),
+    (20000, 9000, 4, 1 << 20, 1.0)])
+def test_one_key_far_above_many(m, fmt, n, window, sinks, split, sink_value):
+    """What sinks are: the first key 8 to 15 nats above thousands of others,
+    which together have a weight like its own and values with a common part.
+    Half of the heads see the others at exactly the same score, so that their
+    probabilities' roundings all go one way.
+
+    Bound: 2^-7 of sum w |V| (tests/_helpers.py), of any number of keys.  A
+    probability of 2^-6 or more, as the largest of its row and tile is, is off by
+    2^-8 of itself, and by 2^-7 down to 2^-7 (scores that differ by up to 0.7
+    nats).  Only the 127 keys beside the first are further below the largest of
+    their tile: with 11 nats or less by at most 2^-3 of themselves, 127 of 4096
+    keys or more, so 2^-8 of the others' weight; with more by all of it, 127 e^-11
+    of sum w at most, where the first key's own value is of the others' size."""
+    g = synth.generator(n + window)
+    H = 16
+    x = g.standard_normal((n, 576)) + 0.5
+    x[0, :512] *= sink_value
+    x[:, 512] = 0.0
+    x[0, 512:] = 0.0
+    x[0, 512] = 8.0
+    sb = 64 if fmt == "e4m3" else int(fmt[1:])
+    pages = -(-n // 64)
+    bt = g.permutation(pages + 1).astype(np.int32)[None, :pages]
+    if fmt == "e4m3":
+        per = np.full((pages + 1, 1), np.float32(np.abs(x).max() / 448))
+    else:
+        per = np.ones((pages + 1, 64 // sb), np.float32)
+        amax = np.abs(x).reshape(-1, sb, 576).max(axis=(1, 2)) if n % sb == 0 else \
+            np.array([np.abs(x[i:i + sb]).max() for i in range(0, n, sb)])
+        at = np.arange(0, n, sb)
+        per[bt[0, at // 64], at % 64 // sb] = np.exp2(np.ceil(np.log2(amax / 448)))
+    codes, c64 = _scaled(g, x, per, bt)
+    q = np.zeros((1, 1, H, 576))
+    gaps = 1.0 + 0.125 * (np.arange(H) // 2 if sink_value else np.arange(H) // 2 % 4)
+    q[0, 0, :, 512] = gaps                            # 8 to 15 nats (11 where the first key has no value)
+    q[0, 0, 1::2, 513:] = 0.03 * g.standard_normal((H // 2, 63))
+    q8 = synth.as_e4m3(q.astype(np.float32))
+    kw = dict(sm_scale=1.0, window=window, sinks=sinks, split_tiles=split)
+    if fmt == "e4m3":
+        out, lse = m.mla_decode_paged_window(q8.cuda(), codes.cuda(), _i32(bt), _i32([n]), k_scale=float(per[0, 0]),
+                                             **kw)
+    else:
+        out, lse = m.mla_decode_paged_scaled(q8.cuda(), codes.cuda(), torch.from_numpy(per).cuda(), _i32(bt),
+                                             _i32([n]), **kw)
+    assert m.mla_get_device_error() == 0
+    j = W.visible(n - 1, window, sinks)
+    rows = c64[bt[0, j // 64], j % 64]
+    q64 = f64(q8)[0, 0]
+    abs_wv, smag, _ = row_terms(q64, rows, rows[:, :512], 1.0)
+    s = q64 @ rows.T
+    top = s.max(axis=1, keepdims=True)
+    p = np.exp(s - top)
+    ref = p @ rows[:, :512] / p.sum(axis=1, keepdims=True)
+    ref_l = top[:, 0] + np.log(p.sum(axis=1))
+    check_attention(f64(out)[0, 0], lse.cpu().numpy()[0, 0], ref, ref_l, AttnTerms(abs_wv, smag),
+                    out_tol=np.inf, lse_tol=np.inf, label=f"{fmt} {n} keys, window {window}, split {split}")
+
+
+@pytest.mark.parametrize("place", ["first", "middle", "last"])
+def test_far_keys_anywhere(m, place):
+    """The key above the others in the first, a middle or the last tile, and
+    every tile with one of its own."""
+    g = synth.generator(230)
+    n, H = 8192, 16
+    x = g.standard_normal((n, 576)) + 0.5
+    x[:, 512] = 0.0
+    hot = {"first": [5], "middle": [4000], "last": [n - 1]}[place]
+    x[hot, 512:] = 0.0
+    x[hot, 512] = 8.0
+    pages = n // 64
+    bt = g.permutation(pages).astype(np.int32)[None]
+    per = np.full((pages, 4), 2.0 ** -6, np.float32)
+    codes, c64 = _scaled(g, x, per, bt)
+    q = np.zeros((1, 1, H, 576))
+    q[0, 0, :, 512] = 1.0 + 0.125 * (np.arange(H) // 2)
+    q[0, 0, 1::2, 513:] = 0.2 * g.standard_normal((H // 2, 63))
+    q8 = synth.as_e4m3(q.astype(np.float32))
+    for split in (0, 1 << 20):
+        out, lse = m.mla_decode_paged_scaled(q8.cuda(), codes.cuda(), torch.from_numpy(per).cuda(), _i32(bt),
+                                             _i32([n]), sm_scale=1.0, split_tiles=split)
+        assert m.mla_get_device_error() == 0
+        rows = c64[bt[0, np.arange(n) // 64], np.arange(n) % 64]
+        q64 = f64(q8)[0, 0]
+        abs_wv, smag, _ = row_terms(q64, rows, rows[:, :512], 1.0)
+        s = q64 @ rows.T
+        top = s.max(axis=1, keepdims=True)
+        p = np.exp(s - top)
+        ref = p @ rows[:, :512] / p.sum(axis=1, keepdims=True)
+        check_attention(f64(out)[0, 0], lse.cpu().numpy()[0, 0], ref, top[:, 0] + np.log(p.sum(axis=1)),
+                        AttnTerms(abs_wv, smag), out_tol=np.inf, lse_tol=np.inf, label=f"{place}, split {split}")
