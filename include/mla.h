@@ -358,7 +358,8 @@ int mla_prefill_attn(const void *q, const void *k, const void *v,
  * (s = block*64 + offset).  No calibration is needed: mla_rope_cache_append
  * finds the scales, mla_decode_paged_scaled and mla_gather_cache_scaled
  * read them.  Scales are >= 0 and at most 2^120; 0 stands for rows of zeros
- * (the decode takes 2^-100 for anything below it).
+ * (the decode takes 2^-100 for anything below it).  Any other value is no
+ * scale: the elements of its block are NaN.
  *
  * Append: mla_rope_cache_write for this cache.  For each new token t < T
  *   q_out[t,h,:] = R(positions[t]) q_pe[t,h,:]      (h < H)
@@ -367,7 +368,7 @@ int mla_prefill_attn(const void *q, const void *k, const void *v,
  * the cache receives kv_c[t] || k_out[t].  For every block that the call
  * writes to, with A the largest finite |element| of its new rows and s the
  * block's scale (0 if the call writes the block's first row: it begins
- * afresh; likewise if s is not a positive finite number),
+ * afresh; likewise if s is no scale),
  *   s' = max(s, 2^max(-100, ceil(log2(A / 448))))
  * becomes its scale, the new rows are stored as e4m3(x / s'), and if
  * 0 < s < s' the block's other rows are stored again as e4m3(code * (s/s'))

@@ -243,7 +243,7 @@ __device__ __forceinline__ void append_block(const AppendArgs &p, unsigned long 
     atomicSub(&members, kept);
   }
   __syncthreads();   // and every thread has the old scale
-  const float old = row_t[0] < 0 && held > 0.f && held < INFINITY ? held : 0.f;
+  const float old = row_t[0] < 0 && held > 0.f && held <= 0x1p120f ? held : 0.f;
   const float now = fmaxf(old, scale_for(__uint_as_float(amax_s << 16)));
   uint8_t *block = p.cache + static_cast<int64_t>(g) * kBlock * kDqk;
   if (tid == 0) p.scales[g] = now;

@@ -916,11 +916,16 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                  (k0 + kPage - 1 <= job.p0 && (k0 >= clean_lo || k0 + kPage <= args.sinks));
         };
         const bool all_clean = clean(page0) && clean(page1);
+        auto seen_keys = [&] {
+          return low_bits(p - key0 + 1) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0));
+        };
+        constexpr int kRun = F::kMine / kBlocks;        // keys of one scale: 16 / 32
         float c[kBlocks], lg[kBlocks];
 #pragma unroll
         for (int g = 0; g < kBlocks; ++g) {
-          // (a scale of 0 stands for zeros: so does the smallest one)
-          const float sigma = fminf(fmaxf(sc[g], 0x1p-100f), 0x1p120f);
+          // (a scale of 0 stands for zeros: so does the smallest one; what is no scale is NaN)
+          const bool is_scale = !FP8 || (sc[g] >= 0.f && sc[g] <= 0x1p120f);
+          const float sigma = is_scale ? fmaxf(sc[g], 0x1p-100f) : __uint_as_float(0x7FC00000u);
           // (at least 2^-126, which makes any score 0 as well as less does: masked
           // scores of -inf times 0 would be NaN)
           c[g] = fminf(fmaxf(sigma * args.scale_pre * args.scale_log2, 0x1p-126f), 0x1.fffffep127f);
@@ -932,20 +937,21 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           lg_min = fminf(lg_min, lg[g]);
           lg_max = fmaxf(lg_max, lg[g]);
         }
-        constexpr int kRun = F::kMine / kBlocks;        // keys of one scale: 16 / 32
         if (!(ok = all_ok(wait_for(&s_full[u % kSBufs], (u / kSBufs) & 1, abort_flag)))) break;
         tc_fence_after();
         float x[F::kMine];
         const uint32_t s_at = lane_base + kColS + F::kTile / 2 * (u % kSBufs);
         if constexpr (FP8) tmem_ld_x64(s_at, reinterpret_cast<uint32_t *>(x));
         else tmem_ld_x32(s_at, reinterpret_cast<uint32_t *>(x));
-        auto seen_keys = [&] {
-          return low_bits(p - key0 + 1) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0));
-        };
         if (masked) {
           const uint64_t seen = seen_keys();
 #pragma unroll
           for (int k = 0; k < F::kMine; ++k) x[k] = seen & (uint64_t(1) << k) ? x[k] : -INFINITY;
+          if constexpr (FP8) {                          // (NaN is for rows that see a key of the block)
+#pragma unroll
+            for (int g = 0; g < kBlocks; ++g)
+              if (!(seen >> (kRun * g) & 0xFFFFu)) lg[g] = 0.f;
+          }
         }
         float top = -INFINITY, raw[kBlocks];            // largest s + log2 sigma; of a block's scores
 #pragma unroll

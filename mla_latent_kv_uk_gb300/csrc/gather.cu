@@ -133,8 +133,10 @@ gather_kernel(const uint8_t *__restrict__ cache, int in_row_bytes,
       const int blk = __ldg(block_table + static_cast<int64_t>(b) * max_blocks + pos / kPage);
       if (blk < 0 || blk >= num_blocks) raise_error(err, MLA_DEVERR_BLOCK_ID);
       else src = cache + (static_cast<int64_t>(blk) * kPage + pos % kPage) * in_row_bytes;
-      if (MODE == kDequantRows && src)
+      if (MODE == kDequantRows && src) {
         k_scale = __ldg(scales + ((static_cast<int64_t>(blk) * kPage + pos % kPage) >> sb_shift));
+        if (!(k_scale >= 0.f && k_scale <= 0x1p120f)) k_scale = __uint_as_float(0x7FC00000u);   // no scale
+      }
     }
   }
   copy_rows<MODE>(src, dst, k_scale, lane);

@@ -88,7 +88,7 @@ def append(codes, scales, rows, slots):
         x = np.stack([rows[t] for t in mine.values()])
         fin = np.abs(x[np.isfinite(x)])
         old = sc[g]
-        if g * sb in mine or not (0.0 < old < math.inf):
+        if g * sb in mine or not (0.0 < old <= 2.0 ** 120):
             old = 0.0
         new = max(old, block_scale(fin.max() if fin.size else 0.0))
         if 0.0 < old < new:

@@ -198,3 +198,35 @@ def test_far_keys_anywhere(m, place):
         ref = p @ rows[:, :512] / p.sum(axis=1, keepdims=True)
         check_attention(f64(out)[0, 0], lse.cpu().numpy()[0, 0], ref, top[:, 0] + np.log(p.sum(axis=1)),
                         AttnTerms(abs_wv, smag), out_tol=np.inf, lse_tol=np.inf, label=f"{place}, split {split}")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -1.0, 2.0 ** 121])
+@pytest.mark.parametrize("window", [0, 90])
+def test_what_is_no_scale(m, bad, window):
+    """A scale that is none makes the rows that see its block NaN, in the decode
+    as in the gather, and no others."""
+    c = Case("s16", [298, 200], 2, 16, window, 0, seed=240)
+    c.scales[c.scales.isnan()] = 1.0
+    good = c.run(m)
+    # the query at 296 sees 207, the last token of its block, and the one at 297
+    # with the window does not
+    c.scales[int(c.bt[0, 207 // 64]), 207 % 64 // 16] = bad
+    out, lse = c.run(m)
+    for i, sees in enumerate((True, window == 0)):
+        for t in (out[0, i], lse[0, i]):
+            assert bool(torch.isnan(t).all()) == sees and bool(torch.isnan(t).any()) == sees
+    assert torch.equal(out[1], good[0][1]) and torch.equal(lse[1], good[1][1])
+    row = m.mla_gather_cache_scaled(c.cache.cuda(), c.scales.cuda(), _i32(c.bt), _i32(c.lens), _i32([0, 1, 1]),
+                                    1, seq_starts=_i32([207, 0]))
+    assert bool(torch.isnan(row).all())
+    assert m.mla_get_device_error() == 0
+
+
+def test_append_over_what_is_no_scale(m):
+    """A block whose scale is none begins afresh, whatever row is written."""
+    kv = torch.ones((3, 576), dtype=torch.bfloat16, device="cuda")
+    cache = torch.zeros((1, 64, 576), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scales = torch.tensor([[2.0 ** 121, -3.0, float("nan"), 2.0 ** 120]], device="cuda")
+    m.mla_rope_cache_append(None, kv[:, 512:], kv[:, :512], _i32([0, 0, 0]), _i32([5, 20, 40]), cache, scales)
+    assert m.mla_get_device_error() == 0
+    assert scales.tolist() == [[2.0 ** -8] * 3 + [2.0 ** 120]]          # 1 <= 448 * 2^-8
