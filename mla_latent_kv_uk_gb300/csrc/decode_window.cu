@@ -1409,7 +1409,8 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
     store8(out + 8 * lane, acc);
     store8(out + 8 * (lane + 32), acc + 8);
   }
-  if (mine == 0 && lane == 0) a.lse[row] = m == -INFINITY ? m : m + logf(z);
+  // (z NaN where a part's logarithm is, which no maximum shows)
+  if (mine == 0 && lane == 0) a.lse[row] = z == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + logf(z);
 }
 
 template <typename T, int SPLIT>

@@ -230,3 +230,20 @@ def test_append_over_what_is_no_scale(m):
     m.mla_rope_cache_append(None, kv[:, 512:], kv[:, :512], _i32([0, 0, 0]), _i32([5, 20, 40]), cache, scales)
     assert m.mla_get_device_error() == 0
     assert scales.tolist() == [[2.0 ** -8] * 3 + [2.0 ** 120]]          # 1 <= 448 * 2^-8
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "s32"])
+@pytest.mark.parametrize("split", [0, 2])
+def test_a_query_that_is_nan(m, fmt, split):
+    """Its row and logarithm are NaN, cut or not; the other rows are right."""
+    c = Case(fmt, [2000, 1500], 1, 16, 0, 0, seed=250)
+    good = c.run(m, split_tiles=split)
+    if fmt == "bf16":
+        c.q.view(torch.int16)[0, 0, 3, 7] = synth.BF16_NAN_BITS
+    else:
+        c.q.view(torch.uint8)[0, 0, 3, 7] = synth.E4M3_NAN_BITS
+    out, lse = c.run(m, split_tiles=split)
+    assert m.mla_get_device_error() == 0
+    assert torch.isnan(out[0, 0, 3]).all() and torch.isnan(lse[0, 0, 3])
+    out[0, 0, 3], lse[0, 0, 3] = good[0][0, 0, 3], good[1][0, 0, 3]
+    c.check(out, lse, f"{fmt} NaN query, split {split}")
