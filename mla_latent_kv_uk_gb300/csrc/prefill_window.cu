@@ -540,11 +540,13 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (any && !(ok = all_ok(wait_for(&pv_done[g], (c - 1) & 1, abort_flag)))) break;
       tc_fence_after();
       {
-        const float other = exchange(l);
+        l += exchange(l);
         if (!told) {
-          l += other;
-          named_and(bar_id, true);               // (taken: the other sum goes the same way)
-          lr += exchange(lr);
+          // the second sum goes into the slot that this thread has just read, and
+          // the other's is in its own: what a thread writes next nobody reads any more
+          *its = lr;
+          told = !named_and(bar_id, true);
+          lr += *mine;
         }
         if (told) {
           ok = false;
