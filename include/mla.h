@@ -461,7 +461,8 @@ int mla_decode_paged_scaled(const void *q, float q_scale, const void *kv_cache,
  * or gathered context, so one call attends to both.  What a query does not
  * see does not reach its row, NaN and infinities included, in rows behind
  * cu_k[B] too (a NaN or infinite value that queries of its key tile do not
- * see costs them a second look at their keys).
+ * see costs them a second look at their keys).  A request whose rows are not
+ * all in [0, Tq) and [0, Nk) sets MLA_DEVERR_RANGE and is left out.
  * B * H * ceil(max_q_len / 256) < 2^31 - 1024. */
 int mla_prefill_attn_window(const void *q, const void *k, const void *v,
                             const int32_t *cu_q, const int32_t *cu_k, int B,

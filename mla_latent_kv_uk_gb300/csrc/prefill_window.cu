@@ -69,7 +69,7 @@ static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct Args {
   const int32_t *cu_q, *cu_k;
-  int B, H, nqp, window, sinks;                  // nqp: items per (head, request)
+  int B, H, Tq, Nk, nqp, window, sinks;          // nqp: items per (head, request)
   int items;
   float scale_log2;
   __nv_bfloat16 *out;
@@ -83,6 +83,7 @@ struct Args {
 struct Item {
   int h, q0, nq, k0, nk, row0;                   // row0: its first query of the request
   int sink_tiles, lo_tile, ntiles;
+  bool outside;                                  // the request is not within the tensors: no items
   int rows[kQT], nt[kQT], skip[kQT];             // query tile g takes entries t < nt[g], t != skip[g]
 
   __device__ __forceinline__ bool load(const Args &a, int i) {
@@ -94,7 +95,8 @@ struct Item {
     k0 = __ldg(a.cu_k + b);
     nk = __ldg(a.cu_k + b + 1) - k0;
     row0 = qp * kQT * kBM;
-    if (row0 >= nq) return false;
+    outside = (q0 | nq | k0 | nk) < 0 || nq > a.Tq - q0 || nk > a.Nk - k0;
+    if (outside || row0 >= nq) return false;
     const int first = row0 + nk - nq;            // the first query's position
     const int lo = max(0, first - a.window + 1);
     lo_tile = lo / kBN;
@@ -264,7 +266,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
       int kc = 0, n = 0;                       // K tiles, items with tiles so far
       for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
         Item it;
-        if (!it.load(args, i) || it.ntiles == 0) continue;
+        const bool item = it.load(args, i);
+        if (it.outside) raise_error(args.err, MLA_DEVERR_RANGE);
+        if (!item || it.ntiles == 0) continue;
         if (n > 0 && !(ok = wait_for(q_empty, (n - 1) & 1, abort_flag))) break;
         ++n;
         mbar_arrive_expect_tx(q_full, (it.rows[1] > 0 ? 2 : 1) * kQBytes);
@@ -673,6 +677,8 @@ extern "C" int mla_prefill_attn_window(const void *q, const void *k, const void 
   a.cu_k = cu_k;
   a.B = B;
   a.H = H;
+  a.Tq = Tq;
+  a.Nk = Nk;
   a.nqp = (max_q_len - 1) / (kQT * kBM) + 1;
   const int64_t items = static_cast<int64_t>(a.nqp) * H * B;
   if (items > INT32_MAX - 1024) return MLA_ERR_INVALID_ARG;   // (and a grid's step on top)
