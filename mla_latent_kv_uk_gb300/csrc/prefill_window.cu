@@ -35,9 +35,13 @@
 // Masked keys and values that are not finite: a product over a tile multiplies
 // every value row, also by 0, so a NaN that a query does not see would reach
 // its row.  Values behind the request's last key (padding, which may hold
-// anything) are cleared in shared memory; a row whose columns come out not
-// finite although its scores are is computed again from the definition, by its
-// warp.  Rows without such values pay one test.
+// anything) are cleared in shared memory.  Where a row comes out not finite
+// although its scores are, the CTA goes through its items a second time: in the
+// tiles that some of an item's queries do not see as a whole (seven at most: the
+// diagonal, the window's edge, the sinks' end) values that are not finite are
+// then cleared as well, and put back into the rows that do see them.  That costs
+// as much again as the items did, however long the window; calls without such
+// values pay one test a row.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -74,7 +78,7 @@ struct Args {
   float scale_log2;
   __nv_bfloat16 *out;
   float *lse;
-  const __nv_bfloat16 *q, *k, *v;
+  const __nv_bfloat16 *v;
   int *err;
 };
 
@@ -119,6 +123,17 @@ struct Item {
     return t < sink_tiles ? t : t - sink_tiles + lo_tile;
   }
   __device__ __forceinline__ bool takes(int g, int t) const { return t < nt[g] && t != skip[g]; }
+  // every query that takes entry t sees all of its keys
+  __device__ __forceinline__ bool whole(const Args &a, int t) const {
+    const int key0 = tile(t) * kBN, first = row0 + nk - nq;
+    bool all = true;
+#pragma unroll
+    for (int g = 0; g < kQT; ++g) {
+      const int p0 = first + g * kBM, p1 = p0 + rows[g] - 1;
+      if (takes(g, t) && (key0 + kBN - 1 > p0 || (key0 <= p1 - a.window && key0 + kBN > a.sinks))) all = false;
+    }
+    return all;
+  }
 };
 
 __device__ __forceinline__ uint32_t elect_one() {
@@ -156,51 +171,84 @@ __device__ __forceinline__ bool named_and(uint32_t id, bool v) {
   return r != 0;
 }
 
-// 32 output columns of one query from the definition, by a whole warp: p =
-// 2^(s - m) over the keys [0, sinks) and [lo, lim), a key per lane at a time.
-// (The others wait for at most a second: a long row has to be done by then.)
-__device__ __noinline__ void row_again(const __nv_bfloat16 *q, const __nv_bfloat16 *k,
-                                       const __nv_bfloat16 *v, int64_t k_stride, int64_t v_stride,
-                                       int sinks, int lo, int lim, float scale_log2, float m,
-                                       float *o) {
-  const int lane = lane_id();
-  auto fma8 = [](uint4 a, uint4 b, float s) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+__device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
+
+// The values of a tile in shared memory, 0 in place of what is not finite, by the
+// 256 threads of a query tile.
+__device__ __forceinline__ void clear_values(uint8_t *sm_v, int thread) {
+  for (int u = thread; u < kVBytes / 16; u += 256) {
+    uint4 *at = reinterpret_cast<uint4 *>(sm_v) + u;
+    const uint4 v = *at;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), s);
-      s = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), s);
+      if (not_finite(w[e])) any = 1, w[e] &= 0xFFFF0000u;
+      if (not_finite(w[e] >> 16)) any = 1, w[e] &= 0xFFFFu;
     }
-    return s;
-  };
+    if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// What the cleared values of a tile's 128 keys from key0 on leave in 64 columns of
+// this thread's row, which sees the keys [0, sinks) and [wlo, lim): a bit for each
+// column in marks[0..1] for infinity, [2..3] for -infinity, [4..5] for NaN.  By a
+// whole warp; v: column 0 of the 64 in the request's first value row.
+__device__ __forceinline__ void mark_values(const __nv_bfloat16 *v, int64_t stride, int key0, int keys, int lim,
+                                            int wlo, int sinks, uint32_t *marks) {
+  const int lane = lane_id();
+  for (int j0 = key0; j0 < min(key0 + kBN, keys); j0 += 32) {
+    bool bad = false;
+    if (j0 + lane < keys) {
+      const uint4 *row = reinterpret_cast<const uint4 *>(v + (j0 + lane) * stride);
+      for (int e = 0; e < 8; ++e) {
+        const uint4 u = __ldg(row + e);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int e = 0; e < 32; ++e) o[e] = 0.f;
-  for (int j0 = 0; j0 < lim; j0 += 32) {
-    if (j0 >= sinks && j0 + 32 <= lo) j0 = lo & ~31;
-    const int j = j0 + lane;
-    if (j >= lim || (j >= sinks && j < lo)) continue;
-    const uint4 *kr = reinterpret_cast<const uint4 *>(k + j * k_stride);
-    const uint4 *qr = reinterpret_cast<const uint4 *>(q), *vr = reinterpret_cast<const uint4 *>(v + j * v_stride);
-    float s = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < kDq / 8; ++d) s = fma8(__ldg(qr + d), __ldg(kr + d), s);
-    const float p = ex2(fmaf(s, scale_log2, -m));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint4 u = __ldg(vr + e);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[8 * e + 2 * i] = fmaf(p, __uint_as_float(w[i] << 16), o[8 * e + 2 * i]);
-        o[8 * e + 2 * i + 1] = fmaf(p, __uint_as_float(w[i] & 0xFFFF0000u), o[8 * e + 2 * i + 1]);
+        for (int k = 0; k < 4; ++k) bad = bad || not_finite(w[k]) || not_finite(w[k] >> 16);
       }
     }
+    for (uint32_t rest = __ballot_sync(0xffffffffu, bad); rest; rest &= rest - 1) {
+      const int j = j0 + __ffs(rest) - 1;
+      if (j >= lim || (j < wlo && j >= sinks)) continue;
+      const uint16_t *row = reinterpret_cast<const uint16_t *>(v + j * stride);
+      for (int c = 0; c < 64; ++c) {
+        const uint32_t x = __ldg(row + c);
+        if (not_finite(x)) marks[(x & 0x7Fu ? 4 : x >> 15 ? 2 : 0) + c / 32] |= 1u << (c % 32);
+      }
+    }
+    __syncwarp();
   }
-  __syncwarp();
-#pragma unroll
-  for (int e = 0; e < 32; ++e)
-#pragma unroll
-    for (int x = 16; x; x >>= 1) o[e] += __shfl_xor_sync(0xffffffffu, o[e], x);
+}
+
+// Entry t of item i, the second time, by a warp of query tile g (rows' first and
+// last keys wlo, lim - 1; columns 64 sub ..).  False if a wait ran out.
+__device__ __noinline__ bool look_again(Args args, int i, int t, int g, int sub, int lim, int wlo,
+                                        uint32_t *marks, uint8_t *sm_v, uint64_t *v_full, uint32_t phase,
+                                        volatile int *abort_flag) {
+  Item it;
+  it.load(args, i);
+  if (it.whole(args, t)) return true;
+  const int64_t stride = static_cast<int64_t>(args.H) * kDv;
+  mark_values(args.v + it.k0 * stride + it.h * kDv + 64 * sub, stride, it.tile(t) * kBN, it.nk, lim, wlo, args.sinks,
+              marks);
+  if (g != 0 && it.takes(0, t)) return true;     // (the first of the two to use it clears it)
+  if (!__all_sync(0xffffffffu, wait_for(v_full, phase, abort_flag))) return false;
+  clear_values(sm_v, static_cast<int>(threadIdx.x) & 255);
+  fence_proxy_async_smem();
+  return true;
+}
+
+// Puts what was cleared back into 64 columns of a row.
+__device__ __noinline__ void put_back(__nv_bfloat16 *row, const uint32_t *marks) {
+  for (int c = 0; c < 64; ++c) {
+    const uint32_t bit = 1u << (c % 32);
+    if (!((marks[c / 32] | marks[2 + c / 32] | marks[4 + c / 32]) & bit)) continue;
+    float x = __bfloat162float(row[c]);
+    if (marks[c / 32] & bit) x += INFINITY;
+    if (marks[2 + c / 32] & bit) x -= INFINITY;
+    if (marks[4 + c / 32] & bit) x = __uint_as_float(0x7FC00000u);
+    row[c] = __float2bfloat16_rn(x);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -223,6 +271,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
   uint64_t *q_full = pv_done + kQT, *q_empty = q_full + 1, *drain = q_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  volatile int *unclean = abort_flag + 1;      // a row came out not finite
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(warp_id()), 0), lane = lane_id();
 
   if (threadIdx.x == 0) {
@@ -241,6 +290,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *unclean = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -258,12 +308,20 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   grid_dep_launch();
+  // Every warp goes through the items once, and together a second time if this says so.
+  auto once_more = [&](bool second) -> bool {
+    __syncthreads();
+    const bool again = !second && *unclean && !*abort_flag;
+    __syncthreads();                           // (all have read the same)
+    return again;
+  };
+  bool second = false;
 
   if (warp == 0) {
     // ------------------------------------------------------ Q and K
-    if (lane == 0) {
+    int kc = 0, n = 0;                         // K tiles, items with tiles so far
+    do if (lane == 0) {
       bool ok = true;
-      int kc = 0, n = 0;                       // K tiles, items with tiles so far
       for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
         Item it;
         const bool item = it.load(args, i);
@@ -293,12 +351,12 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
           mbar_wait(&k_full[u % kKStages], (u / kKStages) & 1, &no_abort);
         if (n > 0) mbar_wait(q_full, (n - 1) & 1, &no_abort);
       }
-    }
+    } while (once_more(second) && (second = true));
   } else if (warp == 2) {
     // ------------------------------------------------------------ V
-    if (lane == 0) {
+    int vc = 0;
+    do if (lane == 0) {
       bool ok = true;
-      int vc = 0;
       for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
         Item it;
         if (!it.load(args, i)) continue;
@@ -313,7 +371,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
         volatile int no_abort = 0;
         mbar_wait(v_full, (vc - 1) & 1, &no_abort);
       }
-    }
+    } while (once_more(second) && (second = true));
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMAs
     const uint32_t me = elect_one();
@@ -341,57 +399,59 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
                sdesc(vb + k * 2048, kBox, 1024, kSwizzle128B), idesc_pv, first && k == 0 ? 0u : 1u, me);
       commit(&pv_done[g], me);
     };
-    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
-      Item it;
-      if (!it.load(args, i) || it.ntiles == 0) continue;
-      bool begun[kQT] = {false, false};
-      if (!(ok = wait(q_full, n++))) break;
-      // QK(0) of both; then per tile t: PV_A(t), QK_A(t+1), PV_B(t), QK_B(t+1).
-      // QK_g(t+1) overwrites S_g after PV_g(t) has read P_g from the same
-      // columns (the tensor core runs one thread's MMAs in order).
-      if (!(ok = wait(&k_full[kc % kKStages], kc / kKStages))) break;
-      tc_fence_after();
+    do {
+      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+        Item it;
+        if (!it.load(args, i) || it.ntiles == 0) continue;
+        bool begun[kQT] = {false, false};
+        if (!(ok = wait(q_full, n++))) break;
+        // QK(0) of both; then per tile t: PV_A(t), QK_A(t+1), PV_B(t), QK_B(t+1).
+        // QK_g(t+1) overwrites S_g after PV_g(t) has read P_g from the same
+        // columns (the tensor core runs one thread's MMAs in order).
+        if (!(ok = wait(&k_full[kc % kKStages], kc / kKStages))) break;
+        tc_fence_after();
 #pragma unroll
-      for (int g = 0; g < kQT; ++g)
-        if (it.takes(g, 0)) issue_qk(g, kc % kKStages);
-      commit(&k_empty[kc % kKStages], me);
-      ++kc;
-      if (it.ntiles == 1) commit(q_empty, me);
-      for (int t = 0; ok && t < it.ntiles; ++t) {
-        if (!(ok = wait(v_full, vc))) break;
-        ++vc;
-        bool k_there = false;
+        for (int g = 0; g < kQT; ++g)
+          if (it.takes(g, 0)) issue_qk(g, kc % kKStages);
+        commit(&k_empty[kc % kKStages], me);
+        ++kc;
+        if (it.ntiles == 1) commit(q_empty, me);
+        for (int t = 0; ok && t < it.ntiles; ++t) {
+          if (!(ok = wait(v_full, vc))) break;
+          ++vc;
+          bool k_there = false;
 #pragma unroll
-        for (int g = 0; g < kQT; ++g) {
+          for (int g = 0; g < kQT; ++g) {
+            if (!ok) break;
+            if (it.takes(g, t)) {
+              if (!(ok = wait(&p_full[g], pc[g]))) break;
+              ++pc[g];
+              tc_fence_after();
+              issue_pv(g, !begun[g]);
+              begun[g] = true;
+            }
+            if (g == kQT - 1) commit(v_empty, me);
+            if (it.takes(g, t + 1)) {
+              if (!k_there && !(ok = wait(&k_full[kc % kKStages], kc / kKStages))) break;
+              tc_fence_after();
+              k_there = true;
+              issue_qk(g, kc % kKStages);
+            }
+          }
           if (!ok) break;
-          if (it.takes(g, t)) {
-            if (!(ok = wait(&p_full[g], pc[g]))) break;
-            ++pc[g];
-            tc_fence_after();
-            issue_pv(g, !begun[g]);
-            begun[g] = true;
+          if (t + 1 < it.ntiles) {
+            commit(&k_empty[kc % kKStages], me);
+            ++kc;
+            if (t + 2 == it.ntiles) commit(q_empty, me);
           }
-          if (g == kQT - 1) commit(v_empty, me);
-          if (it.takes(g, t + 1)) {
-            if (!k_there && !(ok = wait(&k_full[kc % kKStages], kc / kKStages))) break;
-            tc_fence_after();
-            k_there = true;
-            issue_qk(g, kc % kKStages);
-          }
-        }
-        if (!ok) break;
-        if (t + 1 < it.ntiles) {
-          commit(&k_empty[kc % kKStages], me);
-          ++kc;
-          if (t + 2 == it.ntiles) commit(q_empty, me);
         }
       }
-    }
-    if (*abort_flag) {
-      commit(drain, me);
-      volatile int no_abort = 0;
-      mbar_wait(drain, 0, &no_abort);
-    }
+      if (*abort_flag) {
+        commit(drain, me);
+        volatile int no_abort = 0;
+        mbar_wait(drain, 0, &no_abort);
+      }
+    } while (once_more(second) && (second = true));
   } else if (warp >= 4) {
     // -------------------------------------- softmax and results of tile g
     const int g = (warp - 4) >> 3, sub = ((warp - 4) >> 2) & 1, quarter = warp & 3;
@@ -412,225 +472,227 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
     auto all_ok = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
     int c = 0, vc = 0;                           // tiles of query tile g, V tiles so far
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
-      Item it;
-      if (!it.load(args, i)) continue;
-      const int vc0 = vc;
-      vc += it.ntiles;
-      // (selects: an index would put the arrays into local memory)
-      const int nt = g ? it.nt[1] : it.nt[0], skip = g ? it.skip[1] : -1;
-      const int rows = g ? it.rows[1] : it.rows[0];
-      if (rows == 0) continue;
-      const int q = it.row0 + g * kBM + r;       // query of the request
-      const int lim = min(it.nk, q + it.nk - it.nq + 1);
-      const int wlo = lim - args.window;         // the window's first key
-      // sums of the probabilities, for the logarithm, and of their rounded values,
-      // for the results: a large one's rounding is then in both parts of the quotient
-      // (which counts where few keys have most of the weight)
-      float m = -INFINITY, l = 0.f, lr = 0.f;
-      bool any = false;
-      for (int t = 0; t < nt; ++t) {
-        if (t == skip) continue;
-        const int key0 = it.tile(t) * kBN + 64 * sub;
-        const bool masked = key0 + 64 > lim || (key0 < wlo && key0 + 64 > args.sinks);
-        if (!(ok = all_ok(wait_for(&s_full[g], c & 1, abort_flag)))) break;
-        tc_fence_after();
-        // 32 scores at a time, read once for the maximum and once for the
-        // exponentials: 64 at once would not fit the 96 registers that 20
-        // warps have
-        // (a bit for each of the 64 keys that this query sees: three compares
-        // for each score made a masked tile cost twice an unmasked one)
-        const uint64_t seen = masked ? low_bits(lim - key0) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0))
-                                     : ~uint64_t(0);
-        auto load = [&](int h, float *x) {
-          tmem_ld_x32(lane_base + col_s + 32 * h, reinterpret_cast<uint32_t *>(x));
-          if (masked) {
-            const uint32_t w = static_cast<uint32_t>(seen >> (32 * h));
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = w & (1u << k) ? x[k] : -INFINITY;
-          }
-        };
-        // 32 rows by 32 keys that nobody sees need no exponentials: 6 of 16 of
-        // the tiles on the diagonal and at the window's edge, 15 of a few sinks'
-        const bool none[2] = {!__any_sync(0xffffffffu, static_cast<uint32_t>(seen) != 0),
-                              !__any_sync(0xffffffffu, static_cast<uint32_t>(seen >> 32) != 0)};
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (none[h]) continue;
-          float x[32];
-          load(h, x);
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = fmax3(mx[(k >> 1) & 3], x[k], x[k + 1]);
-        }
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * args.scale_log2;
-        const float other = exchange(top);
-        if (told) {
-          ok = false;
-          break;
-        }
-        top = fmaxf(top, other);
-        const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
-        float f = 1.f;
-        if (move) {
-          f = m == -INFINITY ? 0.f : ex2(m - top);
-          m = top;
-          l *= f;
-          lr *= f;
-        }
-        const bool rescale = any && __any_sync(0xffffffffu, move);
-        const float nm = m == -INFINITY ? 0.f : -m, sc = args.scale_log2;
-        float ps[4] = {0.f, 0.f, 0.f, 0.f}, pr[2] = {0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[16];   // over scores that this thread has read: of the first half, then of both
-          if (none[h]) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) pk[k] = 0;
-            tmem_st_x16(lane_base + col_s + 16 * h, pk);
-            continue;
-          }
-          float x[32];
-          load(h, x);
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            fma_f32x2(x[k], x[k + 1], x[k], x[k + 1], sc, sc, nm, nm);
-            fma_f32x2(x[k + 2], x[k + 3], x[k + 2], x[k + 3], sc, sc, nm, nm);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[k + e] = ex2(x[k + e]);
-            add_f32x2(ps[0], ps[1], ps[0], ps[1], x[k], x[k + 1]);
-            add_f32x2(ps[2], ps[3], ps[2], ps[3], x[k + 2], x[k + 3]);
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            pk[k] = bf16x2_rn(x[2 * k], x[2 * k + 1]);
-            add_f32x2(pr[0], pr[1], pr[0], pr[1], __uint_as_float(pk[k] << 16),
-                      __uint_as_float(pk[k] & 0xFFFF0000u));
-          }
-          tmem_st_x16(lane_base + col_s + 16 * h, pk);
-        }
-        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-        lr += pr[0] + pr[1];
-        if (rescale) {
-          // O follows the maximum, now that the last P V is done (64 columns
-          // for either thread of the row)
-          if (!(ok = all_ok(wait_for(&pv_done[g], (c - 1) & 1, abort_flag)))) break;
+    uint32_t marks[6];                           // (second time) by columns: infinity, -infinity, NaN
+    do {
+      for (int i = blockIdx.x; ok && i < args.items; i += gridDim.x) {
+        Item it;
+        if (!it.load(args, i)) continue;
+        const int vc0 = vc;
+        vc += it.ntiles;
+        // (selects: an index would put the arrays into local memory)
+        const int nt = g ? it.nt[1] : it.nt[0], skip = g ? it.skip[1] : -1;
+        const int rows = g ? it.rows[1] : it.rows[0];
+        if (rows == 0) continue;
+        const int q = it.row0 + g * kBM + r;       // query of the request
+        const int lim = min(it.nk, q + it.nk - it.nq + 1);
+        const int wlo = lim - args.window;         // the window's first key
+        // sums of the probabilities, for the logarithm, and of their rounded values,
+        // for the results: a large one's rounding is then in both parts of the quotient
+        // (which counts where few keys have most of the weight)
+        float m = -INFINITY, l = 0.f, lr = 0.f;
+        bool any = false;
+        if (second)
+          for (uint32_t &w : marks) w = 0;
+        for (int t = 0; t < nt; ++t) {
+          if (t == skip) continue;
+          const int key0 = it.tile(t) * kBN + 64 * sub;
+          const bool masked = key0 + 64 > lim || (key0 < wlo && key0 + 64 > args.sinks);
+          if (!(ok = all_ok(wait_for(&s_full[g], c & 1, abort_flag)))) break;
           tc_fence_after();
-#pragma unroll 1
-          for (int o0 = 0; o0 < 64; o0 += 32) {
-            uint32_t o[32];
-            tmem_ld_x32(lane_base + col_o + o0, o);
+          // 32 scores at a time, read once for the maximum and once for the
+          // exponentials: 64 at once would not fit the 96 registers that 20
+          // warps have
+          // (a bit for each of the 64 keys that this query sees: three compares
+          // for each score made a masked tile cost twice an unmasked one)
+          const uint64_t seen = masked ? low_bits(lim - key0) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0))
+                                       : ~uint64_t(0);
+          auto load = [&](int h, float *x) {
+            tmem_ld_x32(lane_base + col_s + 32 * h, reinterpret_cast<uint32_t *>(x));
+            if (masked) {
+              const uint32_t w = static_cast<uint32_t>(seen >> (32 * h));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st_x32(lane_base + col_o + o0, o);
+              for (int k = 0; k < 32; ++k) x[k] = w & (1u << k) ? x[k] : -INFINITY;
+            }
+          };
+          // 32 rows by 32 keys that nobody sees need no exponentials: 6 of 16 of
+          // the tiles on the diagonal and at the window's edge, 15 of a few sinks'
+          const bool none[2] = {!__any_sync(0xffffffffu, static_cast<uint32_t>(seen) != 0),
+                                !__any_sync(0xffffffffu, static_cast<uint32_t>(seen >> 32) != 0)};
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (none[h]) continue;
+            float x[32];
+            load(h, x);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = fmax3(mx[(k >> 1) & 3], x[k], x[k + 1]);
+          }
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * args.scale_log2;
+          const float other = exchange(top);
+          if (told) {
+            ok = false;
+            break;
+          }
+          top = fmaxf(top, other);
+          const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+          float f = 1.f;
+          if (move) {
+            f = m == -INFINITY ? 0.f : ex2(m - top);
+            m = top;
+            l *= f;
+            lr *= f;
+          }
+          const bool rescale = any && __any_sync(0xffffffffu, move);
+          const float nm = m == -INFINITY ? 0.f : -m, sc = args.scale_log2;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f}, pr[2] = {0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];   // over scores that this thread has read: of the first half, then of both
+            if (none[h]) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) pk[k] = 0;
+              tmem_st_x16(lane_base + col_s + 16 * h, pk);
+              continue;
+            }
+            float x[32];
+            load(h, x);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              fma_f32x2(x[k], x[k + 1], x[k], x[k + 1], sc, sc, nm, nm);
+              fma_f32x2(x[k + 2], x[k + 3], x[k + 2], x[k + 3], sc, sc, nm, nm);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[k + e] = ex2(x[k + e]);
+              add_f32x2(ps[0], ps[1], ps[0], ps[1], x[k], x[k + 1]);
+              add_f32x2(ps[2], ps[3], ps[2], ps[3], x[k + 2], x[k + 3]);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              pk[k] = bf16x2_rn(x[2 * k], x[2 * k + 1]);
+              add_f32x2(pr[0], pr[1], pr[0], pr[1], __uint_as_float(pk[k] << 16),
+                        __uint_as_float(pk[k] & 0xFFFF0000u));
+            }
+            tmem_st_x16(lane_base + col_s + 16 * h, pk);
+          }
+          l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+          lr += pr[0] + pr[1];
+          if (rescale) {
+            // O follows the maximum, now that the last P V is done (64 columns
+            // for either thread of the row)
+            if (!(ok = all_ok(wait_for(&pv_done[g], (c - 1) & 1, abort_flag)))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int o0 = 0; o0 < 64; o0 += 32) {
+              uint32_t o[32];
+              tmem_ld_x32(lane_base + col_o + o0, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st_x32(lane_base + col_o + o0, o);
+            }
+          }
+          const int inside = it.nk - it.tile(t) * kBN;   // rows of the tile that are this request's
+          if (inside < kBN && (g == 0 || !it.takes(0, t))) {   // (the first of the two to use it)
+            // (its scores being there, the V tiles before it are: no parity is mistaken)
+            if (!(ok = all_ok(wait_for(v_full, (vc0 + t) & 1, abort_flag)))) break;
+            for (int u = ((warp - 4) & 7) * 32 + lane; u < (kBN - inside) * 16; u += 256)
+              *reinterpret_cast<uint4 *>(sm_v + (u & 8 ? kBox : 0) + (inside + (u >> 4)) * 128 + (u & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          if (second && !(ok = look_again(args, i, t, g, sub, lim, wlo, marks, sm_v, v_full, (vc0 + t) & 1, abort_flag)))
+            break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[g]);
+          any = true;
+          ++c;
+        }
+        if (!ok) break;
+        if (any && !(ok = all_ok(wait_for(&pv_done[g], (c - 1) & 1, abort_flag)))) break;
+        tc_fence_after();
+        {
+          l += exchange(l);
+          if (!told) {
+            // the second sum goes into the slot that this thread has just read, and
+            // the other's is in its own: what a thread writes next nobody reads any more
+            *its = lr;
+            told = !named_and(bar_id, true);
+            lr += *mine;
+          }
+          if (told) {
+            ok = false;
+            break;
           }
         }
-        const int inside = it.nk - it.tile(t) * kBN;   // rows of the tile that are this request's
-        if (inside < kBN && (g == 0 || !it.takes(0, t))) {   // (the first of the two to use it)
-          // (its scores being there, the V tiles before it are: no parity is mistaken)
-          if (!(ok = all_ok(wait_for(v_full, (vc0 + t) & 1, abort_flag)))) break;
-          for (int u = ((warp - 4) & 7) * 32 + lane; u < (kBN - inside) * 16; u += 256)
-            *reinterpret_cast<uint4 *>(sm_v + (u & 8 ? kBox : 0) + (inside + (u >> 4)) * 128 + (u & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
+        const bool row_ok = r < rows;
+        const int64_t orow = static_cast<int64_t>(it.q0 + q) * args.H + it.h;
+        const bool empty = l == 0.f;
+        const float inv = empty ? 0.f : 1.f / lr;
+        float not_fin = 0.f;                       // NaN if a column is not finite
+#pragma unroll 1
+        for (int o0 = 0; o0 < 64; o0 += 32) {
+          uint32_t o[32];
+          if (any) tmem_ld_x32(lane_base + col_o + o0, o);
+          if (__any_sync(0xffffffffu, empty)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (empty) o[k] = 0;
+          }
+          float nan = 0.f, nan2 = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; k += 2)
+            fma_f32x2(nan, nan2, __uint_as_float(o[k]), __uint_as_float(o[k + 1]), 0.f, 0.f, nan, nan2);
+          nan += nan2;
+          const int col = 64 * sub + o0;
+          not_fin += nan;
+          __syncwarp();
+          // four lanes turn their rows' four 16-byte chunks round, so that a
+          // store covers 64 bytes of eight rows and not 16 of 32 (which took
+          // 4000 cycles an item)
+          uint4 w[4];
+          auto f = [&](int k) {
+            float a, b;
+            fma_f32x2(a, b, __uint_as_float(o[k]), __uint_as_float(o[k + 1]), inv, inv, -0.f, -0.f);
+            return bf16x2_rn(a, b);
+          };
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch)
+            w[ch] = make_uint4(f(8 * ch), f(8 * ch + 2), f(8 * ch + 4), f(8 * ch + 6));
+#pragma unroll
+          for (int s = 1; s < 4; s <<= 1) {
+            const bool up = lane & s;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              if (ch & s) continue;
+              uint4 give = up ? w[ch] : w[ch | s];
+              give.x = __shfl_xor_sync(0xffffffffu, give.x, s);
+              give.y = __shfl_xor_sync(0xffffffffu, give.y, s);
+              give.z = __shfl_xor_sync(0xffffffffu, give.z, s);
+              give.w = __shfl_xor_sync(0xffffffffu, give.w, s);
+              if (up) w[ch] = give;
+              else w[ch | s] = give;
+            }
+          }
+          const int r0 = quarter * 32 + (lane & ~3);
+          __nv_bfloat16 *dst = args.out + ((static_cast<int64_t>(it.q0) + it.row0 + g * kBM + r0) * args.H + it.h) * kDv +
+                               col + 8 * (lane & 3);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (r0 + k < rows) *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(k) * args.H * kDv) = w[k];
         }
+        // (a row whose own scores are not finite, l NaN, is as it should be)
+        if (row_ok && l > 0.f && not_fin != 0.f) *unclean = 1;
+        if (second) {
+          __syncwarp();                            // (other lanes have stored the row)
+          if (row_ok) put_back(args.out + orow * kDv + 64 * sub, marks);
+        }
+        if (row_ok && sub == 0)
+          args.lse[orow] = empty ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[g]);
-        any = true;
-        ++c;
       }
-      if (!ok) break;
-      if (any && !(ok = all_ok(wait_for(&pv_done[g], (c - 1) & 1, abort_flag)))) break;
-      tc_fence_after();
-      {
-        l += exchange(l);
-        if (!told) {
-          // the second sum goes into the slot that this thread has just read, and
-          // the other's is in its own: what a thread writes next nobody reads any more
-          *its = lr;
-          told = !named_and(bar_id, true);
-          lr += *mine;
-        }
-        if (told) {
-          ok = false;
-          break;
-        }
-      }
-      const bool row_ok = r < rows;
-      const int64_t orow = static_cast<int64_t>(it.q0 + q) * args.H + it.h;
-      const bool empty = l == 0.f;
-      const float inv = empty ? 0.f : 1.f / lr;
-#pragma unroll 1
-      for (int o0 = 0; o0 < 64; o0 += 32) {
-        uint32_t o[32];
-        if (any) tmem_ld_x32(lane_base + col_o + o0, o);
-        if (__any_sync(0xffffffffu, empty)) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (empty) o[k] = 0;
-        }
-        float nan = 0.f, nan2 = 0.f;   // NaN if a column is not finite
-#pragma unroll
-        for (int k = 0; k < 32; k += 2)
-          fma_f32x2(nan, nan2, __uint_as_float(o[k]), __uint_as_float(o[k + 1]), 0.f, 0.f, nan, nan2);
-        nan += nan2;
-        const int col = 64 * sub + o0;
-        // (a row whose own scores are not finite, l NaN, stays NaN)
-        for (uint32_t again = __ballot_sync(0xffffffffu, row_ok && l > 0.f && nan != 0.f); again;
-             again &= again - 1) {
-          const int from = __ffs(again) - 1;
-          float row[32];
-          const int64_t ks = static_cast<int64_t>(args.H) * kDq, vs = static_cast<int64_t>(args.H) * kDv;
-          const int64_t at = __shfl_sync(0xffffffffu, orow, from);
-          const int h = static_cast<int>(at % args.H), b = i / args.nqp / args.H;
-          const int64_t k0 = __ldg(args.cu_k + b);   // (not kept in a register for this)
-          row_again(args.q + at * kDq, args.k + k0 * ks + h * kDq, args.v + k0 * vs + h * kDv + col, ks, vs,
-                    args.sinks, __shfl_sync(0xffffffffu, wlo, from), __shfl_sync(0xffffffffu, lim, from),
-                    args.scale_log2, __shfl_sync(0xffffffffu, m, from), row);
-          if (lane == from)                    // (of unrounded probabilities)
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(row[k] * (lr / l));
-        }
-        __syncwarp();
-        // four lanes turn their rows' four 16-byte chunks round, so that a
-        // store covers 64 bytes of eight rows and not 16 of 32 (which took
-        // 4000 cycles an item)
-        uint4 w[4];
-        auto f = [&](int k) {
-          float a, b;
-          fma_f32x2(a, b, __uint_as_float(o[k]), __uint_as_float(o[k + 1]), inv, inv, -0.f, -0.f);
-          return bf16x2_rn(a, b);
-        };
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
-          w[ch] = make_uint4(f(8 * ch), f(8 * ch + 2), f(8 * ch + 4), f(8 * ch + 6));
-#pragma unroll
-        for (int s = 1; s < 4; s <<= 1) {
-          const bool up = lane & s;
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            if (ch & s) continue;
-            uint4 give = up ? w[ch] : w[ch | s];
-            give.x = __shfl_xor_sync(0xffffffffu, give.x, s);
-            give.y = __shfl_xor_sync(0xffffffffu, give.y, s);
-            give.z = __shfl_xor_sync(0xffffffffu, give.z, s);
-            give.w = __shfl_xor_sync(0xffffffffu, give.w, s);
-            if (up) w[ch] = give;
-            else w[ch | s] = give;
-          }
-        }
-        const int r0 = quarter * 32 + (lane & ~3);
-        __nv_bfloat16 *dst = args.out + ((static_cast<int64_t>(it.q0) + it.row0 + g * kBM + r0) * args.H + it.h) * kDv +
-                             col + 8 * (lane & 3);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (r0 + k < rows) *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(k) * args.H * kDv) = w[k];
-      }
-      if (row_ok && sub == 0)
-        args.lse[orow] = empty ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-      tc_fence_before();
-    }
-    if (!told) named_and(bar_id, ok && !*abort_flag);
+      if (!told) named_and(bar_id, ok && !*abort_flag);
+    } while (once_more(second) && (second = true));
+  } else {
+    while (once_more(second)) second = true;
   }
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) raise_error(args.err, MLA_DEVERR_TIMEOUT);
@@ -689,8 +751,6 @@ extern "C" int mla_prefill_attn_window(const void *q, const void *k, const void 
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.lse = lse;
-  a.q = static_cast<const __nv_bfloat16 *>(q);
-  a.k = static_cast<const __nv_bfloat16 *>(k);
   a.v = static_cast<const __nv_bfloat16 *>(v);
   const int sms = device_sm_count();
   if (sms < 1 || cudaFuncSetAttribute(prefill_window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
