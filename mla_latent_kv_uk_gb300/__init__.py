@@ -6,7 +6,8 @@ and calls the C entry point of the same name on torch's current CUDA stream
 (the window, sink and block-scaled-cache calls through a compiled module).
 All arithmetic runs in the library's CUDA kernels; there is no fallback.
 Importing this module raises ImportError if the library has not been built
-(``python -c "import __graft_entry__ as g; g.build()"``).
+(``python -c "import __graft_entry__ as g; g.build()"``); so does the first of
+the compiled calls if its module has not.
 """
 
 from __future__ import annotations
@@ -99,9 +100,20 @@ def _check(fn, status):
         raise MlaError(fn, status)
 
 
+class _Binding:
+    """The compiled module, loaded at the first call that needs it: the other
+    calls do without a module built for this interpreter and this PyTorch."""
+
+    def __getattr__(self, name):
+        mod = _load_binding()
+        for call in ("append", "gather", "decode", "prefill"):
+            setattr(self, call, getattr(mod, call))     # (looked up once)
+        return getattr(mod, name)
+
+
 def _load_binding():
-    """The compiled module, which gets the entries' addresses from here: there
-    is one library, this process's."""
+    """The module, which gets the entries' addresses from here: there is one
+    library, this process's."""
     path = _build.binding_path()
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: build the CUDA library first "
@@ -115,7 +127,7 @@ def _load_binding():
     return mod
 
 
-_binding = _load_binding()
+_binding = _Binding()
 
 
 def _stream():
