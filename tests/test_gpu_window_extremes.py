@@ -9,6 +9,7 @@ import synth
 from oracle import window as W
 from tests._helpers import AttnTerms, check_attention, f64, row_terms
 from tests.test_gpu_window_decode import Case, _i32
+from tests.test_gpu_window_prefill import _check as check_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -247,3 +248,53 @@ def test_a_query_that_is_nan(m, fmt, split):
     assert torch.isnan(out[0, 0, 3]).all() and torch.isnan(lse[0, 0, 3])
     out[0, 0, 3], lse[0, 0, 3] = good[0][0, 0, 3], good[1][0, 0, 3]
     c.check(out, lse, f"{fmt} NaN query, split {split}")
+
+
+def test_step_element_by_element(m):
+    """A prompt's chunk and a decode step over a block-scaled cache as a server
+    makes them (append, gather, expand, windowed prefill, append, windowed decode),
+    each result within its own elements' bounds: a weight or a sink that is off by
+    a few percent does not pass."""
+    g = synth.generator(260)
+    H, sb, window, sinks, scale = 4, 16, 90, 3, 1 / np.sqrt(192)
+    old, new = [170, 33], [60, 41]
+    lens = np.array([a + n for a, n in zip(old, new)], np.int32)
+    bt, nb = synth.paged_layout(g, lens + 1)
+    slots = [bt[b, p // 64] * 64 + p % 64 for b in range(2) for p in range(lens[b])]
+    pos = np.concatenate([np.arange(n) for n in lens]).astype(np.int32)
+    cache = torch.zeros((nb, 64, 576), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scales = torch.zeros((nb, 64 // sb), device="cuda")
+    kv = synth.as_bf16(g.standard_normal((len(slots), 576)) + 0.5).cuda()
+    q = synth.as_bf16(g.standard_normal((len(slots), H, 192))).cuda()
+    w = synth.as_bf16(g.standard_normal((H * 256, 512)) * 0.05).cuda()
+    m.mla_get_device_error()
+    m.mla_rope_cache_append(q[:, :, 128:], kv[:, 512:], kv[:, :512], _i32(pos), _i32(slots), cache, scales)
+    cu_k = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    cu_q = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    rows = m.mla_gather_cache_scaled(cache, scales, _i32(bt), _i32(lens), _i32(cu_k), len(slots))
+    K, V = m.mla_expand_kv(rows, w, H)
+    qn = q[torch.from_numpy(np.concatenate([cu_k[b] + old[b] + np.arange(new[b]) for b in range(2)])).cuda()]
+    out, lse = m.mla_prefill_attn_window(qn, K, V, _i32(cu_q), _i32(cu_k), max(new), window=window, sinks=sinks,
+                                         sm_scale=scale)
+    check_prefill(out, lse, qn, K, V, cu_q, cu_k, window, sinks, "prefill stage")
+    kv1 = synth.as_bf16(g.standard_normal((2, 576)) + 0.5).cuda()
+    q1 = g.standard_normal((2, 1, H, 576)).astype(np.float32)
+    qs = float(np.float32(np.abs(q1).max() / 448))
+    q1 = synth.as_e4m3(q1 / np.float32(qs)).cuda()
+    slots1 = [bt[b, lens[b] // 64] * 64 + lens[b] % 64 for b in range(2)]
+    m.mla_rope_cache_append(None, kv1[:, 512:], kv1[:, :512], _i32(lens), _i32(slots1), cache, scales)
+    out, lse = m.mla_decode_paged_scaled(q1, cache, scales, _i32(bt), _i32(lens + 1), sm_scale=scale, q_scale=qs,
+                                         window=window, sinks=sinks)
+    assert m.mla_get_device_error() == 0
+    c64 = W.scaled_values(cache.view(torch.uint8).cpu().numpy(), scales.cpu().numpy())
+    q64 = f64(q1) * qs
+    ref, ref_l = W.window_decode(q64, c64, bt, lens + 1, scale, window, sinks)
+    abs_wv, smag = np.zeros((2, 1, H, 512)), np.zeros((2, 1, H))
+    for b in range(2):
+        j = W.visible(int(lens[b]), window, sinks)
+        r = c64[bt[b, j // 64], j % 64]
+        abs_wv[b, 0], smag[b, 0], _ = row_terms(q64[b, 0], r, r[:, :512], scale)
+    # probabilities of 2^-6 of the largest and more off by 2^-8, fewer by 2^-19 of the
+    # largest (of 93 keys: 2^-12 of the weights): the bound of bf16 ones holds
+    check_attention(f64(out), lse.cpu().numpy(), ref, ref_l, AttnTerms(abs_wv, smag), out_tol=np.inf,
+                    lse_tol=np.inf, label="decode stage")
