@@ -312,7 +312,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
   auto once_more = [&](bool second) -> bool {
     __syncthreads();
     const bool again = !second && *unclean && !*abort_flag;
-    __syncthreads();                           // (all have read the same)
+    if (again) __syncthreads();                // (all read the same before one goes on)
     return again;
   };
   bool second = false;
@@ -694,7 +694,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
   } else {
     while (once_more(second)) second = true;
   }
-  __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) raise_error(args.err, MLA_DEVERR_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
