@@ -418,6 +418,11 @@ int mla_gather_cache_scaled(const void *kv_cache, const float *kv_scales,
  * over the visible j; no visible key (p < 0): out = 0, lse = -inf.  K_j, V_j,
  * q_deq, slots and layouts as in mla_decode_paged; in the scaled form kv_deq
  * takes the block's scale in place of k_scale and q is e4m3.
+ * Over an e4m3 cache a weight is held to 2^-8 of itself.  One that (times its
+ * key's scale) is less than the largest of its tile of 128 keys may be off by
+ * 2^-8 of that one, at most by 2^-3 of itself, and counts as 0 below 2^-11 of
+ * it (in tiles whose largest is 2^-27 of the row's or less, below 2^-38 of the
+ * row's); lse has all of them.  Scores are fp32: sm_scale * |q_deq . K| < 2^127.
  * Cache rows that no query token of a request sees (past seq_lens, behind
  * the window) are never used, whatever they hold, and block-table entries
  * of pages without a visible key are not read.
@@ -460,8 +465,8 @@ int mla_decode_paged_scaled(const void *q, float q_scale, const void *kv_cache,
  * The window is the same whether the keys before the queries are new tokens
  * or gathered context, so one call attends to both.  What a query does not
  * see does not reach its row, NaN and infinities included, in rows behind
- * cu_k[B] too (a NaN or infinite value that queries of its key tile do not
- * see costs them a second look at their keys).  A request whose rows are not
+ * cu_k[B] too (a NaN or infinite value that some queries of its key tile do
+ * not see makes the call take about twice as long).  A request whose rows are not
  * all in [0, Tq) and [0, Nk) sets MLA_DEVERR_RANGE and is left out.
  * B * H * ceil(max_q_len / 256) < 2^31 - 1024. */
 int mla_prefill_attn_window(const void *q, const void *k, const void *v,

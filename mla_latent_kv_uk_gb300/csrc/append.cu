@@ -14,13 +14,13 @@
 // its old rows may have to follow it, so one CTA owns a block: that of the
 // block's first token in the call.  It finds the other members by reading
 // the slot list; most tokens are passed over on seeing that the token before
-// them has the same block.
+// them has the same block.  (Every block reads all slots: at 2048 tokens one
+// round of loads, but the work grows with their square.)
 //
 // What bounds it: a step (32 tokens, 128 heads: 1 MB) is one chain of loads
 // (slots, rows), arithmetic and stores, 4.0 us with the launch.  A chunk moves
 // its queries, read and written: 63 MB in 15.3 us, 4.1 TB/s of the 6.8 that a
-// copy reaches, the first 3 us of which look at slots and fill the memory
-// pipes.  Measured on the way there: a CTA for each token, that looks at the
+// copy reaches, the first 3 us of which pass until that rate is there.  Measured on the way there: a CTA for each token, that looks at the
 // slots and leaves, 18.5 us; rows read again for their codes instead of kept,
 // 15.8; three CTAs to an SM in 40 registers, 16.0 (spilled rows).
 #include <cuda_bf16.h>

@@ -30,8 +30,10 @@
 // weight with lo = e4m3), a row's reference also follows its tiles down: where a
 // tile's largest p falls below 2^-6, to 1, with O (fp32) scaled up; at most 2^16
 // below the highest, so 2^-21 of the row's largest p and more are held like that.
-// What a row loses is then 2^-8 of its weights and, in a tile, what is below
-// 2^-11 of the tile's largest: it does not grow with the number of keys.
+// A weight is then off by 2^-8 of itself; where it (times its key's scale) is less
+// than the largest of its 128 keys, by up to 2^-8 of that one or 2^-3 of itself,
+// whichever is less; and lost below 2^-11 of that one.  None of it grows with the
+// number of keys.
 // (e4m3 for both: half the error on rows whose scores are alike, 7e-4 instead of
 // 1.3e-3 of an output's rms where its own rounding is 1.7e-3.  e5m2 for both
 // has the range without the steps down, at 2.3e-3.)
@@ -64,13 +66,14 @@
 // error from 2.3e-3 to 2.7e-3 of its rms; fp32 ones are twice the bytes, 2 to 5
 // us of a merge).
 //
-// What bounds it now (each key row takes 128 x 1088 x 2 operations a row group):
-// 64 e4m3 requests of up to 16384 tokens 90 us, at 1.65 of the 1.9 PFLOP/s that
-// a bf16 product reaches, near the 1632 cycles of a tile's MMAs; 128 bf16
-// requests of two tokens and a window of 4096 146 us, 1.15 PFLOP/s, where Q K^T
-// of 64 keys takes as long as one of 128; one e4m3 request of 131072 tokens
-// 34.5 us, the smallest calls 8.8: 3 us until the first keys are there, 4 from
-// the last scores to the results, and 3 for the merge where there is one.
+// What bounds it now (each key row takes 128 x 1088 x 2 operations a row group;
+// times of graph replays, in brackets of calls on changing inputs): 64 e4m3
+// requests of up to 16384 tokens 94 us (100), at 1.6 of the 1.9 PFLOP/s that a
+// bf16 product reaches, near the 1632 cycles of a tile's MMAs; 128 bf16 requests
+// of two tokens and a window of 4096 147 us (155), 1.14 PFLOP/s, where Q K^T of 64
+// keys takes as long as one of 128; one e4m3 request of 131072 tokens 35.6 us (35.0),
+// the smallest calls 8.4: 3 us until the first keys are there, 4 from the last
+// scores to the results, and 3 for the merge where there is one.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -178,7 +181,7 @@ struct WindowArgs {
   int *ws_head;                 // C of each group; then per job {first unit, end unit}
   void *ws_o;                   // [slots, 128, 512] fp32, or fp16 for a bf16 output
   float *ws_lse;                // [slots, 128]
-  float *ws_unit;               // [slots, 128, 2, 2] fp16: what 1 stands for, by 128 columns (1, 3; 2, 4)
+  float *ws_unit;               // [slots, 128, 2, 2]: what 1 of the fp16 stands for, by 128 columns (1, 3; 2, 4)
   int *err;
 };
 
@@ -446,7 +449,11 @@ __device__ __forceinline__ void load_3d_hint(void *dst, const CUtensorMap *map, 
 // and a test costs about 70 cycles where try_wait costs about 190.  What the
 // barriers order across the pair is read by the tensor cores and the TMA
 // only, so no wait needs cluster-scope acquire (one took about 200 cycles
-// more, and a cluster-scope release of the probabilities 1600 a tile).
+// more, and a cluster-scope release of the probabilities 1600 a tile): either
+// SM's tensor core reads its rows of P in its own CTA's shared memory, where the
+// CTA-scope release in front of the remote arrival has put them.  That this is
+// enough for a CTA of the pair to say so to the other is how the hardware
+// behaves; the PTX memory model does not promise it without cluster scope.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
   return mbar_test(bar, parity) || mbar_wait(bar, parity, abort_flag);
 }
