@@ -160,7 +160,9 @@ struct Fmt {
   static constexpr float kLazy = FP8 ? 8.75f : 16.f;
   // e4m3: p' of a tile's largest key at which the reference follows it down, at
   // most kDepth below the highest one (-3 in place of -6: on 16384 keys of a
-  // deviation of 3 nats 57 passes over O in 128 tiles and not 21, and no less error)
+  // deviation of 3 nats 57 passes over O in 128 tiles and not 21, and no less error;
+  // 64 requests of 8192 tokens at a deviation of 1.5 / 3 / 5 nats and more: 85.7 /
+  // 97.2 / 109 us, 85.0 / 94.0 / 98.5 without going down)
   static constexpr float kLow = -6.f, kDepth = 16.f;
 };
 
