@@ -57,6 +57,7 @@ enum mla_device_error {
   MLA_DEVERR_SEQ_LEN = 2,     /* seq_len < 0 or > max_blocks * 64           */
   MLA_DEVERR_RANGE = 4,       /* gather range beyond seq_len / workspace    */
   MLA_DEVERR_TIMEOUT = 8,     /* a bounded wait inside a kernel gave up     */
+  MLA_DEVERR_PAGES = 16,      /* no free page, or a page operation refused  */
 };
 
 /* Self-test of the failure detection every kernel relies on (no
@@ -456,6 +457,137 @@ int mla_decode_paged_scaled(const void *q, float q_scale, const void *kv_cache,
                             int window, int sinks, int split_tiles, void *out,
                             int out_dtype, float *lse, void *workspace,
                             size_t ws_bytes, mla_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Decode of a tree of drafted tokens
+ * Speculative decode where a request's new tokens are not a chain: their rows
+ * are the last n = tree_lens[b] of its seq_lens[b] (n = q_len where tree_lens
+ * is NULL), behind a context of c = seq_lens[b] - n tokens, in any order.
+ * For query token i < n, head h:
+ *   visible: j < c, or j = c + t with t < n and bit t of the word
+ *            tree_mask[b * mask_stride + i] set
+ *   s_j, lse, out as in mla_decode_paged_window
+ * Nothing is implied by the order: a token that sees itself has its own bit
+ * set, a tree has those of the token and of all above it, a chain has (2 << i)
+ * - 1; any other mask will do.  Keys at a negative position (n > seq_lens[b])
+ * are not there.  A row that sees no key, and rows i >= n (whose words and
+ * queries may hold anything): out = 0, lse = -inf.
+ * mask_stride: q_len or more, or 0: one tree for all requests (tree_lens
+ * then cuts it).  tree_lens[b] outside [0, q_len] sets MLA_DEVERR_SEQ_LEN and
+ * counts as 0.  kv_scales [num_blocks, 64/scale_block]: a block-scaled e4m3
+ * cache (k_scale is not used), else NULL.  Precision, limits and what is not
+ * read as in mla_decode_paged_window, whose workspace size (window 0, sinks 0)
+ * is this one's. */
+int mla_decode_paged_tree(const void *q, int q_dtype, float q_scale,
+                          const void *kv_cache, int kv_dtype, float k_scale,
+                          const float *kv_scales, int scale_block,
+                          const int32_t *block_table, const int32_t *seq_lens,
+                          const int32_t *tree_lens, const uint64_t *tree_mask,
+                          int64_t mask_stride, int B, int q_len, int H,
+                          int max_blocks, int num_blocks, float sm_scale,
+                          int split_tiles, void *out, int out_dtype, float *lse,
+                          void *workspace, size_t ws_bytes,
+                          mla_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Pages of the cache: who has them, and their copies
+ * A cache's pages belong to sequences, rows of block_table [B,max_blocks] of
+ * which the first ceil(seq_lens[b] / 64) entries are pages; refs [num_blocks]
+ * int32 (16-byte aligned) says how many entries hold each page, 0: it is free.
+ * The calls below keep the three in step, on the device and in a stream's
+ * order; calls on the same state follow one another on a stream.  Free pages
+ * are taken lowest first, so the result depends on the state alone.
+ *
+ * Pools are what a page has in memory: for every layer its cache [num_blocks,
+ * 64,576], its block scales, or anything else of num_blocks rows.  pools and
+ * page_bytes are HOST arrays of n_pools (0 to 200) device pointers and of a
+ * page's bytes in each: multiples of 4; pools whose page is a multiple of 16
+ * and 1024 or more start on 16 bytes, the others on 4.  num_blocks < 2^25.
+ * 1 <= B <= 8192, 1 <= max_blocks <= 2^24 (mla_cache_accept: any B >= 1).
+ *
+ * Copy: page dst[k] of every pool becomes page src[k], k < n (int32 [n]).
+ * A negative id is padding; one >= num_blocks sets MLA_DEVERR_BLOCK_ID, and
+ * the pair is left out.  Of equal destinations the last one's pair counts.  A
+ * destination that is another pair's source is not written and sets
+ * MLA_DEVERR_PAGES.  refs and tables are the caller's business here.  n <
+ * 2^25 (every pair looks at all others: lists of many thousands cost time). */
+int mla_cache_copy(void *const *pools, const int64_t *page_bytes, int n_pools,
+                   int num_blocks, const int32_t *src, const int32_t *dst,
+                   int n, mla_stream_t stream);
+
+/* Resize: sequence b gets the length new_lens[b] [B].  Entries behind it are
+ * released (refs - 1, the entry -1: a page that nobody else holds is free);
+ * then entries that it lacks get the lowest free pages, sequences in their
+ * order, those released by this call among them.  So a new sequence grows from
+ * 0, a finished one goes to 0, and a length inside the last page only changes.
+ * A sequence whose pages, counted with those for the ones in front of it, are
+ * more than are free keeps its length and pages and sets MLA_DEVERR_PAGES;
+ * a length < 0 or > max_blocks * 64, old or new: unchanged, MLA_DEVERR_SEQ_LEN.
+ * An entry that is no page sets MLA_DEVERR_BLOCK_ID, one that was free already
+ * MLA_DEVERR_PAGES.  Pages' contents stay as they are. */
+int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_table,
+                     int32_t *seq_lens, const int32_t *new_lens, int B,
+                     int max_blocks, mla_stream_t stream);
+
+/* Fork: for i < n (at most 8192) sequence children[i], of length 0, becomes the
+ * tokens of parents[i]: full pages are shared (refs + 1), of a last page that
+ * is not full the rows with tokens are copied, in every pool, into a free page
+ * (a pool whose page is no multiple of 1024 bytes, such as scales: the page).
+ * Parents are as they were before the call.  Left out, with MLA_DEVERR_PAGES:
+ * a child that has tokens or came up before, and from where free pages run
+ * out on every fork that needs one; a row outside [0, B): MLA_DEVERR_RANGE; a
+ * parent's length out of range: MLA_DEVERR_SEQ_LEN; a parent's entry that is
+ * no page: MLA_DEVERR_BLOCK_ID, and the child's is -1.
+ * workspace: mla_cache_fork_workspace_size(n) bytes. */
+int mla_cache_fork_workspace_size(int n, size_t *bytes);
+
+int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int n_pools,
+                   int32_t *refs, int num_blocks, int32_t *block_table,
+                   int32_t *seq_lens, int B, int max_blocks,
+                   const int32_t *parents, const int32_t *children, int n,
+                   void *workspace, size_t ws_bytes, mla_stream_t stream);
+
+/* Compact: with N pages in use, those from page N on move, in their order, to
+ * the free pages below N, in theirs: copied in every pool, their refs and all
+ * entries of the B sequences with them.  *n_live (device) becomes N: pages
+ * from N on are free.  What they held stays.  Every page in use is held by
+ * these sequences, or by entries that the caller has elsewhere and updates
+ * himself.  An entry that is no page sets MLA_DEVERR_BLOCK_ID, one that is
+ * free and not below N MLA_DEVERR_PAGES; both stay.
+ * workspace: mla_cache_compact_workspace_size(num_blocks) bytes. */
+int mla_cache_compact_workspace_size(int num_blocks, size_t *bytes);
+
+int mla_cache_compact(void *const *pools, const int64_t *page_bytes,
+                      int n_pools, int32_t *refs, int num_blocks,
+                      int32_t *block_table, const int32_t *seq_lens, int B,
+                      int max_blocks, int32_t *n_live, void *workspace,
+                      size_t ws_bytes, mla_stream_t stream);
+
+/* Accept: of the n = tree_lens[b] (NULL: q_len) drafted tokens that end
+ * sequence b (mla_decode_paged_tree) keeps those of its path, k =
+ * path_lens[b] of them: row c + path[b * path_width + i] of every layer's cache
+ * becomes row c + i, i < k, c = seq_lens[b] - n.  A path ascends.  new_lens[b]
+ * [B] = c + k (mla_cache_resize then takes the length and the pages behind).
+ * Rows behind c + k, and seq_lens, stay as they are.  The rows' pages are the
+ * sequence's own.
+ * kv_scales (a HOST array of n_pools device pointers, each [num_blocks,
+ * 64/scale_block], or NULL): block-scaled e4m3 caches.  The rows are then
+ * appended to their new blocks by the rule of mla_rope_cache_append, from what
+ * they stand for: with A the largest finite of a block's new rows and s its
+ * scale (0 if its first row is among them, or s is no scale), s' = max(s,
+ * 2^max(-100, ceil(log2(A / 448)))); a row of scale r is stored as e4m3(code *
+ * (r / s')), the block's other rows, where s grew, as e4m3(code * (s / s')).
+ * A path that is no such list, k > n or path_width, or c < 0 with k > 0:
+ * MLA_DEVERR_RANGE; lengths out of range: MLA_DEVERR_SEQ_LEN; an entry that is
+ * no page: MLA_DEVERR_BLOCK_ID: the sequence stays as it is, new_lens[b] =
+ * seq_lens[b] (as where c < 0 and k = 0).  pools [num_blocks,64,576] of kv_dtype, 16-byte
+ * aligned.  1 <= q_len, path_width <= 64.  new_lens is not seq_lens. */
+int mla_cache_accept(void *const *pools, int kv_dtype, float *const *kv_scales,
+                     int scale_block, int n_pools, int num_blocks,
+                     const int32_t *block_table, const int32_t *seq_lens,
+                     const int32_t *tree_lens, int q_len, const int32_t *path,
+                     int path_width, const int32_t *path_lens, int B,
+                     int max_blocks, int32_t *new_lens, mla_stream_t stream);
 
 /* ---------------------------------------------------------------------
  * Prefill attention with a sliding window and sinks

@@ -3,7 +3,8 @@
 Argument marshalling only: every function below checks tensor devices,
 dtypes and shapes, allocates outputs with torch when the caller passes none,
 and calls the C entry point of the same name on torch's current CUDA stream
-(the window, sink and block-scaled-cache calls through a compiled module).
+(the window, sink, block-scaled-cache, tree and cache-page calls through a
+compiled module).
 All arithmetic runs in the library's CUDA kernels; there is no fallback.
 Importing this module raises ImportError if the library has not been built
 (``python -c "import __graft_entry__ as g; g.build()"``); so does the first of
@@ -28,7 +29,8 @@ __all__ = [
     "mla_gather_cache_reorg", "mla_expand_kv", "mla_prefill_attn", "mla_rope_cache_write",
     "mla_stage_copy", "mla_rope_cache_append", "mla_gather_cache_scaled",
     "mla_decode_window_workspace_size", "mla_decode_paged_window", "mla_decode_paged_scaled",
-    "mla_prefill_attn_window",
+    "mla_prefill_attn_window", "mla_decode_paged_tree", "mla_cache_copy", "mla_cache_resize",
+    "mla_cache_fork", "mla_cache_compact", "mla_cache_accept",
 ]
 
 BF16, E4M3, F32 = 0, 1, 2
@@ -69,6 +71,15 @@ _SIGNATURES = {
                                  _p, _i, _p, _p, _sz, _p], _i),
     "mla_prefill_attn_window": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p],
                                 _i),
+    "mla_decode_paged_tree": ([_p, _i, _f, _p, _i, _f, _p, _i, _p, _p, _p, _p, _i64, _i, _i, _i,
+                               _i, _i, _f, _i, _p, _i, _p, _p, _sz, _p], _i),
+    "mla_cache_copy": ([_p, _p, _i, _i, _p, _p, _i, _p], _i),
+    "mla_cache_resize": ([_p, _i, _p, _p, _p, _i, _i, _p], _i),
+    "mla_cache_fork_workspace_size": ([_i, ctypes.POINTER(_sz)], _i),
+    "mla_cache_fork": ([_p, _p, _i, _p, _i, _p, _p, _i, _i, _p, _p, _i, _p, _sz, _p], _i),
+    "mla_cache_compact_workspace_size": ([_i, ctypes.POINTER(_sz)], _i),
+    "mla_cache_compact": ([_p, _p, _i, _p, _i, _p, _p, _i, _i, _p, _p, _sz, _p], _i),
+    "mla_cache_accept": ([_p, _i, _p, _i, _i, _i, _p, _p, _p, _i, _p, _i, _p, _i, _i, _p, _p], _i),
 }
 
 
@@ -106,7 +117,8 @@ class _Binding:
 
     def __getattr__(self, name):
         mod = _load_binding()
-        for call in ("append", "gather", "decode", "prefill"):
+        for call in ("append", "gather", "decode", "prefill", "copy", "resize", "fork", "compact",
+                     "accept"):
             setattr(self, call, getattr(mod, call))     # (looked up once)
         return getattr(mod, name)
 
@@ -123,7 +135,10 @@ def _load_binding():
     spec.loader.exec_module(mod)
     mod.bind(_check, *(ctypes.cast(getattr(lib, name), _p).value for name in (
         "mla_rope_cache_append", "mla_gather_cache_scaled", "mla_decode_window_workspace_size",
-        "mla_decode_paged_window", "mla_decode_paged_scaled", "mla_prefill_attn_window")))
+        "mla_decode_paged_window", "mla_decode_paged_scaled", "mla_prefill_attn_window",
+        "mla_decode_paged_tree", "mla_cache_copy", "mla_cache_resize",
+        "mla_cache_fork_workspace_size", "mla_cache_fork", "mla_cache_compact_workspace_size",
+        "mla_cache_compact", "mla_cache_accept")))
     return mod
 
 
@@ -434,7 +449,7 @@ def mla_decode_paged_window(q, kv_cache, block_table, seq_lens, *, sm_scale, win
     """mla_decode_paged (causal) where a query at position p sees the keys
     j > p - window and the first `sinks` (window 0: every earlier key)."""
     return _binding.decode(q, kv_cache, None, block_table, seq_lens, sm_scale, q_scale, k_scale, window,
-                           sinks, split_tiles, out_dtype, out, lse, workspace)
+                           sinks, split_tiles, out_dtype, out, lse, workspace, None, None)
 
 
 def mla_decode_paged_scaled(q, kv_cache, kv_scales, block_table, seq_lens, *, sm_scale,
@@ -445,7 +460,7 @@ def mla_decode_paged_scaled(q, kv_cache, kv_scales, block_table, seq_lens, *, sm
     if kv_scales is None:
         raise TypeError("kv_scales must be a tensor")
     return _binding.decode(q, kv_cache, kv_scales, block_table, seq_lens, sm_scale, q_scale, 1.0, window,
-                           sinks, split_tiles, out_dtype, out, lse, workspace)
+                           sinks, split_tiles, out_dtype, out, lse, workspace, None, None)
 
 
 def mla_prefill_attn_window(q, k, v, cu_q, cu_k, max_q_len, *, window, sinks=0, sm_scale, out=None,
@@ -453,6 +468,60 @@ def mla_prefill_attn_window(q, k, v, cu_q, cu_k, max_q_len, *, window, sinks=0, 
     """mla_prefill_attn (causal) where a query at position p of its request sees
     the keys j > p - window and the first `sinks`."""
     return _binding.prefill(q, k, v, cu_q, cu_k, max_q_len, window, sinks, sm_scale, out, lse)
+
+
+def mla_decode_paged_tree(q, kv_cache, block_table, seq_lens, tree_mask, *, sm_scale,
+                          tree_lens=None, kv_scales=None, q_scale=1.0, k_scale=1.0, split_tiles=0,
+                          out_dtype=torch.bfloat16, out=None, lse=None, workspace=None):
+    """mla_decode_paged where the last tree_lens [B] (None: q_len) tokens of a
+    sequence are a tree of drafted ones: query token i sees the tokens before
+    them, and drafted token t iff bit t of its word is set in tree_mask, int64
+    [B, q_len], or [q_len]: one tree for all.  Rows behind a tree's last token,
+    and those that see no key: out 0, lse -inf.  kv_scales: a block-scaled e4m3
+    cache (as in mla_decode_paged_scaled)."""
+    if tree_mask is None:
+        raise TypeError("tree_mask must be a tensor")
+    return _binding.decode(q, kv_cache, kv_scales, block_table, seq_lens, sm_scale, q_scale, k_scale, 0, 0,
+                           split_tiles, out_dtype, out, lse, workspace, tree_mask, tree_lens)
+
+
+# Pages of the cache.  `pools`: a list (or tuple) of contiguous tensors
+# [num_blocks, ...], one for everything that a page has in memory: every layer's
+# cache, and its block scales; or one such tensor.  refs [num_blocks],
+# block_table [B, max_blocks] and seq_lens [B] are int32 and updated.
+
+
+def mla_cache_copy(pools, src, dst):
+    """Copies pages src [n] to pages dst [n] (int32) in every pool."""
+    _binding.copy(pools, src, dst)
+
+
+def mla_cache_resize(refs, block_table, seq_lens, new_lens):
+    """Gives sequences their new lengths new_lens [B]: releases the pages behind
+    them, then takes the lowest free pages for those that grow."""
+    _binding.resize(refs, block_table, seq_lens, new_lens)
+
+
+def mla_cache_fork(pools, refs, block_table, seq_lens, parents, children, *, workspace=None):
+    """The empty sequences children [n] go on from the sequences parents [n]
+    (int32): full pages are shared, a last one is copied in every pool."""
+    _binding.fork(pools, refs, block_table, seq_lens, parents, children, workspace)
+
+
+def mla_cache_compact(pools, refs, block_table, seq_lens, *, n_live=None, workspace=None):
+    """Moves the pages in use to the front of the pool, in every pool and in the
+    table.  Returns n_live [1] int32, how many they are."""
+    return _binding.compact(pools, refs, block_table, seq_lens, n_live, workspace)
+
+
+def mla_cache_accept(pools, block_table, seq_lens, path, path_lens, q_len, *, tree_lens=None,
+                     kv_scales=None, new_lens=None):
+    """Keeps, of the tree_lens [B] (None: q_len) drafted tokens at a sequence's
+    end, the path_lens [B] ones of its path [B, width] (int32, ascending): their
+    rows move together behind the context in every cache of `pools`
+    [num_blocks, 64, 576] (block-scaled: kv_scales, a list of their scales).
+    Returns new_lens [B], the lengths with them, for mla_cache_resize."""
+    return _binding.accept(pools, block_table, seq_lens, path, path_lens, q_len, tree_lens, kv_scales, new_lens)
 
 
 def mla_stage_copy(dst, src):

@@ -1,5 +1,5 @@
-// Marshalling of the window, sink and block-scaled-cache calls: the checks of
-// their tensors, their results' allocation, and the C entry.
+// Marshalling of the window, sink, block-scaled-cache, tree and cache-page calls:
+// the checks of their tensors, their results' allocation, and the C entry.
 //
 // These calls take 4 to 20 microseconds on the device.  In Python their checks
 // and ctypes took 11 (append) to 18 (decode); here they take 3 to 6 with the
@@ -18,6 +18,7 @@
 
 #include <climits>
 #include <cstdarg>
+#include <cstring>
 
 #include "mla.h"
 
@@ -30,7 +31,16 @@ struct Entries {
   decltype(&mla_decode_paged_window) decode_window;
   decltype(&mla_decode_paged_scaled) decode_scaled;
   decltype(&mla_prefill_attn_window) prefill;
+  decltype(&mla_decode_paged_tree) decode_tree;
+  decltype(&mla_cache_copy) copy;
+  decltype(&mla_cache_resize) resize;
+  decltype(&mla_cache_fork_workspace_size) fork_size;
+  decltype(&mla_cache_fork) fork;
+  decltype(&mla_cache_compact_workspace_size) compact_size;
+  decltype(&mla_cache_compact) compact;
+  decltype(&mla_cache_accept) accept;
 } entries;
+constexpr int kEntries = sizeof(Entries) / sizeof(void *);
 PyObject *fail = nullptr;   // called with (entry, status): raises the library's error
 
 // Thrown with the interpreter's error set.
@@ -248,11 +258,11 @@ PyObject *gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // (q, kv_cache, kv_scales | None, block_table, seq_lens, sm_scale, q_scale, k_scale, window,
-//  sinks, split_tiles, out_dtype, out | None, lse | None, workspace | None): with scales the
-//  block-scaled form
+//  sinks, split_tiles, out_dtype, out | None, lse | None, workspace | None, tree_mask | None,
+//  tree_lens | None): with scales the block-scaled form, with a mask the tree's
 PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    arguments(n, 15);
+    arguments(n, 17);
     const at::Tensor &q0 = tensor(a[0], "q");
     const int dev = current_device(q0, "q");
     const bool scaled = a[2] != Py_None, fp8 = q0.scalar_type() == at::kFloat8_e4m3fn;
@@ -275,6 +285,22 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
       const at::Tensor &s = dense(a[2], "kv_scales", at::kFloat, 2, dev);
       sb = scale_block(s, cache.size(0));
       scales = at_<float>(s);
+    }
+    const uint64_t *mask = nullptr;
+    const int32_t *nodes = nullptr;
+    int64_t mask_stride = 0;
+    if (a[15] != Py_None) {
+      const bool each = tensor(a[15], "tree_mask").dim() == 2;
+      const at::Tensor &t = dense(a[15], "tree_mask", at::kLong, each ? 2 : 1, dev);
+      if (each ? !shape(t, {B, q_len}) : !shape(t, {q_len}))
+        refuse(PyExc_ValueError, "tree_mask must be [B, q_len] or [q_len]");
+      mask = reinterpret_cast<const uint64_t *>(at_<int64_t>(t));
+      mask_stride = each ? q_len : 0;
+      if (a[16] != Py_None) {
+        const at::Tensor &l = dense(a[16], "tree_lens", at::kInt, 1, dev);
+        if (l.size(0) != B) refuse(PyExc_ValueError, "tree_lens must be [B]");
+        nodes = at_<int32_t>(l);
+      }
     }
     const float sm = real(a[5]), qs = real(a[6]), ks = real(a[7]);
     const int window = integer(a[8], "window", true), sinks = integer(a[9], "sinks", true);
@@ -303,7 +329,14 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const size_t bytes = ws.defined() ? static_cast<size_t>(ws.numel()) : 0;
     const int code = fp8 ? MLA_E4M3 : MLA_BF16, out_code = type == at::kFloat ? MLA_F32 : MLA_BF16;
     const auto stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-    if (scaled)
+    if (mask)
+      call("mla_decode_paged_tree", [&] {
+        return entries.decode_tree(q.data_ptr(), code, qs, cache.data_ptr(), code, ks, scales, sb,
+                                   at_<int32_t>(table), at_<int32_t>(lens), nodes, mask, mask_stride, b, q_len, H,
+                                   max_blocks, blocks, sm, split, out.data_ptr(), out_code, at_<float>(lse), w,
+                                   bytes, stream);
+      });
+    else if (scaled)
       call("mla_decode_paged_scaled", [&] {
         return entries.decode_scaled(q.data_ptr(), qs, cache.data_ptr(), scales, sb, at_<int32_t>(table),
                                      at_<int32_t>(lens), b, q_len, H, max_blocks, blocks, sm, window, sinks,
@@ -345,22 +378,220 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// The tensors of a call's pools, in a row.
+struct Pools {
+  static constexpr int kMost = 200;
+  void *at[kMost];
+  int64_t bytes[kMost];         // of a page
+  int n = 0;
+};
+// A list or tuple of contiguous tensors of `blocks` pages (-1: as many as the first has; set), or
+// one such tensor.  type: their dtype, if it has to be one
+void pools_of(PyObject *o, const char *name, int64_t &blocks, int dev, Pools &p, const at::ScalarType *type = nullptr) {
+  PyObject *one[1] = {o};
+  PyObject *const *items = one;
+  Py_ssize_t count = 1;
+  if (PyList_Check(o) || PyTuple_Check(o)) {
+    items = PySequence_Fast_ITEMS(o);
+    count = PySequence_Fast_GET_SIZE(o);
+  }
+  if (count > Pools::kMost) refuse(PyExc_ValueError, "%s: at most %d", name, static_cast<int>(Pools::kMost));
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    const at::Tensor &t = tensor(items[i], name);
+    if (!t.is_cuda() || t.get_device() != dev) refuse(PyExc_ValueError, "%s is not on cuda:%d", name, dev);
+    if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
+    if (type && t.scalar_type() != *type)
+      refuse(PyExc_TypeError, "%s: dtype %s is not %s", name, c10::toString(t.scalar_type()), c10::toString(*type));
+    if (t.dim() < 1 || t.numel() == 0) refuse(PyExc_ValueError, "%s must be [num_blocks, ...]", name);
+    if (blocks < 0) blocks = t.size(0);
+    if (t.size(0) != blocks) refuse(PyExc_ValueError, "%s differ in their number of pages", name);
+    p.at[p.n] = t.data_ptr();
+    p.bytes[p.n++] = t.numel() / blocks * static_cast<int64_t>(t.element_size());
+  }
+}
+at::Tensor scratch(int64_t bytes, int dev) {
+  return at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::kCUDA, dev)));
+}
+// refs, block_table and seq_lens of a call
+struct Sequences {
+  int32_t *refs, *table, *lens;
+  int64_t pages;                // of refs
+  int blocks, B, max_blocks;
+  Sequences(PyObject *r, PyObject *t, PyObject *l, int dev) {
+    const at::Tensor &rt = dense(r, "refs", at::kInt, 1, dev), &tt = dense(t, "block_table", at::kInt, 2, dev);
+    const at::Tensor &lt = dense(l, "seq_lens", at::kInt, 1, dev);
+    if (lt.size(0) != tt.size(0)) refuse(PyExc_ValueError, "block_table and seq_lens must have a row each");
+    refs = at_<int32_t>(rt);
+    table = at_<int32_t>(tt);
+    lens = at_<int32_t>(lt);
+    pages = rt.size(0);
+    blocks = narrow(pages, "num_blocks");
+    B = narrow(tt.size(0), "B");
+    max_blocks = narrow(tt.size(1), "max_blocks");
+  }
+};
+cudaStream_t stream_of(int dev) {
+  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+}
+
+// (pools, src, dst)
+PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    arguments(n, 3);
+    const int dev = current_device(tensor(a[1], "src"), "src");
+    const at::Tensor &src = dense(a[1], "src", at::kInt, 1, dev), &dst = dense(a[2], "dst", at::kInt, 1, dev);
+    if (dst.size(0) != src.size(0)) refuse(PyExc_ValueError, "src and dst must have one length");
+    Pools p;
+    int64_t pages = -1;
+    pools_of(a[0], "pools", pages, dev, p);
+    if (p.n == 0) Py_RETURN_NONE;
+    const int blocks = narrow(pages, "num_blocks"), pairs = narrow(src.size(0), "src");
+    const cudaStream_t stream = stream_of(dev);
+    call("mla_cache_copy", [&] {
+      return entries.copy(p.at, p.bytes, p.n, blocks, at_<int32_t>(src), at_<int32_t>(dst), pairs, stream);
+    });
+    Py_RETURN_NONE;
+  });
+}
+
+// (refs, block_table, seq_lens, new_lens)
+PyObject *resize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    arguments(n, 4);
+    const int dev = current_device(tensor(a[0], "refs"), "refs");
+    const Sequences s(a[0], a[1], a[2], dev);
+    const at::Tensor &lens = dense(a[3], "new_lens", at::kInt, 1, dev);
+    if (lens.size(0) != s.B) refuse(PyExc_ValueError, "new_lens must be [B]");
+    const cudaStream_t stream = stream_of(dev);
+    call("mla_cache_resize", [&] {
+      return entries.resize(s.refs, s.blocks, s.table, s.lens, at_<int32_t>(lens), s.B, s.max_blocks, stream);
+    });
+    Py_RETURN_NONE;
+  });
+}
+
+// (pools, refs, block_table, seq_lens, parents, children, workspace | None)
+PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    arguments(n, 7);
+    const int dev = current_device(tensor(a[1], "refs"), "refs");
+    const Sequences s(a[1], a[2], a[3], dev);
+    const at::Tensor &from = dense(a[4], "parents", at::kInt, 1, dev), &to = dense(a[5], "children", at::kInt, 1, dev);
+    if (to.size(0) != from.size(0)) refuse(PyExc_ValueError, "parents and children must have one length");
+    Pools p;
+    int64_t pages = s.pages;
+    pools_of(a[0], "pools", pages, dev, p);
+    const int forks = narrow(from.size(0), "parents");
+    size_t bytes = 0;
+    call("mla_cache_fork", [&] { return entries.fork_size(forks, &bytes); });
+    const at::Tensor ws = a[6] != Py_None ? dense(a[6], "workspace", at::kByte, 1, dev)
+                                          : scratch(static_cast<int64_t>(bytes), dev);
+    const cudaStream_t stream = stream_of(dev);
+    call("mla_cache_fork", [&] {
+      return entries.fork(p.at, p.bytes, p.n, s.refs, s.blocks, s.table, s.lens, s.B, s.max_blocks,
+                          at_<int32_t>(from), at_<int32_t>(to), forks, ws.data_ptr(),
+                          static_cast<size_t>(ws.numel()), stream);
+    });
+    Py_RETURN_NONE;
+  });
+}
+
+// (pools, refs, block_table, seq_lens, n_live | None, workspace | None)
+PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    arguments(n, 6);
+    const int dev = current_device(tensor(a[1], "refs"), "refs");
+    const Sequences s(a[1], a[2], a[3], dev);
+    Pools p;
+    int64_t pages = s.pages;
+    pools_of(a[0], "pools", pages, dev, p);
+    size_t bytes = 0;
+    call("mla_cache_compact", [&] { return entries.compact_size(s.blocks, &bytes); });
+    at::Tensor live = result(a[4], "n_live", {1}, at::kInt, dev);
+    const at::Tensor ws = a[5] != Py_None ? dense(a[5], "workspace", at::kByte, 1, dev)
+                                          : scratch(static_cast<int64_t>(bytes), dev);
+    const cudaStream_t stream = stream_of(dev);
+    call("mla_cache_compact", [&] {
+      return entries.compact(p.at, p.bytes, p.n, s.refs, s.blocks, s.table, s.lens, s.B, s.max_blocks,
+                             at_<int32_t>(live), ws.data_ptr(), static_cast<size_t>(ws.numel()), stream);
+    });
+    return THPVariable_Wrap(std::move(live));
+  });
+}
+
+// (pools, block_table, seq_lens, path, path_lens, q_len, tree_lens | None, kv_scales | None,
+//  new_lens | None)
+PyObject *accept(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    arguments(n, 9);
+    const int dev = current_device(tensor(a[1], "block_table"), "block_table");
+    const at::Tensor &table = dense(a[1], "block_table", at::kInt, 2, dev);
+    const at::Tensor &lens = dense(a[2], "seq_lens", at::kInt, 1, dev);
+    const at::Tensor &path = dense(a[3], "path", at::kInt, 2, dev);
+    const at::Tensor &count = dense(a[4], "path_lens", at::kInt, 1, dev);
+    const int64_t B = table.size(0);
+    if (lens.size(0) != B || path.size(0) != B || count.size(0) != B)
+      refuse(PyExc_ValueError, "block_table, seq_lens, path and path_lens must have a row each");
+    const int q_len = integer(a[5], "q_len");
+    const int32_t *nodes = nullptr;
+    if (a[6] != Py_None) {
+      const at::Tensor &t = dense(a[6], "tree_lens", at::kInt, 1, dev);
+      if (t.size(0) != B) refuse(PyExc_ValueError, "tree_lens must be [B]");
+      nodes = at_<int32_t>(t);
+    }
+    Pools p, s;
+    int64_t pages = -1;
+    PyObject *first = a[0];
+    if ((PyList_Check(first) || PyTuple_Check(first)) && PySequence_Fast_GET_SIZE(first) > 0)
+      first = PySequence_Fast_ITEMS(first)[0];
+    at::ScalarType type = THPVariable_Check(first) ? tensor(first, "pools").scalar_type() : at::kBFloat16;
+    if (type != at::kBFloat16 && type != at::kFloat8_e4m3fn)
+      refuse(PyExc_TypeError, "pools: dtype %s is neither bf16 nor e4m3", c10::toString(type));
+    const bool fp8 = type == at::kFloat8_e4m3fn;
+    pools_of(a[0], "pools", pages, dev, p, &type);
+    for (int i = 0; i < p.n; ++i)
+      if (p.bytes[i] != 64 * 576 * (fp8 ? 1 : 2)) refuse(PyExc_ValueError, "pools must be [num_blocks, 64, 576]");
+    int sb = 0;
+    if (a[7] != Py_None) {
+      if (!fp8) refuse(PyExc_TypeError, "kv_scales belong to e4m3 pools");
+      const at::ScalarType f32 = at::kFloat;
+      pools_of(a[7], "kv_scales", pages, dev, s, &f32);
+      if (s.n != p.n) refuse(PyExc_ValueError, "kv_scales must be as many as the pools");
+      for (int i = 0; i < s.n; ++i) {
+        const int64_t per = s.bytes[i] / 4;
+        if ((per != 1 && per != 2 && per != 4) || s.bytes[i] != s.bytes[0])
+          refuse(PyExc_ValueError, "kv_scales must be [num_blocks, 64 / scale_block], scale_block 16, 32 or 64");
+        sb = static_cast<int>(64 / per);
+      }
+    }
+    // (without a pool: any page will do, none is looked at)
+    const int blocks = p.n ? narrow(pages, "num_blocks") : (1 << 25) - 1, requests = narrow(B, "B");
+    const int max_blocks = narrow(table.size(1), "max_blocks"), width = narrow(path.size(1), "path");
+    at::Tensor out = result(a[8], "new_lens", {B}, at::kInt, dev);
+    const cudaStream_t stream = stream_of(dev);
+    call("mla_cache_accept", [&] {
+      return entries.accept(p.at, fp8 ? MLA_E4M3 : MLA_BF16, s.n ? reinterpret_cast<float *const *>(s.at) : nullptr,
+                            sb, p.n, blocks, at_<int32_t>(table), at_<int32_t>(lens), nodes, q_len,
+                            at_<int32_t>(path), width, at_<int32_t>(count), requests, max_blocks,
+                            at_<int32_t>(out), stream);
+    });
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
 // (fail, the entries' addresses in the order of Entries)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    arguments(n, 7);
-    void *at[6];
-    for (int i = 0; i < 6; ++i) {
+    arguments(n, 1 + kEntries);
+    void *at[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
       at[i] = PyLong_AsVoidPtr(a[i + 1]);
       if (!at[i]) refuse(PyExc_ValueError, "no address");
     }
     Py_INCREF(a[0]);
     Py_XSETREF(fail, a[0]);
-    entries = {reinterpret_cast<decltype(entries.append)>(at[0]), reinterpret_cast<decltype(entries.gather)>(at[1]),
-               reinterpret_cast<decltype(entries.workspace_size)>(at[2]),
-               reinterpret_cast<decltype(entries.decode_window)>(at[3]),
-               reinterpret_cast<decltype(entries.decode_scaled)>(at[4]),
-               reinterpret_cast<decltype(entries.prefill)>(at[5])};
+    static_assert(sizeof(at) == sizeof(entries), "an address each");
+    memcpy(&entries, at, sizeof(entries));
     Py_RETURN_NONE;
   });
 }
@@ -371,6 +602,11 @@ PyMethodDef methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                          {"gather", FAST(gather), METH_FASTCALL, nullptr},
                          {"decode", FAST(decode), METH_FASTCALL, nullptr},
                          {"prefill", FAST(prefill), METH_FASTCALL, nullptr},
+                         {"copy", FAST(copy), METH_FASTCALL, nullptr},
+                         {"resize", FAST(resize), METH_FASTCALL, nullptr},
+                         {"fork", FAST(fork), METH_FASTCALL, nullptr},
+                         {"compact", FAST(compact), METH_FASTCALL, nullptr},
+                         {"accept", FAST(accept), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mla_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -1,5 +1,6 @@
-// Paged latent decode with a sliding window and sinks, over a bf16, an e4m3
-// or a block-scaled e4m3 cache (mla_decode_paged_window, _scaled).
+// Paged latent decode with a sliding window and sinks, or of a tree of drafted
+// tokens, over a bf16, an e4m3 or a block-scaled e4m3 cache
+// (mla_decode_paged_window, _scaled, _tree).
 //
 // Rows and keys.  The q_len * H query rows of a request (query token outer,
 // head inner) all attend to the same latent rows, so they are taken in groups
@@ -184,6 +185,9 @@ struct WindowArgs {
   void *ws_o;                   // [slots, 128, 512] fp32, or fp16 for a bf16 output
   float *ws_lse;                // [slots, 128]
   float *ws_unit;               // [slots, 128, 2, 2]: what 1 of the fp16 stands for, by 128 columns (1, 3; 2, 4)
+  const uint64_t *tree_mask;    // a tree: word i of a request says which of its drafted tokens token i sees
+  int64_t mask_stride;          // words from request to request (0: one tree for all)
+  const int32_t *tree_lens;     // drafted tokens of a request; nullptr: q_len
   int *err;
 };
 
@@ -198,8 +202,16 @@ struct Job {
   }
 };
 
+// (of a tree any row may see the last token; what all rows see is known to those who have its size)
+template <bool TREE>
 __device__ __forceinline__ Job job_of(int rg, int len, const WindowArgs &a) {
   Job j;
+  if constexpr (TREE) {
+    j.p0 = j.p1 = len - 1;
+    j.lo_page = j.sink_pages = 0;
+    j.pages = (len + kPage - 1) / kPage;
+    return j;
+  }
   int i0 = 0, i1 = a.q_len - 1;               // (one group: no divisions)
   if (a.RG > 1) {
     i0 = rg * 128 / a.H;
@@ -220,11 +232,42 @@ __device__ __forceinline__ int length_of(int b, const WindowArgs &a, bool tell) 
   return min(max(len, 0), most);
 }
 
-template <bool FP8>
+// Row group and request of a job.  Planned apart, the row groups follow one
+// another; a tree's, of which there may be 64 and more, else stand together by
+// request, so that those who read the same pages do so at about the same time.
+template <bool TREE>
+__device__ __forceinline__ void who(int j, const WindowArgs &a, int &rg, int &b) {
+  if (TREE && a.groups == 1) {
+    b = a.RG > 1 ? j / a.RG : j;
+    rg = j - b * a.RG;
+  } else {
+    rg = a.RG > 1 ? j / a.B : 0;
+    b = j - rg * a.B;
+  }
+}
+
+// Drafted tokens of a request; 0 where that cannot be.
+__device__ __forceinline__ int nodes_of(int b, const WindowArgs &a, bool tell) {
+  if (!a.tree_lens) return a.q_len;
+  const int n = __ldg(a.tree_lens + b);
+  if (n >= 0 && n <= a.q_len) return n;
+  if (tell) raise_error(a.err, MLA_DEVERR_SEQ_LEN);
+  return 0;
+}
+
+// Tiles of the row group rg of a request (none where it lies behind a tree's last token).
+template <bool FP8, bool TREE>
+__device__ __forceinline__ int tiles_of(int rg, int b, const WindowArgs &a, int &len) {
+  const bool tell = (blockIdx.x == 0 || a.solo) && rg == 0;
+  len = length_of(b, a, tell);
+  if (TREE && rg * 128 / a.H >= nodes_of(b, a, tell)) return 0;
+  return job_of<TREE>(rg, len, a).tiles(Fmt<FP8>::kPages);
+}
+template <bool FP8, bool TREE>
 __device__ __forceinline__ int tiles_of(int j, const WindowArgs &a, int &len) {
-  const int rg = a.RG > 1 ? j / a.B : 0;
-  len = length_of(j - rg * a.B, a, blockIdx.x == 0 && rg == 0);
-  return job_of(rg, len, a).tiles(Fmt<FP8>::kPages);
+  int rg, b;
+  who<TREE>(j, a, rg, b);
+  return tiles_of<FP8, TREE>(rg, b, a, len);
 }
 
 struct Seg {
@@ -250,7 +293,7 @@ __device__ __forceinline__ int warp_incl_scan(int x, int lane) {
 // parts than pairs, each pair has one part of one job instead of C units of
 // what lies end to end: nobody then switches jobs (a second segment ends
 // about 4 us after a first one of the same tiles).  A part is the unit, C = 1.
-template <bool FP8>
+template <bool FP8, bool TREE>
 struct Walk {
   static constexpr int kHeld = 3;   // jobs of a lane that fit (the pairs are fewer than 96)
   int J, job0, per, lane_excl, total, C, span, span_lo, span_hi;
@@ -276,12 +319,12 @@ struct Walk {
     if (per <= kHeld) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        held[i] = i < per && lane * per + i < J ? tiles_of<FP8>(job0 + lane * per + i, a, len) : 0;
+        held[i] = i < per && lane * per + i < J ? tiles_of<FP8, TREE>(job0 + lane * per + i, a, len) : 0;
         sum += units_of(held[i]);
       }
     } else {
       for (int j = lane * per; j < min(J, (lane + 1) * per); ++j)
-        sum += units_of(tiles_of<FP8>(job0 + j, a, len));
+        sum += units_of(tiles_of<FP8, TREE>(job0 + j, a, len));
     }
     total = __reduce_add_sync(0xffffffffu, sum);
     C = a.forced > 0 ? a.forced : max(Fmt<FP8>::kMinUnits, (total - 1) / a.spans_at_once + 1);
@@ -313,11 +356,9 @@ struct Walk {
   // Uncut: jobs span, span + pairs, ...
   __device__ bool next_solo(const WindowArgs &a, Seg &s) {
     if (span >= J) return false;
-    s.rg = a.RG > 1 ? span / a.B : 0;
-    s.b = span - s.rg * a.B;
-    s.len = length_of(s.b, a, s.rg == 0);
+    who<TREE>(span, a, s.rg, s.b);
     s.tile0 = 0;
-    s.ntiles = job_of(s.rg, s.len, a).tiles(Fmt<FP8>::kPages);
+    s.ntiles = tiles_of<FP8, TREE>(s.rg, s.b, a, s.len);
     s.whole = 1;
     s.slot = 0;
     span += a.spans_at_once;
@@ -328,7 +369,7 @@ struct Walk {
     k = 0;
     units = 0;
     len = 0;
-    if (base + lane < J) units = units_of(tiles_of<FP8>(job0 + base + lane, a, len));
+    if (base + lane < J) units = units_of(tiles_of<FP8, TREE>(job0 + base + lane, a, len));
     const int incl = warp_incl_scan(units, lane);
     excl = before + incl - units;
   }
@@ -359,13 +400,12 @@ struct Walk {
       const int first = t0 + (even ? 0 : Fmt<FP8>::kJobCost), end = t0 + n;
       const int u0 = max(span_lo, first), u1 = min(span_hi, end);
       if (n == 0 || u1 <= u0) continue;
-      s.rg = a.RG > 1 ? j / a.B : 0;
-      s.b = j - s.rg * a.B;
+      who<TREE>(j, a, s.rg, s.b);
       s.len = l;
       s.tile0 = u0 - first;
       s.ntiles = u1 - u0;
       if (even) {               // part tile0 of n, of sizes that differ by one at most
-        const int tiles = job_of(s.rg, l, a).tiles(Fmt<FP8>::kPages), small = tiles / n,
+        const int tiles = job_of<TREE>(s.rg, l, a).tiles(Fmt<FP8>::kPages), small = tiles / n,
                   more = tiles - small * n, i = s.tile0;
         s.tile0 = i * small + min(i, more);
         s.ntiles = small + (i < more ? 1 : 0);
@@ -511,7 +551,7 @@ __device__ __noinline__ float far_sum(uint32_t scores, uint64_t seen, float4 c, 
   return sum;
 }
 
-template <bool FP8>
+template <bool FP8, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
 window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
@@ -636,7 +676,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 
   if (warp == 0) {
     // ------------------------------------------------- plan, Q and K
-    Walk<FP8> walk;
+    Walk<FP8, TREE> walk;
     if (args.solo) {
       walk.init_solo(args);
     } else {
@@ -658,7 +698,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     };
     const uint32_t q_bar = peer_smem(q_full, 0);
     while (ok && (args.solo ? walk.next_solo(args, sg) : walk.next(args, sg, lane))) {
-      const Job job = job_of(sg.rg, sg.len, args);
+      const Job job = job_of<TREE>(sg.rg, sg.len, args);
       Pages pg;
       fetch_blocks(pg, job, sg.b, F::kPages * sg.tile0);
       if (!(ok = publish(sg))) break;
@@ -713,7 +753,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     int vc = 0;
     bool ok = true;
     for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
-      const Job job = job_of(sg.rg, sg.len, args);
+      const Job job = job_of<TREE>(sg.rg, sg.len, args);
       Pages pg;
       fetch_blocks(pg, job, sg.b, F::kPages * sg.tile0);
       for (int t = 0; ok && t < sg.ntiles; ++t) {
@@ -875,13 +915,27 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (tid < n) args.lse[at + tid] = -INFINITY;
         continue;
       }
-      const Job job = job_of(sg.rg, sg.len, args);
+      Job job = job_of<TREE>(sg.rg, sg.len, args);
       const int grow = sg.rg * 128 + 64 * rank + r;     // row of the request
       // (rows behind the request's last are computed and dropped)
-      const int p = grow < R ? sg.len - args.q_len + grow / args.H : job.p1;
-      const int wlo = args.window ? p - args.window + 1 : 0;
+      int p = grow < R ? sg.len - args.q_len + grow / args.H : job.p1;
+      // a tree's rows see the context, keys up to p, and of the tokens behind it
+      // those of their word; rows behind the tree's last token see nothing
+      int tree0 = 0;
+      uint64_t word = 0;
+      if constexpr (TREE) {
+        const int n = nodes_of(sg.b, args, false);
+        tree0 = sg.len - n;
+        job.p0 = p = tree0 - 1;
+        const int token = grow / args.H;
+        if (grow < R) {
+          if (token < n) word = __ldg(args.tree_mask + sg.b * args.mask_stride + token) & low_bits(n);
+          else p = -1;
+        }
+      }
+      const int wlo = !TREE && args.window ? p - args.window + 1 : 0;
       // every query row of the job sees keys [clean_lo, job.p0] and the sinks
-      const int clean_lo = args.window ? job.p1 - args.window + 1 : 0;
+      const int clean_lo = !TREE && args.window ? job.p1 - args.window + 1 : 0;
       // scales of this thread's keys, a tile of its group ahead
       const int32_t *bt = args.block_table + static_cast<int64_t>(sg.b) * args.max_blocks;
       auto load_blk = [&](int t) -> int {
@@ -926,6 +980,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         };
         const bool all_clean = clean(page0) && clean(page1);
         auto seen_keys = [&] {
+          if constexpr (TREE) {
+            const int at = key0 - tree0;
+            return low_bits(p - key0 + 1) | (at >= 64 || at <= -64 ? 0 : at >= 0 ? word >> at : word << -at);
+          }
           return low_bits(p - key0 + 1) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0));
         };
         constexpr int kRun = F::kMine / kBlocks;        // keys of one scale: 16 / 32
@@ -1212,6 +1270,13 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       tc_fence_before();   // (O has been read: the next segment's P V may begin)
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(o_bar);
+      if constexpr (TREE) {
+        // (a row that sees nothing has 0 times every value, which not all of them need make 0)
+        if (empty) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) all[k] = 0;
+        }
+      }
       const bool fp16 = !sg.whole && !args.out_f32;
       float factor = inv;
       if (fp16) {
@@ -1309,7 +1374,10 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % SPLIT;
-  const int j = blockIdx.x, rg = a.RG > 1 ? j / a.B : 0, b = j - rg * a.B;
+  const int j = blockIdx.x;
+  int rg, b;
+  if (a.tree_mask) who<true>(j, a, rg, b);
+  else who<false>(j, a, rg, b);
   const int rr = blockIdx.y * kRows + warp / SPLIT;
   const int R = a.q_len * a.H;
   const bool row_ok = rg * 128 + rr < R;
@@ -1318,7 +1386,9 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   T *out = static_cast<T *>(a.out) + row * kLatent;
   const int group = j / a.group_jobs;
   const int C = a.ws_head[group], first = a.ws_head[a.groups + 2 * j], end = a.ws_head[a.groups + 2 * j + 1];
-  if (job_of(rg, length_of(b, a, false), a).pages == 0) {   // (the words above hold nothing)
+  const int len = length_of(b, a, false);
+  if (a.tree_mask ? len == 0 || rg * 128 / a.H >= nodes_of(b, a, false)
+                  : job_of<false>(rg, len, a).pages == 0) {   // (the words above hold nothing)
     if (mine == 0 && row_ok) {
       const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       for (int k = 0; k < 2; ++k) store8(out + 8 * (lane + 32 * k), zero);
@@ -1472,11 +1542,15 @@ int pairs_for_device() {
   const int sms = device_sm_count();
   int g = sms >= 2 ? sms / 2 : 1, n = 0;
   PairLaunch<false> pl(g, nullptr);   // (the larger of the two formats' shared memory)
-  if (cudaFuncSetAttribute(window_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Fmt<false>::kSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(window_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Fmt<true>::kSmem) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, window_kernel<false>, &pl.cfg) != cudaSuccess) {
+  auto allow = [](const void *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  auto at = [](auto *kernel) { return reinterpret_cast<const void *>(kernel); };
+  if (!allow(at(window_kernel<false, false>), Fmt<false>::kSmem) ||
+      !allow(at(window_kernel<true, false>), Fmt<true>::kSmem) ||
+      !allow(at(window_kernel<false, true>), Fmt<false>::kSmem) ||
+      !allow(at(window_kernel<true, true>), Fmt<true>::kSmem) ||
+      cudaOccupancyMaxActiveClusters(&n, window_kernel<false, false>, &pl.cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -1579,16 +1653,23 @@ int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArg
   }
   if (!ok) return MLA_ERR_CUDA;
   PairLaunch<FP8> pl(pairs, stream);
-  return cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8>, tk, tkr, tv, tq, tqr, a) == cudaSuccess
-             ? MLA_OK
-             : MLA_ERR_CUDA;
+  const cudaError_t e = a.tree_mask
+                            ? cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8, true>, tk, tkr, tv, tq, tqr, a)
+                            : cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8, false>, tk, tkr, tv, tq, tqr, a);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
+
+struct Tree {
+  const uint64_t *mask;
+  int64_t stride;
+  const int32_t *lens;
+};
 
 int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, float k_scale,
                   const float *scales, int sb_shift, const int32_t *block_table,
                   const int32_t *seq_lens, int B, int q_len, int H, int max_blocks, int num_blocks,
                   float sm_scale, int window, int sinks, int split_tiles, void *out, int out_dtype,
-                  float *lse, void *workspace, size_t ws_bytes, mla_stream_t stream) {
+                  float *lse, void *workspace, size_t ws_bytes, mla_stream_t stream, const Tree &tree = {}) {
   if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
   const int pairs = pairs_for_device();
   if (pairs == 0) return MLA_ERR_CUDA;
@@ -1613,6 +1694,9 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.max_blocks = max_blocks;
   a.num_blocks = num_blocks;
   // (a table holds at most 2^30 tokens: sums with these stay within 32 bits)
+  a.tree_mask = tree.mask;
+  a.mask_stride = tree.stride;
+  a.tree_lens = tree.lens;
   a.window = std::min(window, 1 << 30);
   a.sinks = std::min(sinks, 1 << 30);
   a.RG = static_cast<int>((static_cast<int64_t>(q_len) * H + 127) / 128);
@@ -1692,4 +1776,28 @@ extern "C" int mla_decode_paged_scaled(const void *q, float q_scale, const void 
                        scale_block == 64 ? 6 : scale_block == 32 ? 5 : 4, block_table, seq_lens, B,
                        q_len, H, max_blocks, num_blocks, sm_scale, window, sinks, split_tiles, out,
                        out_dtype, lse, workspace, ws_bytes, stream);
+}
+
+extern "C" int mla_decode_paged_tree(const void *q, int q_dtype, float q_scale, const void *kv_cache,
+                                     int kv_dtype, float k_scale, const float *kv_scales,
+                                     int scale_block, const int32_t *block_table,
+                                     const int32_t *seq_lens, const int32_t *tree_lens,
+                                     const uint64_t *tree_mask, int64_t mask_stride, int B, int q_len,
+                                     int H, int max_blocks, int num_blocks, float sm_scale,
+                                     int split_tiles, void *out, int out_dtype, float *lse,
+                                     void *workspace, size_t ws_bytes, mla_stream_t stream) {
+  if (kv_scales && ((scale_block != 16 && scale_block != 32 && scale_block != 64) || kv_dtype != MLA_E4M3))
+    return MLA_ERR_INVALID_ARG;
+  const float ks = kv_scales ? 1.f : k_scale;
+  const int st = check_window(q, q_dtype, q_scale, kv_cache, kv_dtype, ks, block_table, seq_lens, B,
+                              q_len, H, max_blocks, num_blocks, sm_scale, 0, 0, split_tiles, out,
+                              out_dtype, lse);
+  if (st != MLA_OK) return st;
+  if (!tree_mask || (mask_stride != 0 && mask_stride < q_len) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+    return MLA_ERR_INVALID_ARG;
+  return launch_window(q, kv_dtype == MLA_E4M3, q_scale, kv_cache, ks, kv_scales,
+                       scale_block == 64 ? 6 : scale_block == 32 ? 5 : 4, block_table, seq_lens, B,
+                       q_len, H, max_blocks, num_blocks, sm_scale, 0, 0, split_tiles, out, out_dtype,
+                       lse, workspace, ws_bytes, stream, Tree{tree_mask, mask_stride, tree_lens});
 }
