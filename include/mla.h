@@ -475,9 +475,12 @@ int mla_decode_paged_scaled(const void *q, float q_scale, const void *kv_cache,
  * mask_stride: q_len or more, or 0: one tree for all requests (tree_lens
  * then cuts it).  tree_lens[b] outside [0, q_len] sets MLA_DEVERR_SEQ_LEN and
  * counts as 0.  kv_scales [num_blocks, 64/scale_block]: a block-scaled e4m3
- * cache (k_scale is not used), else NULL.  Precision, limits and what is not
- * read as in mla_decode_paged_window, whose workspace size (window 0, sinks 0)
- * is this one's. */
+ * cache (k_scale is not used), else NULL.  Precision, limits, split_tiles, the
+ * workspace's use and what is not read as in mla_decode_paged_window; it has
+ * mla_decode_tree_workspace_size(B, q_len, H, max_blocks*64, split_tiles) bytes. */
+int mla_decode_tree_workspace_size(int B, int q_len, int H, int max_seq_len,
+                                   int split_tiles, size_t *bytes);
+
 int mla_decode_paged_tree(const void *q, int q_dtype, float q_scale,
                           const void *kv_cache, int kv_dtype, float k_scale,
                           const float *kv_scales, int scale_block,

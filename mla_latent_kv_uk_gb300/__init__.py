@@ -29,7 +29,7 @@ __all__ = [
     "mla_gather_cache_reorg", "mla_expand_kv", "mla_prefill_attn", "mla_rope_cache_write",
     "mla_stage_copy", "mla_rope_cache_append", "mla_gather_cache_scaled",
     "mla_decode_window_workspace_size", "mla_decode_paged_window", "mla_decode_paged_scaled",
-    "mla_prefill_attn_window", "mla_decode_paged_tree", "mla_cache_copy", "mla_cache_resize",
+    "mla_prefill_attn_window", "mla_decode_tree_workspace_size", "mla_decode_paged_tree", "mla_cache_copy", "mla_cache_resize",
     "mla_cache_fork", "mla_cache_compact", "mla_cache_accept",
 ]
 
@@ -71,6 +71,7 @@ _SIGNATURES = {
                                  _p, _i, _p, _p, _sz, _p], _i),
     "mla_prefill_attn_window": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p],
                                 _i),
+    "mla_decode_tree_workspace_size": ([_i, _i, _i, _i, _i, ctypes.POINTER(_sz)], _i),
     "mla_decode_paged_tree": ([_p, _i, _f, _p, _i, _f, _p, _i, _p, _p, _p, _p, _i64, _i, _i, _i,
                                _i, _i, _f, _i, _p, _i, _p, _p, _sz, _p], _i),
     "mla_cache_copy": ([_p, _p, _i, _i, _p, _p, _i, _p], _i),
@@ -136,7 +137,7 @@ def _load_binding():
     mod.bind(_check, *(ctypes.cast(getattr(lib, name), _p).value for name in (
         "mla_rope_cache_append", "mla_gather_cache_scaled", "mla_decode_window_workspace_size",
         "mla_decode_paged_window", "mla_decode_paged_scaled", "mla_prefill_attn_window",
-        "mla_decode_paged_tree", "mla_cache_copy", "mla_cache_resize",
+        "mla_decode_tree_workspace_size", "mla_decode_paged_tree", "mla_cache_copy", "mla_cache_resize",
         "mla_cache_fork_workspace_size", "mla_cache_fork", "mla_cache_compact_workspace_size",
         "mla_cache_compact", "mla_cache_accept")))
     return mod
@@ -468,6 +469,13 @@ def mla_prefill_attn_window(q, k, v, cu_q, cu_k, max_q_len, *, window, sinks=0, 
     """mla_prefill_attn (causal) where a query at position p of its request sees
     the keys j > p - window and the first `sinks`."""
     return _binding.prefill(q, k, v, cu_q, cu_k, max_q_len, window, sinks, sm_scale, out, lse)
+
+
+def mla_decode_tree_workspace_size(B, q_len, H, max_seq_len, split_tiles=0) -> int:
+    n = _sz(0)
+    _check("mla_decode_tree_workspace_size", lib.mla_decode_tree_workspace_size(
+        B, q_len, H, max_seq_len, int(split_tiles), ctypes.byref(n)))
+    return n.value
 
 
 def mla_decode_paged_tree(q, kv_cache, block_table, seq_lens, tree_mask, *, sm_scale,

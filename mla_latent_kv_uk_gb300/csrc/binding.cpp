@@ -31,6 +31,7 @@ struct Entries {
   decltype(&mla_decode_paged_window) decode_window;
   decltype(&mla_decode_paged_scaled) decode_scaled;
   decltype(&mla_prefill_attn_window) prefill;
+  decltype(&mla_decode_tree_workspace_size) tree_size;
   decltype(&mla_decode_paged_tree) decode_tree;
   decltype(&mla_cache_copy) copy;
   decltype(&mla_cache_resize) resize;
@@ -317,7 +318,11 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
       size_t bytes = 0;
       const int64_t tokens = static_cast<int64_t>(max_blocks) * 64;
-      if (tokens <= INT_MAX)   // (more are refused below)
+      if (tokens <= INT_MAX && mask)   // (more are refused below)
+        call("mla_decode_tree_workspace_size", [&] {
+          return entries.tree_size(b, q_len, H, static_cast<int>(tokens), split, &bytes);
+        });
+      else if (tokens <= INT_MAX)
         call("mla_decode_window_workspace_size", [&] {
           return entries.workspace_size(b, q_len, H, static_cast<int>(tokens), window, sinks, split, &bytes);
         });

@@ -106,6 +106,7 @@ constexpr int kJobPages = 6;
 // requests of 130 tokens: 8.0 us, cut 10.3; a window of 128: 8.8, cut 11.5; but
 // 32 requests of 18 pages: 24.8, cut 22.4.
 constexpr int kSoloPages = 6;
+constexpr int kWidePages = 64;
 constexpr int kSegSlots = 4;
 constexpr uint32_t kColO = 0, kColS = 256;   // O [0,256), then the S tiles
 constexpr int kSBufs = 4;                    // Q K^T runs two tiles ahead of P V
@@ -117,10 +118,17 @@ constexpr int kSBufs = 4;                    // Q K^T runs two tiles ahead of P 
 // rate, but there is room for one only, in slots that wait 2500 cycles for
 // their next load: the speculative batch took 140 us instead of 146, a window
 // of 128 10.3 instead of 8.8, the batch of 32 the same.)
-template <bool FP8>
+//
+// WIDE (a tree over a bf16 cache): tiles of two pages after all, where the keys
+// come in three pieces by columns and the values in two, one for each of the
+// accumulators, so that the slots are free again long before the next tile needs
+// them: a piece of keys after 384 of a tile's 2208 cycles of MMAs, one of values
+// after 528.  Room for that is P's second tile: the probabilities of a tile wait
+// until P V of the last one is done, which takes no longer than the Q K^T behind it.
+template <bool FP8, bool WIDE = false>
 struct Fmt {
   static constexpr int kEsz = FP8 ? 1 : 2;
-  static constexpr int kPages = FP8 ? 2 : 1;               // pages of a tile
+  static constexpr int kPages = FP8 || WIDE ? 2 : 1;       // pages of a tile
   static constexpr int kTile = kPages * kPage;             // its keys: 128 / 64
   static constexpr int kMine = kTile / 2;                  // keys of one softmax thread
   static constexpr int kMinUnits = (kMinPages + kPages - 1) / kPages;
@@ -132,17 +140,19 @@ struct Fmt {
   static constexpr int kBoxes = FP8 ? 4 : 9;               // whole box columns of a cache row
   // A slot is one load: what a loading warp does for one (wait, expect, issue)
   // takes about 500 cycles, so three loads a tile set the pace themselves.
-  static constexpr int kKSlotBytes = kKRows * kDqk * kEsz; // 36 KB
-  static constexpr int kKSlots = 2;
+  static constexpr int kKParts = WIDE ? 3 : 1;             // slots of a tile, by columns
+  static constexpr int kKSlotBytes = kKRows * kDqk * kEsz / kKParts; // 36 KB (24)
+  static constexpr int kKSlots = WIDE ? 3 : 2;
   static constexpr int kVTok = kPage;                      // keys of a V slot
   static constexpr int kVBoxes = 256 / kCols;              // 2 / 4
   static constexpr int kVBox = kVTok * 128;                // 8 KB
-  static constexpr int kVSlotBytes = kVBoxes * kVBox;      // 16 / 32 KB
+  static constexpr int kVSlotBytes = kVBoxes * kVBox;      // 16 / 32 KB (a page, or half of two pages' columns)
   static constexpr int kVPer = kPages;                     // slots of a tile
-  static constexpr int kVSteps = kVTok * kEsz / 32;        // K steps of a slot: 2 / 4
+  static constexpr int kVSteps = kVTok * kEsz / 32;        // K steps of a page: 2 / 4
   static constexpr int kVSlots = FP8 ? 5 : 2;
-  static constexpr int kPBytes = 64 * 128 * (FP8 ? 2 : 1); // hi and lo, or bf16: 128 bytes a row
-  static constexpr int kPBufs = 2;
+  // hi and lo, or bf16: 128 bytes a row, of one or two pages
+  static constexpr int kPBytes = 64 * 128 * (FP8 || WIDE ? 2 : 1);
+  static constexpr int kPBufs = WIDE ? 1 : 2;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kQBytes;
   static constexpr int kOffV = kOffK + kKSlots * kKSlotBytes;
@@ -232,14 +242,16 @@ __device__ __forceinline__ int length_of(int b, const WindowArgs &a, bool tell) 
   return min(max(len, 0), most);
 }
 
-// Row group and request of a job.  Planned apart, the row groups follow one
-// another; a tree's, of which there may be 64 and more, else stand together by
-// request, so that those who read the same pages do so at about the same time.
+// Row group and request of a job.  Without a tree the row groups are planned
+// apart or follow one another.  A tree's, of which there may be 64 and more, are
+// dealt out to the groups of pairs that are planned apart, and stand together by
+// request there, so that those who read the same pages do so at about the same time.
 template <bool TREE>
 __device__ __forceinline__ void who(int j, const WindowArgs &a, int &rg, int &b) {
-  if (TREE && a.groups == 1) {
-    b = a.RG > 1 ? j / a.RG : j;
-    rg = j - b * a.RG;
+  if constexpr (TREE) {
+    const int per = a.RG / a.groups, group = j / a.group_jobs, i = j - group * a.group_jobs;
+    b = per > 1 ? i / per : i;
+    rg = (i - b * per) * a.groups + group;
   } else {
     rg = a.RG > 1 ? j / a.B : 0;
     b = j - rg * a.B;
@@ -256,18 +268,18 @@ __device__ __forceinline__ int nodes_of(int b, const WindowArgs &a, bool tell) {
 }
 
 // Tiles of the row group rg of a request (none where it lies behind a tree's last token).
-template <bool FP8, bool TREE>
+template <bool FP8, bool TREE, bool WIDE>
 __device__ __forceinline__ int tiles_of(int rg, int b, const WindowArgs &a, int &len) {
   const bool tell = (blockIdx.x == 0 || a.solo) && rg == 0;
   len = length_of(b, a, tell);
   if (TREE && rg * 128 / a.H >= nodes_of(b, a, tell)) return 0;
-  return job_of<TREE>(rg, len, a).tiles(Fmt<FP8>::kPages);
+  return job_of<TREE>(rg, len, a).tiles(Fmt<FP8, WIDE>::kPages);
 }
-template <bool FP8, bool TREE>
+template <bool FP8, bool TREE, bool WIDE>
 __device__ __forceinline__ int tiles_of(int j, const WindowArgs &a, int &len) {
   int rg, b;
   who<TREE>(j, a, rg, b);
-  return tiles_of<FP8, TREE>(rg, b, a, len);
+  return tiles_of<FP8, TREE, WIDE>(rg, b, a, len);
 }
 
 struct Seg {
@@ -293,8 +305,9 @@ __device__ __forceinline__ int warp_incl_scan(int x, int lane) {
 // parts than pairs, each pair has one part of one job instead of C units of
 // what lies end to end: nobody then switches jobs (a second segment ends
 // about 4 us after a first one of the same tiles).  A part is the unit, C = 1.
-template <bool FP8, bool TREE>
+template <bool FP8, bool TREE, bool WIDE>
 struct Walk {
+  using F = Fmt<FP8, WIDE>;
   static constexpr int kHeld = 3;   // jobs of a lane that fit (the pairs are fewer than 96)
   int J, job0, per, lane_excl, total, C, span, span_lo, span_hi;
   int base, k, len, units, excl;
@@ -304,7 +317,7 @@ struct Walk {
 
   __device__ int units_of(int tiles) const {
     if (even) return (tiles + even - 1) / even;
-    return tiles > 0 ? tiles + Fmt<FP8>::kJobCost : 0;
+    return tiles > 0 ? tiles + F::kJobCost : 0;
   }
   __device__ void init(const WindowArgs &a, int lane) {
     const int pair = blockIdx.x >> 1, group = pair / a.spans_at_once;
@@ -319,15 +332,15 @@ struct Walk {
     if (per <= kHeld) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        held[i] = i < per && lane * per + i < J ? tiles_of<FP8, TREE>(job0 + lane * per + i, a, len) : 0;
+        held[i] = i < per && lane * per + i < J ? tiles_of<FP8, TREE, WIDE>(job0 + lane * per + i, a, len) : 0;
         sum += units_of(held[i]);
       }
     } else {
       for (int j = lane * per; j < min(J, (lane + 1) * per); ++j)
-        sum += units_of(tiles_of<FP8, TREE>(job0 + j, a, len));
+        sum += units_of(tiles_of<FP8, TREE, WIDE>(job0 + j, a, len));
     }
     total = __reduce_add_sync(0xffffffffu, sum);
-    C = a.forced > 0 ? a.forced : max(Fmt<FP8>::kMinUnits, (total - 1) / a.spans_at_once + 1);
+    C = a.forced > 0 ? a.forced : max(F::kMinUnits, (total - 1) / a.spans_at_once + 1);
     if (a.forced == 0 && J <= a.spans_at_once && per <= kHeld) {
       even = C;
       int parts = 0;
@@ -358,7 +371,7 @@ struct Walk {
     if (span >= J) return false;
     who<TREE>(span, a, s.rg, s.b);
     s.tile0 = 0;
-    s.ntiles = tiles_of<FP8, TREE>(s.rg, s.b, a, s.len);
+    s.ntiles = tiles_of<FP8, TREE, WIDE>(s.rg, s.b, a, s.len);
     s.whole = 1;
     s.slot = 0;
     span += a.spans_at_once;
@@ -369,7 +382,7 @@ struct Walk {
     k = 0;
     units = 0;
     len = 0;
-    if (base + lane < J) units = units_of(tiles_of<FP8, TREE>(job0 + base + lane, a, len));
+    if (base + lane < J) units = units_of(tiles_of<FP8, TREE, WIDE>(job0 + base + lane, a, len));
     const int incl = warp_incl_scan(units, lane);
     excl = before + incl - units;
   }
@@ -397,7 +410,7 @@ struct Walk {
         continue;
       }
       ++k;
-      const int first = t0 + (even ? 0 : Fmt<FP8>::kJobCost), end = t0 + n;
+      const int first = t0 + (even ? 0 : F::kJobCost), end = t0 + n;
       const int u0 = max(span_lo, first), u1 = min(span_hi, end);
       if (n == 0 || u1 <= u0) continue;
       who<TREE>(j, a, s.rg, s.b);
@@ -405,7 +418,7 @@ struct Walk {
       s.tile0 = u0 - first;
       s.ntiles = u1 - u0;
       if (even) {               // part tile0 of n, of sizes that differ by one at most
-        const int tiles = job_of<TREE>(s.rg, l, a).tiles(Fmt<FP8>::kPages), small = tiles / n,
+        const int tiles = job_of<TREE>(s.rg, l, a).tiles(F::kPages), small = tiles / n,
                   more = tiles - small * n, i = s.tile0;
         s.tile0 = i * small + min(i, more);
         s.ntiles = small + (i < more ? 1 : 0);
@@ -551,12 +564,13 @@ __device__ __noinline__ float far_sum(uint32_t scores, uint64_t seen, float4 c, 
   return sum;
 }
 
-template <bool FP8, bool TREE>
+template <bool FP8, bool TREE, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
 window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
               const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ WindowArgs args) {
-  using F = Fmt<FP8>;
+  using F = Fmt<FP8, WIDE>;
+  static_assert(!WIDE || (TREE && !FP8), "wide tiles");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw;   // (no static shared memory: starts on 1024 bytes)
   uint8_t *sm_q = smem + F::kOffQ, *sm_k = smem + F::kOffK, *sm_v = smem + F::kOffV;
@@ -567,7 +581,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   // leader: written by both CTAs' loads or warps; the others exist in both
   uint64_t *k_full = bars;                    // [kKSlots] leader
   uint64_t *k_empty = k_full + F::kKSlots;    // [kKSlots]
-  uint64_t *v_full = k_empty + F::kKSlots;    // [kVSlots]
+  uint64_t *v_full = k_empty + F::kKSlots;    // [kVSlots] (WIDE: leader)
   uint64_t *v_empty = v_full + F::kVSlots;    // [kVSlots]
   uint64_t *s_full = v_empty + F::kVSlots;    // [kSBufs]
   uint64_t *p_full = s_full + kSBufs;         // [2] leader
@@ -581,9 +595,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   uint64_t *l_read = sum_there + 2;           // [2 row blocks] bf16: the sums in x_max have been read
   uint64_t *o_free = l_read + 2;           // leader: the last segment's O has been read
   uint64_t *drain = o_free + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *out_done = drain + 1;             // [4 row blocks and halves] WIDE: results have left P's tile
+  uint64_t *v_near = out_done + 4;            // WIDE: a tile's values for this CTA's softmax to look at
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + (WIDE ? 6 : 1));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((2 * (F::kKSlots + F::kVSlots) + kSBufs + 4 + 2 + 2 * kSegSlots + 10) * 8 + 8 <= F::kBarBytes,
+  static_assert((2 * (F::kKSlots + F::kVSlots) + kSBufs + 4 + 2 + 2 * kSegSlots + (WIDE ? 15 : 10)) * 8 + 8 <=
+                    F::kBarBytes,
                 "barriers");
   static_assert(sizeof(Seg) <= 32, "segment slot");
 
@@ -621,6 +638,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
     mbar_init(o_free, 2 * kSoftWarps);
     mbar_init(drain, 1);
+    if constexpr (WIDE) {
+      for (int s = 0; s < 4; ++s) mbar_init(&out_done[s], 2);   // a warp of either group
+      mbar_init(v_near, 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -671,12 +692,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (entry < job.pages && lane == 0) raise_error(args.err, MLA_DEVERR_BLOCK_ID);
     return -1;
   };
+  // WIDE: the first tile with a row that not every token of the tree sees (behind a context of ctx)
+  auto first_look = [](int ctx) { return max(ctx, 0) / F::kTile; };
   // rows out of the cache: TMA fills in zeros
   const int no_row = args.num_blocks * kPage;
 
   if (warp == 0) {
     // ------------------------------------------------- plan, Q and K
-    Walk<FP8, TREE> walk;
+    Walk<FP8, TREE, WIDE> walk;
     if (args.solo) {
       walk.init_solo(args);
     } else {
@@ -717,16 +740,19 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         // this CTA's key rows: a page of the two, or half of the one
         const int blk = block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + (F::kPages - 1) * rank);
         const int row = blk < 0 ? no_row : blk * kPage + (2 - F::kPages) * F::kKRows * rank;
-        const int s = kc % F::kKSlots;
-        if (kc >= F::kKSlots &&
-            !(ok = wait_for(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
-          break;
-        ++kc;
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kKSlotBytes);
-          const uint32_t bar = peer_smem(&k_full[s], 0);
-          pair_load(sm_k + s * F::kKSlotBytes, &tm_k, bar, 0, row, 0);
-          if (FP8) pair_load(sm_k + s * F::kKSlotBytes + 4 * F::kKBox, &tm_kr, bar, kLatent, row, 0);
+#pragma unroll 1
+        for (int part = 0; part < F::kKParts; ++part) {
+          const int s = kc % F::kKSlots;
+          if (kc >= F::kKSlots &&
+              !(ok = wait_for(&k_empty[s], ((kc / F::kKSlots) - 1) & 1, abort_flag)))
+            break;
+          ++kc;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&k_full[s], 2 * F::kKSlotBytes);
+            const uint32_t bar = peer_smem(&k_full[s], 0);
+            pair_load(sm_k + s * F::kKSlotBytes, &tm_k, bar, 0, row, F::kBoxes / F::kKParts * part);
+            if (FP8) pair_load(sm_k + s * F::kKSlotBytes + 4 * F::kKBox, &tm_kr, bar, kLatent, row, 0);
+          }
         }
       }
     }
@@ -748,35 +774,67 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------- V
-    const uint64_t policy = l2_evict_first_policy();   // the rows' second and last read
+    // the rows' second and last read; a tree's other row groups read them again (16 trees
+    // of 16 tokens over 4096 bf16 ones: 213 us, evicted first 222)
+    const uint64_t policy = l2_evict_first_policy();
     Seg sg;
-    int vc = 0;
+    int vc = 0, near = 0;                   // slots, and tiles to be looked at, so far
     bool ok = true;
     for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
       const Job job = job_of<TREE>(sg.rg, sg.len, args);
       Pages pg;
       fetch_blocks(pg, job, sg.b, F::kPages * sg.tile0);
+      const int look = WIDE ? first_look(sg.len - nodes_of(sg.b, args, false)) : 0;
       for (int t = 0; ok && t < sg.ntiles; ++t) {
+        int both[2] = {no_row, no_row};       // WIDE: first rows of the tile's pages
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int blk = block_at(pg, job, sg.b, 2 * (sg.tile0 + t) + h);
+            if (blk >= 0) both[h] = blk * kPage;
+          }
+        }
         for (int v = 0; v < F::kVPer; ++v, ++vc) {
-          const int blk = block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + v);
+          const int blk = WIDE ? 0 : block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + v);
           const int s = vc % F::kVSlots;
           if (vc >= F::kVSlots &&
               !(ok = wait_for(&v_empty[s], ((vc / F::kVSlots) - 1) & 1, abort_flag)))
             break;
           const int row = blk < 0 ? no_row : blk * kPage;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
-            load_3d_hint(sm_v + s * F::kVSlotBytes, &tm_v, &v_full[s], 0, row, F::kVBoxes * rank, policy);
+            uint8_t *dst = sm_v + s * F::kVSlotBytes;
+            if constexpr (WIDE) {
+              // tiles that are seen as they are: both CTAs' bytes count for the MMA warp
+              // itself; the others for this CTA's softmax, whose word the MMA warp takes
+              const bool to_look = sg.tile0 + t >= look;
+              uint32_t bar = peer_smem(&v_full[s], 0);
+              if (!to_look) {
+                if (rank == 0) mbar_arrive_expect_tx(&v_full[s], 2 * F::kVSlotBytes);
+              } else {
+                if (rank == 0) mbar_arrive(&v_full[s]);
+                if (v == 0) mbar_arrive_expect_tx(v_near, 2 * F::kVSlotBytes);
+                bar = peer_smem(v_near, rank);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                pair_load(dst + h * 2 * F::kVBox, &tm_v, bar, 0, both[h], 4 * rank + 2 * v);
+            } else {
+              mbar_arrive_expect_tx(&v_full[s], F::kVSlotBytes);
+              if (TREE) tma_load_3d(dst, &tm_v, &v_full[s], 0, row, F::kVBoxes * rank);
+              else load_3d_hint(dst, &tm_v, &v_full[s], 0, row, F::kVBoxes * rank, policy);
+            }
           }
         }
+        if (WIDE && sg.tile0 + t >= look) ++near;
       }
     }
     for (int u = max(0, vc - F::kVSlots); ok && u < vc; ++u)
       ok = wait_for(&v_empty[u % F::kVSlots], (u / F::kVSlots) & 1, abort_flag);
     if (*abort_flag && lane == 0) {
       volatile int no_abort = 0;
-      for (int u = max(0, vc - F::kVSlots); u < vc; ++u)
+      for (int u = max(0, vc - F::kVSlots); (!WIDE || rank == 0) && u < vc; ++u)
         wait_for(&v_full[u % F::kVSlots], (u / F::kVSlots) & 1, &no_abort);
+      if (WIDE && near > 0) wait_for(v_near, (near - 1) & 1, &no_abort);
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -795,18 +853,26 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       bool ok = true;
       auto issue_qk = [&](int u) -> bool {
         const uint32_t d = tmem + kColS + F::kTile / 2 * (u % kSBufs);
-        const int s = kc % F::kKSlots;
-        if (!wait(&k_full[s], kc / F::kKSlots)) return false;
-        ++kc;
-        tc_fence_after();
-        // one descriptor a slot; steps add to its address field (16-byte units)
-        const uint32_t kd = desc_lo(sm_k + s * F::kKSlotBytes, 16);
+        constexpr int kSteps = 4 * F::kBoxes / F::kKParts;
+        int s;
 #pragma unroll
-        for (int k = 0; k < 4 * F::kBoxes; ++k)
-          pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qd + (k >> 2) * 512 + (k & 3) * 2),
-                        desc_at<1024, kSwizzle128B>(kd + (k >> 2) * (F::kKBox / 16) + (k & 3) * 2),
-                        idesc_qk, k > 0, me);
+        for (int part = 0; part < F::kKParts; ++part) {
+          s = kc % F::kKSlots;
+          if (!wait(&k_full[s], kc / F::kKSlots)) return false;
+          ++kc;
+          tc_fence_after();
+          // one descriptor a slot; steps add to its address field (16-byte units)
+          const uint32_t kd = desc_lo(sm_k + s * F::kKSlotBytes, 16);
+          const uint32_t qp = qd + part * (kSteps / 4) * 512;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            pair_mma<FP8>(d, desc_at<1024, kSwizzle128B>(qp + (k >> 2) * 512 + (k & 3) * 2),
+                          desc_at<1024, kSwizzle128B>(kd + (k >> 2) * (F::kKBox / 16) + (k & 3) * 2),
+                          idesc_qk, part > 0 || k > 0, me);
+          if (part + 1 < F::kKParts) pair_commit(&k_empty[s], me);
+        }
         if constexpr (FP8) {
+          const uint32_t kd = desc_lo(sm_k + s * F::kKSlotBytes, 16);
 #pragma unroll
           for (int k = 0; k < 2; ++k)         // the rope columns: rows of 64 bytes
             pair_mma<FP8>(d, desc_at<512, kSwizzle64B>(qd + 4 * 512 + 2 * k),
@@ -818,31 +884,39 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       };
       // All steps of one accumulator, then of the other: an MMA that adds to
       // what the last but one wrote waits for it (232 cycles a change).
-      auto issue_pv = [&](int u, bool first) {
+      auto issue_pv = [&](int u, bool first) -> bool {
         const uint32_t pd = desc_lo(sm_p + (u % F::kPBufs) * F::kPBytes, 16);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {         // value columns 128j .. 128j + 127 of either CTA
 #pragma unroll
           for (int v = 0; v < F::kVPer; ++v) {
-            const int s = (vc + v) % F::kVSlots;
+            // (WIDE: slot j has the columns of accumulator j, page v behind page 0)
+            const int s = (vc + (WIDE ? j : v)) % F::kVSlots;
+            if (WIDE && v == 0) {
+              if (!wait(&v_full[s], (vc + j) / F::kVSlots)) return false;
+              tc_fence_after();
+            }
             const uint32_t vd = desc_lo(sm_v + s * F::kVSlotBytes, F::kVBox);
 #pragma unroll
             for (int kk = 0; kk < F::kVSteps; ++kk) {   // 32 bytes of P: 32 e4m3 or 16 bf16 keys
               const int step = F::kVSteps * v + kk;
-              const uint32_t pa = pd + step * 2;
+              const uint32_t pa = pd + (WIDE ? v * 512 + kk * 2 : step * 2);
               const uint64_t bd = desc_at<1024, kSwizzle128B>(
-                  vd + (FP8 ? j * F::kVBox + kk * 4096 : 2 * j * F::kVBox + kk * 2048) / 16);
+                  vd + (FP8    ? j * F::kVBox + kk * 4096
+                        : WIDE ? 2 * v * F::kVBox + kk * 2048
+                               : 2 * j * F::kVBox + kk * 2048) / 16);
               pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa), bd, idesc_pv,
                             first && step == 0 ? 0u : 1u, me);
               if constexpr (FP8)
                 pair_mma<FP8>(tmem + kColO + 128 * j, desc_at<1024, kSwizzle128B>(pa + 512), bd,
                               idesc_lo, 1, me);
             }
-            if (j == 1) pair_commit(&v_empty[s], me);
+            if (WIDE ? v == 1 : j == 1) pair_commit(&v_empty[s], me);
           }
         }
         vc += F::kVPer;
         pair_commit(&pv_done[u & 1], me);
+        return true;
       };
       Seg sg;
       int nq = 0;
@@ -863,7 +937,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           if (t == 0 && nq > 1 && !(ok = wait(o_free, nq - 2))) break;
           if (!(ok = wait(&p_full[uc & 1], uc >> 1))) break;
           tc_fence_after();
-          issue_pv(uc, t == 0);
+          if (!(ok = issue_pv(uc, t == 0))) break;
         }
       }
       if (ok && nq > 0) wait(o_free, nq - 1);   // (the other CTA's last signals are in)
@@ -902,6 +976,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     auto all_ok = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
     Seg sg;
     int uc = 0, segs = 0;                               // tiles and segments (with tiles) so far
+    int near = 0;                                       // WIDE: tiles of v_near so far
     bool ok = true;
     for (int ns = 0; ok && take_seg(ns, sg); ++ns) {
       const int R = args.q_len * args.H;
@@ -957,6 +1032,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       load_scales(load_blk(t_first), sc);
       const int uc0 = uc;
       uc += sg.ntiles;
+      const int look = WIDE ? first_look(tree0) : 0;
       // e4m3: the sum in units of 2^ln.  bf16: sums in units of 2^ref, of the
       // probabilities for the logarithm and of their rounded values for the
       // results, where a large one's rounding then is in the numerator and the
@@ -1008,7 +1084,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         tc_fence_after();
         float x[F::kMine];
         const uint32_t s_at = lane_base + kColS + F::kTile / 2 * (u % kSBufs);
-        if constexpr (FP8) tmem_ld_x64(s_at, reinterpret_cast<uint32_t *>(x));
+        if constexpr (F::kMine == 64) tmem_ld_x64(s_at, reinterpret_cast<uint32_t *>(x));
         else tmem_ld_x32(s_at, reinterpret_cast<uint32_t *>(x));
         if (masked) {
           const uint64_t seen = seen_keys();
@@ -1093,9 +1169,17 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             lr += r0 + r1;
           }
         }
-        // P goes where the P V of this group's last tile read
-        if (u >= 2 && !(ok = all_ok(wait_for(&pv_done[group], (half_u - 1) & 1, abort_flag)))) break;
-        uint8_t *pbuf = sm_p + group * F::kPBytes;
+        // P goes where the P V of this group's last tile read (WIDE: of the last tile; and
+        // where the last segment's results were staged)
+        if constexpr (WIDE) {
+          if (u >= 1 && !(ok = all_ok(wait_for(&pv_done[group ^ 1], ((u - 1) >> 1) & 1, abort_flag)))) break;
+          if (t <= 1 && segs > 0 &&
+              !(ok = all_ok(wait_for(&out_done[2 * block + half], (segs - 1) & 1, abort_flag))))
+            break;
+        } else {
+          if (u >= 2 && !(ok = all_ok(wait_for(&pv_done[group], (half_u - 1) & 1, abort_flag)))) break;
+        }
+        uint8_t *pbuf = sm_p + (WIDE ? half * 8192 : group * F::kPBytes);
         if constexpr (FP8) {
           uint4 *hi = reinterpret_cast<uint4 *>(pbuf + r * 128);
           uint4 *lo = reinterpret_cast<uint4 *>(pbuf + 8192 + r * 128);
@@ -1117,8 +1201,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         } else {
           uint4 *row = reinterpret_cast<uint4 *>(pbuf + r * 128);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            row[(4 * half + q) ^ (r & 7)] =
+          for (int q = 0; q < F::kMine / 8; ++q)
+            row[((WIDE ? 0 : 4 * half) + q) ^ (r & 7)] =
                 make_uint4(__float_as_uint(x[8 * q]), __float_as_uint(x[8 * q + 2]),
                            __float_as_uint(x[8 * q + 4]), __float_as_uint(x[8 * q + 6]));
         }
@@ -1148,10 +1232,15 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           }
         }
         // the values are here (the MMA thread goes by this CTA's word)
+        if constexpr (WIDE) {
+          const int n = sg.tile0 + t - max(look, sg.tile0);
+          if (n >= 0) ok = wait_for(v_near, (near + n) & 1, abort_flag);
+        } else {
 #pragma unroll
-        for (int v = 0; v < F::kVPer; ++v) {
-          const int w = F::kVPer * u + v;
-          ok = ok && wait_for(&v_full[w % F::kVSlots], (w / F::kVSlots) & 1, abort_flag);
+          for (int v = 0; v < F::kVPer; ++v) {
+            const int w = F::kVPer * u + v;
+            ok = ok && wait_for(&v_full[w % F::kVSlots], (w / F::kVSlots) & 1, abort_flag);
+          }
         }
         if (ok && !all_clean) {
           // rows that not every query row sees: 0 where none does, and where
@@ -1159,7 +1248,8 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           // others).  A row of this CTA's columns is one (bf16) or half a
           // (e4m3) warp's 16-byte chunks.
           constexpr int kChunks = F::kVBoxes * 8, kRowsAtOnce = 32 / kChunks;
-          const int lr = lane / kChunks, at = ((lane % kChunks) >> 3) * F::kVBox + (lane & 7) * 16;
+          const int box = (lane % kChunks) >> 3;      // of 64 or 128 columns
+          const int lr = lane / kChunks, at = (WIDE ? box & 1 : box) * F::kVBox + (lane & 7) * 16;
 #pragma unroll 1
           for (int h = 0; h < F::kPages; ++h) {
             const int page = h ? page1 : page0;
@@ -1171,9 +1261,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll 1
             for (int i = quarter * kRowsAtOnce + lr; i < n; i += 4 * kRowsAtOnce) {
               const int tok = i < b - a ? a + i : c + i - (b - a);
-              const int slot = (F::kVPer * u + (h * kPage + tok) / F::kVTok) % F::kVSlots;
+              const int slot = (F::kVPer * u + (WIDE ? box >> 1 : (h * kPage + tok) / F::kVTok)) % F::kVSlots;
               uint4 *w = reinterpret_cast<uint4 *>(sm_v + slot * F::kVSlotBytes + at +
-                                                   (tok % F::kVTok) * 128);
+                                                   (WIDE ? h * 2 * F::kVBox : 0) + (tok % F::kVTok) * 128);
               uint4 val = make_uint4(0, 0, 0, 0);
               const int key = page + tok;
               if (job.p0 != job.p1 && key <= job.p1 &&
@@ -1214,6 +1304,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         for (int g = 0; g < kBlocks; ++g) sc[g] = sc_next[g];
       }
       if (!ok) break;
+      if constexpr (WIDE) near += max(0, sg.tile0 + sg.ntiles - max(look, sg.tile0));
       // ---- results: O / l of this row, value columns [256 half + 128 group, +128)
       const int last = uc - 1, lg_last = last & 1;
       if (!(ok = all_ok(wait_for(&ref_there[2 * lg_last + block], (last >> 1) & 1, abort_flag) &&
@@ -1301,8 +1392,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       // pieces of 64 bytes a row, staged through 2 KB of this warp's own in its
       // group's P tile (in its row block, which the pair writes again behind
       // its next barrier), so that stores cover whole sectors
-      uint4 *buf = reinterpret_cast<uint4 *>(sm_p + group * F::kPBytes + block * 4096 + half * 2048);
-      static_assert(F::kPBytes >= 4 * 2048, "staging");
+      // (WIDE: in its half and row block of the one P tile, beside the other group's warp of these)
+      uint4 *buf = reinterpret_cast<uint4 *>(
+          sm_p + (WIDE ? half * 8192 + block * 4096 + group * 2048 : group * F::kPBytes + block * 4096 + half * 2048));
+      static_assert(F::kPBytes * F::kPBufs >= 8 * 2048, "staging");
       // (a body for each type of element: 0 bf16, 1 fp16, 2 fp32)
       auto write = [&](auto type) {
         constexpr int kType = decltype(type)::value, kPer = kType == 2 ? 16 : 32;   // values of a piece
@@ -1338,6 +1431,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       if (args.out_f32) write(std::integral_constant<int, 2>{});
       else if (fp16) write(std::integral_constant<int, 1>{});
       else write(std::integral_constant<int, 0>{});
+      if constexpr (WIDE) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&out_done[2 * block + half]);
+      }
     }
     if (!told) named_and(1 + 2 * group + block, 64, ok && !*abort_flag);
   }
@@ -1508,14 +1605,14 @@ cudaError_t merge(int64_t parts, const WindowArgs &a, mla_stream_t stream) {
 }
 
 // ------------------------------------------------------------------- host
-template <bool FP8>
+template <bool FP8, bool WIDE = false>
 struct PairLaunch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   PairLaunch(int pairs, cudaStream_t stream) {
     cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Fmt<FP8>::kSmem;
+    cfg.dynamicSmemBytes = Fmt<FP8, WIDE>::kSmem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -1546,11 +1643,12 @@ int pairs_for_device() {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
   auto at = [](auto *kernel) { return reinterpret_cast<const void *>(kernel); };
-  if (!allow(at(window_kernel<false, false>), Fmt<false>::kSmem) ||
-      !allow(at(window_kernel<true, false>), Fmt<true>::kSmem) ||
-      !allow(at(window_kernel<false, true>), Fmt<false>::kSmem) ||
-      !allow(at(window_kernel<true, true>), Fmt<true>::kSmem) ||
-      cudaOccupancyMaxActiveClusters(&n, window_kernel<false, false>, &pl.cfg) != cudaSuccess) {
+  if (!allow(at(window_kernel<false, false, false>), Fmt<false>::kSmem) ||
+      !allow(at(window_kernel<true, false, false>), Fmt<true>::kSmem) ||
+      !allow(at(window_kernel<false, true, false>), Fmt<false>::kSmem) ||
+      !allow(at(window_kernel<false, true, true>), Fmt<false, true>::kSmem) ||
+      !allow(at(window_kernel<true, true, false>), Fmt<true>::kSmem) ||
+      cudaOccupancyMaxActiveClusters(&n, window_kernel<false, false, false>, &pl.cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -1571,8 +1669,11 @@ struct WsLayout {
   bool solo, fits;              // fits: the units of all jobs count in 32 bits
 };
 
+// (uneven: a tree whose sizes only the device knows)
+enum Rows { kChain, kTree, kUnevenTrees };
+
 WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sinks,
-                   int split_tiles, int pairs) {
+                   int split_tiles, int pairs, Rows rows = kChain) {
   const int64_t RG = (static_cast<int64_t>(q_len) * H + 127) / 128, J = B * RG;
   // most pages of a job: the sinks' and the window's, which may begin inside
   // a page and is q_len - 1 tokens longer for the job's queries together
@@ -1588,13 +1689,28 @@ WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sin
   // Row groups of a request read the same pages.  Planned apart, each over its
   // share of the pairs, they do so at the same time, and all but one read from
   // L2 - unless that leaves more than a sixteenth of the pairs idle.
-  if (RG <= pairs && pairs / RG * RG * 16 >= static_cast<int64_t>(pairs) * 15) w.groups = static_cast<int>(RG);
+  // Trees' row groups are dealt out to as many groups of pairs as divide them evenly
+  // (24 requests of 16 tokens over 8192 bf16 ones: 544 us, all in one plan 593); but of
+  // trees of different sizes the later row groups have less to do: they are planned
+  // together (8 trees of 17 to 33 tokens over up to 8192 e4m3 ones, 20 heads: 42 us, apart
+  // 50; 32 trees of 4 over 4096 bf16 ones, sizes given: 122, not given: 105).
+  auto evenly = [&](int64_t n) { return n <= pairs && pairs / n * n * 16 >= static_cast<int64_t>(pairs) * 15; };
+  if (rows == kChain) {
+    if (evenly(RG)) w.groups = static_cast<int>(RG);
+  } else if (rows == kTree) {
+    for (int64_t n = std::min<int64_t>(RG, pairs); n > 1 && w.groups == 1; --n)
+      if (RG % n == 0 && evenly(n)) w.groups = static_cast<int>(n);
+  }
   // (a forced split counts tiles: the smaller ones, of one page, make more)
-  w.group_spans = split_tiles > 0 ? (J / w.groups * (pages + kJobPages) + split_tiles - 1) / split_tiles
-                                  : pairs / w.groups;
-  const size_t slots = static_cast<size_t>(2 * w.groups) * w.group_spans;
+  auto spans_of = [&](int64_t groups) {
+    return split_tiles > 0 ? (J / groups * (pages + kJobPages) + split_tiles - 1) / split_tiles : pairs / groups;
+  };
+  w.group_spans = spans_of(w.groups);
+  // (trees of any sizes: the most of either plan)
+  const size_t slots = rows == kChain ? static_cast<size_t>(2 * w.groups) * w.group_spans
+                                      : 2 * std::max<size_t>(spans_of(1), split_tiles > 0 ? RG * spans_of(RG) : 0);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  w.o_off = up((w.groups + 2 * static_cast<size_t>(J)) * sizeof(int));
+  w.o_off = up(((rows == kChain ? w.groups : RG) + 2 * static_cast<size_t>(J)) * sizeof(int));
   w.lse_off = w.o_off + slots * 128 * kLatent * sizeof(float);
   w.unit_off = w.lse_off + slots * 128 * sizeof(float);
   w.total = w.unit_off + slots * 128 * 4 * sizeof(float);
@@ -1623,10 +1739,10 @@ int check_window(const void *q, int q_dtype, float q_scale, const void *kv_cache
   return MLA_OK;
 }
 
-template <bool FP8>
+template <bool FP8, bool TREE, bool WIDE>
 int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArgs &a,
                  mla_stream_t stream) {
-  using F = Fmt<FP8>;
+  using F = Fmt<FP8, WIDE>;
   const CUtensorMapDataType dt =
       FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   // {columns of a 128-byte box row, rows, box columns}; the e4m3 rope columns
@@ -1637,8 +1753,8 @@ int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArg
   const uint64_t q_rows = static_cast<uint64_t>(a.B) * a.q_len * a.H;
   const uint64_t kv_dims[3] = {F::kCols, kv_rows, F::kBoxes}, q_dims[3] = {F::kCols, q_rows, F::kBoxes};
   const uint64_t kvr_dims[3] = {kDqk, kv_rows, 1}, qr_dims[3] = {kDqk, q_rows, 1};
-  const uint32_t box_k[3] = {F::kCols, F::kKRows, F::kBoxes}, box_q[3] = {F::kCols, 64, F::kBoxes};
-  const uint32_t box_v[3] = {F::kCols, F::kVTok, F::kVBoxes}, box_r[3] = {64, 64, 1};
+  const uint32_t box_k[3] = {F::kCols, F::kKRows, F::kBoxes / F::kKParts}, box_q[3] = {F::kCols, 64, F::kBoxes};
+  const uint32_t box_v[3] = {F::kCols, F::kVTok, WIDE ? 2 : F::kVBoxes}, box_r[3] = {64, 64, 1};
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, sw_r = CU_TENSOR_MAP_SWIZZLE_64B;
   CUtensorMap tk, tkr, tv, tq, tqr;
   bool ok = make_tmap(&tk, dt, 3, kv_cache, kv_dims, strides, box_k, sw) &&
@@ -1652,11 +1768,10 @@ int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArg
     tqr = tq;
   }
   if (!ok) return MLA_ERR_CUDA;
-  PairLaunch<FP8> pl(pairs, stream);
-  const cudaError_t e = a.tree_mask
-                            ? cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8, true>, tk, tkr, tv, tq, tqr, a)
-                            : cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8, false>, tk, tkr, tv, tq, tqr, a);
-  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  PairLaunch<FP8, WIDE> pl(pairs, stream);
+  return cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8, TREE, WIDE>, tk, tkr, tv, tq, tqr, a) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }
 
 struct Tree {
@@ -1673,7 +1788,8 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
   const int pairs = pairs_for_device();
   if (pairs == 0) return MLA_ERR_CUDA;
-  const WsLayout w = ws_layout(B, q_len, H, max_blocks * kPage, window, sinks, split_tiles, pairs);
+  const WsLayout w = ws_layout(B, q_len, H, max_blocks * kPage, window, sinks, split_tiles, pairs,
+                               !tree.mask ? kChain : tree.lens ? kUnevenTrees : kTree);
   if (!w.fits) return MLA_ERR_INVALID_ARG;
   if (!w.solo && (!workspace || ws_bytes < w.total)) return MLA_ERR_WORKSPACE;
   WindowArgs a{};
@@ -1715,8 +1831,17 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.ws_o = ws + w.o_off;
   a.ws_lse = reinterpret_cast<float *>(ws + w.lse_off);
   a.ws_unit = reinterpret_cast<float *>(ws + w.unit_off);
-  const int st = fp8 ? launch_pairs<true>(q, kv_cache, a.spans_at_once * w.groups, a, stream)
-                     : launch_pairs<false>(q, kv_cache, a.spans_at_once * w.groups, a, stream);
+  const int n = a.spans_at_once * w.groups;
+  // A tree's wide tiles, where a pair may have kWidePages pages and more: 24 requests of 16
+  // tokens over 8192 (650 pages a pair) 557 us, with tiles of one page 605; 16 over 4096 (217)
+  // 196, 214; 64 of 4 over up to 2000 (107) 91.5, 93.1; but 32 of 8 over 500 (29) 61.7, 60.4; 4
+  // of 8 with 16 heads over 4000 (3) 19.0, 17.8
+  const bool wide = tree.mask && !fp8 && jobs * max_blocks >= static_cast<int64_t>(kWidePages) * pairs;
+  auto launch = fp8 ? tree.mask ? launch_pairs<true, true, false> : launch_pairs<true, false, false>
+                : !tree.mask ? launch_pairs<false, false, false>
+                : wide       ? launch_pairs<false, true, true>
+                             : launch_pairs<false, true, false>;
+  const int st = launch(q, kv_cache, n, a, stream);
   if (st != MLA_OK || w.solo) return st;
   const int64_t parts = pairs / jobs;   // of a job, about
   const cudaError_t e = a.out_f32 ? merge<float>(parts, a, stream) : merge<__nv_bfloat16>(parts, a, stream);
@@ -1737,6 +1862,16 @@ extern "C" int mla_decode_window_workspace_size(int B, int q_len, int H, int max
   // (without a device: what an upper bound of pairs needs)
   const int pairs = pairs_for_device();
   const WsLayout w = ws_layout(B, q_len, H, max_seq_len, window, sinks, split_tiles, pairs ? pairs : 128);
+  if (!w.fits) return MLA_ERR_INVALID_ARG;
+  *bytes = w.total;
+  return MLA_OK;
+}
+
+extern "C" int mla_decode_tree_workspace_size(int B, int q_len, int H, int max_seq_len, int split_tiles,
+                                              size_t *bytes) {
+  if (!bytes || !shape_ok(B, q_len, H) || max_seq_len < 0 || split_tiles < 0) return MLA_ERR_INVALID_ARG;
+  const int pairs = pairs_for_device();
+  const WsLayout w = ws_layout(B, q_len, H, max_seq_len, 0, 0, split_tiles, pairs ? pairs : 128, kTree);
   if (!w.fits) return MLA_ERR_INVALID_ARG;
   *bytes = w.total;
   return MLA_OK;
