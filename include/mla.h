@@ -541,7 +541,7 @@ int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_table,
  * out on every fork that needs one; a row outside [0, B): MLA_DEVERR_RANGE; a
  * parent's length out of range: MLA_DEVERR_SEQ_LEN; a parent's entry that is
  * no page: MLA_DEVERR_BLOCK_ID, and the child's is -1.
- * workspace: mla_cache_fork_workspace_size(n) bytes. */
+ * workspace: mla_cache_fork_workspace_size(n) bytes, 4-byte aligned. */
 int mla_cache_fork_workspace_size(int n, size_t *bytes);
 
 int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int n_pools,
@@ -557,7 +557,8 @@ int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int n_pools,
  * these sequences, or by entries that the caller has elsewhere and updates
  * himself.  An entry that is no page sets MLA_DEVERR_BLOCK_ID, one that is
  * free and not below N MLA_DEVERR_PAGES; both stay.
- * workspace: mla_cache_compact_workspace_size(num_blocks) bytes. */
+ * workspace: mla_cache_compact_workspace_size(num_blocks) bytes, 8-byte
+ * aligned. */
 int mla_cache_compact_workspace_size(int num_blocks, size_t *bytes);
 
 int mla_cache_compact(void *const *pools, const int64_t *page_bytes,

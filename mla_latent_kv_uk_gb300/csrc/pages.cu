@@ -31,7 +31,7 @@ namespace mla {
 namespace {
 
 constexpr int kMaxPools = 200;       // (their addresses and sizes are kernel arguments, of 4 KB at most)
-constexpr int kMaxRows = 8192;       // sequences of a call, and forks: 3 words of shared memory each
+constexpr int kMaxRows = 8192;       // sequences of a call, and forks: 5 words of shared memory for both
 constexpr int kCtas = 8, kThreads = 1024, kWarps = kThreads / 32, kAllWarps = kCtas * kWarps;
 
 __device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
@@ -177,10 +177,25 @@ struct Seqs {
   int *err;
 };
 
+// The rows' entries dealt out to the cluster's warps: where there are few rows
+// several warps share one.
+constexpr int kAtOnce = 4;             // entries of a lane on their way
+struct Share {
+  int first, step, lane0, lanes;
+  __device__ Share(int rows, int wid) {
+    const int per = rows >= kAllWarps ? 1 : 1 << (31 - __clz(kAllWarps / rows));
+    first = wid / per;
+    step = kAllWarps / per;
+    lane0 = 32 * (wid % per);
+    lanes = 32 * per;
+  }
+};
+
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 resize_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ new_lens) {
   extern __shared__ int rows[];
-  int *had = rows, *want = rows + s.B, *end = rows + 2 * s.B;   // pages; needed ones up to and with this row
+  // pages; needed ones up to and with this row; the new length (-1: it stays as it is)
+  int *had = rows, *want = rows + s.B, *end = rows + 2 * s.B, *goal = rows + 3 * s.B;
   cluster_started();
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
@@ -197,6 +212,7 @@ resize_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ new_le
     const int h = valid ? pages_of(old) : 0, w = valid ? pages_of(now) : 0;
     had[b] = h;
     want[b] = w;
+    goal[b] = valid ? now : -1;
     drops |= w < h;
     end[b] = sum += max(0, w - h);
   }
@@ -205,15 +221,27 @@ resize_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ new_le
   for (int b = r0; b < r1; ++b) end[b] += before;
   cluster_wait();
   if (__syncthreads_or(drops)) {
-    for (int b = wid; b < s.B; b += kAllWarps) {
+    const Share share(s.B, wid);
+    for (int b = share.first; b < s.B; b += share.step) {
       int32_t *row = s.table + static_cast<int64_t>(b) * s.max_blocks;
-      for (int k = want[b] + lane; k < had[b]; k += 32) {
-        const int page = row[k];
-        row[k] = -1;
-        if (page < 0 || page >= s.num_blocks) {
-          raise_error(s.err, MLA_DEVERR_BLOCK_ID);
-        } else if (atomicSub(s.refs + page, 1) <= 0) {   // it was free
-          atomicAdd(s.refs + page, 1);
+      const int k1 = had[b];
+      for (int k0 = want[b] + share.lane0 + lane; k0 < k1; k0 += kAtOnce * share.lanes) {
+        int page[kAtOnce], was[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) page[i] = k0 + i * share.lanes < k1 ? row[k0 + i * share.lanes] : 0;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int k = k0 + i * share.lanes;
+          was[i] = 1;
+          if (k >= k1) continue;
+          row[k] = -1;
+          if (page[i] >= 0 && page[i] < s.num_blocks) was[i] = atomicSub(s.refs + page[i], 1);
+          else raise_error(s.err, MLA_DEVERR_BLOCK_ID);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          if (was[i] > 0) continue;
+          atomicAdd(s.refs + page[i], 1);          // it was free
           raise_error(s.err, MLA_DEVERR_PAGES);
         }
       }
@@ -226,10 +254,9 @@ resize_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ new_le
   // every CTA has read the lengths
   if (rank == 0) {
     for (int b = r0; b < r1; ++b) {
-      const int now = new_lens[b];
-      if (!ok(s.lens[b]) || !ok(now)) continue;
+      if (goal[b] < 0) continue;
       if (want[b] > had[b] && end[b] > scan.all) raise_error(s.err, MLA_DEVERR_PAGES);
-      else s.lens[b] = now;
+      else s.lens[b] = goal[b];
     }
   }
   scan.each(is_free, total, [&](int page, int number) {
@@ -249,90 +276,102 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 fork_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ parents,
             const int32_t *__restrict__ children, int n, const __grid_constant__ List list) {
   extern __shared__ int rows[];
-  int *first = rows, *end = rows + s.B;   // first fork to a row; own pages up to and with this fork
+  // first fork to a row; own pages up to and with this fork; parent, child and length (-1: left out)
+  int *first = rows, *end = rows + s.B, *from = end + n, *to = from + n, *length = to + n;
   cluster_started();
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, rank = static_cast<int>(sm100::cluster_rank());
   const int wid = rank * kWarps + (tid >> 5), most = s.max_blocks * kPage;
-  for (int b = tid; b < s.B; b += kThreads) first[b] = INT_MAX;
-  __syncthreads();
   const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
   auto row_ok = [&](int b) { return b >= 0 && b < s.B; };
+  for (int b = tid; b < s.B; b += kThreads) first[b] = INT_MAX;
   for (int i = i0; i < i1; ++i) {
-    const int c = children[i];
-    if (row_ok(c)) atomicMin(first + c, i);
+    from[i] = parents[i];
+    to[i] = children[i];
   }
   __syncthreads();
-  // the length of fork i, or -1 where it cannot be
-  auto length = [&](int i, bool tell) -> int {
-    const int p = parents[i], c = children[i];
-    int bits = 0, len = -1;
-    if (!row_ok(p) || !row_ok(c)) bits = MLA_DEVERR_RANGE;
-    else if (first[c] != i || s.lens[c] != 0) bits = MLA_DEVERR_PAGES;
-    else if ((len = s.lens[p]) < 0 || len > most) bits = MLA_DEVERR_SEQ_LEN;
-    if (bits && tell) raise_error(s.err, bits);
-    return bits ? -1 : len;
-  };
+  int child_len = 0;                        // of the last of this thread's forks (of several: read again)
+  for (int i = i0; i < i1; ++i) {
+    if (row_ok(to[i])) {
+      atomicMin(first + to[i], i);
+      child_len = s.lens[to[i]];
+    }
+    length[i] = row_ok(from[i]) ? s.lens[from[i]] : 0;
+  }
+  __syncthreads();
   int sum = 0;
   for (int i = i0; i < i1; ++i) {
-    const int len = length(i, rank == 0);
-    end[i] = sum += len > 0 && len % kPage ? 1 : 0;
+    const int p = from[i], c = to[i], len = length[i];
+    int bits = 0;
+    if (!row_ok(p) || !row_ok(c)) bits = MLA_DEVERR_RANGE;
+    else if (first[c] != i || (per == 1 ? child_len : s.lens[c]) != 0) bits = MLA_DEVERR_PAGES;
+    else if (len < 0 || len > most) bits = MLA_DEVERR_SEQ_LEN;
+    if (bits && rank == 0) raise_error(s.err, bits);
+    if (bits) length[i] = -1;
+    end[i] = sum += !bits && len % kPage ? 1 : 0;
   }
   int total;
   const int before = block_excl(sum, total);
   for (int i = i0; i < i1; ++i) end[i] += before;
   cluster_wait();
   __syncthreads();
-  // what the warps' forks need of the lengths, before these change
-  constexpr int kMine = kMaxRows / kAllWarps;
-  int mine = -1;                            // lane k: that of fork wid + k * kAllWarps
-  static_assert(kMine <= 32, "a lane a fork");
-  if (wid + lane * kAllWarps < n) mine = length(wid + lane * kAllWarps, false);
+  // the entries of the warp's first fork are asked for along with the pages' counts
+  const Share share(n, wid);
+  auto entry = [&](int p, int e) { return s.table[static_cast<int64_t>(p) * s.max_blocks + e]; };
+  int page[kAtOnce];
+  auto fetch = [&](int p, int len, int e0) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      page[i] = e0 + i * share.lanes < len / kPage ? entry(p, e0 + i * share.lanes) : -1;
+  };
+  const int e_first = share.lane0 + lane;
+  if (share.first < n) fetch(from[share.first], length[share.first], e_first);
   Scan scan(s.refs, s.num_blocks, rank);
   if (total == 0) scan.first = s.num_blocks;
   scan.count(is_free, rank);
-  for (int k = 0, i = wid; i < n; ++k, i += kAllWarps) {
-    const int len = __shfl_sync(0xffffffffu, mine, k);
-    const bool own = len > 0 && len % kPage, fails = own && end[i] > scan.all;
-    if (lane == 0) {
+  for (int i = share.first; i < n; i += share.step) {
+    const int len = length[i], p = from[i], c = to[i];
+    const bool own = len > 0 && len % kPage, fails = own && end[i] > scan.all, one = lane + share.lane0 == 0;
+    if (one) {
       if (fails) raise_error(s.err, MLA_DEVERR_PAGES);
       if (!own || fails) list.dst[i] = -1;
     }
     if (len < 0 || fails) continue;
-    const int p = parents[i], c = children[i];
-    const int32_t *from = s.table + static_cast<int64_t>(p) * s.max_blocks;
-    int32_t *to = s.table + static_cast<int64_t>(c) * s.max_blocks;
-    for (int e = lane; e < len / kPage; e += 32) {
-      const int page = from[e];
-      const bool good = page >= 0 && page < s.num_blocks;
-      to[e] = good ? page : -1;
-      if (good) atomicAdd(s.refs + page, 1);
-      else raise_error(s.err, MLA_DEVERR_BLOCK_ID);
-    }
-    if (lane == 0) {
+    int32_t *row = s.table + static_cast<int64_t>(c) * s.max_blocks;
+    if (one) {
       s.lens[c] = len;
       if (own) {
-        const int page = from[len / kPage];
-        const bool good = page >= 0 && page < s.num_blocks;
+        const int last = entry(p, len / kPage);
+        const bool good = last >= 0 && last < s.num_blocks;
         if (!good) raise_error(s.err, MLA_DEVERR_BLOCK_ID);
-        list.src[i] = good ? page : -1;
+        list.src[i] = good ? last : -1;
         list.rows[i] = len % kPage;
+      }
+    }
+    for (int e0 = e_first; e0 < len / kPage; e0 += kAtOnce * share.lanes) {
+      if (i != share.first || e0 != e_first) fetch(p, len, e0);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int e = e0 + j * share.lanes;
+        if (e >= len / kPage) continue;
+        const bool good = page[j] >= 0 && page[j] < s.num_blocks;
+        row[e] = good ? page[j] : -1;
+        if (good) atomicAdd(s.refs + page[j], 1);
+        else raise_error(s.err, MLA_DEVERR_BLOCK_ID);
       }
     }
   }
   scan.each(is_free, total, [&](int page, int number) {
     const int i = first_over(end, n, number);
-    // (its row's length may be there already or not: the parent's is the same)
-    const int c = children[i], len = s.lens[parents[i]];
-    s.table[static_cast<int64_t>(c) * s.max_blocks + len / kPage] = page;
+    s.table[static_cast<int64_t>(to[i]) * s.max_blocks + length[i] / kPage] = page;
     s.refs[page] = 1;
     list.dst[i] = page;
   });
 }
 
 // Where the pages in use go: of n in use those from page n on, in their order, to
-// the free ones below, in theirs.  head: {n, how many move}; number[page]: which
+// the free ones below, in theirs.  head: {n, how many move, a counter}; number[page]: which
 // of the list a page from n on is, -1 for one that is not in use.
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 compact_plan_kernel(const int32_t *__restrict__ refs, int num_blocks, int32_t *head, int32_t *n_live,
@@ -368,6 +407,7 @@ compact_plan_kernel(const int32_t *__restrict__ refs, int num_blocks, int32_t *h
   if (rank == 0 && threadIdx.x == 0) {
     head[0] = n;
     head[1] = n - kept;
+    head[2] = head[3] = 0;                 // items taken so far
     *n_live = n;
   }
   const int warp_end = scan.end();
@@ -398,6 +438,7 @@ compact_plan_kernel(const int32_t *__restrict__ refs, int num_blocks, int32_t *h
 constexpr int kCopyThreads = 256;
 constexpr int kChunk = 36864;        // of a page at a time: 9 words of 16 bytes a thread
 constexpr int kLoads = kChunk / (16 * kCopyThreads);
+constexpr int kMostCtas = 8192;
 constexpr int kSmall = 1024;         // pages below this, or of no whole 16-byte words, by 4-byte words together
 
 struct Pools {
@@ -411,93 +452,116 @@ static_assert(sizeof(Pools) <= 3900, "kernel arguments");
 enum CopyMode { kListed = 0, kForks = 1, kCompaction = 2 };
 
 struct CopyArgs {
-  const int32_t *src, *dst, *rows, *head, *number;
-  int n;
+  const int32_t *src, *dst, *rows;
+  int32_t *head;
+  const int32_t *number;
+  int n, few;                        // few: chunks below which they are cut
   Seqs s;
 };
 
-template <int L>
-__device__ __forceinline__ void move(uint8_t *to, const uint8_t *from, uint32_t bytes) {
-  uint4 v[L];
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const uint32_t at = (i * kCopyThreads + threadIdx.x) * 16;
-    if (at < bytes) v[i] = __ldcs(reinterpret_cast<const uint4 *>(from + at));
-  }
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const uint32_t at = (i * kCopyThreads + threadIdx.x) * 16;
-    if (at < bytes) __stcs(reinterpret_cast<uint4 *>(to + at), v[i]);
-  }
-}
-
 // Items are a chunk (or a third, or a ninth of one) of a pair of pages in one
-// pool; a CTA takes a run of them, so that what is looked up for a pair is
-// looked up once.
+// pool.  A CTA takes a run of them: one, up to kMostCtas items (500 pages of 12
+// e4m3 layers, 442 MB, in 6000 CTAs 69 us; in 608 that stay, four to an SM, 76: some
+// SMs are slower, and the last ones' runs are what is waited for).  Of a compaction
+// only the device knows how many there are: 608 CTAs take them from a counter (48
+// requests, 280 MB in 4 layers, with two resizes around it: 58.7 us, in runs 63.4,
+// in 4096 CTAs 57.2, but then one that moves nothing 9.3 in place of 5.2).  A pair's
+// ids are looked at while the first item's loads are on their way.
 template <int MODE, int L>
 __device__ __forceinline__ void copy_items(const CopyArgs &a, const Pools &p, int pairs) {
   constexpr int kParts = kLoads / L;
   const int per_pair = p.chunks * kParts + (p.n > p.large ? 1 : 0);
   const int64_t items = static_cast<int64_t>(pairs) * per_pair;
-  const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  int64_t item = MODE == kCompaction ? blockIdx.x : items * blockIdx.x / gridDim.x;
+  const int64_t end_item = MODE == kCompaction ? items : items * (blockIdx.x + 1) / gridDim.x;
+  __shared__ int64_t next;
+  int64_t ahead = 0;
   int pair = -1, s = -1, d = -1, rows = kPage;
-  for (int64_t item = i0; item < i1; ++item) {
+  auto page = [&](int id) { return id >= 0 && id < a.s.num_blocks; };
+  auto advance = [&] {
+    if constexpr (MODE == kCompaction) {
+      if (threadIdx.x == 0) next = ahead;
+      __syncthreads();
+      item = next;
+      __syncthreads();
+    } else {
+      ++item;
+    }
+  };
+  for (; item < end_item; advance()) {
+    if (MODE == kCompaction && threadIdx.x == 0)
+      ahead = gridDim.x + static_cast<int64_t>(atomicAdd(reinterpret_cast<unsigned long long *>(a.head + 2), 1ull));
     const int now = static_cast<int>(item / per_pair), part = static_cast<int>(item - static_cast<int64_t>(now) * per_pair);
-    if (now != pair) {
+    const bool other = now != pair;
+    if (other) {
       pair = now;
       s = a.src[pair];
       d = a.dst[pair];
       if constexpr (MODE == kForks) rows = a.rows[pair];
-      auto page = [&](int id) { return id >= 0 && id < a.s.num_blocks; };
-      if constexpr (MODE == kListed) {
-        // of equal destinations the last one's source stays; a destination that is
-        // another pair's source is refused: which of the two came first is not defined
-        bool later = false, read = false;
-        if (page(s) && page(d) && s != d) {
-          for (int k = threadIdx.x; k < a.n; k += kCopyThreads) {
-            const int sk = __ldg(a.src + k), dk = __ldg(a.dst + k);
-            if (!page(sk) || !page(dk) || sk == dk) continue;
-            later |= dk == d && k > pair;
-            read |= sk == d;
-          }
-        } else if (threadIdx.x == 0 && (s >= a.s.num_blocks || d >= a.s.num_blocks)) {
-          raise_error(a.s.err, MLA_DEVERR_BLOCK_ID);
-        }
-        read = __syncthreads_or(read);
-        if (read && threadIdx.x == 0) raise_error(a.s.err, MLA_DEVERR_PAGES);
-        if (__syncthreads_or(later) || read) d = -1;
-      }
+      if (MODE == kListed && threadIdx.x == 0 && (s >= a.s.num_blocks || d >= a.s.num_blocks))
+        raise_error(a.s.err, MLA_DEVERR_BLOCK_ID);
       if (!page(s) || !page(d) || s == d) d = -1;
     }
     if (d < 0) continue;
-    if (part == p.chunks * kParts) {
+    const bool small = part == p.chunks * kParts;
+    uint4 v[L];
+    uint8_t *to = nullptr;
+    uint32_t bytes = 0;
+    if (!small) {
+      const int chunk = part / kParts, third = part - chunk * kParts;
+      int k;
+      if (p.same) {
+        k = chunk / p.same;
+      } else {
+        int lo = 0, hi = p.large - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (p.first[mid] <= static_cast<uint32_t>(chunk)) lo = mid;
+          else hi = mid - 1;
+        }
+        k = lo;
+      }
+      const uint32_t size = p.bytes[k], at = (chunk - p.first[k]) * kChunk + third * (L * 16 * kCopyThreads);
+      const uint32_t end = MODE == kForks && size % (16 * kPage) == 0 ? size / kPage * rows : size;
+      if (at < end) bytes = end - at;
+      const uint8_t *from = static_cast<const uint8_t *>(p.at[k]) + static_cast<int64_t>(s) * size + at;
+      to = static_cast<uint8_t *>(p.at[k]) + static_cast<int64_t>(d) * size + at;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const uint32_t w = (i * kCopyThreads + threadIdx.x) * 16;
+        if (w < bytes) v[i] = __ldcs(reinterpret_cast<const uint4 *>(from + w));
+      }
+    }
+    if (MODE == kListed && other) {
+      // of equal destinations the last one's source stays; a destination that is
+      // another pair's source is refused: which of the two came first is not defined
+      bool later = false, read = false;
+      for (int k = threadIdx.x; k < a.n; k += kCopyThreads) {
+        const int sk = __ldg(a.src + k), dk = __ldg(a.dst + k);
+        if (!page(sk) || !page(dk) || sk == dk) continue;
+        later |= dk == d && k > pair;
+        read |= sk == d;
+      }
+      read = __syncthreads_or(read);
+      if (read && threadIdx.x == 0) raise_error(a.s.err, MLA_DEVERR_PAGES);
+      if (__syncthreads_or(later) || read) d = -1;
+      if (d < 0) continue;
+    }
+    if (small) {
       // the small pools, 16 threads to a page
       for (int k = p.large + threadIdx.x / 16; k < p.n; k += kCopyThreads / 16) {
         const uint32_t words = p.bytes[k] / 4;
-        const uint32_t *from = static_cast<const uint32_t *>(p.at[k]) + static_cast<int64_t>(s) * words;
-        uint32_t *to = static_cast<uint32_t *>(p.at[k]) + static_cast<int64_t>(d) * words;
-        for (uint32_t w = threadIdx.x % 16; w < words; w += 16) to[w] = from[w];
+        const uint32_t *f = static_cast<const uint32_t *>(p.at[k]) + static_cast<int64_t>(s) * words;
+        uint32_t *t = static_cast<uint32_t *>(p.at[k]) + static_cast<int64_t>(d) * words;
+        for (uint32_t w = threadIdx.x % 16; w < words; w += 16) t[w] = f[w];
       }
       continue;
     }
-    const int chunk = part / kParts, third = part - chunk * kParts;
-    int k;
-    if (p.same) {
-      k = chunk / p.same;
-    } else {
-      int lo = 0, hi = p.large - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.first[mid] <= static_cast<uint32_t>(chunk)) lo = mid;
-        else hi = mid - 1;
-      }
-      k = lo;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const uint32_t w = (i * kCopyThreads + threadIdx.x) * 16;
+      if (w < bytes) __stcs(reinterpret_cast<uint4 *>(to + w), v[i]);
     }
-    const uint32_t bytes = p.bytes[k], at = (chunk - p.first[k]) * kChunk + third * (L * 16 * kCopyThreads);
-    const uint32_t end = MODE == kForks && bytes % (16 * kPage) == 0 ? bytes / kPage * rows : bytes;
-    if (at >= end) continue;
-    uint8_t *pool = static_cast<uint8_t *>(p.at[k]);
-    move<L>(pool + static_cast<int64_t>(d) * bytes + at, pool + static_cast<int64_t>(s) * bytes + at, end - at);
   }
 }
 
@@ -530,10 +594,10 @@ copy_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ Pools p)
       }
     }
   }
-  // (as large a piece as leaves every CTA some)
+  // (as large a piece as leaves every SM some)
   const int64_t chunks = static_cast<int64_t>(pairs) * p.chunks;
-  if (chunks >= gridDim.x / 2) copy_items<MODE, kLoads>(a, p, pairs);
-  else if (chunks * 3 >= gridDim.x / 2) copy_items<MODE, kLoads / 3>(a, p, pairs);
+  if (chunks >= a.few) copy_items<MODE, kLoads>(a, p, pairs);
+  else if (chunks * 3 >= a.few) copy_items<MODE, kLoads / 3>(a, p, pairs);
   else copy_items<MODE, 1>(a, p, pairs);
 }
 
@@ -566,11 +630,16 @@ int gather_pools(void *const *pools, const int64_t *page_bytes, int n, Pools &p)
   return MLA_OK;
 }
 
+// most: pairs that there may be
 template <int MODE>
-int launch_copy(const CopyArgs &a, const Pools &p, mla_stream_t stream) {
+int launch_copy(CopyArgs &a, const Pools &p, int64_t most, mla_stream_t stream) {
   const int sms = device_sm_count();
   if (sms == 0) return MLA_ERR_CUDA;
-  return launch_pdl(copy_kernel<MODE>, dim3(4 * sms), dim3(kCopyThreads), 0, stream, a, p) == cudaSuccess
+  a.few = 2 * sms;
+  const int64_t chunks = most * p.chunks, cut = chunks >= a.few ? 1 : chunks * 3 >= a.few ? 3 : 9;
+  const int64_t items = chunks * cut + (p.n > p.large ? most : 0);
+  const int ctas = MODE == kCompaction ? 4 * sms : static_cast<int>(std::clamp<int64_t>(items, 1, kMostCtas));
+  return launch_pdl(copy_kernel<MODE>, dim3(ctas), dim3(kCopyThreads), 0, stream, a, p) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }
@@ -812,7 +881,7 @@ extern "C" int mla_cache_copy(void *const *pools, const int64_t *page_bytes, int
   a.s.num_blocks = num_blocks;
   a.s.err = device_error_word();
   if (!a.s.err) return MLA_ERR_CUDA;
-  return launch_copy<kListed>(a, p, stream);
+  return launch_copy<kListed>(a, p, n, stream);
 }
 
 extern "C" int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_table, int32_t *seq_lens,
@@ -823,7 +892,7 @@ extern "C" int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_ta
   if (!new_lens) return MLA_ERR_INVALID_ARG;
   s.err = device_error_word();
   if (!s.err) return MLA_ERR_CUDA;
-  const size_t smem = 3 * sizeof(int) * B;
+  const size_t smem = 4 * sizeof(int) * B;
   if (!allow_smem(resize_kernel, smem)) return MLA_ERR_CUDA;
   return launch_pdl(resize_kernel, dim3(kCtas), dim3(kThreads), smem, stream, s, new_lens) == cudaSuccess
              ? MLA_OK
@@ -855,7 +924,7 @@ extern "C" int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int
   if (!s.err) return MLA_ERR_CUDA;
   int32_t *ws = static_cast<int32_t *>(workspace);
   const List list{ws, ws + n, ws + 2 * n};
-  const size_t smem = sizeof(int) * (static_cast<size_t>(B) + n);
+  const size_t smem = sizeof(int) * (static_cast<size_t>(B) + 4 * n);
   if (!allow_smem(fork_kernel, smem)) return MLA_ERR_CUDA;
   if (launch_pdl(fork_kernel, dim3(kCtas), dim3(kThreads), smem, stream, s, parents, children, n, list) !=
       cudaSuccess)
@@ -867,7 +936,7 @@ extern "C" int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int
   a.rows = list.rows;
   a.n = n;
   a.s = s;
-  return launch_copy<kForks>(a, p, stream);
+  return launch_copy<kForks>(a, p, n, stream);
 }
 
 extern "C" int mla_cache_compact_workspace_size(int num_blocks, size_t *bytes) {
@@ -885,7 +954,7 @@ extern "C" int mla_cache_compact(void *const *pools, const int64_t *page_bytes, 
   if (st != MLA_OK) return st;
   Pools p;
   if ((st = gather_pools(pools, page_bytes, n_pools, p)) != MLA_OK) return st;
-  if (!n_live || (reinterpret_cast<uintptr_t>(workspace) & 3u)) return MLA_ERR_INVALID_ARG;
+  if (!n_live || (reinterpret_cast<uintptr_t>(workspace) & 7u)) return MLA_ERR_INVALID_ARG;
   size_t need = 0;
   mla_cache_compact_workspace_size(num_blocks, &need);
   if (!workspace || ws_bytes < need) return MLA_ERR_WORKSPACE;
@@ -902,7 +971,7 @@ extern "C" int mla_cache_compact(void *const *pools, const int64_t *page_bytes, 
   a.head = head;
   a.number = number;
   a.s = s;
-  return launch_copy<kCompaction>(a, p, stream);
+  return launch_copy<kCompaction>(a, p, num_blocks / 2, stream);
 }
 
 extern "C" int mla_cache_accept(void *const *pools, int kv_dtype, float *const *kv_scales, int scale_block,
