@@ -740,7 +740,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         // this CTA's key rows: a page of the two, or half of the one
         const int blk = block_at(pg, job, sg.b, F::kPages * (sg.tile0 + t) + (F::kPages - 1) * rank);
         const int row = blk < 0 ? no_row : blk * kPage + (2 - F::kPages) * F::kKRows * rank;
-#pragma unroll 1
+#pragma unroll
         for (int part = 0; part < F::kKParts; ++part) {
           const int s = kc % F::kKSlots;
           if (kc >= F::kKSlots &&
@@ -1458,7 +1458,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 // 26.6 / 19.8 / 26.5, 8 requests (9) 22.5 / 22.8 / 34.1.
 constexpr int kMergeWarps = 8;
 
-template <typename T, int SPLIT>
+template <typename T, int SPLIT, bool TREE>
 __global__ void __launch_bounds__(kMergeWarps * 32, SPLIT == 8 ? 1 : SPLIT == 4 ? 2 : 4)
 window_merge_kernel(const __grid_constant__ WindowArgs a) {
   constexpr int kRows = kMergeWarps / SPLIT;    // rows of this CTA
@@ -1473,8 +1473,7 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % SPLIT;
   const int j = blockIdx.x;
   int rg, b;
-  if (a.tree_mask) who<true>(j, a, rg, b);
-  else who<false>(j, a, rg, b);
+  who<TREE>(j, a, rg, b);
   const int rr = blockIdx.y * kRows + warp / SPLIT;
   const int R = a.q_len * a.H;
   const bool row_ok = rg * 128 + rr < R;
@@ -1484,8 +1483,7 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   const int group = j / a.group_jobs;
   const int C = a.ws_head[group], first = a.ws_head[a.groups + 2 * j], end = a.ws_head[a.groups + 2 * j + 1];
   const int len = length_of(b, a, false);
-  if (a.tree_mask ? len == 0 || rg * 128 / a.H >= nodes_of(b, a, false)
-                  : job_of<false>(rg, len, a).pages == 0) {   // (the words above hold nothing)
+  if (job_of<TREE>(rg, len, a).pages == 0 || (TREE && rg * 128 / a.H >= nodes_of(b, a, false))) {   // (the words above hold nothing)
     if (mine == 0 && row_ok) {
       const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       for (int k = 0; k < 2; ++k) store8(out + 8 * (lane + 32 * k), zero);
@@ -1589,19 +1587,19 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   if (mine == 0 && lane == 0) a.lse[row] = z == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + logf(z);
 }
 
-template <typename T, int SPLIT>
+template <typename T, int SPLIT, bool TREE>
 cudaError_t launch_merge(const WindowArgs &a, mla_stream_t stream) {
   constexpr int kRows = kMergeWarps / SPLIT;
   const int rows = std::min(128, a.q_len * a.H);
-  return launch_pdl(window_merge_kernel<T, SPLIT>, dim3(a.B * a.RG, (rows + kRows - 1) / kRows),
+  return launch_pdl(window_merge_kernel<T, SPLIT, TREE>, dim3(a.B * a.RG, (rows + kRows - 1) / kRows),
                     dim3(kMergeWarps * 32), 0, stream, a);
 }
 
-template <typename T>
+template <typename T, bool TREE>
 cudaError_t merge(int64_t parts, const WindowArgs &a, mla_stream_t stream) {
-  return parts > 40   ? launch_merge<T, 8>(a, stream)
-         : parts > 10 ? launch_merge<T, 4>(a, stream)
-                      : launch_merge<T, 1>(a, stream);
+  return parts > 40   ? launch_merge<T, 8, TREE>(a, stream)
+         : parts > 10 ? launch_merge<T, 4, TREE>(a, stream)
+                      : launch_merge<T, 1, TREE>(a, stream);
 }
 
 // ------------------------------------------------------------------- host
@@ -1844,7 +1842,10 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   const int st = launch(q, kv_cache, n, a, stream);
   if (st != MLA_OK || w.solo) return st;
   const int64_t parts = pairs / jobs;   // of a job, about
-  const cudaError_t e = a.out_f32 ? merge<float>(parts, a, stream) : merge<__nv_bfloat16>(parts, a, stream);
+  auto join = tree.mask ? a.out_f32 ? merge<float, true> : merge<__nv_bfloat16, true>
+              : a.out_f32 ? merge<float, false>
+                          : merge<__nv_bfloat16, false>;
+  const cudaError_t e = join(parts, a, stream);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
