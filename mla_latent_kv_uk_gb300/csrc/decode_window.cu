@@ -564,7 +564,11 @@ __device__ __noinline__ float far_sum(uint32_t scores, uint64_t seen, float4 c, 
   return sum;
 }
 
-template <bool FP8, bool TREE, bool WIDE>
+// SCALES: of a thread's 64 keys of a tile.  Trees over an e4m3 cache with one scale for
+// all or one for 64 tokens have one where the others have room for four, so that a
+// thread has one unit, maximum and sum for its keys (the same 64 tokens: 168 us in place
+// of 172, 8 uneven trees over up to 8192 keys 41.3, 42.5).
+template <bool FP8, bool TREE, bool WIDE, int SCALES>
 __global__ void __launch_bounds__(kThreads, 1)
 window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
@@ -973,6 +977,11 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       v = fmaxf(v, x_max[64 * (half ^ 1) + r]);
       return !told;
     };
+    // A tree's reference goes down only so far that the tile's largest p' is 2^-5, still
+    // above kLow: the next tile's may be 2^13 times as large before it has to go up again
+    // (64 tokens over 16384 keys whose blocks' scales differ by up to 2^4: 163 us, down to
+    // where it is 1, as without a tree, 170)
+    constexpr float kBack = TREE ? 5.f : 0.f;
     auto all_ok = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
     Seg sg;
     int uc = 0, segs = 0;                               // tiles and segments (with tiles) so far
@@ -1018,7 +1027,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (!FP8 || !args.scales || t >= sg.ntiles || e >= job.pages) return -1;
         return __ldg(bt + job.page(e));   // (looked at a tile later: nothing waits for it here)
       };
-      constexpr int kBlocks = FP8 ? 4 : 1;   // scales of 64 keys
+      constexpr int kBlocks = SCALES;
       auto load_scales = [&](int blk, float *sc) {
 #pragma unroll
         for (int g = 0; g < kBlocks; ++g)
@@ -1062,7 +1071,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           }
           return low_bits(p - key0 + 1) & (~low_bits(wlo - key0) | low_bits(args.sinks - key0));
         };
-        constexpr int kRun = F::kMine / kBlocks;        // keys of one scale: 16 / 32
+        constexpr int kRun = F::kMine / kBlocks;        // keys of one scale
         float c[kBlocks], lg[kBlocks];
 #pragma unroll
         for (int g = 0; g < kBlocks; ++g) {
@@ -1093,7 +1102,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           if constexpr (FP8) {                          // (NaN is for rows that see a key of the block)
 #pragma unroll
             for (int g = 0; g < kBlocks; ++g)
-              if (!(seen >> (kRun * g) & 0xFFFFu)) lg[g] = 0.f;
+              if (!(seen >> (kRun * g) & low_bits(kRun))) lg[g] = 0.f;
           }
         }
         float top = -INFINITY, raw[kBlocks];            // largest s + log2 sigma; of a block's scores
@@ -1129,7 +1138,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const bool moves = __any_sync(0xffffffffu, top - F::kLazy > old || down);
         const bool up = moves && top - F::kTop > old, move = up || down;
         float now = up ? top - F::kTop : old;
-        if (down) now = fmaxf(top, fmaxf(highest, old) - F::kDepth);
+        if (down) now = fmaxf(top + kBack, fmaxf(highest, old) - F::kDepth);
         if (half == 0) x_ref[64 * group + r] = now;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ref_there[2 * group + block]);
@@ -1214,8 +1223,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         };
         if constexpr (FP8) {
           if (again)
-            rest = far_sum(s_at, masked ? seen_keys() : ~uint64_t(0), make_float4(c[0], c[1], c[2], c[3]),
-                           make_float4(lg[0], lg[1], lg[2], lg[3]), base, next_unit());
+            rest = far_sum(s_at, masked ? seen_keys() : ~uint64_t(0),
+                           make_float4(c[0], c[kBlocks / 4], c[kBlocks / 2], c[kBlocks - 1]),
+                           make_float4(lg[0], lg[kBlocks / 4], lg[kBlocks / 2], lg[kBlocks - 1]), base, next_unit());
+          static_assert(kBlocks == 1 || kBlocks == 4, "runs of 64 or 16 keys");
         }
         if (rescale) {
           // O follows the reference, now that the last P V is done
@@ -1227,9 +1238,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             tmem_ld_x64(lane_base + kColO + q, o);
 #pragma unroll
             for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st_x32(lane_base + kColO + q, o);
-            tmem_st_x32(lane_base + kColO + q + 32, o + 32);
+            tmem_st_x32_async(lane_base + kColO + q, o);
+            tmem_st_x32_async(lane_base + kColO + q + 32, o + 32);
           }
+          tmem_wait_st();
         }
         // the values are here (the MMA thread goes by this CTA's word)
         if constexpr (WIDE) {
@@ -1641,12 +1653,13 @@ int pairs_for_device() {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
   auto at = [](auto *kernel) { return reinterpret_cast<const void *>(kernel); };
-  if (!allow(at(window_kernel<false, false, false>), Fmt<false>::kSmem) ||
-      !allow(at(window_kernel<true, false, false>), Fmt<true>::kSmem) ||
-      !allow(at(window_kernel<false, true, false>), Fmt<false>::kSmem) ||
-      !allow(at(window_kernel<false, true, true>), Fmt<false, true>::kSmem) ||
-      !allow(at(window_kernel<true, true, false>), Fmt<true>::kSmem) ||
-      cudaOccupancyMaxActiveClusters(&n, window_kernel<false, false, false>, &pl.cfg) != cudaSuccess) {
+  if (!allow(at(window_kernel<false, false, false, 1>), Fmt<false>::kSmem) ||
+      !allow(at(window_kernel<true, false, false, 4>), Fmt<true>::kSmem) ||
+      !allow(at(window_kernel<false, true, false, 1>), Fmt<false>::kSmem) ||
+      !allow(at(window_kernel<false, true, true, 1>), Fmt<false, true>::kSmem) ||
+      !allow(at(window_kernel<true, true, false, 1>), Fmt<true>::kSmem) ||
+      !allow(at(window_kernel<true, true, false, 4>), Fmt<true>::kSmem) ||
+      cudaOccupancyMaxActiveClusters(&n, window_kernel<false, false, false, 1>, &pl.cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -1737,7 +1750,7 @@ int check_window(const void *q, int q_dtype, float q_scale, const void *kv_cache
   return MLA_OK;
 }
 
-template <bool FP8, bool TREE, bool WIDE>
+template <bool FP8, bool TREE, bool WIDE, int SCALES>
 int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArgs &a,
                  mla_stream_t stream) {
   using F = Fmt<FP8, WIDE>;
@@ -1767,7 +1780,7 @@ int launch_pairs(const void *q, const void *kv_cache, int pairs, const WindowArg
   }
   if (!ok) return MLA_ERR_CUDA;
   PairLaunch<FP8, WIDE> pl(pairs, stream);
-  return cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8, TREE, WIDE>, tk, tkr, tv, tq, tqr, a) == cudaSuccess
+  return cudaLaunchKernelEx(&pl.cfg, window_kernel<FP8, TREE, WIDE, SCALES>, tk, tkr, tv, tq, tqr, a) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }
@@ -1835,10 +1848,11 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   // 196, 214; 64 of 4 over up to 2000 (107) 91.5, 93.1; but 32 of 8 over 500 (29) 61.7, 60.4; 4
   // of 8 with 16 heads over 4000 (3) 19.0, 17.8
   const bool wide = tree.mask && !fp8 && jobs * max_blocks >= static_cast<int64_t>(kWidePages) * pairs;
-  auto launch = fp8 ? tree.mask ? launch_pairs<true, true, false> : launch_pairs<true, false, false>
-                : !tree.mask ? launch_pairs<false, false, false>
-                : wide       ? launch_pairs<false, true, true>
-                             : launch_pairs<false, true, false>;
+  const bool one_scale = !scales || sb_shift == 6;
+  auto launch = !tree.mask ? fp8 ? launch_pairs<true, false, false, 4> : launch_pairs<false, false, false, 1>
+                : fp8      ? one_scale ? launch_pairs<true, true, false, 1> : launch_pairs<true, true, false, 4>
+                : wide     ? launch_pairs<false, true, true, 1>
+                           : launch_pairs<false, true, false, 1>;
   const int st = launch(q, kv_cache, n, a, stream);
   if (st != MLA_OK || w.solo) return st;
   const int64_t parts = pairs / jobs;   // of a job, about
