@@ -501,6 +501,10 @@ int mla_decode_paged_tree(const void *q, int q_dtype, float q_scale,
  * order; calls on the same state follow one another on a stream.  Free pages
  * are taken lowest first, so the result depends on the state alone.
  *
+ * A page that several entries hold is not to be written: a sequence that was
+ * shortened to end inside one is continued by a fork of it, which has a last page
+ * of its own.
+ *
  * Pools are what a page has in memory: for every layer its cache [num_blocks,
  * 64,576], its block scales, or anything else of num_blocks rows.  pools and
  * page_bytes are HOST arrays of n_pools (0 to 200) device pointers and of a
@@ -534,8 +538,9 @@ int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_table,
 
 /* Fork: for i < n (at most 8192) sequence children[i], of length 0, becomes the
  * tokens of parents[i]: full pages are shared (refs + 1), of a last page that
- * is not full the rows with tokens are copied, in every pool, into a free page
- * (a pool whose page is no multiple of 1024 bytes, such as scales: the page).
+ * is not full the tokens are copied, in every pool, into a free page: of the
+ * first n_by_rows pools, whose pages are 64 rows of equal size (of 4-byte words),
+ * their rows; of the others (scales) the page.
  * Parents are as they were before the call.  Left out, with MLA_DEVERR_PAGES:
  * a child that has tokens or came up before, and from where free pages run
  * out on every fork that needs one; a row outside [0, B): MLA_DEVERR_RANGE; a
@@ -545,8 +550,8 @@ int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_table,
 int mla_cache_fork_workspace_size(int n, size_t *bytes);
 
 int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int n_pools,
-                   int32_t *refs, int num_blocks, int32_t *block_table,
-                   int32_t *seq_lens, int B, int max_blocks,
+                   int n_by_rows, int32_t *refs, int num_blocks,
+                   int32_t *block_table, int32_t *seq_lens, int B, int max_blocks,
                    const int32_t *parents, const int32_t *children, int n,
                    void *workspace, size_t ws_bytes, mla_stream_t stream);
 

@@ -77,7 +77,7 @@ _SIGNATURES = {
     "mla_cache_copy": ([_p, _p, _i, _i, _p, _p, _i, _p], _i),
     "mla_cache_resize": ([_p, _i, _p, _p, _p, _i, _i, _p], _i),
     "mla_cache_fork_workspace_size": ([_i, ctypes.POINTER(_sz)], _i),
-    "mla_cache_fork": ([_p, _p, _i, _p, _i, _p, _p, _i, _i, _p, _p, _i, _p, _sz, _p], _i),
+    "mla_cache_fork": ([_p, _p, _i, _i, _p, _i, _p, _p, _i, _i, _p, _p, _i, _p, _sz, _p], _i),
     "mla_cache_compact_workspace_size": ([_i, ctypes.POINTER(_sz)], _i),
     "mla_cache_compact": ([_p, _p, _i, _p, _i, _p, _p, _i, _i, _p, _p, _sz, _p], _i),
     "mla_cache_accept": ([_p, _i, _p, _i, _i, _i, _p, _p, _p, _i, _p, _i, _p, _i, _i, _p, _p], _i),
@@ -512,7 +512,8 @@ def mla_cache_resize(refs, block_table, seq_lens, new_lens):
 
 def mla_cache_fork(pools, refs, block_table, seq_lens, parents, children, *, workspace=None):
     """The empty sequences children [n] go on from the sequences parents [n]
-    (int32): full pages are shared, a last one is copied in every pool."""
+    (int32): full pages are shared, of a last one the tokens are copied in every
+    pool: rows of the pools [num_blocks, 64, ...], whole pages of the others."""
     _binding.fork(pools, refs, block_table, seq_lens, parents, children, workspace)
 
 

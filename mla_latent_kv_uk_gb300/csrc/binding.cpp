@@ -388,7 +388,24 @@ struct Pools {
   static constexpr int kMost = 200;
   void *at[kMost];
   int64_t bytes[kMost];         // of a page
+  bool rows[kMost];             // a row for each of its 64 tokens
   int n = 0;
+  // Those by rows first; returns how many they are.
+  int rows_first() {
+    void *a[kMost];
+    int64_t b[kMost];
+    int k = 0, by_rows = 0;
+    for (int pass = 0; pass < 2; ++pass)
+      for (int i = 0; i < n; ++i)
+        if (rows[i] == (pass == 0)) {
+          a[k] = at[i];
+          b[k++] = bytes[i];
+          by_rows += pass == 0;
+        }
+    memcpy(at, a, sizeof(void *) * n);
+    memcpy(bytes, b, sizeof(int64_t) * n);
+    return by_rows;
+  }
 };
 // A list or tuple of contiguous tensors of `blocks` pages (-1: as many as the first has; set), or
 // one such tensor.  type: their dtype, if it has to be one
@@ -411,6 +428,7 @@ void pools_of(PyObject *o, const char *name, int64_t &blocks, int dev, Pools &p,
     if (blocks < 0) blocks = t.size(0);
     if (t.size(0) != blocks) refuse(PyExc_ValueError, "%s differ in their number of pages", name);
     p.at[p.n] = t.data_ptr();
+    p.rows[p.n] = t.dim() > 1 && t.size(1) == 64;
     p.bytes[p.n++] = t.numel() / blocks * static_cast<int64_t>(t.element_size());
   }
 }
@@ -486,6 +504,7 @@ PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Pools p;
     int64_t pages = s.pages;
     pools_of(a[0], "pools", pages, dev, p);
+    const int by_rows = p.rows_first();
     const int forks = narrow(from.size(0), "parents");
     size_t bytes = 0;
     call("mla_cache_fork", [&] { return entries.fork_size(forks, &bytes); });
@@ -493,7 +512,7 @@ PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                           : scratch(static_cast<int64_t>(bytes), dev);
     const cudaStream_t stream = stream_of(dev);
     call("mla_cache_fork", [&] {
-      return entries.fork(p.at, p.bytes, p.n, s.refs, s.blocks, s.table, s.lens, s.B, s.max_blocks,
+      return entries.fork(p.at, p.bytes, p.n, by_rows, s.refs, s.blocks, s.table, s.lens, s.B, s.max_blocks,
                           at_<int32_t>(from), at_<int32_t>(to), forks, ws.data_ptr(),
                           static_cast<size_t>(ws.numel()), stream);
     });

@@ -9,7 +9,7 @@
 // lowest free pages, so what comes out depends on the state alone.
 //
 // Bookkeeping runs in one cluster of 8 CTAs: every CTA works out the calls'
-// rows for itself (a prefix sum over them in shared memory), the cluster's 256
+// rows for itself (a prefix sum over them in shared memory), the cluster's
 // warps count the free pages of a run of refs each, the CTAs' counts cross
 // through distributed shared memory, and each free page then finds the row that
 // it goes to by the number of free pages in front of it.  Two cluster barriers
@@ -32,7 +32,16 @@ namespace {
 
 constexpr int kMaxPools = 200;       // (their addresses and sizes are kernel arguments, of 4 KB at most)
 constexpr int kMaxRows = 8192;       // sequences of a call, and forks: 5 words of shared memory for both
-constexpr int kCtas = 8, kThreads = 1024, kWarps = kThreads / 32, kAllWarps = kCtas * kWarps;
+constexpr int kCtas = 8, kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
+static_assert(kMaxWarps <= 32 && kCtas <= 32, "a lane each");
+
+// Threads of a CTA: few where there is little to count (64 forks of 8 sequences in a
+// pool of 1500 pages, with the free in front of it, 256 / 512 / 1024 threads: 10.0 / 10.8 /
+// 11.6 us; a resize in one of 60000 pages 5.2 / 5.1 / 5.4, of 500000 20.3 / 11.7 / 8.3).
+int threads_for(int num_blocks, int rows) {
+  return num_blocks <= (1 << 14) && rows <= 512 ? 256 : num_blocks <= (1 << 17) && rows <= 1024 ? 512 : kMaxThreads;
+}
+__device__ __forceinline__ int warps_of() { return blockDim.x >> 5; }
 
 __device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
 
@@ -48,12 +57,12 @@ __device__ __forceinline__ int warp_incl(int x) {
 
 // Sum over the CTA's threads in front of this one; total: over all of them.
 __device__ __forceinline__ int block_excl(int x, int &total) {
-  __shared__ int sums[kWarps];
+  __shared__ int sums[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, incl = warp_incl(x);
   __syncthreads();
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  const int of = warp_incl(sums[lane]);
+  const int of = warp_incl(lane < warps_of() ? sums[lane] : 0);
   total = __shfl_sync(0xffffffffu, of, 31);
   const int before = __shfl_sync(0xffffffffu, of, max(warp - 1, 0));
   return incl - x + (warp ? before : 0);
@@ -98,8 +107,9 @@ struct Scan {
   int before, all;
 
   __device__ Scan(const int32_t *r, int n, int rank) : refs(r), num_blocks(n), held(0) {
-    per = ((n + kAllWarps - 1) / kAllWarps + 127) / 128 * 128;
-    first = min(static_cast<int64_t>(rank * kWarps + (threadIdx.x >> 5)) * per, static_cast<int64_t>(n));
+    const int all_warps = kCtas * warps_of();
+    per = ((n + all_warps - 1) / all_warps + 127) / 128 * 128;
+    first = min(static_cast<int64_t>(rank * warps_of() + (threadIdx.x >> 5)) * per, static_cast<int64_t>(n));
   }
   // Four pages' bits at a time (refs is written by other SMs in this launch: read from L2)
   template <typename Is>
@@ -118,7 +128,7 @@ struct Scan {
   // (refs and sums of the cluster's CTAs; the barrier in it orders what they wrote before)
   template <typename Is>
   __device__ void count(Is is, int rank) {
-    __shared__ int of_warp[kWarps], of_cta[kCtas];
+    __shared__ int of_warp[kMaxWarps], of_cta[kCtas];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int n = 0;
     for (int id = first + 4 * lane, r = 0; id < end(); id += 512) {
@@ -135,7 +145,7 @@ struct Scan {
     if (lane == 0) of_warp[warp] = n;
     __syncthreads();
     if (warp == 0) {
-      const int sum = __reduce_add_sync(0xffffffffu, of_warp[lane]);
+      const int sum = __reduce_add_sync(0xffffffffu, lane < warps_of() ? of_warp[lane] : 0);
       if (lane < kCtas)
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(sm100::peer_smem(&of_cta[rank], lane)), "r"(sum)
                      : "memory");
@@ -183,15 +193,15 @@ constexpr int kAtOnce = 4;             // entries of a lane on their way
 struct Share {
   int first, step, lane0, lanes;
   __device__ Share(int rows, int wid) {
-    const int per = rows >= kAllWarps ? 1 : 1 << (31 - __clz(kAllWarps / rows));
+    const int all_warps = kCtas * warps_of(), per = rows >= all_warps ? 1 : 1 << (31 - __clz(all_warps / rows));
     first = wid / per;
-    step = kAllWarps / per;
+    step = all_warps / per;
     lane0 = 32 * (wid % per);
     lanes = 32 * per;
   }
 };
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kMaxThreads, 1)
 resize_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ new_lens) {
   extern __shared__ int rows[];
   // pages; needed ones up to and with this row; the new length (-1: it stays as it is)
@@ -200,11 +210,10 @@ resize_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ new_le
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, rank = static_cast<int>(sm100::cluster_rank());
-  const int wid = rank * kWarps + (tid >> 5), most = s.max_blocks * kPage;
-  const int per = (s.B + kThreads - 1) / kThreads, r0 = min(tid * per, s.B), r1 = min(r0 + per, s.B);
+  const int wid = rank * warps_of() + (tid >> 5), most = s.max_blocks * kPage;
+  const int per = (s.B + blockDim.x - 1) / blockDim.x, r0 = min(tid * per, s.B), r1 = min(r0 + per, s.B);
   auto ok = [&](int len) { return len >= 0 && len <= most; };
   int sum = 0;
-  bool drops = false;
   for (int b = r0; b < r1; ++b) {
     const int old = s.lens[b], now = new_lens[b];
     const bool valid = ok(old) && ok(now);
@@ -213,14 +222,14 @@ resize_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ new_le
     had[b] = h;
     want[b] = w;
     goal[b] = valid ? now : -1;
-    drops |= w < h;
     end[b] = sum += max(0, w - h);
   }
   int total;
   const int before = block_excl(sum, total);
   for (int b = r0; b < r1; ++b) end[b] += before;
   cluster_wait();
-  if (__syncthreads_or(drops)) {
+  __syncthreads();
+  {
     const Share share(s.B, wid);
     for (int b = share.first; b < s.B; b += share.step) {
       int32_t *row = s.table + static_cast<int64_t>(b) * s.max_blocks;
@@ -246,8 +255,8 @@ resize_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ new_le
         }
       }
     }
-    cluster_barrier();   // (all CTAs take this branch or none: they have the same rows)
   }
+  cluster_barrier();   // (whether or not there was anything: no CTA goes by what it alone has read)
   Scan scan(s.refs, s.num_blocks, rank);
   if (total == 0) scan.first = s.num_blocks;   // (nothing to count)
   scan.count(is_free, rank);
@@ -272,7 +281,7 @@ struct List {
   int32_t *src, *dst, *rows;
 };
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kMaxThreads, 1)
 fork_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ parents,
             const int32_t *__restrict__ children, int n, const __grid_constant__ List list) {
   extern __shared__ int rows[];
@@ -282,10 +291,10 @@ fork_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ parents,
   sm100::grid_dep_wait();
   sm100::grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, rank = static_cast<int>(sm100::cluster_rank());
-  const int wid = rank * kWarps + (tid >> 5), most = s.max_blocks * kPage;
-  const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+  const int wid = rank * warps_of() + (tid >> 5), most = s.max_blocks * kPage;
+  const int per = (n + blockDim.x - 1) / blockDim.x, i0 = min(tid * per, n), i1 = min(i0 + per, n);
   auto row_ok = [&](int b) { return b >= 0 && b < s.B; };
-  for (int b = tid; b < s.B; b += kThreads) first[b] = INT_MAX;
+  for (int b = tid; b < s.B; b += blockDim.x) first[b] = INT_MAX;
   for (int i = i0; i < i1; ++i) {
     from[i] = parents[i];
     to[i] = children[i];
@@ -373,7 +382,7 @@ fork_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ parents,
 // Where the pages in use go: of n in use those from page n on, in their order, to
 // the free ones below, in theirs.  head: {n, how many move, a counter}; number[page]: which
 // of the list a page from n on is, -1 for one that is not in use.
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kMaxThreads, 1)
 compact_plan_kernel(const int32_t *__restrict__ refs, int num_blocks, int32_t *head, int32_t *n_live,
                     int32_t *src, int32_t *dst, int32_t *number) {
   __shared__ int below;                    // pages in use in front of page n
@@ -439,13 +448,15 @@ constexpr int kCopyThreads = 256;
 constexpr int kChunk = 36864;        // of a page at a time: 9 words of 16 bytes a thread
 constexpr int kLoads = kChunk / (16 * kCopyThreads);
 constexpr int kMostCtas = 8192;
-constexpr int kSmall = 1024;         // pages below this, or of no whole 16-byte words, by 4-byte words together
+constexpr int kSmall = 1024;         // pages below this, or of no whole 16-byte words, go by 4-byte words, together
 
 struct Pools {
   void *at[kMaxPools];
   uint32_t bytes[kMaxPools];         // of a page
   uint32_t first[kMaxPools];         // chunks of the large pools in front of this one
+  uint32_t by_rows[(kMaxPools + 31) / 32];   // a bit each: a page is the rows of its 64 tokens
   int large, n, chunks, same;        // the large ones come first; same: chunks of each, 0 if they differ
+  __device__ bool rows_of(int k) const { return by_rows[k >> 5] >> (k & 31) & 1; }
 };
 static_assert(sizeof(Pools) <= 3900, "kernel arguments");
 
@@ -522,7 +533,7 @@ __device__ __forceinline__ void copy_items(const CopyArgs &a, const Pools &p, in
         k = lo;
       }
       const uint32_t size = p.bytes[k], at = (chunk - p.first[k]) * kChunk + third * (L * 16 * kCopyThreads);
-      const uint32_t end = MODE == kForks && size % (16 * kPage) == 0 ? size / kPage * rows : size;
+      const uint32_t end = MODE == kForks && p.rows_of(k) ? size / kPage * rows : size;
       if (at < end) bytes = end - at;
       const uint8_t *from = static_cast<const uint8_t *>(p.at[k]) + static_cast<int64_t>(s) * size + at;
       to = static_cast<uint8_t *>(p.at[k]) + static_cast<int64_t>(d) * size + at;
@@ -553,7 +564,8 @@ __device__ __forceinline__ void copy_items(const CopyArgs &a, const Pools &p, in
         const uint32_t words = p.bytes[k] / 4;
         const uint32_t *f = static_cast<const uint32_t *>(p.at[k]) + static_cast<int64_t>(s) * words;
         uint32_t *t = static_cast<uint32_t *>(p.at[k]) + static_cast<int64_t>(d) * words;
-        for (uint32_t w = threadIdx.x % 16; w < words; w += 16) t[w] = f[w];
+        const uint32_t end = MODE == kForks && p.rows_of(k) ? words / kPage * rows : words;
+        for (uint32_t w = threadIdx.x % 16; w < end; w += 16) t[w] = f[w];
       }
       continue;
     }
@@ -601,17 +613,21 @@ copy_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ Pools p)
   else copy_items<MODE, 1>(a, p, pairs);
 }
 
-int gather_pools(void *const *pools, const int64_t *page_bytes, int n, Pools &p) {
-  if (n < 0 || n > kMaxPools || (n > 0 && (!pools || !page_bytes))) return MLA_ERR_INVALID_ARG;
+// The first `by_rows` pools are copied by rows where a page is copied in part.
+int gather_pools(void *const *pools, const int64_t *page_bytes, int n, Pools &p, int by_rows = 0) {
+  if (n < 0 || n > kMaxPools || (n > 0 && (!pools || !page_bytes)) || by_rows < 0 || by_rows > n)
+    return MLA_ERR_INVALID_ARG;
   p.n = n;
   p.large = p.chunks = 0;
   p.same = 0;
+  for (uint32_t &w : p.by_rows) w = 0;
   for (int pass = 0, at = 0; pass < 2; ++pass) {
     for (int k = 0; k < n; ++k) {
       const int64_t bytes = page_bytes[k];
       if (!pools[k] || bytes < 4 || bytes % 4 || bytes > (1ll << 28) || (reinterpret_cast<uintptr_t>(pools[k]) & 3u))
         return MLA_ERR_INVALID_ARG;
-      const bool large = bytes >= kSmall && bytes % 16 == 0;
+      if (k < by_rows && bytes % (4 * kPage)) return MLA_ERR_INVALID_ARG;
+      const bool large = bytes >= kSmall && bytes % (k < by_rows ? 16 * kPage : 16) == 0;
       if (large && !aligned16(pools[k])) return MLA_ERR_INVALID_ARG;
       if (large != (pass == 0)) continue;
       p.at[at] = pools[k];
@@ -624,6 +640,7 @@ int gather_pools(void *const *pools, const int64_t *page_bytes, int n, Pools &p)
         p.chunks += c;
         ++p.large;
       }
+      if (k < by_rows) p.by_rows[at >> 5] |= 1u << (at & 31);
       ++at;
     }
   }
@@ -894,7 +911,7 @@ extern "C" int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_ta
   if (!s.err) return MLA_ERR_CUDA;
   const size_t smem = 4 * sizeof(int) * B;
   if (!allow_smem(resize_kernel, smem)) return MLA_ERR_CUDA;
-  return launch_pdl(resize_kernel, dim3(kCtas), dim3(kThreads), smem, stream, s, new_lens) == cudaSuccess
+  return launch_pdl(resize_kernel, dim3(kCtas), dim3(threads_for(num_blocks, B)), smem, stream, s, new_lens) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
 }
@@ -905,8 +922,8 @@ extern "C" int mla_cache_fork_workspace_size(int n, size_t *bytes) {
   return MLA_OK;
 }
 
-extern "C" int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int n_pools, int32_t *refs,
-                              int num_blocks, int32_t *block_table, int32_t *seq_lens, int B, int max_blocks,
+extern "C" int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int n_pools, int n_by_rows,
+                              int32_t *refs, int num_blocks, int32_t *block_table, int32_t *seq_lens, int B, int max_blocks,
                               const int32_t *parents, const int32_t *children, int n, void *workspace,
                               size_t ws_bytes, mla_stream_t stream) {
   Seqs s{refs, num_blocks, block_table, seq_lens, B, max_blocks, nullptr};
@@ -914,7 +931,7 @@ extern "C" int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int
   if (st != MLA_OK) return st;
   if (n < 0 || n > kMaxRows) return MLA_ERR_INVALID_ARG;
   Pools p;
-  if ((st = gather_pools(pools, page_bytes, n_pools, p)) != MLA_OK) return st;
+  if ((st = gather_pools(pools, page_bytes, n_pools, p, n_by_rows)) != MLA_OK) return st;
   if (n == 0) return MLA_OK;
   if (!parents || !children || (reinterpret_cast<uintptr_t>(workspace) & 3u)) return MLA_ERR_INVALID_ARG;
   size_t need = 0;
@@ -926,7 +943,7 @@ extern "C" int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int
   const List list{ws, ws + n, ws + 2 * n};
   const size_t smem = sizeof(int) * (static_cast<size_t>(B) + 4 * n);
   if (!allow_smem(fork_kernel, smem)) return MLA_ERR_CUDA;
-  if (launch_pdl(fork_kernel, dim3(kCtas), dim3(kThreads), smem, stream, s, parents, children, n, list) !=
+  if (launch_pdl(fork_kernel, dim3(kCtas), dim3(threads_for(num_blocks, std::max(B, n))), smem, stream, s, parents, children, n, list) !=
       cudaSuccess)
     return MLA_ERR_CUDA;
   if (n_pools == 0) return MLA_OK;
@@ -962,7 +979,7 @@ extern "C" int mla_cache_compact(void *const *pools, const int64_t *page_bytes, 
   if (!s.err) return MLA_ERR_CUDA;
   int32_t *head = static_cast<int32_t *>(workspace), *src = head + 4, *dst = src + num_blocks / 2 + 1,
           *number = dst + num_blocks / 2 + 1;
-  if (launch_pdl(compact_plan_kernel, dim3(kCtas), dim3(kThreads), 0, stream, static_cast<const int32_t *>(refs),
+  if (launch_pdl(compact_plan_kernel, dim3(kCtas), dim3(threads_for(num_blocks, 0)), 0, stream, static_cast<const int32_t *>(refs),
                  num_blocks, head, n_live, src, dst, number) != cudaSuccess)
     return MLA_ERR_CUDA;
   CopyArgs a{};

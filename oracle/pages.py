@@ -77,9 +77,9 @@ def resize(refs, table, lens, new_lens):
     return errors
 
 
-def fork(pools, refs, table, lens, parents, children):
-    """Rows of a pool's page: those of its second dim, if it has 64 and a page is a multiple of
-    1024 bytes; else the whole page."""
+def fork(pools, refs, table, lens, parents, children, by_rows=None):
+    """by_rows: whether a pool's page is 64 rows (None: all of them are); else the whole page
+    is copied."""
     errors = set()
     B, most = table.shape[0], table.shape[1] * BLOCK
     free, wanted, seen = _free(refs), 0, set()
@@ -120,10 +120,10 @@ def fork(pools, refs, table, lens, parents, children):
             if not 0 <= src < len(refs):
                 errors.add("block")
             else:
-                for pool in pools:
-                    by_rows = pool[0].nbytes % 1024 == 0
-                    flat = pool.reshape(pool.shape[0], BLOCK if by_rows else 1, -1)
-                    flat[dst, :part if by_rows else 1] = flat[src, :part if by_rows else 1]
+                for k, pool in enumerate(pools):
+                    rows = by_rows is None or by_rows[k]
+                    flat = pool.reshape(pool.shape[0], BLOCK if rows else 1, -1)
+                    flat[dst, :part if rows else 1] = flat[src, :part if rows else 1]
         lens[c] = n
     return errors
 

@@ -38,6 +38,8 @@ SHAPES = {
     # pages of 4, 20, 1020, 1024, 1040, 36880 and 81920 bytes
     "odd": [((n,), torch.int32) for n in (1, 5, 255, 256, 260, 9220, 20480)],
     "small": [((2,), torch.float32), ((3,), torch.int32)],
+    # rows of 4, 20, 16, 48 and 1152 bytes, and pages of as many that are no rows
+    "rows": [((64, n), torch.int32) for n in (1, 5, 4, 12, 288)] + [((32, 2 * n), torch.int32) for n in (1, 5, 4)],
 }
 
 
@@ -48,6 +50,7 @@ class State:
         g = self.g = synth.generator(21000 + seed)
         self.pools = [torch.from_numpy(g.integers(0, 256, (nb, int(np.prod(s)) * t.itemsize), dtype=np.uint8))
                       .view(t).view(nb, *s).cuda() for s, t in SHAPES[shapes]]
+        self.by_rows = [s[0] == 64 for s, _ in SHAPES[shapes]]
         self.refs = np.zeros(nb, np.int32)
         self.table = np.full((B, mb), -1, np.int32)
         self.lens = np.zeros(B, np.int32)
@@ -74,7 +77,7 @@ class State:
 
     def fork(self, m, parents, children, **kw):
         m.mla_cache_fork(self.pools, *self.d, _i32(parents), _i32(children), **kw)
-        self.check(m, P.fork(self.bytes, self.refs, self.table, self.lens, parents, children))
+        self.check(m, P.fork(self.bytes, self.refs, self.table, self.lens, parents, children, self.by_rows))
 
     def compact(self, m, **kw):
         live = m.mla_cache_compact(self.pools, *self.d, **kw)
@@ -199,7 +202,7 @@ def test_broken_tables_are_flagged(m):
 
 
 # ------------------------------------------------------------------- fork
-@pytest.mark.parametrize("shapes", ["bf16", "scaled", "odd"])
+@pytest.mark.parametrize("shapes", ["bf16", "scaled", "odd", "rows"])
 def test_fork(m, shapes):
     s = State(shapes, 60, 10, 6, [100, 64, 1, 320, 0, 383], seed=4)
     s.fork(m, [0, 1, 2, 4], [6, 7, 8, 9])              # partial, whole, one token, none
@@ -268,9 +271,9 @@ def test_compact_leaves_what_it_cannot_move(m):
     s.compact(m)
 
 
-@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("seed", range(5))
 def test_any_order_of_calls(m, seed):
-    s = State(["scaled", "bf16", "odd", "small"][seed], 60, 9, 7, seed=50 + seed)
+    s = State(["scaled", "bf16", "odd", "small", "rows"][seed], 60, 9, 7, seed=50 + seed)
     for _ in range(25):
         what = s.g.integers(0, 5)
         if what < 2:
@@ -425,7 +428,7 @@ def test_captured_calls_on_a_stream(m):
             graph.replay()
             stream.synchronize()
             errors = P.resize(s.refs, s.table, s.lens, np.array(want))
-            errors |= P.fork(s.bytes, s.refs, s.table, s.lens, [0, 2], [3, 4])
+            errors |= P.fork(s.bytes, s.refs, s.table, s.lens, [0, 2], [3, 4], s.by_rows)
             n, more = P.compact(s.bytes, s.refs, s.table, s.lens)
             s.check(m, errors | more)
             assert live.tolist() == [n]

@@ -38,9 +38,9 @@ class Case:
     """fmt: bf16, e4m3, or s16 / s32 / s64 (block-scaled).  kind of masks: tree,
     chain, any (random words, some of them 0) or one (a tree for all).  Rows
     that nobody sees hold NaN, their scales NaN; queries behind a tree's last
-    token are NaN; pages behind a sequence have bad ids."""
+    token are NaN; pages behind a sequence, up to `width`, have bad ids."""
 
-    def __init__(self, fmt, lens, q_len, H, kind="tree", tree_lens=None, seed=0):
+    def __init__(self, fmt, lens, q_len, H, kind="tree", tree_lens=None, seed=0, width=0):
         g = synth.generator(12000 + seed)
         self.fmt, self.kind = fmt, kind
         self.lens, B = np.asarray(lens, np.int32), len(lens)
@@ -57,6 +57,8 @@ class Case:
             words = np.stack([tree_words(g, q_len) for _ in range(B)])
         self.words = words
         self.bt, self.nb = synth.paged_layout(g, np.maximum(self.lens, 1))
+        more = max(0, width - self.bt.shape[1])
+        self.bt = np.concatenate([self.bt, np.full((B, more), -1, self.bt.dtype)], axis=1)
         x = g.standard_normal((self.nb, 64, 576), dtype=np.float32)
         x *= np.exp2(g.uniform(-1, 1, (self.nb, 4, 1, 1)).astype(np.float32)).repeat(16, 1).reshape(self.nb, 64, 1)
         q = g.standard_normal((B, q_len, H, 576), dtype=np.float32)
@@ -152,6 +154,43 @@ def test_against_oracle(m, fmt, lens, q_len, H, kind, tree_lens):
     c.check(out, lse, f"{fmt} {lens} {kind}")
 
 
+WIDE = 5000       # pages of a table with which bf16 keys are taken 128 at a time
+
+
+@pytest.mark.parametrize("lens,q_len,H,kind,tree_lens,split", [
+    ([37, 130], 4, 16, "tree", None, 0),
+    ([64, 65, 67, 128, 129, 132, 1000], 5, 16, "tree", None, 0),
+    ([5, 5, 9, 3, 0, 1], 5, 5, "any", None, 0),
+    ([300, 192, 256, 257], 1, 16, "any", None, 1),
+    ([200, 90, 64], 64, 2, "any", None, 0),
+    ([700], 64, 16, "tree", None, 0),
+    ([333, 40, 7, 90], 33, 20, "tree", [33, 7, 0, 20], 0),
+    ([333, 40, 7, 90, 1500], 33, 20, "any", [1, 33, 7, 32, 33], 2),
+    ([150, 20, 64], 6, 24, "one", [6, 2, 5], 0),
+    ([650, 130, 1300], 3, 200, "tree", None, 0),
+    ([2300, 3, 700, 0, 1500], 9, 32, "any", [9, 3, 5, 0, 9], 1),
+    ([2300, 3, 700, 0, 1500], 9, 32, "any", [9, 3, 5, 0, 9], 5),
+    ([130] * 12, 20, 128, "tree", None, 0),
+])
+def test_wide_tiles(m, lens, q_len, H, kind, tree_lens, split):
+    """The tiles of two pages that many pages of a bf16 cache are taken by."""
+    c = Case("bf16", lens, q_len, H, kind, tree_lens, seed=300 + len(lens) + q_len, width=WIDE)
+    m.mla_get_device_error()
+    out, lse = c.run(m, split_tiles=split)
+    assert m.mla_get_device_error() == 0
+    c.check(out, lse, f"wide {lens} {kind} split {split}")
+    again = c.run(m, split_tiles=split)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_wide_tiles_of_uncut_jobs(m):
+    """Many jobs of so few pages that none is cut."""
+    c = Case("bf16", [(37 * b) % 200 for b in range(210)], 8, 60, "tree", seed=320, width=6)
+    out, lse = c.run(m)
+    assert m.mla_get_device_error() == 0
+    c.check(out, lse, "wide, uncut")
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "s32"])
 @pytest.mark.parametrize("split", [0, 1, 2, 5])
 def test_splits_and_fp32_output(m, fmt, split):
@@ -189,10 +228,10 @@ def test_a_chain_is_the_causal_decode(m, fmt):
     c.check(*want, "causal")
 
 
-@pytest.mark.parametrize("fmt", ["bf16", "s64"])
-def test_nan_of_a_drafted_token_stays_with_those_that_see_it(m, fmt):
+@pytest.mark.parametrize("fmt,width", [("bf16", 0), ("bf16", WIDE), ("s64", 0)])
+def test_nan_of_a_drafted_token_stays_with_those_that_see_it(m, fmt, width):
     """And NaN in the context makes the tree's rows NaN, but no row behind it."""
-    c = Case(fmt, [200, 77], 6, 16, "tree", [6, 4], seed=70)
+    c = Case(fmt, [200, 77], 6, 16, "tree", [6, 4], seed=70, width=width)
     out, lse = c.run(m)
     at = c.bt[0, 197 // 64], 197 % 64                     # node 3 of 6
     bits = (lambda t: t.view(torch.int16)) if fmt == "bf16" else (lambda t: t.view(torch.uint8))
@@ -245,12 +284,12 @@ def test_offsets_beyond_32_bits(m):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-@pytest.mark.parametrize("fmt", ["bf16", "s32"])
-def test_streams_and_graphs(m, fmt):
+@pytest.mark.parametrize("fmt,width", [("bf16", 0), ("bf16", WIDE), ("s32", 0)])
+def test_streams_and_graphs(m, fmt, width):
     """Two calls at once on streams and workspaces of their own, and a captured
     call replayed on new lengths and masks."""
-    a = Case(fmt, [900, 40, 333], 6, 32, "chain", [6, 6, 4], seed=100)
-    b = Case(fmt, [64, 700], 20, 16, "tree", seed=101)
+    a = Case(fmt, [900, 40, 333], 6, 32, "chain", [6, 6, 4], seed=100, width=width)
+    b = Case(fmt, [64, 700], 20, 16, "tree", seed=101, width=width)
     want = [c.run(m) for c in (a, b)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]

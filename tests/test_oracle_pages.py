@@ -139,7 +139,7 @@ def test_pages_are_held_as_often_as_counted():
             P.resize(refs, table, lens, np.where(g.random(B) < 0.5, lens, g.integers(0, mb * 64 + 1, B)))
         elif what == 2:
             n = g.integers(1, 4)
-            P.fork([pool], refs, table, lens, g.integers(0, B, n), g.integers(0, B, n))
+            P.fork([pool], refs, table, lens, g.integers(0, B, n), g.integers(0, B, n), [False])
         else:
             n, err = P.compact([pool], refs, table, lens)
             assert err == set() and n == (refs > 0).sum() and not refs[n:].any()

@@ -83,14 +83,14 @@ def test_resize(m, bad):
     assert m.lib.mla_cache_resize(*_change(RESIZE, **bad)) == INVALID
 
 
-FORK = dict(pools=None, bytes=None, n_pools=2, refs=A, nb=5, bt=A, lens=A, B=2, mb=3, parents=A, children=A, n=4,
+FORK = dict(pools=None, bytes=None, n_pools=2, rows=1, refs=A, nb=5, bt=A, lens=A, B=2, mb=3, parents=A, children=A, n=4,
             ws=A, size=48, s=P(0))
 
 
 def test_fork(m):
     for bad in _bad_pools(FORK):
         assert m.lib.mla_cache_fork(*bad.values()) == INVALID
-    for bad in SEQS + [dict(n=-1), dict(n=8193), dict(parents=P(0)), dict(children=P(0)), dict(ws=ODDER)]:
+    for bad in SEQS + [dict(rows=-1), dict(rows=2), dict(rows=3), dict(n=-1), dict(n=8193), dict(parents=P(0)), dict(children=P(0)), dict(ws=ODDER)]:
         assert m.lib.mla_cache_fork(*_change(_with_pools(FORK), **bad)) == INVALID
     assert m.lib.mla_cache_fork(*_change(_with_pools(FORK), size=47)) == WORKSPACE
     assert m.lib.mla_cache_fork(*_change(_with_pools(FORK), ws=P(0))) == WORKSPACE
@@ -236,3 +236,40 @@ def test_other_python_refusals(m):
         m.mla_cache_copy(calls[m.mla_cache_copy]["pools"] * 101, *[kw["seq_lens"]] * 2)
     assert m.mla_cache_copy([], kw["seq_lens"], kw["seq_lens"]) is None
     m.mla_get_device_error()
+
+
+def test_tree_workspace(m):
+    n = ctypes.c_size_t(0)
+    size = m.lib.mla_decode_tree_workspace_size
+    assert size(2, 8, 16, 64 * 99, 0, ctypes.byref(n)) == OK and n.value > 8
+    assert m.mla_decode_tree_workspace_size(2, 8, 16, 64 * 99) == n.value
+    assert size(2, 8, 16, 64 * 3, 0, ctypes.byref(n)) == OK and n.value == 0
+    assert size(2, 8, 16, 64 * 3, 2, ctypes.byref(n)) == OK and n.value > 0
+    for bad in ((0, 1, 16, 64, 0), (1, 65, 16, 64, 0), (1, 0, 16, 64, 0), (1, 1, 4097, 64, 0), (1, 1, 16, -1, 0),
+                (1, 1, 16, 64, -1), (1024, 64, 128, 1 << 22, 0)):
+        assert size(*bad, ctypes.byref(n)) == INVALID
+    assert size(1, 1, 16, 64, 0, None) == INVALID
+
+
+@pytest.mark.gpu
+def test_tree_workspace_missing(m):
+    """(The size depends on the device.)  Refused before any launch; what the
+    query says is enough, trees of any sizes."""
+    assert m.lib.mla_decode_paged_tree(*_change(TREE, mb=99, ws=P(0))) == WORKSPACE
+    assert m.lib.mla_decode_paged_tree(*_change(TREE, mb=99, n=8)) == WORKSPACE
+    many = dict(B=1024, q_len=64, H=128, mb=1 << 16, stride=64)
+    assert m.lib.mla_decode_paged_tree(*_change(TREE, **many)) == INVALID
+    for q_len, H, split in ((6, 128, 0), (12, 64, 3), (16, 128, 0), (33, 20, 5), (64, 16, 0)):
+        n = m.mla_decode_tree_workspace_size(3, q_len, H, 64 * 40, split)
+        q = torch.zeros((3, q_len, H, 576), dtype=torch.bfloat16, device="cuda")
+        cache = torch.zeros((40, 64, 576), dtype=torch.bfloat16, device="cuda")
+        args = (q, cache, torch.arange(40, dtype=torch.int32, device="cuda").repeat(3, 1),
+                torch.full((3,), 64 * 40, dtype=torch.int32, device="cuda"),
+                torch.ones(q_len, dtype=torch.int64, device="cuda"))
+        for lens in (None, torch.tensor([q_len, 1, 0], dtype=torch.int32, device="cuda")):
+            ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+            m.mla_decode_paged_tree(*args, sm_scale=1.0, split_tiles=split, tree_lens=lens, workspace=ws)
+            with pytest.raises(m.MlaError):
+                m.mla_decode_paged_tree(*args, sm_scale=1.0, split_tiles=split, tree_lens=lens,
+                                        workspace=ws[:n // 2].contiguous())
+    assert m.mla_get_device_error() == 0
