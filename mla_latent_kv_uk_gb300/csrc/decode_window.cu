@@ -849,7 +849,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       volatile int no_abort = 0;
       for (int u = max(0, vc - F::kVSlots); (!WIDE || rank == 0) && u < vc; ++u)
         wait_for(&v_full[u % F::kVSlots], (u / F::kVSlots) & 1, &no_abort);
+      // (of a tile that was left half way, none completes the phase: a while will do)
       if (WIDE && near > 0) wait_for(v_near, (near - 1) & 1, &no_abort);
+      if (WIDE) mbar_wait_for(v_near, near & 1, &no_abort, 1000000);
     }
   } else if (warp == 1) {
     if (rank == 0) {
