@@ -1508,7 +1508,8 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   const int group = j / a.group_jobs;
   const int C = a.ws_head[group], first = a.ws_head[a.groups + 2 * j], end = a.ws_head[a.groups + 2 * j + 1];
   const int len = length_of(b, a, false);
-  if (job_of<TREE>(rg, len, a).pages == 0 || (TREE && rg * 128 / a.H >= nodes_of(b, a, false))) {   // (the words above hold nothing)
+  // (the words above hold nothing)
+  if (job_of<TREE>(rg, len, a).pages == 0 || (TREE && rg * 128 / a.H >= nodes_of(b, a, false))) {
     if (mine == 0 && row_ok) {
       const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       for (int k = 0; k < 2; ++k) store8(out + 8 * (lane + 32 * k), zero);

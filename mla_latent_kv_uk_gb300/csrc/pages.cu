@@ -506,7 +506,8 @@ __device__ __forceinline__ void copy_items(const CopyArgs &a, const Pools &p, in
   for (; item < end_item; advance()) {
     if (MODE == kCompaction && threadIdx.x == 0)
       ahead = gridDim.x + static_cast<int64_t>(atomicAdd(reinterpret_cast<unsigned long long *>(a.head + 2), 1ull));
-    const int now = static_cast<int>(item / per_pair), part = static_cast<int>(item - static_cast<int64_t>(now) * per_pair);
+    const int now = static_cast<int>(item / per_pair);
+    const int part = static_cast<int>(item - static_cast<int64_t>(now) * per_pair);
     const bool other = now != pair;
     if (other) {
       pair = now;
@@ -596,7 +597,8 @@ copy_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ Pools p)
       a.s.refs[a.src[i]] = 0;
     }
     for (int64_t i = blockIdx.x * kCopyThreads + threadIdx.x; pairs > 0 && i < all; i += step) {
-      const int b = static_cast<int>(i / a.s.max_blocks), e = static_cast<int>(i - static_cast<int64_t>(b) * a.s.max_blocks);
+      const int b = static_cast<int>(i / a.s.max_blocks);
+      const int e = static_cast<int>(i - static_cast<int64_t>(b) * a.s.max_blocks);
       const int len = a.s.lens[b];
       if (e == 0 && (len < 0 || len > a.s.max_blocks * kPage)) raise_error(a.s.err, MLA_DEVERR_SEQ_LEN);
       if (e >= pages_of(min(len, a.s.max_blocks * kPage))) continue;
@@ -918,9 +920,9 @@ extern "C" int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_ta
   if (!s.err) return MLA_ERR_CUDA;
   const size_t smem = 4 * sizeof(int) * B;
   if (!allow_smem(resize_kernel, smem)) return MLA_ERR_CUDA;
-  return launch_pdl(resize_kernel, dim3(kCtas), dim3(threads_for(num_blocks, B)), smem, stream, s, new_lens) == cudaSuccess
-             ? MLA_OK
-             : MLA_ERR_CUDA;
+  const dim3 threads(threads_for(num_blocks, B));
+  return launch_pdl(resize_kernel, dim3(kCtas), threads, smem, stream, s, new_lens) == cudaSuccess ? MLA_OK
+                                                                                                  : MLA_ERR_CUDA;
 }
 
 extern "C" int mla_cache_fork_workspace_size(int n, size_t *bytes) {
@@ -930,7 +932,8 @@ extern "C" int mla_cache_fork_workspace_size(int n, size_t *bytes) {
 }
 
 extern "C" int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int n_pools, int n_by_rows,
-                              int32_t *refs, int num_blocks, int32_t *block_table, int32_t *seq_lens, int B, int max_blocks,
+                              int32_t *refs, int num_blocks, int32_t *block_table, int32_t *seq_lens, int B,
+                              int max_blocks,
                               const int32_t *parents, const int32_t *children, int n, void *workspace,
                               size_t ws_bytes, mla_stream_t stream) {
   Seqs s{refs, num_blocks, block_table, seq_lens, B, max_blocks, nullptr};
@@ -950,8 +953,8 @@ extern "C" int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int
   const List list{ws, ws + n, ws + 2 * n};
   const size_t smem = sizeof(int) * (static_cast<size_t>(B) + 4 * n);
   if (!allow_smem(fork_kernel, smem)) return MLA_ERR_CUDA;
-  if (launch_pdl(fork_kernel, dim3(kCtas), dim3(threads_for(num_blocks, std::max(B, n))), smem, stream, s, parents, children, n, list) !=
-      cudaSuccess)
+  const dim3 threads(threads_for(num_blocks, std::max(B, n)));
+  if (launch_pdl(fork_kernel, dim3(kCtas), threads, smem, stream, s, parents, children, n, list) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (n_pools == 0) return MLA_OK;
   CopyArgs a{};
@@ -986,8 +989,9 @@ extern "C" int mla_cache_compact(void *const *pools, const int64_t *page_bytes, 
   if (!s.err) return MLA_ERR_CUDA;
   int32_t *head = static_cast<int32_t *>(workspace), *src = head + 4, *dst = src + num_blocks / 2 + 1,
           *number = dst + num_blocks / 2 + 1;
-  if (launch_pdl(compact_plan_kernel, dim3(kCtas), dim3(threads_for(num_blocks, 0)), 0, stream, static_cast<const int32_t *>(refs),
-                 num_blocks, head, n_live, src, dst, number) != cudaSuccess)
+  const dim3 threads(threads_for(num_blocks, 0));
+  if (launch_pdl(compact_plan_kernel, dim3(kCtas), threads, 0, stream, static_cast<const int32_t *>(refs), num_blocks,
+                 head, n_live, src, dst, number) != cudaSuccess)
     return MLA_ERR_CUDA;
   CopyArgs a{};
   a.src = src;
