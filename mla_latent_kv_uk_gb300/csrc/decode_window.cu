@@ -203,6 +203,8 @@ struct WindowArgs {
   int out_f32;
   float *lse;
   int *ws_head;                 // C of each group; then per job {first unit, end unit}
+  int *ws_cut;                  // per span the job that begins in it and goes on behind it, or -1; by_span only
+  int by_span;                  // the merge goes by these
   void *ws_o;                   // [slots, 128, 512] fp32, or fp16 for a bf16 output
   float *ws_lse;                // [slots, 128]
   float *ws_unit;               // [slots, 128, 2, 2]: what 1 of the fp16 stands for, by 128 columns (1, 3; 2, 4)
@@ -323,7 +325,7 @@ struct Walk {
   int J, job0, per, lane_excl, total, C, span, span_lo, span_hi;
   int base, k, len, units, excl;
   int even;                         // C of the test, or 0
-  int slot0;
+  int slot0, cut;
   bool open;
 
   __device__ int units_of(int tiles) const {
@@ -373,6 +375,9 @@ struct Walk {
     open = false;
     if (span == 0 && J > 0 && (blockIdx.x & 1) == 0 && lane == 0) a.ws_head[group] = C;
   }
+  __device__ void tell_cut(const WindowArgs &a, int j, int lane) const {
+    if (a.by_span && (blockIdx.x & 1) == 0 && lane == 0) a.ws_cut[slot0 + span] = j;
+  }
   __device__ void init_solo(const WindowArgs &a) {
     J = a.B * a.RG;
     span = blockIdx.x >> 1;
@@ -400,9 +405,13 @@ struct Walk {
   __device__ bool next(const WindowArgs &a, Seg &s, int lane) {
     while (true) {
       if (!open) {
-        if (static_cast<int64_t>(span) * C >= total) return false;
+        if (static_cast<int64_t>(span) * C >= total) {
+          if (span < a.group_spans) tell_cut(a, -1, lane);   // (one that has no units)
+          return false;
+        }
         span_lo = span * C;
         span_hi = min(total, span_lo + C);
+        cut = -1;
         // the last lane whose jobs begin at or before the span
         const uint32_t le = __ballot_sync(0xffffffffu, lane_excl <= span_lo);
         const int own = 31 - __clz(le);
@@ -416,6 +425,7 @@ struct Walk {
       const int n = __shfl_sync(0xffffffffu, units, k & 31);
       const int l = __shfl_sync(0xffffffffu, len, k & 31);
       if (base + k >= J || t0 >= span_hi) {
+        tell_cut(a, cut, lane);
         span += a.spans_at_once;
         open = false;
         continue;
@@ -438,6 +448,7 @@ struct Walk {
       // two partials a span at most: one of a job that began before it, one
       // of a job that goes on behind it
       s.slot = 2 * (slot0 + span) + (first >= span_lo ? 1 : 0);
+      if (first >= span_lo && end > span_hi) cut = j;
       if (first >= span_lo && (blockIdx.x & 1) == 0 && lane == 0) {
         a.ws_head[a.groups + 2 * j] = first;
         a.ws_head[a.groups + 2 * j + 1] = end;
@@ -1483,7 +1494,9 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 // 26.6 / 19.8 / 26.5, 8 requests (9) 22.5 / 22.8 / 34.1.
 constexpr int kMergeWarps = 8;
 
-template <typename T, int SPLIT, bool TREE>
+// SPANS: a row of CTAs for each span, which merges the job that begins in it and goes on
+// behind it: fewer rows than jobs where there are many of these, most of them uncut.
+template <typename T, int SPLIT, bool TREE, bool SPANS>
 __global__ void __launch_bounds__(kMergeWarps * 32, SPLIT == 8 ? 1 : SPLIT == 4 ? 2 : 4)
 window_merge_kernel(const __grid_constant__ WindowArgs a) {
   constexpr int kRows = kMergeWarps / SPLIT;    // rows of this CTA
@@ -1496,22 +1509,45 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % SPLIT;
-  const int j = blockIdx.x;
+  int j = blockIdx.x;
   int rg, b;
-  who<TREE>(j, a, rg, b);
   const int rr = blockIdx.y * kRows + warp / SPLIT;
   const int R = a.q_len * a.H;
+  const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if constexpr (SPANS) {
+    // rows of jobs without a key: 32 jobs at a time
+    const int jobs = a.groups * a.group_jobs;
+    const int mine_j = a.ws_cut[blockIdx.x];
+    for (int j0 = blockIdx.x; j0 < jobs; j0 += 32 * gridDim.x) {
+      const int k = j0 + lane * gridDim.x;
+      bool empty = false;
+      if (k < jobs) {
+        who<TREE>(k, a, rg, b);
+        empty = job_of<TREE>(rg, length_of(b, a, false), a).pages == 0 ||
+                (TREE && rg * 128 / a.H >= nodes_of(b, a, false));
+      }
+      for (uint32_t left = __ballot_sync(0xffffffffu, empty); left; left &= left - 1) {
+        who<TREE>(j0 + (__ffs(left) - 1) * gridDim.x, a, rg, b);
+        if (rg * 128 + rr >= R) continue;
+        const int64_t row = static_cast<int64_t>(b) * R + rg * 128 + rr;
+        for (int i = 0; i < 2; ++i) store8(static_cast<T *>(a.out) + row * kLatent + 8 * (lane + 32 * i), zero);
+        if (lane == 0) a.lse[row] = -INFINITY;
+      }
+    }
+    if (mine_j < 0) return;
+    j = mine_j;
+  }
+  who<TREE>(j, a, rg, b);
   const bool row_ok = rg * 128 + rr < R;
   if (SPLIT == 1 && !row_ok) return;
   const int64_t row = static_cast<int64_t>(b) * R + rg * 128 + rr;
   T *out = static_cast<T *>(a.out) + row * kLatent;
   const int group = j / a.group_jobs;
   const int C = a.ws_head[group], first = a.ws_head[a.groups + 2 * j], end = a.ws_head[a.groups + 2 * j + 1];
-  const int len = length_of(b, a, false);
+  const int len = SPANS ? 0 : length_of(b, a, false);
   // (the words above hold nothing)
-  if (job_of<TREE>(rg, len, a).pages == 0 || (TREE && rg * 128 / a.H >= nodes_of(b, a, false))) {
+  if (!SPANS && (job_of<TREE>(rg, len, a).pages == 0 || (TREE && rg * 128 / a.H >= nodes_of(b, a, false)))) {
     if (mine == 0 && row_ok) {
-      const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       for (int k = 0; k < 2; ++k) store8(out + 8 * (lane + 32 * k), zero);
       if (lane == 0) a.lse[row] = -INFINITY;
     }
@@ -1613,17 +1649,19 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   if (mine == 0 && lane == 0) a.lse[row] = z == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + logf(z);
 }
 
-template <typename T, int SPLIT, bool TREE>
+template <typename T, int SPLIT, bool TREE, bool SPANS = false>
 cudaError_t launch_merge(const WindowArgs &a, mla_stream_t stream) {
   constexpr int kRows = kMergeWarps / SPLIT;
   const int rows = std::min(128, a.q_len * a.H);
-  return launch_pdl(window_merge_kernel<T, SPLIT, TREE>, dim3(a.B * a.RG, (rows + kRows - 1) / kRows),
+  return launch_pdl(window_merge_kernel<T, SPLIT, TREE, SPANS>,
+                    dim3(SPANS ? a.groups * a.group_spans : a.B * a.RG, (rows + kRows - 1) / kRows),
                     dim3(kMergeWarps * 32), 0, stream, a);
 }
 
 template <typename T, bool TREE>
 cudaError_t merge(int64_t parts, const WindowArgs &a, mla_stream_t stream) {
-  return parts > 40   ? launch_merge<T, 8, TREE>(a, stream)
+  return a.by_span    ? launch_merge<T, 1, TREE, true>(a, stream)
+         : parts > 40 ? launch_merge<T, 8, TREE>(a, stream)
          : parts > 10 ? launch_merge<T, 4, TREE>(a, stream)
                       : launch_merge<T, 1, TREE>(a, stream);
 }
@@ -1688,7 +1726,7 @@ bool shape_ok(int B, int q_len, int H) {
 }
 
 struct WsLayout {
-  size_t o_off, lse_off, unit_off, total;
+  size_t cut_off, o_off, lse_off, unit_off, total;
   int groups;
   int64_t group_spans;
   bool solo, fits;              // fits: the units of all jobs count in 32 bits
@@ -1735,7 +1773,8 @@ WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sin
   const size_t slots = rows == kChain ? static_cast<size_t>(2 * w.groups) * w.group_spans
                                       : 2 * std::max<size_t>(spans_of(1), split_tiles > 0 ? RG * spans_of(RG) : 0);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  w.o_off = up(((rows == kChain ? w.groups : RG) + 2 * static_cast<size_t>(J)) * sizeof(int));
+  w.cut_off = ((rows == kChain ? w.groups : RG) + 2 * static_cast<size_t>(J)) * sizeof(int);
+  w.o_off = up(w.cut_off + slots / 2 * sizeof(int));
   w.lse_off = w.o_off + slots * 128 * kLatent * sizeof(float);
   w.unit_off = w.lse_off + slots * 128 * sizeof(float);
   w.total = w.unit_off + slots * 128 * 4 * sizeof(float);
@@ -1853,6 +1892,10 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   a.lse = lse;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.ws_head = reinterpret_cast<int *>(ws);
+  a.ws_cut = reinterpret_cast<int *>(ws + w.cut_off);
+  // (54 trees of 5 tokens over up to 507 keys, 128 heads, 270 jobs: 50.6 us, by job 55.2; 128
+  // windowed requests of two tokens 151, 154)
+  a.by_span = !w.solo && split_tiles == 0 && jobs > pairs;
   a.ws_o = ws + w.o_off;
   a.ws_lse = reinterpret_cast<float *>(ws + w.lse_off);
   a.ws_unit = reinterpret_cast<float *>(ws + w.unit_off);
