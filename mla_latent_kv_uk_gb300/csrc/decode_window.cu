@@ -1534,7 +1534,7 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
         if (lane == 0) a.lse[row] = -INFINITY;
       }
     }
-    if (mine_j < 0) return;
+    if (mine_j < 0 || mine_j >= jobs) return;
     j = mine_j;
   }
   who<TREE>(j, a, rg, b);
@@ -1555,6 +1555,8 @@ window_merge_kernel(const __grid_constant__ WindowArgs a) {
   }
   const int s0 = first / C + group * a.group_spans, n = (end - 1) / C - first / C + 1;
   if (n == 1) return;   // written by its pair
+  // (words that a pair did not write, having given up)
+  if (C < 1 || n < 1 || s0 < group * a.group_spans || s0 + n > (group + 1) * a.group_spans) return;
   // lane's values: columns 8 lane .. and 256 + 8 lane ..
   float acc[16], z = 0.f, m = -INFINITY;
 #pragma unroll
