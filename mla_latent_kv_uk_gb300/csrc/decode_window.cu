@@ -77,12 +77,12 @@
 // times of graph replays, in brackets of calls on changing inputs): 64 e4m3
 // requests of up to 16384 tokens 94 us (100), at 1.6 of the 1.9 PFLOP/s that a
 // bf16 product reaches, near the 1632 cycles of a tile's MMAs; 128 bf16 requests
-// of two tokens and a window of 4096 147 us (155), 1.14 PFLOP/s, where Q K^T of 64
+// of two tokens and a window of 4096 143 us (151), 1.17 PFLOP/s, where Q K^T of 64
 // keys takes as long as one of 128; one e4m3 request of 131072 tokens 35.6 us (35.0),
 // the smallest calls 8.4: 3 us until the first keys are there, 4 from the last
 // scores to the results, and 3 for the merge where there is one.  Trees: 24
 // requests of 16 tokens over 8192 bf16 keys 544 us, 1.61 PFLOP/s, where a long bf16
-// product is at 1.73 for the power that it takes; 16 over 4096 193 (208): 2830
+// product is at 1.73 for the power that it takes; 16 over 4096 200 (208): 2830
 // cycles a tile of 128 keys, 2208 of them MMAs, 280 waits for keys (L2 gives an SM 48
 // bytes a clock, of 58 at most), 220 for probabilities; 64 tokens over 16384 keys
 // of blocks of 64 tokens 165 (166): the passes over O where a block's scale differs.
