@@ -500,7 +500,7 @@ def mla_decode_paged_tree(q, kv_cache, block_table, seq_lens, tree_mask, *, sm_s
 
 
 def mla_cache_copy(pools, src, dst):
-    """Copies pages src [n] to pages dst [n] (int32) in every pool."""
+    """Copies pages src [n] to pages dst [n] (int32, n <= 65536) in every pool."""
     _binding.copy(pools, src, dst)
 
 

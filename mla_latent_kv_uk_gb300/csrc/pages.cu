@@ -35,6 +35,7 @@ namespace mla {
 namespace {
 
 constexpr int kMaxPools = 200;       // (their addresses and sizes are kernel arguments, of 4 KB at most)
+constexpr int kMaxPairs = 1 << 16;   // of mla_cache_copy
 constexpr int kMaxRows = 8192;       // sequences of a call, and forks: 5 words of shared memory for both
 constexpr int kCtas = 8, kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 static_assert(kMaxWarps <= 32 && kCtas <= 32, "a lane each");
@@ -667,17 +668,18 @@ int launch_copy(CopyArgs &a, const Pools &p, int64_t most, mla_stream_t stream) 
              : MLA_ERR_CUDA;
 }
 
-// Shared memory of the bookkeeping kernels beyond the usual 48 KB (some of it is static).
+// Shared memory of the bookkeeping kernels beyond the usual 48 KB (some of it is
+// static): the most that there may be, so that calls of several threads do not take
+// it from each other.
 template <typename K>
 bool allow_smem(K *kernel, size_t bytes) {
-  return bytes <= 40 * 1024 ||
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
-             cudaSuccess;
+  return bytes <= 40 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    5 * sizeof(int) * kMaxRows) == cudaSuccess;
 }
 
 int check_seqs(const Seqs &s) {
   if (s.num_blocks < 1 || s.num_blocks >= (1 << 25) || s.B < 1 || s.B > kMaxRows || s.max_blocks < 1 ||
-      s.max_blocks > (1 << 24))
+      s.max_blocks > (1 << 24) || static_cast<int64_t>(s.B) * s.max_blocks > INT_MAX)   // (sums of pages)
     return MLA_ERR_INVALID_ARG;
   if (!s.refs || !aligned16(s.refs) || !s.table || !s.lens) return MLA_ERR_INVALID_ARG;
   return MLA_OK;
@@ -894,7 +896,7 @@ using namespace mla;
 
 extern "C" int mla_cache_copy(void *const *pools, const int64_t *page_bytes, int n_pools, int num_blocks,
                               const int32_t *src, const int32_t *dst, int n, mla_stream_t stream) {
-  if (num_blocks < 1 || num_blocks >= (1 << 25) || n < 0 || n >= (1 << 25)) return MLA_ERR_INVALID_ARG;
+  if (num_blocks < 1 || num_blocks >= (1 << 25) || n < 0 || n > kMaxPairs) return MLA_ERR_INVALID_ARG;
   Pools p;
   const int st = gather_pools(pools, page_bytes, n_pools, p);
   if (st != MLA_OK) return st;

@@ -123,6 +123,20 @@ def test_copy_without_large_pools_and_one_tensor(m):
     assert torch.equal(p, want)
 
 
+def test_copy_of_the_longest_list(m):
+    n = 1 << 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pools = [torch.randint(1 << 30, (2 * n + 9, w), dtype=torch.int32, device="cuda", generator=g) for w in (4, 256)]
+    order = torch.randperm(2 * n + 9, device="cuda", generator=g, dtype=torch.int64).int()
+    src, dst = order[:n].contiguous(), order[n:2 * n].contiguous()
+    want = [p.clone() for p in pools]
+    for w in want:
+        w[dst.long()] = w[src.long()]
+    m.mla_cache_copy(pools, src, dst)
+    assert m.mla_get_device_error() == 0
+    assert all(torch.equal(p, w) for p, w in zip(pools, want))
+
+
 def test_copy_beyond_32_bits(m):
     pool = torch.zeros((60000, 64, 576), dtype=torch.bfloat16, device="cuda")
     pool[59990] = 3.0

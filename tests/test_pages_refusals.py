@@ -67,7 +67,7 @@ def _bad_pools(base):
 def test_copy(m):
     for bad in _bad_pools(COPY):
         assert m.lib.mla_cache_copy(*bad.values()) == INVALID
-    for bad in (dict(nb=0), dict(nb=1 << 25), dict(n=-1), dict(n=1 << 25), dict(src=P(0)), dict(dst=P(0))):
+    for bad in (dict(nb=0), dict(nb=1 << 25), dict(n=-1), dict(n=(1 << 16) + 1), dict(n=1 << 25), dict(src=P(0)), dict(dst=P(0))):
         assert m.lib.mla_cache_copy(*_change(_with_pools(COPY), **bad)) == INVALID
     assert m.lib.mla_cache_copy(*_change(_with_pools(COPY), n=0, src=P(0), dst=P(0))) == OK
     assert m.lib.mla_cache_copy(*_change(COPY, n_pools=0)) == OK
@@ -75,7 +75,7 @@ def test_copy(m):
 
 RESIZE = dict(refs=A, nb=5, bt=A, lens=A, new=A, B=2, mb=3, s=P(0))
 SEQS = [dict(refs=P(0)), dict(refs=ODD), dict(nb=0), dict(nb=1 << 25), dict(bt=P(0)), dict(lens=P(0)), dict(B=0),
-        dict(B=8193), dict(mb=0), dict(mb=(1 << 24) + 1)]
+        dict(B=8193), dict(mb=0), dict(mb=(1 << 24) + 1), dict(B=128, mb=1 << 24)]
 
 
 @pytest.mark.parametrize("bad", SEQS + [dict(new=P(0))])
