@@ -85,7 +85,7 @@
 // product is at 1.73 for the power that it takes; 16 over 4096 200 (208): 2830
 // cycles a tile of 128 keys, 2208 of them MMAs, 280 waits for keys (L2 gives an SM 48
 // bytes a clock, of 58 at most), 220 for probabilities; 64 tokens over 16384 keys
-// of blocks of 64 tokens 165 (166): the passes over O where a block's scale differs.
+// of blocks of 64 tokens 160 (160): the passes over O where a block's scale differs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -144,6 +144,7 @@ struct Fmt {
   static constexpr int kMine = kTile / 2;                  // keys of one softmax thread
   static constexpr int kMinUnits = (kMinPages + kPages - 1) / kPages;
   static constexpr int kJobCost = kJobPages / kPages;      // in tiles, as all units
+  static constexpr int kUncut = 4 / kPages;                // (see Walk)
   static constexpr int kCols = 128 / kEsz;                 // columns of a 128-byte box row
   static constexpr int kQBytes = 64 * kDqk * kEsz;         // 64 query rows: 36 / 72 KB
   static constexpr int kKRows = kTile / 2;                 // key rows of one CTA
@@ -196,7 +197,7 @@ struct WindowArgs {
   const int32_t *block_table, *seq_lens;
   int B, q_len, H, max_blocks, num_blocks, window, sinks;
   int RG, forced, solo;
-  int groups, group_jobs;       // row groups planned apart (RG or 1), jobs of each
+  int groups, group_jobs;       // groups of pairs, planned apart, and the jobs of each
   int spans_at_once;            // pairs of a group
   int group_spans;              // most spans of a group
   void *out;
@@ -318,6 +319,10 @@ __device__ __forceinline__ int warp_incl_scan(int x, int lane) {
 // parts than pairs, each pair has one part of one job instead of C units of
 // what lies end to end: nobody then switches jobs (a second segment ends
 // about 4 us after a first one of the same tiles).  A part is the unit, C = 1.
+// Trees' jobs are left whole, as many for each pair, which spares the merge too, where that
+// is no more than kUncut over C (8 of 8 tokens over 3000 e4m3 keys, 64 jobs: 38.9 us, cut
+// 43.8; with twice the slack 48 jobs took 37.3 in place of 36.7, of 7 over bf16 47.8 in place
+// of 46.5; 54 of 4 over 700 keys of blocks of 32, three jobs a pair, 50.1, cut 56.4).
 template <bool FP8, bool TREE, bool WIDE>
 struct Walk {
   using F = Fmt<FP8, WIDE>;
@@ -366,6 +371,22 @@ struct Walk {
         C = 1;
       } else {
         even = 0;
+      }
+    }
+    if (TREE && a.forced == 0 && per <= kHeld && even == 0) {
+      int top = 0, jobs = 0;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        top = max(top, held[i]);
+        jobs += held[i] > 0;
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      const int all = __reduce_add_sync(0xffffffffu, jobs), most = (all - 1) / a.spans_at_once + 1;
+      if (all > 0 && most * (top + F::kJobCost) <= C + F::kJobCost + F::kUncut) {
+        even = top;
+        sum = jobs;
+        total = all;
+        C = most;
       }
     }
     lane_excl = warp_incl_scan(sum, lane) - sum;
@@ -1738,7 +1759,7 @@ struct WsLayout {
 enum Rows { kChain, kTree, kUnevenTrees };
 
 WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sinks,
-                   int split_tiles, int pairs, Rows rows = kChain) {
+                   int split_tiles, int pairs, Rows rows = kChain, int64_t page_bytes = 0) {
   const int64_t RG = (static_cast<int64_t>(q_len) * H + 127) / 128, J = B * RG;
   // most pages of a job: the sinks' and the window's, which may begin inside
   // a page and is q_len - 1 tokens longer for the job's queries together
@@ -1754,8 +1775,12 @@ WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sin
   // Row groups of a request read the same pages.  Planned apart, each over its
   // share of the pairs, they do so at the same time, and all but one read from
   // L2 - unless that leaves more than a sixteenth of the pairs idle.
-  // Trees' row groups are dealt out to as many groups of pairs as divide them evenly
-  // (24 requests of 16 tokens over 8192 bf16 ones: 544 us, all in one plan 593); but of
+  // Trees' row groups are dealt out to n groups of pairs, of which the share of pairs that
+  // then idles and `apart` / n are the least: reading apart costs little while the pages that
+  // there may be stay in L2 anyway, more where they are over 48 MB (n = 8, of 72 pairs, and 4,
+  // of 76: 16 trees of 16 tokens over 4096 e4m3 keys, 38 MB, 157.5 us and 152.4; 24 over 8192
+  // bf16 ones, 226 MB, 558 and 578; n = 7, of 70, and 1: 16 of 7 over 4096 e4m3 ones 81.1 and
+  // 79.7, 40 over 8192, 189 MB, 315 and 338).  But of
   // trees of different sizes the later row groups have less to do: they are planned
   // together (8 trees of 17 to 33 tokens over up to 8192 e4m3 ones, 20 heads: 42 us, apart
   // 50; 32 trees of 4 over 4096 bf16 ones, sizes given: 122, not given: 105).
@@ -1763,8 +1788,14 @@ WsLayout ws_layout(int B, int q_len, int H, int max_seq_len, int window, int sin
   if (rows == kChain) {
     if (evenly(RG)) w.groups = static_cast<int>(RG);
   } else if (rows == kTree) {
-    for (int64_t n = std::min<int64_t>(RG, pairs); n > 1 && w.groups == 1; --n)
-      if (RG % n == 0 && evenly(n)) w.groups = static_cast<int>(n);
+    const double apart = B * pages * page_bytes > (48 << 20) ? 0.45 : 0.05;
+    double least = 2;
+    for (int n = 1; n <= std::min<int64_t>(RG, pairs); ++n) {
+      const double cost = static_cast<double>(pairs % n) / pairs + apart / n;
+      if (RG % n != 0 || cost >= least) continue;
+      least = cost;
+      w.groups = n;
+    }
   }
   // (a forced split counts tiles: the smaller ones, of one page, make more)
   auto spans_of = [&](int64_t groups) {
@@ -1855,7 +1886,8 @@ int launch_window(const void *q, bool fp8, float q_scale, const void *kv_cache, 
   const int pairs = pairs_for_device();
   if (pairs == 0) return MLA_ERR_CUDA;
   const WsLayout w = ws_layout(B, q_len, H, max_blocks * kPage, window, sinks, split_tiles, pairs,
-                               !tree.mask ? kChain : tree.lens ? kUnevenTrees : kTree);
+                               !tree.mask ? kChain : tree.lens ? kUnevenTrees : kTree,
+                               kPage * kDqk * (fp8 ? 1 : 2));
   if (!w.fits) return MLA_ERR_INVALID_ARG;
   if (!w.solo && (!workspace || ws_bytes < w.total)) return MLA_ERR_WORKSPACE;
   WindowArgs a{};

@@ -45,6 +45,8 @@ def check(m, c, label, dtype):
     (lengths(100, 500), 5, 40, "any", [b * 3 % 6 for b in range(100)], 0),
     ([0] * 79 + [9000], 3, 16, "tree", None, 0),                         # all spans but a few of one job
     ([0] * 100, 2, 16, "any", None, 9),                                  # nothing at all
+    ([700] * 36 + [0, 660, 0, 0], 4, 128, "tree", None, 0),               # two whole jobs a pair
+    ([0, 700, 690, 641] * 24, 3, 16, "any", None, 0),                    # one
 ])
 def test_trees(m, fmt, dtype, lens, q_len, H, kind, tree_lens, width):
     c = TreeCase(fmt, lens, q_len, H, kind, tree_lens, seed=500 + len(lens) + width, width=width)
