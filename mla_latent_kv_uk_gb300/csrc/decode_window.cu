@@ -85,7 +85,7 @@
 // product is at 1.73 for the power that it takes; 16 over 4096 200 (208): 2830
 // cycles a tile of 128 keys, 2208 of them MMAs, 280 waits for keys (L2 gives an SM 48
 // bytes a clock, of 58 at most), 220 for probabilities; 64 tokens over 16384 keys
-// of blocks of 64 tokens 160 (160): the passes over O where a block's scale differs.
+// of blocks of 64 tokens 160 (163): the passes over O where a block's scale differs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
