@@ -545,8 +545,9 @@ int mla_cache_resize(int32_t *refs, int num_blocks, int32_t *block_table,
  * Parents are as they were before the call.  Left out, with MLA_DEVERR_PAGES:
  * a child that has tokens or came up before, and from where free pages run
  * out on every fork that needs one; a row outside [0, B): MLA_DEVERR_RANGE; a
- * parent's length out of range: MLA_DEVERR_SEQ_LEN; a parent's entry that is
- * no page: MLA_DEVERR_BLOCK_ID, and the child's is -1.
+ * parent's length out of range: MLA_DEVERR_SEQ_LEN.  Where a parent's entry is
+ * no page (MLA_DEVERR_BLOCK_ID), or a free one (MLA_DEVERR_PAGES), the child's
+ * is -1: nothing is shared, copied or taken for it.
  * workspace: mla_cache_fork_workspace_size(n) bytes, 4-byte aligned. */
 int mla_cache_fork_workspace_size(int n, size_t *bytes);
 

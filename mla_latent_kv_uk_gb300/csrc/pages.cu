@@ -130,11 +130,10 @@ struct Scan {
     return m;
   }
   __device__ int end() const { return min(first + per, num_blocks); }
-  // (refs and sums of the cluster's CTAs; the barrier in it orders what they wrote before)
+  // Of a lane's pages
   template <typename Is>
-  __device__ void count(Is is, int rank) {
-    __shared__ int of_warp[kMaxWarps], of_cta[kCtas];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __device__ int count_mine(Is is) {
+    const int lane = threadIdx.x & 31;
     int n = 0;
     for (int id = first + 4 * lane, r = 0; id < end(); id += 512) {
       uint32_t m[4];
@@ -146,6 +145,16 @@ struct Scan {
         if (r < kHeld) held |= static_cast<uint64_t>(m[k]) << (4 * r);
       }
     }
+    return n;
+  }
+  // (refs and sums of the cluster's CTAs; the barrier in it orders what they wrote before)
+  template <typename Is>
+  __device__ void count(Is is, int rank) {
+    join(count_mine(is), rank);
+  }
+  __device__ void join(int n, int rank) {
+    __shared__ int of_warp[kMaxWarps], of_cta[kCtas];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) of_warp[warp] = n;
     __syncthreads();
@@ -290,7 +299,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kMaxThreads, 1)
 fork_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ parents,
             const int32_t *__restrict__ children, int n, const __grid_constant__ List list) {
   extern __shared__ int rows[];
-  // first fork to a row; own pages up to and with this fork; parent, child and length (-1: left out)
+  // first fork to a row; own pages up to and with this fork (before that: its parent's last
+  // page); parent, child (-1: left out) and length
   int *first = rows, *end = rows + s.B, *from = end + n, *to = from + n, *length = to + n;
   cluster_started();
   sm100::grid_dep_wait();
@@ -299,6 +309,14 @@ fork_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ parents,
   const int wid = rank * warps_of() + (tid >> 5), most = s.max_blocks * kPage;
   const int per = (n + blockDim.x - 1) / blockDim.x, i0 = min(tid * per, n), i1 = min(i0 + per, n);
   auto row_ok = [&](int b) { return b >= 0 && b < s.B; };
+  auto len_ok = [&](int len) { return len >= 0 && len <= most; };
+  auto entry = [&](int p, int e) { return s.table[static_cast<int64_t>(p) * s.max_blocks + e]; };
+  // A page can be shared, or copied from, if somebody holds it: one that nobody does is
+  // given away by this very call.  0, or the error (refs: read from L2, see Scan)
+  auto fault_of = [&](int page) {
+    if (page < 0 || page >= s.num_blocks) return static_cast<int>(MLA_DEVERR_BLOCK_ID);
+    return __ldcg(s.refs + page) > 0 ? 0 : static_cast<int>(MLA_DEVERR_PAGES);
+  };
   for (int b = tid; b < s.B; b += blockDim.x) first[b] = INT_MAX;
   for (int i = i0; i < i1; ++i) {
     from[i] = parents[i];
@@ -306,76 +324,99 @@ fork_kernel(const __grid_constant__ Seqs s, const int32_t *__restrict__ parents,
   }
   __syncthreads();
   int child_len = 0;                        // of the last of this thread's forks (of several: read again)
+  bool some = false;
   for (int i = i0; i < i1; ++i) {
     if (row_ok(to[i])) {
       atomicMin(first + to[i], i);
       child_len = s.lens[to[i]];
     }
-    length[i] = row_ok(from[i]) ? s.lens[from[i]] : 0;
+    const int len = row_ok(from[i]) ? s.lens[from[i]] : 0;
+    const bool part = len_ok(len) && len % kPage;
+    length[i] = len;
+    end[i] = part ? entry(from[i], len / kPage) : -1;
+    some |= part;
   }
-  __syncthreads();
+  some = __syncthreads_or(some);
+  // The entries of the warp's first fork are asked for along with the pages' counts, and
+  // then the counts of them, and of the last pages
+  const Share share(n, wid);
+  int page[kAtOnce], fault[kAtOnce];
+  auto fetch = [&](int p, int len, int e0) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      page[i] = e0 + i * share.lanes < len / kPage ? entry(p, e0 + i * share.lanes) : -1;
+  };
+  auto look = [&] {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) fault[i] = fault_of(page[i]);
+  };
+  const int e_first = share.lane0 + lane, f = share.first;
+  fetch(f < n ? from[f] : 0, f < n && row_ok(from[f]) && len_ok(length[f]) ? length[f] : 0, e_first);
+  Scan scan(s.refs, s.num_blocks, rank);
+  if (!some) scan.first = s.num_blocks;     // (nothing to count)
+  const int mine = scan.count_mine(is_free);
+  look();
   int sum = 0;
   for (int i = i0; i < i1; ++i) {
     const int p = from[i], c = to[i], len = length[i];
     int bits = 0;
     if (!row_ok(p) || !row_ok(c)) bits = MLA_DEVERR_RANGE;
     else if (first[c] != i || (per == 1 ? child_len : s.lens[c]) != 0) bits = MLA_DEVERR_PAGES;
-    else if (len < 0 || len > most) bits = MLA_DEVERR_SEQ_LEN;
+    else if (!len_ok(len)) bits = MLA_DEVERR_SEQ_LEN;
+    bool own = false;
+    if (bits) {
+      to[i] = -1;
+    } else if (len % kPage) {
+      // (a last page that is none: the child has a hole there too, and takes no page)
+      bits = fault_of(end[i]);
+      own = !bits;
+    }
     if (bits && rank == 0) raise_error(s.err, bits);
-    if (bits) length[i] = -1;
-    end[i] = sum += !bits && len % kPage ? 1 : 0;
+    end[i] = sum += own;
   }
   int total;
   const int before = block_excl(sum, total);
   for (int i = i0; i < i1; ++i) end[i] += before;
   cluster_wait();
   __syncthreads();
-  // the entries of the warp's first fork are asked for along with the pages' counts
-  const Share share(n, wid);
-  auto entry = [&](int p, int e) { return s.table[static_cast<int64_t>(p) * s.max_blocks + e]; };
-  int page[kAtOnce];
-  auto fetch = [&](int p, int len, int e0) {
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-      page[i] = e0 + i * share.lanes < len / kPage ? entry(p, e0 + i * share.lanes) : -1;
-  };
-  const int e_first = share.lane0 + lane;
-  if (share.first < n) fetch(from[share.first], length[share.first], e_first);
-  Scan scan(s.refs, s.num_blocks, rank);
-  if (total == 0) scan.first = s.num_blocks;
-  scan.count(is_free, rank);
+  scan.join(mine, rank);
   for (int i = share.first; i < n; i += share.step) {
     const int len = length[i], p = from[i], c = to[i];
-    const bool own = len > 0 && len % kPage, fails = own && end[i] > scan.all, one = lane + share.lane0 == 0;
+    const bool own = end[i] > (i > 0 ? end[i - 1] : 0), fails = own && end[i] > scan.all;
+    const bool one = lane + share.lane0 == 0;
     if (one) {
       if (fails) raise_error(s.err, MLA_DEVERR_PAGES);
       if (!own || fails) list.dst[i] = -1;
     }
-    if (len < 0 || fails) continue;
+    if (c < 0 || fails) continue;
     int32_t *row = s.table + static_cast<int64_t>(c) * s.max_blocks;
     if (one) {
       s.lens[c] = len;
       if (own) {
-        const int last = entry(p, len / kPage);
-        const bool good = last >= 0 && last < s.num_blocks;
-        if (!good) raise_error(s.err, MLA_DEVERR_BLOCK_ID);
-        list.src[i] = good ? last : -1;
+        list.src[i] = entry(p, len / kPage);
         list.rows[i] = len % kPage;
+      } else if (len % kPage) {
+        row[len / kPage] = -1;
       }
     }
     for (int e0 = e_first; e0 < len / kPage; e0 += kAtOnce * share.lanes) {
-      if (i != share.first || e0 != e_first) fetch(p, len, e0);
+      if (i != share.first || e0 != e_first) {
+        fetch(p, len, e0);
+        look();
+      }
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         const int e = e0 + j * share.lanes;
         if (e >= len / kPage) continue;
-        const bool good = page[j] >= 0 && page[j] < s.num_blocks;
-        row[e] = good ? page[j] : -1;
-        if (good) atomicAdd(s.refs + page[j], 1);
-        else raise_error(s.err, MLA_DEVERR_BLOCK_ID);
+        row[e] = fault[j] ? -1 : page[j];
+        if (fault[j]) raise_error(s.err, fault[j]);
+        else atomicAdd(s.refs + page[j], 1);
       }
     }
   }
+  // Free pages stay free until every entry has been looked at (in front of the counts'
+  // barrier, where the rows' first batches are all that there may be)
+  if (share.step < n || s.max_blocks > kAtOnce * share.lanes) cluster_barrier();
   scan.each(is_free, total, [&](int page, int number) {
     const int i = first_over(end, n, number);
     s.table[static_cast<int64_t>(to[i]) * s.max_blocks + length[i] / kPage] = page;

@@ -83,7 +83,19 @@ def fork(pools, refs, table, lens, parents, children, by_rows=None):
     errors = set()
     B, most = table.shape[0], table.shape[1] * BLOCK
     free, wanted, seen = _free(refs), 0, set()
-    table0, lens0 = table.copy(), lens.copy()
+    refs0, table0, lens0 = refs.copy(), table.copy(), lens.copy()
+
+    def held(p, k):
+        """The parent's k-th page; -1 where the entry is none, or one that nobody holds."""
+        page = int(table0[p, k])
+        if not 0 <= page < len(refs0):
+            errors.add("block")
+        elif refs0[page] <= 0:
+            errors.add("pages")
+        else:
+            return page
+        return -1
+
     for p, c in zip(parents, children):
         p, c = int(p), int(c)
         if not (0 <= p < B and 0 <= c < B):
@@ -101,29 +113,24 @@ def fork(pools, refs, table, lens, parents, children, by_rows=None):
             errors.add("len")
             continue
         part = n % BLOCK
-        wanted += part > 0
-        if part and wanted > len(free):
+        last = held(p, n // BLOCK) if part else -1
+        wanted += last >= 0
+        if last >= 0 and wanted > len(free):
             errors.add("pages")
             continue
         for k in range(n // BLOCK):
-            page = int(table0[p, k])
-            good = 0 <= page < len(refs)
-            table[c, k] = page if good else -1
-            if good:
+            page = table[c, k] = held(p, k)
+            if page >= 0:
                 refs[page] += 1
-            else:
-                errors.add("block")
-        if part:
-            src, dst = int(table0[p, n // BLOCK]), free[wanted - 1]
-            table[c, n // BLOCK] = dst
+        if part and last < 0:
+            table[c, n // BLOCK] = -1
+        elif part:
+            dst = table[c, n // BLOCK] = free[wanted - 1]
             refs[dst] = 1
-            if not 0 <= src < len(refs):
-                errors.add("block")
-            else:
-                for k, pool in enumerate(pools):
-                    rows = by_rows is None or by_rows[k]
-                    flat = pool.reshape(pool.shape[0], BLOCK if rows else 1, -1)
-                    flat[dst, :part if rows else 1] = flat[src, :part if rows else 1]
+            for k, pool in enumerate(pools):
+                rows = by_rows is None or by_rows[k]
+                flat = pool.reshape(pool.shape[0], BLOCK if rows else 1, -1)
+                flat[dst, :part if rows else 1] = flat[last, :part if rows else 1]
         lens[c] = n
     return errors
 

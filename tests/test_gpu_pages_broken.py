@@ -1,0 +1,56 @@
+"""The cache-page calls on state that is broken already: what they flag, what they
+leave, and that it does not spread, bit for bit as their oracle."""
+
+import numpy as np
+import pytest
+
+from tests.test_gpu_cache_pages import State, _i32, m  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _load(s):
+    for d, x in zip(s.d, (s.refs, s.table, s.lens)):
+        d.copy_(_i32(x))
+
+
+@pytest.mark.parametrize("shapes", ["bf16", "scaled", "rows"])
+def test_fork_of_a_broken_last_page(m, shapes):
+    s = State(shapes, 30, 12, 4, [100, 30, 70, 200, 130], seed=60)
+    s.table[0, 1], s.table[1, 0] = 30, -1              # no pages
+    s.refs[s.table[2, 1]] = 0                          # held, and free
+    s.refs[s.table[4, 2]] = -1
+    _load(s)
+    s.fork(m, [0, 3, 1, 2, 3, 4], [5, 6, 7, 8, 9, 10])
+    assert s.lens.tolist() == [100, 30, 70, 200, 130, 100, 200, 30, 70, 200, 130, 0]
+    assert [s.table[b, k] for b, k in ((5, 1), (7, 0), (8, 1), (10, 2))] == [-1] * 4
+    s.resize(m, [0] * 12)
+
+
+def test_fork_of_broken_pages_leaves_the_last_pages_to_others(m):
+    s = State("bf16", 6, 8, 2, [100, 64, 70], seed=61)      # five pages held, one free
+    s.table[0, 1] = 2 ** 31 - 1
+    _load(s)
+    s.fork(m, [0, 0, 2, 2], [3, 4, 5, 6])
+    assert s.lens[3:].tolist() == [100, 100, 70, 0, 0]
+
+
+@pytest.mark.parametrize("nb", [2000, 20000, 140000])
+@pytest.mark.parametrize("n", [1, 3, 100])
+def test_a_free_page_goes_to_one_owner(m, nb, n):
+    """Of parents' pages one in three is free: they are the lowest free ones, which
+    the same call gives to the children that need one."""
+    s = State("small", nb, 2 + n, 400, [300 * 64 + 5, 399 * 64 + 63], seed=nb + n)
+    held = s.table[0, :301], s.table[1, :400]
+    for row in held:
+        row[:] = np.sort(row)
+    every = np.sort(np.concatenate(held))
+    s.refs[:] = 1
+    s.refs[every[s.g.random(every.size) < 0.33]] = 0
+    s.refs[s.table[0, 300]] = s.refs[s.table[1, 399]] = 1
+    _load(s)
+    s.fork(m, np.arange(n) % 2, 2 + np.arange(n))
+    last = s.table[2:, [300, 399]][np.arange(n), np.arange(n) % 2]
+    assert len(set(last.tolist())) == n and (s.refs[last] == 1).all()
+    shared = s.table[2:, :300]
+    assert not np.isin(last, shared).any()
