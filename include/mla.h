@@ -563,7 +563,8 @@ int mla_cache_fork(void *const *pools, const int64_t *page_bytes, int n_pools,
  * from N on are free.  What they held stays.  Every page in use is held by
  * these sequences, or by entries that the caller has elsewhere and updates
  * himself.  An entry that is no page sets MLA_DEVERR_BLOCK_ID, one that is
- * free and not below N MLA_DEVERR_PAGES; both stay.
+ * free and not below N MLA_DEVERR_PAGES; both stay.  A length out of range sets
+ * MLA_DEVERR_SEQ_LEN and counts as the nearest in it.
  * workspace: mla_cache_compact_workspace_size(num_blocks) bytes, 8-byte
  * aligned. */
 int mla_cache_compact_workspace_size(int num_blocks, size_t *bytes);

@@ -631,26 +631,35 @@ copy_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ Pools p)
   sm100::grid_dep_launch();
   int pairs = a.n;
   if constexpr (MODE == kCompaction) {
+    // The rows' entries, a warp or several to a row, four entries a lane (looked at where
+    // nothing moves, too: what is wrong with them is flagged whether or not there were free
+    // pages in between)
+    const int threads = gridDim.x * kCopyThreads, thread = blockIdx.x * kCopyThreads + threadIdx.x;
+    const int warps = threads / 32, wid = thread / 32;
+    const int per = max(1, min(warps / a.s.B, (a.s.max_blocks + 127) / 128)), step = warps / per;
+    const int first = wid < step * per ? wid / per : a.s.B;
+    const int len0 = first < a.s.B ? a.s.lens[first] : 0;
     const int live = a.head[0];
     pairs = a.head[1];
-    const int64_t all = static_cast<int64_t>(a.s.B) * a.s.max_blocks, step = gridDim.x * kCopyThreads;
-    for (int64_t i = blockIdx.x * kCopyThreads + threadIdx.x; i < pairs; i += step) {
+    for (int i = thread; i < pairs; i += threads) {
       a.s.refs[a.dst[i]] = a.s.refs[a.src[i]];
       a.s.refs[a.src[i]] = 0;
     }
-    for (int64_t i = blockIdx.x * kCopyThreads + threadIdx.x; pairs > 0 && i < all; i += step) {
-      const int b = static_cast<int>(i / a.s.max_blocks);
-      const int e = static_cast<int>(i - static_cast<int64_t>(b) * a.s.max_blocks);
-      const int len = a.s.lens[b];
-      if (e == 0 && (len < 0 || len > a.s.max_blocks * kPage)) raise_error(a.s.err, MLA_DEVERR_SEQ_LEN);
-      if (e >= pages_of(min(len, a.s.max_blocks * kPage))) continue;
-      const int page = a.s.table[i];
-      if (page < 0 || page >= a.s.num_blocks) {
-        raise_error(a.s.err, MLA_DEVERR_BLOCK_ID);
-      } else if (page >= live) {
-        const int k = a.number[page];
-        if (k >= 0) a.s.table[i] = a.dst[k];
-        else raise_error(a.s.err, MLA_DEVERR_PAGES);
+    for (int b = first; b < a.s.B; b += step) {
+      const int len = b == first ? len0 : a.s.lens[b], lane = thread % 32 + 32 * (wid % per);
+      if (lane == 0 && (len < 0 || len > a.s.max_blocks * kPage)) raise_error(a.s.err, MLA_DEVERR_SEQ_LEN);
+      int32_t *row = a.s.table + static_cast<int64_t>(b) * a.s.max_blocks;
+      const int end = pages_of(min(len, a.s.max_blocks * kPage));
+#pragma unroll 4
+      for (int e = lane; e < end; e += 32 * per) {
+        const int page = row[e];
+        if (page < 0 || page >= a.s.num_blocks) {
+          raise_error(a.s.err, MLA_DEVERR_BLOCK_ID);
+        } else if (page >= live) {
+          const int k = a.number[page];
+          if (k >= 0) row[e] = a.dst[k];
+          else raise_error(a.s.err, MLA_DEVERR_PAGES);
+        }
       }
     }
   }

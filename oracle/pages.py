@@ -147,8 +147,6 @@ def compact(pools, refs, table, lens):
             pool[d] = pool[s]
         refs[d], refs[s] = refs[s], 0
     for b in range(table.shape[0]):
-        if not now:
-            break
         if not 0 <= lens[b] <= table.shape[1] * BLOCK:
             errors.add("len")
         for k in range(min(max(_pages(lens[b]), 0), table.shape[1])):

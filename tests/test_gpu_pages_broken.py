@@ -54,3 +54,38 @@ def test_a_free_page_goes_to_one_owner(m, nb, n):
     assert len(set(last.tolist())) == n and (s.refs[last] == 1).all()
     shared = s.table[2:, :300]
     assert not np.isin(last, shared).any()
+
+
+@pytest.mark.parametrize("row,entry,error", [(0, -1, 1), (7, 40, 1), (40, 39, 16), (4999, 2 ** 31 - 1, 1), (4999, 38, 16)])
+def test_compact_flags_entries_where_nothing_moves(m, row, entry, error):
+    """Of few sequences and of many: whatever a warp has of the table."""
+    for B in (row + 1, 5000):
+        s = State("small", 40, B, 9, seed=row)
+        s.lens[row], s.table[row, :9] = 9 * 64 - 5, np.arange(9)
+        s.refs[:9] = 1
+        _load(s)
+        s.compact(m)
+        s.table[row, 8] = entry
+        _load(s)
+        s.compact(m)
+        s.table[row, 8], s.lens[row] = 8, 9 * 64 + 1
+        _load(s)
+        m.mla_cache_compact(s.pools, *s.d)
+        assert m.mla_get_device_error() == 2
+        s.lens[row], s.table[row, 3] = 2 ** 31 - 1, entry
+        _load(s)
+        s.compact(m)
+        s.lens[row] = -2 ** 31
+        _load(s)
+        s.compact(m)
+
+
+def test_compact_of_one_long_row(m):
+    """More entries than the grid has lanes for at once."""
+    nb, n = 400000, 300000
+    s = State("small", nb, 1, nb, [64 * n - 1], seed=77)
+    s.table[0, n - 1] = nb
+    s.table[0, 7] = -1
+    _load(s)
+    s.compact(m)
+    s.compact(m)

@@ -30,3 +30,12 @@ def test_forks_of_a_broken_last_page_leave_the_pages_to_the_others():
     refs, table, lens = np.array([2, 0]), np.array([[5], [0], [0], [-1], [-1]]), np.array([3, 7, 9, 0, 0])
     assert P.fork([np.zeros((2, 64, 1))], refs, table, lens, [0, 1], [3, 4]) == {"block"}
     assert table[:, 0].tolist() == [5, 0, 0, -1, 1] and refs.tolist() == [2, 1] and lens.tolist() == [3, 7, 9, 3, 7]
+
+
+def test_compact_looks_at_entries_where_nothing_moves():
+    refs = np.array([1, 1, 1, 0, 0])
+    table, lens = np.array([[0, 1], [2, 9], [4, -1]]), np.array([128, 100, 64])
+    assert P.compact([], refs, table, lens) == (3, {"block", "pages"})
+    assert table.tolist() == [[0, 1], [2, 9], [4, -1]] and refs.tolist() == [1, 1, 1, 0, 0]
+    assert P.compact([], refs, table, np.array([128, 64, 129])) == (3, {"len", "pages", "block"})
+    assert P.compact([], refs, table, np.array([128, 64, 0])) == (3, set())
