@@ -510,11 +510,13 @@ def mla_cache_resize(refs, block_table, seq_lens, new_lens):
     _binding.resize(refs, block_table, seq_lens, new_lens)
 
 
-def mla_cache_fork(pools, refs, block_table, seq_lens, parents, children, *, workspace=None):
+def mla_cache_fork(pools, refs, block_table, seq_lens, parents, children, *, by_rows=None, workspace=None):
     """The empty sequences children [n] go on from the sequences parents [n]
     (int32): full pages are shared, of a last one the tokens are copied in every
-    pool: rows of the pools [num_blocks, 64, ...], whole pages of the others."""
-    _binding.fork(pools, refs, block_table, seq_lens, parents, children, workspace)
+    pool.  by_rows, a list of bool, says of each pool whether its pages are 64 rows,
+    one a token, of which those of the tokens are copied, or are copied whole (None:
+    those [num_blocks, 64, ...] are, if their rows are whole 4-byte words)."""
+    _binding.fork(pools, refs, block_table, seq_lens, parents, children, by_rows, workspace)
 
 
 def mla_cache_compact(pools, refs, block_table, seq_lens, *, n_live=None, workspace=None):

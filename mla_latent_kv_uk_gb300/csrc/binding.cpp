@@ -388,7 +388,7 @@ struct Pools {
   static constexpr int kMost = 200;
   void *at[kMost];
   int64_t bytes[kMost];         // of a page
-  bool rows[kMost];             // a row for each of its 64 tokens
+  bool rows[kMost];             // a row, of whole 4-byte words, for each of its 64 tokens
   int n = 0;
   // Those by rows first; returns how many they are.
   int rows_first() {
@@ -428,8 +428,21 @@ void pools_of(PyObject *o, const char *name, int64_t &blocks, int dev, Pools &p,
     if (blocks < 0) blocks = t.size(0);
     if (t.size(0) != blocks) refuse(PyExc_ValueError, "%s differ in their number of pages", name);
     p.at[p.n] = t.data_ptr();
-    p.rows[p.n] = t.dim() > 1 && t.size(1) == 64;
-    p.bytes[p.n++] = t.numel() / blocks * static_cast<int64_t>(t.element_size());
+    p.bytes[p.n] = t.numel() / blocks * static_cast<int64_t>(t.element_size());
+    p.rows[p.n] = t.dim() > 1 && t.size(1) == 64 && p.bytes[p.n] % 256 == 0;
+    ++p.n;
+  }
+}
+// A list (or tuple) that says of each pool whether it goes by rows.
+void rows_of(PyObject *o, Pools &p) {
+  if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(PyExc_TypeError, "by_rows must be a list");
+  if (PySequence_Fast_GET_SIZE(o) != p.n) refuse(PyExc_ValueError, "by_rows must be as many as the pools");
+  for (int i = 0; i < p.n; ++i) {
+    PyObject *item = PySequence_Fast_ITEMS(o)[i];
+    if (!PyBool_Check(item)) refuse(PyExc_TypeError, "by_rows must hold truth values");
+    p.rows[i] = item == Py_True;
+    if (p.rows[i] && p.bytes[i] % 256)
+      refuse(PyExc_ValueError, "by_rows: a page of pool %d is not 64 rows of whole 4-byte words", i);
   }
 }
 at::Tensor scratch(int64_t bytes, int dev) {
@@ -493,10 +506,10 @@ PyObject *resize(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// (pools, refs, block_table, seq_lens, parents, children, workspace | None)
+// (pools, refs, block_table, seq_lens, parents, children, by_rows | None, workspace | None)
 PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    arguments(n, 7);
+    arguments(n, 8);
     const int dev = current_device(tensor(a[1], "refs"), "refs");
     const Sequences s(a[1], a[2], a[3], dev);
     const at::Tensor &from = dense(a[4], "parents", at::kInt, 1, dev), &to = dense(a[5], "children", at::kInt, 1, dev);
@@ -504,11 +517,12 @@ PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Pools p;
     int64_t pages = s.pages;
     pools_of(a[0], "pools", pages, dev, p);
+    if (a[6] != Py_None) rows_of(a[6], p);
     const int by_rows = p.rows_first();
     const int forks = narrow(from.size(0), "parents");
     size_t bytes = 0;
     call("mla_cache_fork", [&] { return entries.fork_size(forks, &bytes); });
-    const at::Tensor ws = a[6] != Py_None ? dense(a[6], "workspace", at::kByte, 1, dev)
+    const at::Tensor ws = a[7] != Py_None ? dense(a[7], "workspace", at::kByte, 1, dev)
                                           : scratch(static_cast<int64_t>(bytes), dev);
     const cudaStream_t stream = stream_of(dev);
     call("mla_cache_fork", [&] {
