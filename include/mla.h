@@ -593,7 +593,8 @@ int mla_cache_compact(void *const *pools, const int64_t *page_bytes,
  * MLA_DEVERR_RANGE; lengths out of range: MLA_DEVERR_SEQ_LEN; an entry that is
  * no page: MLA_DEVERR_BLOCK_ID: the sequence stays as it is, new_lens[b] =
  * seq_lens[b] (as where c < 0 and k = 0).  pools [num_blocks,64,576] of kv_dtype, 16-byte
- * aligned.  1 <= q_len, path_width <= 64.  new_lens is not seq_lens. */
+ * aligned.  1 <= q_len, path_width <= 64.  new_lens shares no memory with the
+ * arrays that are read. */
 int mla_cache_accept(void *const *pools, int kv_dtype, float *const *kv_scales,
                      int scale_block, int n_pools, int num_blocks,
                      const int32_t *block_table, const int32_t *seq_lens,

@@ -1065,8 +1065,15 @@ extern "C" int mla_cache_accept(void *const *pools, int kv_dtype, float *const *
     return MLA_ERR_INVALID_ARG;
   if (kv_scales && (kv_dtype != MLA_E4M3 || (scale_block != 16 && scale_block != 32 && scale_block != 64)))
     return MLA_ERR_INVALID_ARG;
-  if (!block_table || !seq_lens || !path || !path_lens || !new_lens || new_lens == seq_lens ||
-      (n_pools > 0 && !pools))
+  if (!block_table || !seq_lens || !path || !path_lens || !new_lens || (n_pools > 0 && !pools))
+    return MLA_ERR_INVALID_ARG;
+  // (a request's CTAs all read these, and one of them writes its new length)
+  auto meets = [&](const int32_t *p, int64_t n) {
+    const auto at = reinterpret_cast<uintptr_t>(p), out = reinterpret_cast<uintptr_t>(new_lens);
+    return p && at < out + sizeof(int32_t) * B && out < at + sizeof(int32_t) * n;
+  };
+  if (meets(seq_lens, B) || meets(tree_lens, B) || meets(path_lens, B) ||
+      meets(path, static_cast<int64_t>(B) * path_width) || meets(block_table, static_cast<int64_t>(B) * max_blocks))
     return MLA_ERR_INVALID_ARG;
   AcceptArgs a{};
   for (int k = 0; k < n_pools; ++k) {
