@@ -85,7 +85,11 @@
 // product is at 1.73 for the power that it takes; 16 over 4096 200 (208): 2830
 // cycles a tile of 128 keys, 2208 of them MMAs, 280 waits for keys (L2 gives an SM 48
 // bytes a clock, of 58 at most), 220 for probabilities; 64 tokens over 16384 keys
-// of blocks of 64 tokens 160 (163): the passes over O where a block's scale differs.
+// of blocks of 64 tokens 161 (163): the passes over O where a block's scale differs.
+// How a decode is cut goes by the table's width, not by the lengths, which only the device
+// knows: over a table of 2048 columns the smallest tree takes 13 us in place of 10 (it may
+// be long, so it is cut), that over 16384 keys 167 in place of 161, the batch of 16 204 to
+// 210 in place of 200.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -127,8 +131,9 @@ constexpr int kSBufs = 4;                    // Q K^T runs two tiles ahead of P 
 // hold two tiles of keys and values, so that a tile's values are on their way
 // while the last one's are read.  (A two-page tile runs Q K^T at twice the
 // rate, but there is room for one only, in slots that wait 2500 cycles for
-// their next load: the speculative batch took 140 us instead of 146, a window
-// of 128 10.3 instead of 8.8, the batch of 32 the same.)
+// their next load: when this was measured the speculative batch took 140 us instead of
+// 146 (143 with parts merged by spans), a window of 128 10.3 instead of 8.8, the batch of
+// 32 the same.)
 //
 // WIDE (a tree over a bf16 cache): tiles of two pages after all, where the keys
 // come in three pieces by columns and the values in two, one for each of the

@@ -14,13 +14,13 @@
 // through distributed shared memory, and each free page then finds the row that
 // it goes to by the number of free pages in front of it.  Latency is all it costs:
 // two or three cluster barriers and as many rounds of loads.  On the device, calls
-// behind one another: a resize 2.5 us that has nothing to do, 3.6 to 5 otherwise, in
-// pools of up to 60000 pages; the bookkeeping of 64 forks of 100 pages each 5.2; a
-// compaction that finds nothing to move 4.3 with its empty copy.
+// behind one another: a resize 2.5 to 2.9 us that has nothing to do, 4.1 to 5.2 otherwise,
+// in pools of up to 60000 pages; the bookkeeping of 64 forks of 100 pages each 6.9; a
+// compaction of 48 sequences that finds nothing to move 4.9 with its empty copy.
 //
 // Copies take a list of pages from the bookkeeping kernel (or the caller) and
 // go over all layers' caches in one launch: 500 pages of 12 e4m3 layers, 442 MB, in
-// 68 to 69 us, 0.96 of a plain copy's rate; 6 pages of 4 bf16 layers in 3.
+// 69.4 us, 0.95 of a plain copy's rate; 6 pages of 4 bf16 layers in 3.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -41,8 +41,9 @@ constexpr int kCtas = 8, kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 static_assert(kMaxWarps <= 32 && kCtas <= 32, "a lane each");
 
 // Threads of a CTA: few where there is little to count (64 forks of 8 sequences in a
-// pool of 1500 pages, with the free in front of it, 256 / 512 / 1024 threads: 10.0 / 10.8 /
-// 11.6 us; a resize in one of 60000 pages 5.2 / 5.1 / 5.4, of 500000 20.3 / 11.7 / 8.3).
+// pool of 1500 pages, with the free in front of it and no copies, 256 / 512 / 1024 threads:
+// 11.3 / 12.0 / 13.1 us; a resize of 8 sequences in one of 1500 pages 4.1 / 4.3 / 5.0, of
+// 60000 5.2 / 5.2 / 5.7, of 140000 6.5 / 5.9 / 6.3, of 500000 11.0 / 8.4 / 7.7).
 int threads_for(int num_blocks, int rows) {
   return num_blocks <= (1 << 14) && rows <= 512 ? 256 : num_blocks <= (1 << 17) && rows <= 1024 ? 512 : kMaxThreads;
 }
@@ -521,9 +522,9 @@ struct CopyArgs {
 // e4m3 layers, 442 MB, in 6000 CTAs 69 us; in 608 that stay, four to an SM, 76: some
 // SMs are slower, and the last ones' runs are what is waited for).  Of a compaction
 // only the device knows how many there are: 608 CTAs take them from a counter (48
-// requests, 280 MB in 4 layers, with two resizes around it: 58.7 us, in runs 63.4,
-// in 4096 CTAs 57.2, but then one that moves nothing 9.3 in place of 5.2).  A pair's
-// ids are looked at while the first item's loads are on their way.
+// requests, 280 MB in 4 layers, with two resizes around it: 57.4 us; when this was chosen,
+// 58.7, in runs 63.4, in 4096 CTAs 57.2, but then one that moves nothing 9.3 in place of
+// 5.2, now 4.9).  A pair's ids are looked at while the first item's loads are on their way.
 template <int MODE, int L>
 __device__ __forceinline__ void copy_items(const CopyArgs &a, const Pools &p, int pairs) {
   constexpr int kParts = kLoads / L;
