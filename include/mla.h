@@ -477,7 +477,9 @@ int mla_decode_paged_scaled(const void *q, float q_scale, const void *kv_cache,
  * counts as 0.  kv_scales [num_blocks, 64/scale_block]: a block-scaled e4m3
  * cache (k_scale is not used), else NULL.  Precision, limits, split_tiles, the
  * workspace's use and what is not read as in mla_decode_paged_window; it has
- * mla_decode_tree_workspace_size(B, q_len, H, max_blocks*64, split_tiles) bytes. */
+ * mla_decode_tree_workspace_size(B, q_len, H, max_blocks*64, split_tiles) bytes.
+ * How a call is cut goes by max_blocks: a table far wider than its sequences
+ * costs short calls up to 3 us. */
 int mla_decode_tree_workspace_size(int B, int q_len, int H, int max_seq_len,
                                    int split_tiles, size_t *bytes);
 
@@ -507,19 +509,19 @@ int mla_decode_paged_tree(const void *q, int q_dtype, float q_scale,
  *
  * Pools are what a page has in memory: for every layer its cache [num_blocks,
  * 64,576], its block scales, or anything else of num_blocks rows, each given
- * once (no two share memory).  pools and
- * page_bytes are HOST arrays of n_pools (0 to 200) device pointers and of a
- * page's bytes in each: multiples of 4; pools whose page is a multiple of 16
- * and 1024 or more start on 16 bytes, the others on 4.  num_blocks < 2^25.
+ * once (no two share memory).  pools and page_bytes are HOST arrays of n_pools
+ * (0 to 200) device pointers and of a page's bytes in each: multiples of 4;
+ * pools whose page is a multiple of 16 and 1024 or more start on 16 bytes, the
+ * others on 4.  num_blocks < 2^25.
  * 1 <= B <= 8192, 1 <= max_blocks <= 2^24, B * max_blocks < 2^31
  * (mla_cache_accept: any B >= 1).
  *
  * Copy: page dst[k] of every pool becomes page src[k], k < n (int32 [n]).
  * A negative id is padding, and so is a page onto itself; an id >= num_blocks
- * sets MLA_DEVERR_BLOCK_ID, and the pair is left out.  Of equal destinations the last one's pair counts.  A
- * destination that is another pair's source is not written and sets
- * MLA_DEVERR_PAGES.  refs and tables are the caller's business here.
- * 0 <= n <= 65536.  Every pair looks at all others, which takes 24 us of 4096
+ * sets MLA_DEVERR_BLOCK_ID, and the pair is left out.  Of equal destinations
+ * the last one's pair counts.  A destination that is another pair's source is
+ * not written and sets MLA_DEVERR_PAGES.  refs and tables are the caller's
+ * business here.  0 <= n <= 65536.  Every pair looks at all others, which takes 24 us of 4096
  * pairs, 250 of 16384 and 3.7 ms of 65536: long lists are better cut. */
 int mla_cache_copy(void *const *pools, const int64_t *page_bytes, int n_pools,
                    int num_blocks, const int32_t *src, const int32_t *dst,

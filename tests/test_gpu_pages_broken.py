@@ -89,3 +89,30 @@ def test_compact_of_one_long_row(m):
     _load(s)
     s.compact(m)
     s.compact(m)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_any_calls_on_any_state(m, seed):
+    """Tables over any pages, counted, and then broken here and there."""
+    g = np.random.default_rng(9000 + seed)
+    nb, B, mb = (int(np.exp(g.uniform(0, np.log(n)))) for n in (20000, 700, 300))
+    s = State("rows" if nb < 100 else "small", nb, B, mb, seed=seed)
+    s.lens[:] = g.integers(0, mb * 64 + 1, B) * (g.random(B) < 0.6)
+    s.lens[np.cumsum(-(-s.lens // 64)) > nb * g.uniform(0.2, 1.5)] = 0
+    for b, n in enumerate(-(-s.lens // 64)):
+        s.table[b, :n] = g.integers(0, nb, n)
+        np.add.at(s.refs, s.table[b, :n], 1)
+    for x, values in ((s.table, [-1, nb, nb - 1, 0, 2 ** 31 - 1, -2 ** 31]), (s.refs, [0, 0, 1, 5, -1, -7]),
+                      (s.lens, [-1, mb * 64 + 1, 2 ** 31 - 1, -2 ** 31])):
+        here = g.random(x.shape) < g.choice([0, 0.001, 0.02, 0.2])
+        x[here] = g.choice(values, here.sum())
+    _load(s)
+    for _ in range(4):
+        what = int(g.integers(0, 4))
+        if what == 0:
+            s.resize(m, np.where(g.random(B) < 0.5, s.lens, g.integers(0, mb * 64 + 1, B)))
+        elif what < 3:
+            n = int(np.exp(g.uniform(0, np.log(1500))))
+            s.fork(m, g.integers(-1, B, n), g.integers(0, B + 1, n))
+        else:
+            s.compact(m)
